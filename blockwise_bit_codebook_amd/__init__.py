@@ -9,7 +9,10 @@ not been built, the first call raises ``ImportError``: there is no fallback.
 Entry points carry the C names (``quantize_kbit_bf16_k4``,
 ``quantize_kbit_e4m4_bf16_k4``, ``dequantize_4bit_nested_fp16``, ...) and a
 few dtype/K-dispatching conveniences (``quantize_kbit``, ``dequantize_kbit``,
-``dequantize_4bit_nested``, ``quantize_act_fwht_k4_bf16``).  The block scales
+``dequantize_4bit_nested``, ``quantize_act_fwht_k4_bf16``).  The operators
+around a quantized layer (int8 linear, rotary positions, head norms, paged
+cache; C ABI in ``include/kbit_layer.h``) are in ``layer.py`` and reached from
+here as well.  The block scales
 are fp32 absmax values or, with ``absmax_format="e4m4"``, one E4M4 byte per
 block (uint8 tensor).
 """
@@ -474,3 +477,19 @@ def _install_named():
 
 
 _install_named()
+
+# The operators around a quantized layer need torch at import; they are bound
+# on first use, so that the host-only functions stay usable without it.
+_LAYER = ("quantize_rows_int8", "linear_int8", "linear_int8_dynamic", "rope_frequencies", "rope_table", "rope",
+          "qk_norm_rope", "qk_norm_rope_backward", "append_kv_paged")
+__all__ += _LAYER
+
+
+def __getattr__(name):
+    if name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import layer
+    g = globals()
+    for n in _LAYER:
+        g[n] = getattr(layer, n)
+    return g[name]

@@ -58,19 +58,52 @@ def _signatures():
 SIGNATURES = _signatures()
 
 
+def _layer_signatures():
+    """(name, argtypes) for every C entry point declared in include/kbit_layer.h."""
+    f64 = ct.c_double
+    view = [_p, _i64, _i64, _i64]
+    turn = [_p, _i32, _p, _i32, _i64, _i32]  # positions, their bytes, table, rot, max_pos, layout
+    sig = [
+        ("linear_int8_workspace_bytes", [_i64, _i32, _i32]),
+        ("linear_int8_dynamic_workspace_bytes", [_i64, _i32, _i32]),
+        ("qk_norm_rope_backward_workspace_bytes", [_i32]),
+        ("rope_frequencies", [_i32, f64, _i32, f64, f64, f64, f64, _p, _p]),
+        ("rope_table", [_p, _i32, _i64, f64, _p, _p]),
+    ]
+    for t in DTYPES:
+        sig += [
+            (f"quantize_rows_int8_{t}", [_p, _i64, _i32, _i64, _p, _i64, _p, _p]),
+            (f"linear_int8_{t}", [_p, _p, _i64, _i32, _i64, _p, _p, _i32, _i64, _p, _p, _i64, _p, _i64, _p]),
+            (f"linear_int8_dynamic_{t}", [_p, _i64, _i32, _i64, _p, _p, _i32, _i64, _p, _p, _i64, _p, _i64, _p]),
+            (f"rope_{t}", view * 2 + [_i64, _i64, _i32, _i32] + turn + [_i32, _p]),
+            (f"qk_norm_rope_{t}", view * 4 + [_i64, _i64, _i32, _i32, _i32, _p, _p, _i32, _f32] + turn + [_p]),
+            (f"qk_norm_rope_backward_{t}",
+             view * 6 + [_i64, _i64, _i32, _i32, _i32, _p, _p, _i32, _p, _p, _f32] + turn + [_p, _i64, _p]),
+            (f"append_kv_paged_{t}",
+             [_p, _i64, _i64] * 2 + [_i64, _i32, _i32, _i32, _p, _i32] + view * 2 + [_i64, _i32] + turn + [_p]),
+        ]
+    return sig
+
+
+LAYER_SIGNATURES = _layer_signatures()
+
+
 def load(path=LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
             f"libkbit.so not found at {path}; build it with "
             "`python -m blockwise_bit_codebook_amd.build` (hipcc, gfx950)")
     lib = ct.CDLL(path)
-    for name, args in SIGNATURES:
+    for name, args in SIGNATURES + LAYER_SIGNATURES:
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = {"kbit_strerror": ct.c_char_p, "kbit_nested_workspace_bytes": ct.c_int64,
                       "kbit_nested_noalloc_scratch_bytes": ct.c_int64,
                       "kbit_quantize_nested_workspace_bytes": ct.c_int64,
-                      "kbit_act_tables_bytes": ct.c_int64}.get(name, ct.c_int)
+                      "kbit_act_tables_bytes": ct.c_int64,
+                      "linear_int8_workspace_bytes": ct.c_int64,
+                      "linear_int8_dynamic_workspace_bytes": ct.c_int64,
+                      "qk_norm_rope_backward_workspace_bytes": ct.c_int64}.get(name, ct.c_int)
     return lib
 
 

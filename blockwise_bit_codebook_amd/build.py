@@ -27,8 +27,8 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 
 HIP_SOURCES = ["quantize.hip", "dequantize.hip", "nested_encode.hip", "linear.hip", "act_fwht.hip",
-               "act_block.hip"]
-CXX_SOURCES = ["api.cpp", "codebook.cpp"]
+               "act_block.hip", "heads.hip", "int8.hip"]
+CXX_SOURCES = ["api.cpp", "codebook.cpp", "layer_api.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 HIP_FLAGS = [

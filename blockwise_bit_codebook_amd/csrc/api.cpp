@@ -130,6 +130,8 @@ int device_cu_count() {
     return v > 0 ? v : 1;
 }
 
+bool device_usable() { return current_device_cus() > 0; }
+
 int current_device_index() {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0) return -1;

@@ -1,0 +1,585 @@
+// Passes over the heads of queries, keys and values: rotary positions, the
+// RMS norm of every head with the rotation in the same pass, its gradient,
+// and the append to a paged cache with the rotation on the way.
+//
+// Mathematics, per row (one head of one token, D elements, the first `rot`
+// of them rotated):
+//   norm      x <- x / sqrt(mean(x^2) + eps) * w
+//   rotation  (a, b) -> (a c - b s, b c + a s) for every pair; c and s are
+//             the token's row of the table (amplitude times cosine and sine
+//             of position times frequency, fp64 rounded once to fp32).  The
+//             pairs are (i, i + rot / 2) in the half layout and (2i, 2i + 1)
+//             in the interleaved one; elements from `rot` on pass through.
+//   gradient  of the norm with rotation: u = R^T g (the rotation with s
+//             negated), xhat = x / sqrt(mean(x^2) + eps) =: x r,
+//             dw = sum over tokens and heads of u xhat,
+//             dx = r (u w - xhat mean(u w xhat)).
+// All of it in fp32 without contraction, rounded once to the element type.
+//
+// Layout: a group of GP lanes (a power of two) holds one row, each lane two
+// 16-byte (32-byte for fp32) pieces chosen so that both elements of every
+// pair are in the same lane: pieces j and j + rot/16 in the half layout, 2j
+// and 2j + 1 in the interleaved one.  So a row is read once, the sum of
+// squares needs log2(GP) exchanges, and writing in place is safe.  A lane
+// group takes R heads of one token, so that the token's cosines and sines
+// are fetched once for R rows and all R rows' loads are in flight together.
+// Rows whose sizes or addresses do not allow 16-byte pieces go element by
+// element, one wave a row, with the same arithmetic.
+#include "device.h"
+#include "kbit_internal.h"
+#include "launch.h"
+#include "layer_internal.h"
+
+namespace kbit {
+namespace {
+
+// Workgroups of a pass over heads at most; beyond it a group takes several units.
+constexpr unsigned kMaxHeadsGrid = 1u << 22;
+
+constexpr int kHalf = 0, kInterleaved = 1;
+
+// Element types: 8 consecutive elements as raw vectors, widened exactly.
+struct HF32 {
+    using T = float;
+    static constexpr int kVec = 2;
+    static __device__ float one(T v) { return v; }
+    static __device__ T narrow(float v) { return v; }
+    static __device__ void widen(const u32x4* r, float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = __uint_as_float(r[0][i]);
+            x[4 + i] = __uint_as_float(r[1][i]);
+        }
+    }
+    static __device__ void store8(T* p, const float (&v)[8]) {
+        store16<false>(p, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                __float_as_uint(v[3])});
+        store16<false>(p + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                                    __float_as_uint(v[7])});
+    }
+};
+
+struct HF16 {
+    using T = uint16_t;
+    static constexpr int kVec = 1;
+    static __device__ float one(T v) { return Fp16::h2f(v); }
+    static __device__ T narrow(float v) { return static_cast<T>(pack_f16x2(v, 0.0f) & 0xFFFFu); }
+    static __device__ void widen(const u32x4* r, float (&x)[8]) { Fp16::unpack(r, x); }
+    static __device__ void store8(T* p, const float (&v)[8]) {
+        store16<false>(p, u32x4{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
+                                pack_f16x2(v[6], v[7])});
+    }
+};
+
+struct HB16 {
+    using T = uint16_t;
+    static constexpr int kVec = 1;
+    static __device__ float one(T v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+    static __device__ T narrow(float v) { return static_cast<T>(pack_bf16x2(v, 0.0f) & 0xFFFFu); }
+    static __device__ void widen(const u32x4* r, float (&x)[8]) { Bf16::unpack(r, x); }
+    static __device__ void store8(T* p, const float (&v)[8]) {
+        store16<false>(p, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                pack_bf16x2(v[6], v[7])});
+    }
+};
+
+// Which 16 elements of its row a lane holds.  Vector form: piece A is the 8
+// elements from `a`, piece B the 8 from `b` (negative: none).  Element form
+// (one wave a row): pair i of the lane is pair slot lane + 64 i.
+struct Slots {
+    int a, b;        // vector form: first elements, or -1
+    int pair;        // vector form: first of the lane's 8 pairs in the table row
+    bool ra, rb;     // vector form: piece A (and in the half layout B with it) / piece B rotated
+};
+
+template <int LAYOUT>
+__device__ __forceinline__ Slots vector_slots(int j, int D, int rot) {
+    Slots s;
+    s.pair = 8 * j;
+    if constexpr (LAYOUT == kHalf) {
+        const int half = rot >> 1;
+        if (8 * j < half) {
+            s.a = 8 * j;
+            s.b = half + 8 * j;
+            s.ra = s.rb = true;
+        } else {
+            const int base = rot + 16 * (j - (half >> 3));
+            s.a = base < D ? base : -1;
+            s.b = base + 8 < D ? base + 8 : -1;
+            s.ra = s.rb = false;
+        }
+    } else {
+        s.a = 16 * j < D ? 16 * j : -1;
+        s.b = 16 * j + 8 < D ? 16 * j + 8 : -1;
+        s.ra = 16 * j < rot;
+        s.rb = 16 * j + 8 < rot;
+    }
+    return s;
+}
+
+// Element form: elements (ea, eb) of pair slot p (negative: none) and
+// whether they are rotated.
+template <int LAYOUT>
+__device__ __forceinline__ void element_pair(int p, int D, int rot, int& ea, int& eb, bool& turned) {
+    if constexpr (LAYOUT == kHalf) {
+        const int half = rot >> 1;
+        turned = p < half;
+        ea = turned ? p : rot + 2 * (p - half);
+        eb = turned ? p + half : ea + 1;
+    } else {
+        ea = 2 * p;
+        eb = ea + 1;
+        turned = ea < rot;
+    }
+    if (ea >= D) ea = -1;
+    if (eb >= D) eb = -1;
+}
+
+// The 16 raw elements of a lane before widening.
+template <class E, bool VEC>
+struct Raw {
+    u32x4 v[VEC ? 2 * E::kVec : 1];
+    typename E::T s[VEC ? 1 : 16];
+};
+
+template <class E, int LAYOUT, bool VEC>
+__device__ __forceinline__ void load_row(const typename E::T* p, int lane, int D, int rot, const Slots& sl,
+                                         Raw<E, VEC>& r) {
+    if constexpr (VEC) {
+        constexpr int V = E::kVec;
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) r.v[i] = u32x4{0u, 0u, 0u, 0u};
+        if (sl.a >= 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) r.v[i] = load16<false>(p + sl.a + 4 * i);
+        }
+        if (sl.b >= 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) r.v[V + i] = load16<false>(p + sl.b + 4 * i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            int ea, eb;
+            bool turned;
+            element_pair<LAYOUT>(lane + kWave * i, D, rot, ea, eb, turned);
+            r.s[i] = ea >= 0 ? p[ea] : typename E::T(0);
+            r.s[8 + i] = eb >= 0 ? p[eb] : typename E::T(0);
+        }
+    }
+}
+
+template <class E, bool VEC>
+__device__ __forceinline__ void widen_row(const Raw<E, VEC>& r, float (&a)[8], float (&b)[8]) {
+    if constexpr (VEC) {
+        E::widen(r.v, a);
+        E::widen(r.v + E::kVec, b);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a[i] = E::one(r.s[i]);
+            b[i] = E::one(r.s[8 + i]);
+        }
+    }
+}
+
+template <class E, int LAYOUT, bool VEC>
+__device__ __forceinline__ void store_row(typename E::T* p, int lane, int D, int rot, const Slots& sl,
+                                          const float (&a)[8], const float (&b)[8]) {
+    if constexpr (VEC) {
+        if (sl.a >= 0) E::store8(p + sl.a, a);
+        if (sl.b >= 0) E::store8(p + sl.b, b);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            int ea, eb;
+            bool turned;
+            element_pair<LAYOUT>(lane + kWave * i, D, rot, ea, eb, turned);
+            if (ea >= 0) p[ea] = E::narrow(a[i]);
+            if (eb >= 0) p[eb] = E::narrow(b[i]);
+        }
+    }
+}
+
+// The lane's 8 cosines and sines (1 and 0 where nothing is rotated, so that
+// the rotation leaves those elements as they are: x * 1 - y * 0 is x for
+// finite y only, hence turn() skips them instead).
+struct Angles {
+    float c[8], s[8];
+};
+
+template <int LAYOUT, bool VEC>
+__device__ __forceinline__ void load_angles(const float* table, int64_t pos, int64_t max_pos, int lane, int D, int rot,
+                                            const Slots& sl, float sign, Angles& g) {
+    // A position outside the table poisons the rotated elements.
+    const bool ok = pos >= 0 && pos < max_pos;
+    const float* row = table + (ok ? pos : 0) * rot;
+    const float bad = __uint_as_float(0x7FC00000u);
+    if constexpr (VEC) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool live = LAYOUT == kHalf ? sl.ra : (h == 0 ? sl.ra : sl.rb);
+            u32x4 c = u32x4{0u, 0u, 0u, 0u}, s = c;
+            if (live) {
+                c = load16<false>(row + sl.pair + 4 * h);
+                s = load16<false>(row + (rot >> 1) + sl.pair + 4 * h);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                g.c[4 * h + i] = ok ? __uint_as_float(c[i]) : bad;
+                g.s[4 * h + i] = ok ? sign * __uint_as_float(s[i]) : bad;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int p = lane + kWave * i;
+            const bool live = p < (rot >> 1);
+            g.c[i] = ok ? (live ? row[p] : 1.0f) : bad;
+            g.s[i] = ok ? (live ? sign * row[(rot >> 1) + p] : 0.0f) : bad;
+        }
+    }
+}
+
+__device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s, bool on) {
+    const float nx = x * c - y * s, ny = y * c + x * s;
+    x = on ? nx : x;
+    y = on ? ny : y;
+}
+
+template <int LAYOUT, bool VEC>
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const Angles& g, int lane, int D, int rot,
+                                     const Slots& sl) {
+    if constexpr (!VEC) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn_pair(a[i], b[i], g.c[i], g.s[i], lane + kWave * i < (rot >> 1));
+    } else if constexpr (LAYOUT == kHalf) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn_pair(a[i], b[i], g.c[i], g.s[i], sl.ra);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            turn_pair(a[2 * i], a[2 * i + 1], g.c[i], g.s[i], sl.ra);
+            turn_pair(b[2 * i], b[2 * i + 1], g.c[4 + i], g.s[4 + i], sl.rb);
+        }
+    }
+}
+
+// Sum over the lane group (lanes = 1 .. 64, uniform over the grid).
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+    if (lanes >= 2) v += dpp_f32<kDppXor1>(v);
+    if (lanes >= 4) v += dpp_f32<kDppXor2>(v);
+    if (lanes >= 8) v += dpp_f32<kDppHalfMirror>(v);
+    if (lanes >= 16) v += dpp_f32<kDppMirror>(v);
+    if (lanes >= 32) v += shfl_xor_f32(v, 16);
+    if (lanes >= 64) v += shfl_xor_f32(v, 32);
+    return v;
+}
+
+__device__ __forceinline__ int64_t load_index(const void* p, int64_t i, bool wide) {
+    return wide ? static_cast<const int64_t*>(p)[i] : static_cast<const int32_t*>(p)[i];
+}
+
+template <class E, int LAYOUT, bool VEC>
+__device__ __forceinline__ void load_weight(const void* w, bool w_fp32, int lane, int D, int rot, const Slots& sl,
+                                            float (&a)[8], float (&b)[8]) {
+    if (w_fp32) {
+        Raw<HF32, VEC> r;
+        load_row<HF32, LAYOUT, VEC>(static_cast<const float*>(w), lane, D, rot, sl, r);
+        widen_row<HF32, VEC>(r, a, b);
+    } else {
+        Raw<E, VEC> r;
+        load_row<E, LAYOUT, VEC>(static_cast<const typename E::T*>(w), lane, D, rot, sl, r);
+        widen_row<E, VEC>(r, a, b);
+    }
+}
+
+// One pass over up to two sets of heads (queries and keys, or keys and
+// values).  NORM: norm before the rotation.  PAGED: the output row is found
+// through the token's slot; set 1 is copied.
+template <class E, int LAYOUT, bool NORM, bool PAGED, bool VEC, int R>
+__global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs p) {
+    using T = typename E::T;
+    const int lg = VEC ? p.log2_lanes : 6;
+    const int lane = threadIdx.x & ((1 << lg) - 1);
+    const uint32_t step = gridDim.x * (kThreads >> lg);
+    const uint32_t per_token = p.set[0].units + p.set[1].units;
+    const int64_t b = blockIdx.y;
+    for (uint32_t unit = blockIdx.x * (kThreads >> lg) + (threadIdx.x >> lg); unit < p.units; unit += step) {
+        const uint32_t t = unit / per_token;
+        uint32_t u = unit - t * per_token;
+        const bool second = u >= static_cast<uint32_t>(p.set[0].units);
+        const HeadSet& set = p.set[second ? 1 : 0];
+        if (second) u -= p.set[0].units;
+        const int h0 = static_cast<int>(u) * R;
+        const int D = set.dim, rot = set.rot;
+        const Slots sl = vector_slots<LAYOUT>(lane, D, rot);
+
+        int64_t at = 0;
+        if constexpr (PAGED) {
+            const int64_t slot = load_index(p.slots, t, p.slots_wide);
+            if (slot < 0 || slot >= p.n_slots) continue;  // padding, or outside the cache: nothing is written
+            const uint32_t page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page_size);
+            const uint32_t off = static_cast<uint32_t>(slot) - page * p.page_size;
+            at = page * set.out_b + off * set.out_s;
+        } else {
+            at = b * set.out_b + t * set.out_s;
+        }
+        T* out = static_cast<T*>(set.out) + at;
+        const T* in = static_cast<const T*>(set.in) + b * set.in_b + t * set.in_s;
+        Raw<E, VEC> raw[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (h0 + r < set.heads) load_row<E, LAYOUT, VEC>(in + (h0 + r) * set.in_h, lane, D, rot, sl, raw[r]);
+        Angles g;
+        if (rot > 0) {
+            const int64_t pos = load_index(p.positions, b * p.tokens + t, p.positions_wide);
+            load_angles<LAYOUT, VEC>(p.table, pos, p.max_pos, lane, D, rot, sl, p.sign, g);
+        }
+        float wa[8], wb[8];
+        if constexpr (NORM) load_weight<E, LAYOUT, VEC>(set.weight, p.weight_fp32, lane, D, rot, sl, wa, wb);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (h0 + r >= set.heads) break;
+            float xa[8], xb[8];
+            widen_row<E, VEC>(raw[r], xa, xb);
+            if constexpr (NORM) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
+                ss = group_sum(ss, 1 << lg);
+                const float rs = 1.0f / sqrtf(ss / static_cast<float>(D) + p.eps);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    xa[i] = xa[i] * rs * wa[i];
+                    xb[i] = xb[i] * rs * wb[i];
+                }
+            }
+            if (rot > 0) turn<LAYOUT, VEC>(xa, xb, g, lane, D, rot, sl);
+            store_row<E, LAYOUT, VEC>(out + (h0 + r) * set.out_h, lane, D, rot, sl, xa, xb);
+        }
+    }
+}
+
+// Gradient of the norm with rotation.  Workgroups below `first_groups` work
+// through the rows of set 0, the others through set 1's; each keeps its sum
+// of u * xhat in registers, adds its lane groups in LDS in a fixed order and
+// stores one partial row of D sums, which norm_weight_grad_kernel adds in a
+// fixed order: the result does not depend on scheduling.
+template <class E, int LAYOUT, bool VEC>
+__global__ __launch_bounds__(kThreads) void norm_back_kernel(const NormBackArgs p) {
+    using T = typename E::T;
+    __shared__ float red[kThreads * 16];
+    const int lg = VEC ? p.log2_lanes : 6;
+    const int groups = kThreads >> lg;
+    const int lane = threadIdx.x & ((1 << lg) - 1);
+    const int group = threadIdx.x >> lg;
+    const bool second = blockIdx.x >= static_cast<unsigned>(p.first_groups);
+    const BackSet& set = p.set[second ? 1 : 0];
+    const int block = blockIdx.x - (second ? p.first_groups : 0);
+    const int blocks = second ? gridDim.x - p.first_groups : p.first_groups;
+    const int D = p.dim, rot = p.rot;
+    const Slots sl = vector_slots<LAYOUT>(lane, D, rot);
+    float wa[8], wb[8], da[8], db[8];
+    load_weight<E, LAYOUT, VEC>(set.weight, p.weight_fp32, lane, D, rot, sl, wa, wb);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) da[i] = db[i] = 0.0f;
+
+    const uint32_t rows = set.rows;
+    for (uint32_t row = block * groups + group; row < rows; row += blocks * groups) {
+        const uint32_t bt = row / static_cast<uint32_t>(set.heads);
+        const uint32_t h = row - bt * set.heads;
+        const uint32_t b = bt / static_cast<uint32_t>(p.tokens);
+        const uint32_t t = bt - b * p.tokens;
+        const T* x = static_cast<const T*>(set.x) + b * set.x_b + t * set.x_s + h * set.x_h;
+        const T* gr = static_cast<const T*>(set.g) + b * set.g_b + t * set.g_s + h * set.g_h;
+        T* dx = static_cast<T*>(set.dx) + b * set.dx_b + t * set.dx_s + h * set.dx_h;
+        Raw<E, VEC> rx, rg;
+        load_row<E, LAYOUT, VEC>(x, lane, D, rot, sl, rx);
+        load_row<E, LAYOUT, VEC>(gr, lane, D, rot, sl, rg);
+        Angles g;
+        const int64_t pos = load_index(p.positions, bt, p.positions_wide);
+        load_angles<LAYOUT, VEC>(p.table, pos, p.max_pos, lane, D, rot, sl, -1.0f, g);
+        float xa[8], xb[8], ga[8], gb[8];
+        widen_row<E, VEC>(rx, xa, xb);
+        widen_row<E, VEC>(rg, ga, gb);
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
+        ss = group_sum(ss, 1 << lg);
+        const float rs = 1.0f / sqrtf(ss / static_cast<float>(D) + p.eps);
+        turn<LAYOUT, VEC>(ga, gb, g, lane, D, rot, sl);
+        float inner = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            xa[i] *= rs;
+            xb[i] *= rs;
+            da[i] += ga[i] * xa[i];
+            db[i] += gb[i] * xb[i];
+            ga[i] *= wa[i];
+            gb[i] *= wb[i];
+            inner += ga[i] * xa[i] + gb[i] * xb[i];
+        }
+        inner = group_sum(inner, 1 << lg) / static_cast<float>(D);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            xa[i] = rs * (ga[i] - xa[i] * inner);
+            xb[i] = rs * (gb[i] - xb[i] * inner);
+        }
+        store_row<E, LAYOUT, VEC>(dx, lane, D, rot, sl, xa, xb);
+    }
+    float* mine = red + group * D;  // groups * D <= kThreads * 16
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (sl.a >= 0) mine[sl.a + i] = da[i];
+            if (sl.b >= 0) mine[sl.b + i] = db[i];
+        }
+    } else {
+        store_row<HF32, LAYOUT, false>(mine, lane, D, rot, sl, da, db);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < D; e += kThreads) {
+        float sum = red[e];
+        for (int q = 1; q < groups; ++q) sum += red[q * D + e];
+        p.partial[static_cast<int64_t>(blockIdx.x) * D + e] = sum;
+    }
+}
+
+// Adds the partial rows: 16 columns a workgroup, 64 row strides, then a tree.
+constexpr int kGradCols = 16, kGradSplits = 64;
+__global__ __launch_bounds__(kGradCols* kGradSplits) void norm_weight_grad_kernel(const float* __restrict__ partial,
+                                                                                 int D, int first, int total,
+                                                                                 float* __restrict__ d0,
+                                                                                 float* __restrict__ d1) {
+    __shared__ float red[kGradSplits][kGradCols + 1];
+    const int c = threadIdx.x % kGradCols, r = threadIdx.x / kGradCols;
+    const int e = blockIdx.x * kGradCols + c;
+    const int lo = blockIdx.y == 0 ? 0 : first, hi = blockIdx.y == 0 ? first : total;
+    float sum = 0.0f;
+    if (e < D)
+        for (int i = lo + r; i < hi; i += kGradSplits) sum += partial[static_cast<int64_t>(i) * D + e];
+    red[r][c] = sum;
+    __syncthreads();
+    for (int s = kGradSplits / 2; s > 0; s >>= 1) {
+        if (r < s) red[r][c] += red[r + s][c];
+        __syncthreads();
+    }
+    if (r == 0 && e < D) (blockIdx.y == 0 ? d0 : d1)[e] = red[0][c];
+}
+
+// table[p][i] = RN32(amplitude cos(p f_i)), table[p][rot/2 + i] the sine.
+__global__ __launch_bounds__(kThreads) void rope_table_kernel(const double* __restrict__ freq, int half,
+                                                              int64_t max_pos, double amplitude,
+                                                              float* __restrict__ table) {
+    const int64_t n = max_pos * half;
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; k < n;
+         k += static_cast<int64_t>(gridDim.x) * kThreads) {
+        const int64_t pos = k / half;
+        const int i = static_cast<int>(k - pos * half);
+        double s, c;
+        sincos(static_cast<double>(pos) * freq[i], &s, &c);
+        table[pos * 2 * half + i] = static_cast<float>(amplitude * c);
+        table[pos * 2 * half + half + i] = static_cast<float>(amplitude * s);
+    }
+}
+
+template <class E, int LAYOUT, bool NORM, bool PAGED, bool VEC, int R>
+int launch_heads_r(HeadsArgs& p, int64_t batch, void* stream) {
+    for (auto& s : p.set) s.units = (s.heads + R - 1) / R;
+    const int lg = VEC ? p.log2_lanes : 6;
+    p.units = static_cast<uint32_t>(p.tokens * (p.set[0].units + p.set[1].units));
+    unsigned grid = (p.units + (kThreads >> lg) - 1) / (kThreads >> lg);
+    if (grid > kMaxHeadsGrid) grid = kMaxHeadsGrid;  // a launch holds fewer than 2^32 threads
+    hipLaunchKernelGGL((heads_kernel<E, LAYOUT, NORM, PAGED, VEC, R>), dim3(grid, static_cast<unsigned>(batch)),
+                       dim3(kThreads), 0, static_cast<hipStream_t>(stream), p);
+    return static_cast<int>(hipGetLastError());
+}
+
+template <class E, int LAYOUT, bool NORM, bool PAGED>
+int launch_heads_l(HeadsArgs& p, int64_t batch, bool vec, void* stream) {
+    if (!vec) return launch_heads_r<E, LAYOUT, NORM, PAGED, false, 1>(p, batch, stream);
+    return launch_heads_r<E, LAYOUT, NORM, PAGED, true, 1>(p, batch, stream);
+}
+
+template <class E>
+int launch_heads_e(HeadsArgs& p, int64_t batch, HeadsKind kind, int layout, bool vec, void* stream) {
+    if (layout == kHalf) {
+        switch (kind) {
+            case HeadsKind::rope: return launch_heads_l<E, kHalf, false, false>(p, batch, vec, stream);
+            case HeadsKind::norm: return launch_heads_l<E, kHalf, true, false>(p, batch, vec, stream);
+            default: return launch_heads_l<E, kHalf, false, true>(p, batch, vec, stream);
+        }
+    }
+    switch (kind) {
+        case HeadsKind::rope: return launch_heads_l<E, kInterleaved, false, false>(p, batch, vec, stream);
+        case HeadsKind::norm: return launch_heads_l<E, kInterleaved, true, false>(p, batch, vec, stream);
+        default: return launch_heads_l<E, kInterleaved, false, true>(p, batch, vec, stream);
+    }
+}
+
+template <class E, int LAYOUT, bool VEC>
+int launch_back_v(const NormBackArgs& p, int grid, void* stream) {
+    hipLaunchKernelGGL((norm_back_kernel<E, LAYOUT, VEC>), dim3(grid), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), p);
+    return static_cast<int>(hipGetLastError());
+}
+
+template <class E>
+int launch_back_e(const NormBackArgs& p, int layout, bool vec, int grid, void* stream) {
+    if (layout == kHalf)
+        return vec ? launch_back_v<E, kHalf, true>(p, grid, stream) : launch_back_v<E, kHalf, false>(p, grid, stream);
+    return vec ? launch_back_v<E, kInterleaved, true>(p, grid, stream)
+               : launch_back_v<E, kInterleaved, false>(p, grid, stream);
+}
+
+}  // namespace
+
+int launch_heads(Dtype t, HeadsArgs& p, int64_t batch, HeadsKind kind, int layout, bool vec, void* stream) {
+    switch (t) {
+        case Dtype::fp32: return launch_heads_e<HF32>(p, batch, kind, layout, vec, stream);
+        case Dtype::fp16: return launch_heads_e<HF16>(p, batch, kind, layout, vec, stream);
+        default: return launch_heads_e<HB16>(p, batch, kind, layout, vec, stream);
+    }
+}
+
+int launch_norm_back(Dtype t, NormBackArgs& p, int layout, bool vec, float* d0, float* d1, void* stream) {
+    const int lg = vec ? p.log2_lanes : 6;
+    const int groups = kThreads >> lg;
+    // Workgroups in the proportion of the two sets' rows, at least one each
+    // (a set without rows has its weight gradient written as zeros).
+    const int64_t n0 = (p.set[0].rows + groups - 1) / groups, n1 = (p.set[1].rows + groups - 1) / groups;
+    int64_t cap = kNormBackGroups;
+    int64_t g0 = n0, g1 = n1;
+    if (n0 + n1 > cap) {
+        g0 = n0 * cap / (n0 + n1);
+        g1 = cap - g0;
+        if (g1 > n1) g1 = n1;
+    }
+    if (g0 < 1) g0 = 1;
+    if (g1 < 1) g1 = 1;
+    p.first_groups = static_cast<int>(g0);
+    const int grid = static_cast<int>(g0 + g1);
+    int e;
+    switch (t) {
+        case Dtype::fp32: e = launch_back_e<HF32>(p, layout, vec, grid, stream); break;
+        case Dtype::fp16: e = launch_back_e<HF16>(p, layout, vec, grid, stream); break;
+        default: e = launch_back_e<HB16>(p, layout, vec, grid, stream); break;
+    }
+    if (e != 0) return e;
+    hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((p.dim + kGradCols - 1) / kGradCols, 2),
+                       dim3(kGradCols * kGradSplits), 0, static_cast<hipStream_t>(stream), p.partial, p.dim,
+                       p.first_groups, grid, d0, d1);
+    return static_cast<int>(hipGetLastError());
+}
+
+int launch_rope_table(const double* freq, int rot, int64_t max_pos, double amplitude, float* table, void* stream) {
+    const int64_t n = max_pos * (rot / 2);
+    int64_t grid = (n + kThreads - 1) / kThreads;
+    if (grid > 65536) grid = 65536;
+    hipLaunchKernelGGL(rope_table_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), freq, rot / 2, max_pos, amplitude, table);
+    return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace kbit

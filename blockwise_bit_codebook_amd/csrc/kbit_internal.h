@@ -71,6 +71,9 @@ int launch_act_tables(const float* codebook16, void* tables, void* stream);
 // CU count of the current device (at least 1).
 int device_cu_count();
 
+// Whether the current device is a gfx950 GPU.
+bool device_usable();
+
 // Ordinal of the current device, or -1 if none can be queried.
 int current_device_index();
 
