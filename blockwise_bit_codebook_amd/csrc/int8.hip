@@ -42,6 +42,7 @@ struct QF16 {
     static constexpr int kVec = 1;
     static __device__ float one(T v) { return Fp16::h2f(v); }
     static __device__ T narrow(float v) { return static_cast<T>(pack_f16x2(v, 0.0f) & 0xFFFFu); }
+    static __device__ uint32_t pack(float lo, float hi) { return pack_f16x2(lo, hi); }
     static __device__ void widen(const u32x4* r, float (&x)[8]) { Fp16::unpack(r, x); }
 };
 struct QB16 {
@@ -49,6 +50,7 @@ struct QB16 {
     static constexpr int kVec = 1;
     static __device__ float one(T v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
     static __device__ T narrow(float v) { return static_cast<T>(pack_bf16x2(v, 0.0f) & 0xFFFFu); }
+    static __device__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
     static __device__ void widen(const u32x4* r, float (&x)[8]) { Bf16::unpack(r, x); }
 };
 
@@ -153,14 +155,38 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const typename 
 // ---------------------------------------------------------------------------
 // product
 // ---------------------------------------------------------------------------
-// 16 codes of a row from column k (zeros beyond K and outside the matrix).
+// 16 codes of a row from column k, zeros beyond K; nothing beyond K is read.
+// ALIGNED: row + k is a multiple of 16, so that the last, partial piece is at
+// most one load each of 8, 4, 2 and 1 codes.
 template <bool ALIGNED>
-__device__ __forceinline__ u32x4 load_codes(const int8_t* row, bool live, int k, int K) {
+__device__ __forceinline__ u32x4 load_codes(const int8_t* row, int k, int K) {
     u32x4 r = u32x4{0u, 0u, 0u, 0u};
-    if (!live || k >= K) return r;
-    if (ALIGNED && k + 16 <= K) return load16<false>(row + k);
-    const int n = min(16, K - k);
-    for (int i = 0; i < n; ++i) r[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k + i])) << (8 * (i & 3));
+    if (k >= K) return r;
+    const int8_t* p = row + k;
+    if constexpr (ALIGNED) {
+        if (k + 16 <= K) return load16<false>(p);
+        const int n = K - k;
+        if (n & 8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            r[0] = v.x;
+            r[1] = v.y;
+        }
+        uint32_t last = 0;
+        if (n & 2) last = *reinterpret_cast<const uint16_t*>(p + (n & 12));
+        if (n & 1) last |= static_cast<uint32_t>(static_cast<uint8_t>(p[n - 1])) << (8 * (n & 2));
+        const uint32_t word = (n & 4) ? *reinterpret_cast<const uint32_t*>(p + (n & 8)) : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if ((n & 4) && i == (n & 8) >> 2) r[i] = word;
+            if ((n & 3) && i == n >> 2) r[i] = last;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t v = static_cast<uint8_t>(p[min(i, K - 1 - k)]);
+            r[i >> 2] |= (i < K - k ? v : 0u) << (8 * (i & 3));
+        }
+    }
     return r;
 }
 
@@ -176,7 +202,7 @@ __device__ __forceinline__ void store_out(const Int8Product& p, int64_t m, int n
 // 64 codes deep a step through LDS (rows 80 bytes apart, so that the 16 rows
 // of a fragment start in different banks).
 constexpr int kGenTile = 64, kGenStep = 64, kGenPitch = 80;
-template <class E, bool ALIGNED>
+template <class E>
 __global__ __launch_bounds__(kThreads) void int8_generic_kernel(const Int8Product p) {
     __shared__ __align__(16) uint8_t lds[2][kGenTile * kGenPitch];
     const int lane = __lane_id(), wave = threadIdx.x / kWave;
@@ -190,8 +216,8 @@ __global__ __launch_bounds__(kThreads) void int8_generic_kernel(const Int8Produc
     const int8_t* wr = p.w + static_cast<int64_t>(n0 + row) * p.ldw;
     i32x4 acc[2][2] = {};
     for (int k = 0; k < p.K; k += kGenStep) {
-        const u32x4 xv = load_codes<ALIGNED>(xr, x_ok, k + piece, p.K);
-        const u32x4 wv = load_codes<ALIGNED>(wr, w_ok, k + piece, p.K);
+        const u32x4 xv = x_ok ? load_codes<false>(xr, k + piece, p.K) : u32x4{0u, 0u, 0u, 0u};
+        const u32x4 wv = w_ok ? load_codes<false>(wr, k + piece, p.K) : u32x4{0u, 0u, 0u, 0u};
         __syncthreads();
         *reinterpret_cast<u32x4*>(&lds[0][row * kGenPitch + piece]) = xv;
         *reinterpret_cast<u32x4*>(&lds[1][row * kGenPitch + piece]) = wv;
@@ -221,16 +247,588 @@ __global__ __launch_bounds__(kThreads) void int8_generic_kernel(const Int8Produc
             }
 }
 
+// ---------------------------------------------------------------------------
+// What the two product kernels share
+// ---------------------------------------------------------------------------
+// Operands reach the matrix cores through LDS, 128 codes of a row a step: one
+// cache line, and all banks of the LDS.  A lane needs 16 codes of row
+// lane % 16, so reading them from memory directly would touch 16 rows with
+// every 16 lanes (measured: 38 GB/s a CU against 115 for whole lines).  The
+// loads write LDS themselves, linearly; the 16-byte pieces of a row stand at
+// positions xor-ed with a key of the row, so that the 8 rows which a read
+// touches at a time lie in different banks (no conflicts counted), and each
+// lane fetches the piece that belongs at its position.
+//
+// The weight is the first matrix operand, so that lane l holds channels
+// 4 (l / 16) .. + 3 of row l % 16; channel 4 TN (i / 4) + 4 j + i % 4 sits in
+// row i of operand j, which makes a lane's 4 TN channels neighbours.
+constexpr int kDepth = 128;
+
+template <int TN>
+__device__ __forceinline__ int operand_channel(int j, int i) {
+    return 4 * TN * (i >> 2) + 4 * j + (i & 3);
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 bytes a lane from memory to LDS: lane l's go to lds + 16 l.
+__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, void* lds, int lane_offset, int offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, lane_offset, offset, 0, 0);
+}
+
+__device__ __forceinline__ int key_x(int row) { return row & 7; }
+template <int TN>
+__device__ __forceinline__ int key_w(int row) {  // see operand_channel
+    return (row & 3) | (row / (4 * TN) & 1) << 2;
+}
+
+// Four neighbouring outputs of a row.
 template <class E>
-int launch_product_e(const Int8Product& p, bool aligned, void* stream) {
-    const dim3 grid((p.N + kGenTile - 1) / kGenTile, static_cast<unsigned>((p.M + kGenTile - 1) / kGenTile));
-    if (aligned)
-        hipLaunchKernelGGL((int8_generic_kernel<E, true>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream),
-                           p);
-    else
-        hipLaunchKernelGGL((int8_generic_kernel<E, false>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream),
-                           p);
+__device__ __forceinline__ void store_out4(const Int8Product& p, int64_t m, int n, const i32x4& acc, float xs,
+                                           bool packed) {
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int c = min(n + r, p.N - 1);
+        v[r] = static_cast<float>(acc[r]) * xs;
+        v[r] = v[r] * p.ws[c];
+        if (p.bias) v[r] = v[r] + E::one(static_cast<const typename E::T*>(p.bias)[c]);
+    }
+    typename E::T* out = static_cast<typename E::T*>(p.out) + m * p.ldo + n;
+    if (packed && n + 4 <= p.N) {
+        if constexpr (sizeof(typename E::T) == 4)
+            store16<false>(out, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                      __float_as_uint(v[3])});
+        else
+            *reinterpret_cast<uint2*>(out) = make_uint2(E::pack(v[0], v[1]), E::pack(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (n + r < p.N) out[r] = E::narrow(v[r]);
+    }
+}
+
+// Whether every row of the output starts at a multiple of `bytes`.
+bool out_aligned(const Int8Product& p, int64_t esize, int64_t bytes) {
+    return reinterpret_cast<uintptr_t>(p.out) % bytes == 0 && (p.M == 1 || p.ldo * esize % bytes == 0);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows
+// ---------------------------------------------------------------------------
+// A workgroup takes 16 MT rows and 16 TN channels.  Its waves split the depth
+// and work alone, each with two steps of both operands in LDS of its own and
+// no barrier: while one step is multiplied the next is on its way.  At the
+// end they add their int32 tiles in LDS with integer additions, whose order
+// does not matter.  The weights are read from memory once; the rows of x come
+// from cache.  Bound by the weights' bytes and, for the smallest, by the
+// latency of one load and the launch.
+template <class E, int MT, int TN, int WAVES>
+__global__ __launch_bounds__(WAVES* kWave) void int8_few_rows_kernel(const Int8Product p, int m_tiles, bool packed) {
+    constexpr int BM = MT * 16, BN = TN * 16, kStep = (BM + BN) * kDepth, kPitch = BN + 4;
+    __shared__ __align__(1024) uint8_t even[WAVES * kStep], odd[WAVES * kStep];
+    static_assert(BM * kPitch * 4 <= WAVES * kStep, "the sums fit over the operands");
+    const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l16 = lane & 15, q = lane >> 4;
+    // Workgroups id, id + 8, ... run on one XCD: the m tiles of a block of
+    // channels follow each other there and share its weights in that L2.
+    const int id = blockIdx.x, turn = id >> 3;
+    const int n_tile = (turn / m_tiles) * 8 + (id & 7);
+    const int64_t m0 = static_cast<int64_t>(turn % m_tiles) * BM;
+    const int n0 = n_tile * BN;
+    if (n0 >= p.N) return;
+    const int rows = static_cast<int>(min<int64_t>(p.M - m0, BM)), cols = min(p.N - n0, BN);
+    const int8_t* xb = p.x + m0 * p.ldx;
+    const int8_t* wb = p.w + static_cast<int64_t>(n0) * p.ldw;
+    const int ldx = static_cast<int>(p.ldx), ldw = static_cast<int>(p.ldw);
+
+    // Load i covers rows 8 i .. 8 i + 7 of a tile; rows past the matrix read
+    // its last row, their outputs are not stored.
+    const int row0 = lane >> 3, piece0 = lane & 7;
+    int xo[2 * MT], wo[2 * TN];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i)
+        xo[i] = min(8 * i + row0, rows - 1) * ldx + 16 * (piece0 ^ key_x(8 * i + row0));
+#pragma unroll
+    for (int i = 0; i < 2 * TN; ++i)
+        wo[i] = min(8 * i + row0, cols - 1) * ldw + 16 * (piece0 ^ key_w<TN>(8 * i + row0));
+    auto fetch = [&](int s, uint8_t* to, bool live) {
+        const int range = live ? 0x7FFFFFFF : 0;  // not live: issued, but reads nothing
+        const auto xr = buf_rsrc(xb, range), wr = buf_rsrc(wb, range);
+#pragma unroll
+        for (int i = 0; i < 2 * TN; ++i) load16_to_lds(wr, to + (BM + 8 * i) * kDepth, wo[i], s * kDepth);
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i)
+            load16_to_lds(xr, to + 8 * i * kDepth, xo[i], s * kDepth);
+    };
+    i32x4 acc[MT][TN] = {}, x[2][MT], w[2][TN];
+    auto read = [&](const uint8_t* from) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int row = operand_channel<TN>(j, l16);
+                w[h][j] = *reinterpret_cast<const i32x4*>(from + (BM + row) * kDepth + 16 * ((4 * h + q) ^ key_w<TN>(row)));
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                x[h][i] = *reinterpret_cast<const i32x4*>(from + (16 * i + l16) * kDepth + 16 * ((4 * h + q) ^ key_x(l16)));
+        }
+    };
+    auto multiply = [&] {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][j], x[h][i], acc[i][j], 0, 0, 0);
+    };
+    const int steps = p.K / kDepth;
+    uint8_t *const e = even + wave * kStep, *const o = odd + wave * kStep;
+    // A step's operands have left LDS (lgkmcnt(0)) before the loads of the
+    // step after the next go over them.  Past the last step everything but
+    // the products is done all the same: branches around loads to LDS make
+    // the compiler wait for all of them.
+    auto turn_step = [&](int s, uint8_t* at) {
+        read(at);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        fetch(s + 2 * WAVES, at, s + 2 * WAVES < steps);
+        if (s < steps) multiply();
+    };
+    fetch(wave, e, wave < steps);
+    fetch(wave + WAVES, o, wave + WAVES < steps);
+    for (int s = wave; s < steps; s += 2 * WAVES) {
+        turn_step(s, e);
+        turn_step(s + WAVES, o);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    if (steps * kDepth < p.K && steps % WAVES == wave) {  // the depth's partial step, zeros past K
+        const int k = steps * kDepth;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            const int row = 8 * i + row0;
+            *reinterpret_cast<u32x4*>(e + 8 * i * kDepth + lane * 16) = load_codes<true>(
+                xb + static_cast<int64_t>(min(row, rows - 1)) * ldx, k + 16 * (piece0 ^ key_x(row)), p.K);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * TN; ++i) {
+            const int row = 8 * i + row0;
+            *reinterpret_cast<u32x4*>(e + (BM + 8 * i) * kDepth + lane * 16) = load_codes<true>(
+                wb + static_cast<int64_t>(min(row, cols - 1)) * ldw, k + 16 * (piece0 ^ key_w<TN>(row)), p.K);
+        }
+        read(e);
+        multiply();
+    }
+    __syncthreads();
+    int* sum = reinterpret_cast<int*>(even);  // [BM][kPitch]
+    for (int i = threadIdx.x; i < BM * kPitch; i += WAVES * kWave) sum[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                __hip_atomic_fetch_add(sum + (16 * i + l16) * kPitch + 4 * TN * q + 4 * j + r, acc[i][j][r],
+                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    __syncthreads();
+    for (int i = threadIdx.x; i < BM * BN / 4; i += WAVES * kWave) {
+        const int r = i / (BN / 4), c = (i % (BN / 4)) * 4;
+        if (r < rows && c < cols)
+            store_out4<E>(p, m0 + r, n0 + c, *reinterpret_cast<const i32x4*>(sum + r * kPitch + c), p.xs[m0 + r], packed);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: tiles through LDS.
+// ---------------------------------------------------------------------------
+// A workgroup of WM x WN waves takes a tile of 16 TM WM rows and 64 WN
+// channels, two steps of both operands in LDS: while the matrix cores work on
+// one, the loads of the next go into the other.
+// A wave's 16 TM x 64 outputs, through a region of LDS that is the wave's own,
+// so that a row leaves as one run of 64 channels: a lane's 16 channels alone
+// are 32 bytes of a line, and writing those cost 36 us a tile of 256 x 256.
+// The 16-byte pieces of a row are xor-ed with the row like the operands'.
+// m, n: the wave's first row and channel.
+template <class E, int TM, int kRegion>
+__device__ __forceinline__ void store_tile(const Int8Product& p, uint8_t* region, int lane, int64_t m, int n,
+                                           const i32x4 (&acc)[TM][4], bool packed) {
+    using T = typename E::T;
+    constexpr int kSize = sizeof(T), kRow = 64 * kSize;
+    constexpr int kFit = kRegion / (16 * kRow) < TM ? kRegion / (16 * kRow) : TM;
+    constexpr int kPass = TM % kFit == 0 ? kFit : 1;  // blocks of 16 rows a pass
+    static_assert(kFit >= 1, "a block fits");
+    const int l16 = lane & 15, q = lane >> 4;
+    float sc[16], bias[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        sc[e] = p.ws[n + 16 * q + e];
+        bias[e] = 0.0f;
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) bias[e] = E::one(static_cast<const T*>(p.bias)[n + 16 * q + e]);
+    }
+    T* out = static_cast<T*>(p.out) + m * p.ldo + n;
+#pragma unroll
+    for (int i0 = 0; i0 < TM; i0 += kPass) {
+#pragma unroll
+        for (int i = 0; i < kPass; ++i) {
+            const int row = 16 * i + l16;
+            const float xs = p.xs[m + 16 * i0 + row];
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                v[e] = static_cast<float>(acc[i0 + i][e >> 2][e & 3]) * xs * sc[e];
+                if (p.bias) v[e] = v[e] + bias[e];
+            }
+#pragma unroll
+            for (int c = 0; c < kSize; ++c) {  // the lane's 16 kSize bytes
+                u32x4 d;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (kSize == 4) d[r] = __float_as_uint(v[4 * c + r]);
+                    else d[r] = E::pack(v[8 * c + 2 * r], v[8 * c + 2 * r + 1]);
+                }
+                *reinterpret_cast<u32x4*>(region + row * kRow + 16 * ((q * kSize + c) ^ (row & 7))) = d;
+            }
+        }
+        // One wave's LDS accesses are executed in order: no barrier.
+        if (packed) {
+            constexpr int kPieces = kRow / 16, kRows = kWave / kPieces;  // rows a store instruction
+#pragma unroll
+            for (int r0 = 0; r0 < kPass * 16; r0 += kRows) {
+                const int row = r0 + lane / kPieces, piece = lane % kPieces;
+                const u32x4 d = *reinterpret_cast<const u32x4*>(region + row * kRow + 16 * (piece ^ (row & 7)));
+                store16<false>(out + (16 * i0 + row) * p.ldo + piece * (16 / kSize), d);
+            }
+        } else {
+            for (int row = 0; row < kPass * 16; ++row) {
+                const int piece = lane / (16 / kSize), at = lane % (16 / kSize);
+                out[(16 * i0 + row) * p.ldo + lane] = reinterpret_cast<const T*>(
+                    region + row * kRow + 16 * (piece ^ (row & 7)))[at];
+            }
+        }
+    }
+}
+
+template <class E, int KG, int WM, int WN, int TM>
+__global__ __launch_bounds__(KG* WM* WN* kWave) void int8_tile_kernel(const Int8Product p, int m_tiles, int n_tiles,
+                                                                  bool packed) {
+    constexpr int TN = 4, kT = WM * WN * kWave;
+    constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
+    constexpr int kXLoads = BM * 8 / kT, kWLoads = BN * 8 / kT;
+    static_assert(BM * 8 % kT == 0 && BN * 8 % kT == 0, "whole rounds of loads");
+    // Four arrays by name, and code that names the one it means: the compiler
+    // then sees that the operands it reads are not those on their way, and
+    // puts no wait for the loads before the reads.
+    __shared__ __align__(1024) uint8_t x_even_all[KG * BM * kDepth], x_odd_all[KG * BM * kDepth],
+        w_even_all[KG * BN * kDepth], w_odd_all[KG * BN * kDepth];
+    const int lane = __lane_id(), wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int part = KG == 1 ? 0 : wave_id / (WM * WN), wave = KG == 1 ? wave_id : wave_id % (WM * WN);
+    uint8_t *const x_even = x_even_all + part * BM * kDepth, *const x_odd = x_odd_all + part * BM * kDepth;
+    uint8_t *const w_even = w_even_all + part * BN * kDepth, *const w_odd = w_odd_all + part * BN * kDepth;
+    const int l16 = lane & 15, q = lane >> 4;
+    const int wm = (wave % WM) * TM * 16, wn = (wave / WM) * TN * 16;
+
+    // Each XCD works through a contiguous range of tiles, in groups of 8 rows
+    // of tiles, so that its L2 holds the operands its workgroups share.
+    const int tiles = m_tiles * n_tiles;
+    const int per = (tiles + 7) / 8;
+    const int t = static_cast<int>(blockIdx.x & 7) * per + static_cast<int>(blockIdx.x >> 3);
+    if (t >= tiles || static_cast<int>(blockIdx.x >> 3) >= per) return;
+    constexpr int kGroupM = 8;
+    const int group = t / (kGroupM * n_tiles), in = t - group * kGroupM * n_tiles;
+    const int gm = min(kGroupM, m_tiles - group * kGroupM);
+    // The last tiles of a row or column are moved inside the matrix (M >= BM,
+    // N >= BN): outputs computed twice get the same values twice.
+    const int64_t m0 = min<int64_t>(static_cast<int64_t>(group * kGroupM + in % gm) * BM, p.M - BM);
+    const int n0 = min(in / gm * BN, p.N - BN);
+
+    const int8_t* xb = p.x + m0 * p.ldx;
+    const int8_t* wb = p.w + static_cast<int64_t>(n0) * p.ldw;
+    // A round of loads covers kRound rows; the keys repeat from round to
+    // round, but for the weights' where a round is shorter than their period.
+    constexpr int kRound = kT / 8;
+    constexpr bool kTwoKeys = kRound % (8 * TN) != 0;
+    const int row0 = (wave * kWave + lane) >> 3, piece0 = lane & 7;
+    const int ldx = static_cast<int>(p.ldx), ldw = static_cast<int>(p.ldw);
+    const int xo = row0 * ldx + 16 * (piece0 ^ key_x(row0));
+    const int wo0 = row0 * ldw + 16 * (piece0 ^ key_w<TN>(row0));
+    const int wo1 = kTwoKeys ? row0 * ldw + 16 * (piece0 ^ key_w<TN>(row0 + kRound)) : wo0;
+    // Loads that are not `live` are issued all the same, to an empty range, and
+    // read no memory: a branch around them would make the compiler wait.
+    auto fetch = [&](int k, uint8_t* xd, uint8_t* wd, bool live) {
+        const int range = live ? 0x7FFFFFFF : 0;
+        const auto xr = buf_rsrc(xb, range), wr = buf_rsrc(wb, range);
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i)
+            load16_to_lds(xr, xd + (i * kT + wave * kWave) * 16, xo, k + i * kRound * ldx);
+#pragma unroll
+        for (int i = 0; i < kWLoads; ++i)
+            load16_to_lds(wr, wd + (i * kT + wave * kWave) * 16, (i & 1) ? wo1 : wo0, k + i * kRound * ldw);
+    };
+
+    // Half a step's operands (64 codes deep) in LDS; the keys do not change
+    // with i and j, 16 and 4 rows on.
+    const int w_row = operand_channel<TN>(0, l16);
+    const int xp[2] = {(wm + l16) * kDepth + 16 * (q ^ key_x(l16)), (wm + l16) * kDepth + 16 * ((4 + q) ^ key_x(l16))};
+    const int wp[2] = {(wn + w_row) * kDepth + 16 * (q ^ key_w<TN>(w_row)),
+                       (wn + w_row) * kDepth + 16 * ((4 + q) ^ key_w<TN>(w_row))};
+    i32x4 acc[TM][TN] = {};
+    i32x4 x[TM], w0[TN], w1[TN];
+    auto read_x = [&](const uint8_t* xd, int h, int i) {
+        x[i] = *reinterpret_cast<const i32x4*>(xd + xp[h] + 16 * i * kDepth);
+    };
+    auto read_w = [&](const uint8_t* wd, int h, int j) {
+        return *reinterpret_cast<const i32x4*>(wd + wp[h] + 4 * j * kDepth);
+    };
+    auto read = [&](const uint8_t* xd, const uint8_t* wd, int h, i32x4 (&w)[TN]) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) w[j] = read_w(wd, h, j);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) read_x(xd, h, i);
+    };
+    // The products of half a step; each operand of x is replaced by half h of
+    // (xn, wn) as soon as its last product is issued, and the next weights are
+    // read on the way.
+    constexpr int kPer = TM < TN ? TN / TM : 1;
+    auto multiply = [&](const i32x4 (&w)[TN], const uint8_t* xn, const uint8_t* wn, int h, i32x4 (&w_next)[TN]) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], x[i], acc[i][j], 0, 0, 0);
+            read_x(xn, h, i);
+#pragma unroll
+            for (int j = i * kPer; j < (i + 1) * kPer && j < TN; ++j) w_next[j] = read_w(wn, h, j);
+            __builtin_amdgcn_sched_group_barrier(0x008, TN, 0);
+            if (i * kPer < TN) __builtin_amdgcn_sched_group_barrier(0x100, 1 + kPer, 0);
+            else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+    };
+    auto multiply_all = [&](const i32x4 (&w)[TN]) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], x[i], acc[i][j], 0, 0, 0);
+    };
+
+    // Software pipeline: while half a step is multiplied the next half is read
+    // from LDS, and the step after it is on its way from memory.  The one
+    // barrier of a step stands between its halves: past it every wave's loads
+    // of step s + 1 have arrived and nobody reads step s any more, so that
+    // step s + 2 may be fetched over it.
+    auto arrive = [&] {
+        __builtin_amdgcn_s_waitcnt(0);  // loads to LDS are counted with the vector loads: a barrier does not wait for them
+        __syncthreads();
+    };
+    // The pipeline takes pairs of steps.  What the depth has beyond them comes
+    // first (the sums are exact in any order), piece by piece through
+    // registers, zeros past K.
+    const int pairs = p.K / (2 * kDepth);
+#pragma clang loop unroll(disable)
+    for (int k = pairs * 2 * kDepth; k < p.K; k += kDepth) {
+#pragma clang loop unroll(disable)
+        for (int i = 0; i < kXLoads + kWLoads; ++i) {
+            const bool w = i >= kXLoads;
+            const int row = (w ? i - kXLoads : i) * kRound + row0;
+            const int key = w ? key_w<TN>(row) : key_x(row);
+            const int8_t* from = w ? wb + static_cast<int64_t>(row) * ldw : xb + static_cast<int64_t>(row) * ldx;
+            uint8_t* to = (w ? w_even : x_even) + row * kDepth + piece0 * 16;
+            if (part == 0) *reinterpret_cast<u32x4*>(to) = load_codes<true>(from, k + 16 * (piece0 ^ key), p.K);
+        }
+        __syncthreads();
+        if (part == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                read(x_even, w_even, h, w0);
+                multiply_all(w0);
+            }
+        }
+        __syncthreads();
+    }
+    // This part's pairs; all parts go through the most that one has.
+    const int most = 2 * ((pairs + KG - 1) / KG);
+    const int first = 2 * (pairs * part / KG), steps = 2 * (pairs * (part + 1) / KG) - first;
+    // One step from (xd, wd), the next one's first half from (xn, wn).
+    auto step = [&](int s, uint8_t* xd, uint8_t* wd, const uint8_t* xn, const uint8_t* wn) {
+        if (KG == 1 || s < steps) multiply(w0, xd, wd, 1, w1);
+        arrive();
+        fetch((first + s + 2) * kDepth, xd, wd, s + 2 < steps);
+        if (KG == 1 || s < steps) multiply(w1, xn, wn, 0, w0);
+    };
+    fetch(first * kDepth, x_even, w_even, steps > 0);
+    fetch((first + 1) * kDepth, x_odd, w_odd, steps > 0);
+    arrive();
+    read(x_even, w_even, 0, w0);
+    for (int s = 0; s < most; s += 2) {  // past the last step it reads operands that nobody multiplies
+        step(s, x_even, w_even, x_odd, w_odd);
+        step(s + 1, x_odd, w_odd, x_even, w_even);
+    }
+    // What follows runs once: its addresses are made anew from the thread's
+    // number, so that the loop above keeps no registers for them.
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    arrive();  // the operands are read, and the empty loads of the last steps are done
+    if constexpr (KG > 1) {
+        // The second part's sums go to the first through LDS, over the
+        // operands, half of a lane's rows at a time.
+        static_assert(KG == 2 && TM % 2 == 0, "two parts, halves of their rows");
+        constexpr int kHalfRows = TM / 2;
+        i32x4* pass = reinterpret_cast<i32x4*>(wave % 2 == 0 ? x_even_all : w_even_all) +
+                      (wave / 2) * (kHalfRows * TN * kWave);
+        static_assert(WM * WN / 2 * kHalfRows * TN * kWave * 16 <= KG * BM * kDepth && BM <= BN, "the sums fit");
+#pragma unroll
+        for (int i0 = 0; i0 < TM; i0 += kHalfRows) {
+#pragma unroll
+            for (int i = 0; i < kHalfRows; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    if (part == 1) pass[(i * TN + j) * kWave + (tid & 63)] = acc[i0 + i][j];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kHalfRows; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    if (part == 0) acc[i0 + i][j] += pass[(i * TN + j) * kWave + (tid & 63)];
+            __syncthreads();
+        }
+        if (part == 1) return;
+    }
+    // A region for each wave, in the array that has room for it.
+    constexpr int kPart = (BM < BN ? BM : BN) >= 256 ? 16384 : 8192;
+    static_assert(kPart <= BM * kDepth && kPart <= BN * kDepth, "a region fits into either array");
+    constexpr int kInX = BM * kDepth / kPart, kInW = BN * kDepth / kPart;
+    static_assert(2 * kInX + 2 * kInW >= WM * WN, "a region for every wave");
+    uint8_t* region = wave < kInX ? x_even_all + wave * kPart
+                      : wave < 2 * kInX ? x_odd_all + (wave - kInX) * kPart
+                      : wave < 2 * kInX + kInW ? w_even_all + (wave - 2 * kInX) * kPart
+                                               : w_odd_all + (wave - 2 * kInX - kInW) * kPart;
+    store_tile<E, TM, kPart>(p, region, tid & 63, m0 + wm, n0 + wn, acc, packed && (n0 * sizeof(typename E::T)) % 16 == 0);
+}
+
+template <class E, int MT, int TN, int WAVES>
+int launch_few(const Int8Product& p, void* stream) {
+    const int m_tiles = static_cast<int>((p.M + MT * 16 - 1) / (MT * 16)), n_tiles = (p.N + TN * 16 - 1) / (TN * 16);
+    const unsigned grid = static_cast<unsigned>((n_tiles + 7) / 8 * 8 * m_tiles);
+    hipLaunchKernelGGL((int8_few_rows_kernel<E, MT, TN, WAVES>), dim3(grid), dim3(WAVES * kWave), 0,
+                       static_cast<hipStream_t>(stream), p, m_tiles, out_aligned(p, sizeof(typename E::T), 4 * sizeof(typename E::T)));
     return static_cast<int>(hipGetLastError());
+}
+
+template <class E, int KG, int WM, int WN, int TM>
+int launch_tile(const Int8Product& p, void* stream) {
+    constexpr int BM = WM * TM * 16, BN = WN * 64;
+    const int m_tiles = static_cast<int>((p.M + BM - 1) / BM), n_tiles = (p.N + BN - 1) / BN;
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
+    hipLaunchKernelGGL((int8_tile_kernel<E, KG, WM, WN, TM>), dim3(grid), dim3(KG * WM * WN * kWave), 0,
+                       static_cast<hipStream_t>(stream), p, m_tiles, n_tiles, out_aligned(p, sizeof(typename E::T), 16));
+    return static_cast<int>(hipGetLastError());
+}
+
+template <class E>
+int launch_generic(const Int8Product& p, void* stream) {
+    const dim3 grid((p.N + kGenTile - 1) / kGenTile, static_cast<unsigned>((p.M + kGenTile - 1) / kGenTile));
+    hipLaunchKernelGGL((int8_generic_kernel<E>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream), p);
+    return static_cast<int>(hipGetLastError());
+}
+
+// Which kernel and tile: the least estimated time in microseconds, from what
+// the variants measured over M = 1 .. 8192, N = 512 .. 11008, K = 4096 with
+// operands from memory (256 compute units).  A round is one workgroup on every
+// compute unit.  Few-rows tiles: 4 us + rounds * (bytes of a workgroup's
+// operands) / 45 GB/s, and 0.4 us a 16 rows for a depth that
+// ends inside a step (1 x 4096: 7.1 us, 77 x 11008: 17.9 us, 256 x 4096: 14.9
+// us with 64 x 64 tiles, against 23.0 for the best of the others).  Tiles
+// through LDS, per step of 128: 64 x 128 in two parts 0.62 us a round (512 x
+// 4096: 23.8 us; 26.6 for few rows), 128 x 128 in two parts 0.80 us a round
+// (1024 x 4096: 29.7 us; 33.3 in one part), 128 x 128 in one part, two
+// workgroups a compute unit, 0.90 us or 0.59 a round (2048 x 4096: 41.4 us; 56.7
+// in two parts), 256 x 256 1.55 us and 9 us a round (4096 x 4096: 60.8 us; 75.9
+// with 128 x 128).
+enum class Int8Form { few, tile2_64, tile2_128, tile_128, tile_256 };
+
+struct Int8Choice {
+    Int8Form form;
+    int mt, tn;
+};
+
+constexpr int kFewTiles[][2] = {{1, 1}, {1, 3}, {1, 4}, {2, 1}, {2, 2}, {2, 4}, {3, 2}, {3, 4}, {4, 2}, {4, 4}, {5, 3}, {5, 4}};
+
+Int8Choice choose_form(int64_t M, int N, int K) {
+    const double cus = device_cu_count(), steps = (K + kDepth - 1) / kDepth;
+    auto rounds = [&](int bm, int bn) {
+        const double tiles = static_cast<double>((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+        const int64_t r = static_cast<int64_t>((tiles + cus - 1) / cus);
+        return static_cast<double>(r);
+    };
+    Int8Choice best{};
+    double least = 1e30;
+    auto consider = [&](double us, Int8Form form, int mt, int tn) {
+        if (us < least) {
+            least = us;
+            best = Int8Choice{form, mt, tn};
+        }
+    };
+    for (const auto& t : kFewTiles)
+        consider(4.0 + rounds(16 * t[0], 16 * t[1]) * (t[0] + t[1]) * (16.0 * K / 45e3 + (K % kDepth ? 0.4 : 0.0)),
+                 Int8Form::few, t[0], t[1]);
+    if (M >= 64 && N >= 128) consider(4.0 + rounds(64, 128) * steps * 0.62, Int8Form::tile2_64, 0, 0);
+    if (M >= 128 && N >= 128) {
+        const double r = rounds(128, 128);
+        consider(4.0 + r * steps * 0.80, Int8Form::tile2_128, 0, 0);
+        consider(4.0 + steps * (0.59 * r > 0.90 ? 0.59 * r : 0.90), Int8Form::tile_128, 0, 0);
+    }
+    if (M >= 256 && N >= 256) consider(rounds(256, 256) * (9.0 + steps * 1.55), Int8Form::tile_256, 0, 0);
+    return best;
+}
+
+template <class E>
+int launch_few_tile(const Int8Product& p, int mt, int tn, void* stream) {
+    switch (10 * mt + tn) {
+        case 11: return launch_few<E, 1, 1, 16>(p, stream);
+        case 13: return launch_few<E, 1, 3, 8>(p, stream);
+        case 14: return launch_few<E, 1, 4, 7>(p, stream);
+        case 21: return launch_few<E, 2, 1, 12>(p, stream);
+        case 22: return launch_few<E, 2, 2, 8>(p, stream);
+        case 24: return launch_few<E, 2, 4, 6>(p, stream);
+        case 32: return launch_few<E, 3, 2, 6>(p, stream);
+        case 34: return launch_few<E, 3, 4, 5>(p, stream);
+        case 42: return launch_few<E, 4, 2, 6>(p, stream);
+        case 44: return launch_few<E, 4, 4, 4>(p, stream);
+        case 53: return launch_few<E, 5, 3, 4>(p, stream);
+        default: return launch_few<E, 5, 4, 4>(p, stream);
+    }
+}
+
+template <class E>
+int launch_product_e(const Int8Product& whole, bool aligned, void* stream) {
+    // Row blocks keep the grids (below 2^32 threads) and the kernels' 32-bit
+    // offsets in range.
+    constexpr int64_t kRowBlock = int64_t(1) << 15;
+    for (int64_t m = 0; m < whole.M; m += kRowBlock) {
+        Int8Product p = whole;
+        p.M = whole.M - m < kRowBlock ? whole.M - m : kRowBlock;
+        p.x += m * p.ldx;
+        p.xs += m;
+        p.out = static_cast<typename E::T*>(p.out) + m * p.ldo;
+        int e;
+        if (!aligned || p.ldx >= (1 << 22) || p.ldw >= (1 << 22)) {
+            e = launch_generic<E>(p, stream);
+        } else {
+            const Int8Choice c = choose_form(p.M, p.N, p.K);
+            switch (c.form) {
+                case Int8Form::few: e = launch_few_tile<E>(p, c.mt, c.tn, stream); break;
+                case Int8Form::tile2_64: e = launch_tile<E, 2, 2, 2, 2>(p, stream); break;
+                case Int8Form::tile2_128: e = launch_tile<E, 2, 2, 2, 4>(p, stream); break;
+                case Int8Form::tile_128: e = launch_tile<E, 1, 2, 2, 4>(p, stream); break;
+                default: e = launch_tile<E, 1, 2, 4, 8>(p, stream); break;
+            }
+        }
+        if (e != 0) return e;
+    }
+    return 0;
 }
 
 template <class E>

@@ -71,12 +71,15 @@ int do_linear_int8(Dtype t, const Int8Product& p, void* workspace, int64_t works
 }
 
 // Workspace of the dynamic form: the codes, their scales, the product's own.
+// Its rows of codes are whole cache lines, so that no step of 128 codes lies
+// across two.
+int64_t dynamic_ld(int32_t K) { return round_up(K, 128); }
 struct DynamicParts {
     int64_t scale, product, total;
 };
 DynamicParts dynamic_parts(int64_t M, int32_t N, int32_t K) {
     DynamicParts w;
-    w.scale = M * round_up(K, 16);
+    w.scale = M * dynamic_ld(K);
     w.product = w.scale + round_up(4 * M, 16);
     w.total = w.product + int8_product_workspace(M, N, K);
     return w;
@@ -84,7 +87,7 @@ DynamicParts dynamic_parts(int64_t M, int32_t N, int32_t K) {
 
 int do_linear_int8_dynamic(Dtype t, const void* X, int64_t ldX, Int8Product p, void* workspace,
                            int64_t workspace_bytes, void* stream) {
-    p.ldx = p.K >= 1 ? round_up(p.K, 16) : 0;
+    p.ldx = p.K >= 1 ? dynamic_ld(p.K) : 0;
     const int c = check_product(t, p);
     if (c != 1) return c;
     if (!X || !workspace || !rows_shape_ok(p.M, p.K, ldX)) return KBIT_EINVAL;
