@@ -66,6 +66,7 @@ def _layer_signatures():
     sig = [
         ("linear_int8_workspace_bytes", [_i64, _i32, _i32]),
         ("linear_int8_dynamic_workspace_bytes", [_i64, _i32, _i32]),
+        ("linear_int8_dynamic_fused", [_i64, _i32, _i32, _i64]),
         ("qk_norm_rope_backward_workspace_bytes", [_i32]),
         ("rope_frequencies", [_i32, f64, _i32, f64, f64, f64, f64, _p, _p]),
         ("rope_table", [_p, _i32, _i64, f64, _p, _p]),

@@ -441,6 +441,153 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_few_rows_kernel(const Int8P
 }
 
 // ---------------------------------------------------------------------------
+// A few tokens, quantized on the way
+// ---------------------------------------------------------------------------
+// The few-rows kernel for a few tokens whose codes every workgroup makes for
+// itself, in LDS, while its first weights are on their way: one launch
+// instead of two (one token x 4096: see the layer's table of measurements),
+// for a reading of the tokens from cache by each workgroup.  A wave takes 512
+// values of a row at a time, at most kItems times.
+constexpr int kItems = 4;
+constexpr int kTokenBytes = 28 * 1024;  // of codes, rows kTokenPad apart from whole steps
+constexpr int kTokenPad = 16;
+constexpr int kMaxTokens = 8;
+
+template <class E, int TN, int WAVES, bool VEC>
+__global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Product p,
+                                                                   const typename E::T* __restrict__ X, int64_t ldX,
+                                                                   bool packed) {
+    constexpr int BN = TN * 16, kStep = BN * kDepth, kPitch = BN + 4;
+    __shared__ __align__(1024) uint8_t even[WAVES * kStep], odd[WAVES * kStep];
+    __shared__ __align__(16) int8_t codes[kTokenBytes];
+    __shared__ uint32_t amax[WAVES * kItems];
+    __shared__ float scale[kMaxTokens];
+    static_assert(16 * kPitch * 4 <= WAVES * kStep, "the sums fit over the operands");
+    const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l16 = lane & 15, q = lane >> 4;
+    const int rows = static_cast<int>(p.M), n0 = blockIdx.x * BN, cols = min(p.N - n0, BN);
+    const int8_t* wb = p.w + static_cast<int64_t>(n0) * p.ldw;
+    const int ldw = static_cast<int>(p.ldw);
+    const int row0 = lane >> 3, piece0 = lane & 7;
+    int wo[2 * TN];
+#pragma unroll
+    for (int i = 0; i < 2 * TN; ++i)
+        wo[i] = min(8 * i + row0, cols - 1) * ldw + 16 * (piece0 ^ key_w<TN>(8 * i + row0));
+    auto fetch = [&](int s, uint8_t* to, bool live) {
+        const auto wr = buf_rsrc(wb, live ? 0x7FFFFFFF : 0);
+#pragma unroll
+        for (int i = 0; i < 2 * TN; ++i) load16_to_lds(wr, to + 8 * i * kDepth, wo[i], s * kDepth);
+    };
+    const int steps = p.K / kDepth;
+    uint8_t *const e = even + wave * kStep, *const o = odd + wave * kStep;
+    fetch(wave, e, wave < steps);
+    fetch(wave + WAVES, o, wave + WAVES < steps);
+
+    // The tokens' codes.
+    const int per_row = (p.K + 511) / 512, items = rows * per_row;
+    const int pitch = (p.K + kDepth - 1) / kDepth * kDepth + kTokenPad;
+    float keep[kItems][8];
+#pragma unroll
+    for (int t = 0; t < kItems; ++t) {
+        const int item = wave + t * WAVES;
+        if (item < items) {
+            const int r = item / per_row;
+            load8<E, VEC>(X + r * ldX, (item - r * per_row) * 512 + lane * 8, p.K, keep[t]);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kItems; ++t) {
+        const int item = wave + t * WAVES;
+        if (item < items) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(keep[t][i]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int d = 1; d < kWave; d <<= 1) m = max(m, shfl_xor_u32(m, d));
+            if (lane == 0) amax[item] = m;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kItems; ++t) {
+        const int item = wave + t * WAVES;
+        if (item < items) {
+            const int r = item / per_row, c = (item - r * per_row) * 512 + lane * 8;
+            uint32_t m = 0;
+            for (int i = 0; i < per_row; ++i) m = max(m, amax[r * per_row + i]);
+            float sc, inv;
+            row_scale(m, sc, inv);
+            uint2 v = make_uint2(pack_codes(keep[t], inv), pack_codes(keep[t] + 4, inv));
+            if (m >= 0x7F800000u) v = make_uint2(0u, 0u);
+            if (c < pitch - kTokenPad) *reinterpret_cast<uint2*>(codes + r * pitch + c) = v;
+            if (c == 0) scale[r] = sc;
+        }
+    }
+    __syncthreads();
+
+    i32x4 acc[TN] = {}, x[2], w[2][TN];
+    const int8_t* mine = codes + min(l16, rows - 1) * pitch + 16 * q;  // rows past the last repeat it
+    auto read = [&](const uint8_t* from, int s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int row = operand_channel<TN>(j, l16);
+                w[h][j] = *reinterpret_cast<const i32x4*>(from + row * kDepth + 16 * ((4 * h + q) ^ key_w<TN>(row)));
+            }
+            x[h] = *reinterpret_cast<const i32x4*>(mine + min(s, (p.K - 1) / kDepth) * kDepth + 64 * h);
+        }
+    };
+    auto multiply = [&] {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][j], x[h], acc[j], 0, 0, 0);
+    };
+    auto turn_step = [&](int s, uint8_t* at) {  // as in the few-rows kernel
+        read(at, s);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        fetch(s + 2 * WAVES, at, s + 2 * WAVES < steps);
+        if (s < steps) multiply();
+    };
+    for (int s = wave; s < steps; s += 2 * WAVES) {
+        turn_step(s, e);
+        turn_step(s + WAVES, o);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    if (steps * kDepth < p.K && steps % WAVES == wave) {
+        const int k = steps * kDepth;
+#pragma unroll
+        for (int i = 0; i < 2 * TN; ++i) {
+            const int row = 8 * i + row0;
+            *reinterpret_cast<u32x4*>(e + 8 * i * kDepth + lane * 16) = load_codes<true>(
+                wb + static_cast<int64_t>(min(row, cols - 1)) * ldw, k + 16 * (piece0 ^ key_w<TN>(row)), p.K);
+        }
+        read(e, steps);
+        multiply();
+    }
+    __syncthreads();
+    int* sum = reinterpret_cast<int*>(even);  // [rows][kPitch]
+    for (int i = threadIdx.x; i < rows * kPitch; i += WAVES * kWave) sum[i] = 0;
+    __syncthreads();
+    if (l16 < rows) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                __hip_atomic_fetch_add(sum + l16 * kPitch + 4 * TN * q + 4 * j + r, acc[j][r], __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * BN / 4; i += WAVES * kWave) {
+        const int r = i / (BN / 4), c = (i % (BN / 4)) * 4;
+        if (c < cols)
+            store_out4<E>(p, r, n0 + c, *reinterpret_cast<const i32x4*>(sum + r * kPitch + c), scale[r], packed);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Many rows: tiles through LDS.
 // ---------------------------------------------------------------------------
 // A workgroup of WM x WN waves takes a tile of 16 TM WM rows and 64 WN
@@ -831,6 +978,30 @@ int launch_product_e(const Int8Product& whole, bool aligned, void* stream) {
     return 0;
 }
 
+template <class E, int TN, int WAVES>
+int launch_tokens_t(const Int8Product& p, const void* X, int64_t ldX, bool vec, void* stream) {
+    const dim3 grid((p.N + TN * 16 - 1) / (TN * 16)), block(WAVES * kWave);
+    const auto* x = static_cast<const typename E::T*>(X);
+    const bool packed = out_aligned(p, sizeof(typename E::T), 4 * sizeof(typename E::T));
+    if (vec)
+        hipLaunchKernelGGL((int8_tokens_kernel<E, TN, WAVES, true>), grid, block, 0, static_cast<hipStream_t>(stream), p,
+                           x, ldX, packed);
+    else
+        hipLaunchKernelGGL((int8_tokens_kernel<E, TN, WAVES, false>), grid, block, 0, static_cast<hipStream_t>(stream),
+                           p, x, ldX, packed);
+    return static_cast<int>(hipGetLastError());
+}
+
+// Channels a workgroup: 16 while those fill the compute units once, else 48
+// or 64, as many rounds less.
+template <class E>
+int launch_tokens_e(const Int8Product& p, const void* X, int64_t ldX, bool vec, void* stream) {
+    const int cus = device_cu_count();
+    if (p.N <= 16 * cus) return launch_tokens_t<E, 1, 16>(p, X, ldX, vec, stream);
+    if (p.N <= 48 * cus) return launch_tokens_t<E, 3, 8>(p, X, ldX, vec, stream);
+    return launch_tokens_t<E, 4, 8>(p, X, ldX, vec, stream);
+}
+
 template <class E>
 int launch_rows_e(const void* X, int64_t rows, int d, int64_t ldx, int8_t* codes, int64_t ldc, float* scale, bool vec,
                   void* stream) {
@@ -853,6 +1024,20 @@ int launch_quantize_rows(Dtype t, const void* X, int64_t rows, int d, int64_t ld
         case Dtype::fp32: return launch_rows_e<QF32>(X, rows, d, ldx, codes, ldc, scale, vec, stream);
         case Dtype::fp16: return launch_rows_e<QF16>(X, rows, d, ldx, codes, ldc, scale, vec, stream);
         default: return launch_rows_e<QB16>(X, rows, d, ldx, codes, ldc, scale, vec, stream);
+    }
+}
+
+bool int8_tokens_fit(int64_t M, int N, int K, int64_t ldw) {
+    if (M > kMaxTokens || ldw >= (1 << 22)) return false;
+    const int64_t per_row = (K + 511) / 512, steps = (K + kDepth - 1) / kDepth;
+    return M * (steps * kDepth + kTokenPad) <= kTokenBytes && M * per_row <= 8 * kItems;
+}
+
+int launch_int8_tokens(Dtype t, const Int8Product& p, const void* X, int64_t ldX, bool vec, void* stream) {
+    switch (t) {
+        case Dtype::fp32: return launch_tokens_e<QF32>(p, X, ldX, vec, stream);
+        case Dtype::fp16: return launch_tokens_e<QF16>(p, X, ldX, vec, stream);
+        default: return launch_tokens_e<QB16>(p, X, ldX, vec, stream);
     }
 }
 

@@ -90,14 +90,16 @@ int do_linear_int8_dynamic(Dtype t, const void* X, int64_t ldX, Int8Product p, v
     p.ldx = p.K >= 1 ? dynamic_ld(p.K) : 0;
     const int c = check_product(t, p);
     if (c != 1) return c;
-    if (!X || !workspace || !rows_shape_ok(p.M, p.K, ldX)) return KBIT_EINVAL;
-    const DynamicParts w = dynamic_parts(p.M, p.N, p.K);
-    if (workspace_bytes < w.total) return KBIT_EINVAL;
+    if (!X || !rows_shape_ok(p.M, p.K, ldX)) return KBIT_EINVAL;
     if (!aligned(X, elem_size(t)) || !aligned(workspace, 16)) return KBIT_EALIGN;
+    const bool one_kernel = aligned(p.w, 16) && linear_int8_dynamic_fused(p.M, p.N, p.K, p.ldw);
+    const DynamicParts w = dynamic_parts(p.M, p.N, p.K);
+    if (!one_kernel && (workspace_bytes < w.total || !workspace)) return KBIT_EINVAL;
     if (!device_usable()) return KBIT_EDEVICE;
+    const bool vec = aligned(X, 16) && (p.M == 1 || ldX * elem_size(t) % 16 == 0);
+    if (one_kernel) return map_launch(launch_int8_tokens(t, p, X, ldX, vec, stream));
     int8_t* codes = static_cast<int8_t*>(workspace);
     float* scale = reinterpret_cast<float*>(codes + w.scale);
-    const bool vec = aligned(X, 16) && (p.M == 1 || ldX * elem_size(t) % 16 == 0);
     const int q = launch_quantize_rows(t, X, p.M, p.K, ldX, codes, p.ldx, scale, vec, stream);
     if (q != 0) return KBIT_ELAUNCH;
     p.x = codes;
@@ -322,6 +324,11 @@ int64_t linear_int8_workspace_bytes(int64_t M, int32_t N, int32_t K) {
 int64_t linear_int8_dynamic_workspace_bytes(int64_t M, int32_t N, int32_t K) {
     if (M < 0 || M > kbit::kMaxRows || N < 1 || K < 1 || K > kbit::kMaxInt8Depth) return -1;
     return kbit::dynamic_parts(M, N, K).total;
+}
+
+int linear_int8_dynamic_fused(int64_t M, int32_t N, int32_t K, int64_t ldw) {
+    return M >= 1 && M <= kbit::kMaxRows && N >= 1 && K >= 1 && K <= kbit::kMaxInt8Depth && ldw % 16 == 0 &&
+           kbit::int8_tokens_fit(M, N, K, ldw);
 }
 
 int64_t qk_norm_rope_backward_workspace_bytes(int32_t D) {

@@ -30,7 +30,7 @@ def test_header_compiles_as_c_and_cpp():
 def test_every_declared_symbol_is_exported_and_bound():
     out = subprocess.run(["gcc", "-E", "-P", "-x", "c", HEADER], capture_output=True, text=True, check=True).stdout
     names = sorted(set(re.findall(r"\b(?:int|int64_t)\s+(\w+)\s*\(", out)))
-    assert len(names) == 5 + 3 * 7, names
+    assert len(names) == 6 + 3 * 7, names
     nm = subprocess.run(["nm", "-D", "--defined-only", os.path.join(ROOT, "blockwise_bit_codebook_amd", "libkbit.so")],
                         capture_output=True, text=True, check=True).stdout
     exported = set(l.split()[-1] for l in nm.splitlines() if " T " in l)
@@ -73,6 +73,9 @@ def test_int8_validation_codes():
     dy = lib.linear_int8_dynamic_fp32
     need = lib.linear_int8_dynamic_workspace_bytes(4, 64, 100)
     assert dy(None, 0, 100, 100, None, None, 64, 100, None, None, 64, None, 0, None) == 0
+    fused = lib.linear_int8_dynamic_fused
+    assert fused(1, 4096, 4096, 4096) == 1 and fused(1, 4096, 4096, 4100) == 0       # unaligned rows of weights
+    assert fused(9, 4096, 64, 64) == 0 and fused(0, 64, 64, 64) == 0 and fused(1, 64, 32768, 32768) == 0
     assert dy(A, 4, 100, 100, A, A, 64, 100, None, A, 64, A, need - 1, None) == -1
     assert dy(A, 4, 100, 100, A, A, 64, 100, None, A, 64, None, need, None) == -1
     assert dy(A, 4, 100, 100, A, A, 64, 100, None, A, 64, B4, need, None) == -3
