@@ -18,8 +18,8 @@
 //
 // Layout: a group of GP lanes (a power of two) holds one row, each lane two
 // 16-byte (32-byte for fp32) pieces chosen so that both elements of every
-// pair are in the same lane: pieces j and j + rot/16 in the half layout, 2j
-// and 2j + 1 in the interleaved one.  So a row is read once, the sum of
+// pair are in the same lane: pieces j and j + rot/16 in the half layout, j
+// and j + half of the pieces in the interleaved one.  So a row is read once, the sum of
 // squares needs log2(GP) exchanges, and writing in place is safe.  A lane
 // group takes R heads of one token, so that the token's cosines and sines
 // are fetched once for R rows and all R rows' loads are in flight together.
@@ -52,9 +52,9 @@ struct HF32 {
         }
     }
     static __device__ void store8(T* p, const float (&v)[8]) {
-        store16<false>(p, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+        store16<true>(p, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                                 __float_as_uint(v[3])});
-        store16<false>(p + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+        store16<true>(p + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
                                     __float_as_uint(v[7])});
     }
 };
@@ -66,7 +66,7 @@ struct HF16 {
     static __device__ T narrow(float v) { return static_cast<T>(pack_f16x2(v, 0.0f) & 0xFFFFu); }
     static __device__ void widen(const u32x4* r, float (&x)[8]) { Fp16::unpack(r, x); }
     static __device__ void store8(T* p, const float (&v)[8]) {
-        store16<false>(p, u32x4{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
+        store16<true>(p, u32x4{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
                                 pack_f16x2(v[6], v[7])});
     }
 };
@@ -78,7 +78,7 @@ struct HB16 {
     static __device__ T narrow(float v) { return static_cast<T>(pack_bf16x2(v, 0.0f) & 0xFFFFu); }
     static __device__ void widen(const u32x4* r, float (&x)[8]) { Bf16::unpack(r, x); }
     static __device__ void store8(T* p, const float (&v)[8]) {
-        store16<false>(p, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+        store16<true>(p, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                 pack_bf16x2(v[6], v[7])});
     }
 };
@@ -87,32 +87,37 @@ struct HB16 {
 // elements from `a`, piece B the 8 from `b` (negative: none).  Element form
 // (one wave a row): pair i of the lane is pair slot lane + 64 i.
 struct Slots {
-    int a, b;        // vector form: first elements, or -1
-    int pair;        // vector form: first of the lane's 8 pairs in the table row
-    bool ra, rb;     // vector form: piece A (and in the half layout B with it) / piece B rotated
+    int a, b;    // vector form: first elements, or -1
+    int pa, pb;  // vector form: table columns of the lane's first and second 4 pairs
+    bool ra, rb; // vector form: piece A (and in the half layout B with it) / piece B rotated
 };
 
 template <int LAYOUT>
 __device__ __forceinline__ Slots vector_slots(int j, int D, int rot) {
+    // Neighbouring lanes hold neighbouring pieces, so that a load or store of
+    // a wave covers whole lines.
     Slots s;
-    s.pair = 8 * j;
     if constexpr (LAYOUT == kHalf) {
         const int half = rot >> 1;
-        if (8 * j < half) {
+        s.ra = s.rb = 8 * j < half;
+        s.pa = 8 * j;
+        s.pb = 8 * j + 4;
+        if (s.ra) {
             s.a = 8 * j;
             s.b = half + 8 * j;
-            s.ra = s.rb = true;
-        } else {
-            const int base = rot + 16 * (j - (half >> 3));
-            s.a = base < D ? base : -1;
-            s.b = base + 8 < D ? base + 8 : -1;
-            s.ra = s.rb = false;
+        } else {  // the elements that pass through, in two runs of pieces
+            const int u = j - (half >> 3), pieces = (D - rot) >> 3, run = (pieces + 1) >> 1;
+            s.a = u < run ? rot + 8 * u : -1;
+            s.b = u < run && u + run < pieces ? rot + 8 * (u + run) : -1;
         }
     } else {
-        s.a = 16 * j < D ? 16 * j : -1;
-        s.b = 16 * j + 8 < D ? 16 * j + 8 : -1;
-        s.ra = 16 * j < rot;
-        s.rb = 16 * j + 8 < rot;
+        const int pieces = D >> 3, run = (pieces + 1) >> 1;
+        s.a = j < run ? 8 * j : -1;
+        s.b = j < run && j + run < pieces ? 8 * (j + run) : -1;
+        s.ra = s.a >= 0 && s.a < rot;
+        s.rb = s.b >= 0 && s.b < rot;
+        s.pa = s.a >> 1;
+        s.pb = s.b >> 1;
     }
     return s;
 }
@@ -221,8 +226,9 @@ __device__ __forceinline__ void load_angles(const float* table, int64_t pos, int
             const bool live = LAYOUT == kHalf ? sl.ra : (h == 0 ? sl.ra : sl.rb);
             u32x4 c = u32x4{0u, 0u, 0u, 0u}, s = c;
             if (live) {
-                c = load16<false>(row + sl.pair + 4 * h);
-                s = load16<false>(row + (rot >> 1) + sl.pair + 4 * h);
+                const int at = h == 0 ? sl.pa : sl.pb;
+                c = load16<false>(row + at);
+                s = load16<false>(row + (rot >> 1) + at);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -306,12 +312,18 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs p) {
     const uint32_t per_token = p.set[0].units + p.set[1].units;
     const int64_t b = blockIdx.y;
     for (uint32_t unit = blockIdx.x * (kThreads >> lg) + (threadIdx.x >> lg); unit < p.units; unit += step) {
-        const uint32_t t = unit / per_token;
-        uint32_t u = unit - t * per_token;
+        // Neighbouring lane groups take neighbouring rows in memory: heads of
+        // a token, or tokens of a head where those are closer.
+        const uint32_t tokens = static_cast<uint32_t>(p.tokens);
+        const uint32_t major = unit / (p.tokens_first ? tokens : per_token);
+        const uint32_t minor = unit - major * (p.tokens_first ? tokens : per_token);
+        const uint32_t t = p.tokens_first ? minor : major;
+        uint32_t u = p.tokens_first ? major : minor;
         const bool second = u >= static_cast<uint32_t>(p.set[0].units);
         const HeadSet& set = p.set[second ? 1 : 0];
         if (second) u -= p.set[0].units;
-        const int h0 = static_cast<int>(u) * R;
+        // Heads u, u + units, ...: a load of the wave covers neighbouring rows.
+        const int h0 = static_cast<int>(u), dh = set.units;
         const int D = set.dim, rot = set.rot;
         const Slots sl = vector_slots<LAYOUT>(lane, D, rot);
 
@@ -330,7 +342,8 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs p) {
         Raw<E, VEC> raw[R];
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            if (h0 + r < set.heads) load_row<E, LAYOUT, VEC>(in + (h0 + r) * set.in_h, lane, D, rot, sl, raw[r]);
+            if (h0 + r * dh < set.heads)
+                load_row<E, LAYOUT, VEC>(in + (h0 + r * dh) * set.in_h, lane, D, rot, sl, raw[r]);
         Angles g;
         if (rot > 0) {
             const int64_t pos = load_index(p.positions, b * p.tokens + t, p.positions_wide);
@@ -340,15 +353,15 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs p) {
         if constexpr (NORM) load_weight<E, LAYOUT, VEC>(set.weight, p.weight_fp32, lane, D, rot, sl, wa, wb);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (h0 + r >= set.heads) break;
+            if (h0 + r * dh >= set.heads) break;
             float xa[8], xb[8];
             widen_row<E, VEC>(raw[r], xa, xb);
             if constexpr (NORM) {
                 float ss = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
+                for (int i = 0; i < 8; ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
                 ss = group_sum(ss, 1 << lg);
-                const float rs = 1.0f / sqrtf(ss / static_cast<float>(D) + p.eps);
+                const float rs = rsqrtf(ss * p.inv_dim + p.eps);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     xa[i] = xa[i] * rs * wa[i];
@@ -356,7 +369,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs p) {
                 }
             }
             if (rot > 0) turn<LAYOUT, VEC>(xa, xb, g, lane, D, rot, sl);
-            store_row<E, LAYOUT, VEC>(out + (h0 + r) * set.out_h, lane, D, rot, sl, xa, xb);
+            store_row<E, LAYOUT, VEC>(out + (h0 + r * dh) * set.out_h, lane, D, rot, sl, xa, xb);
         }
     }
 }
@@ -405,22 +418,22 @@ __global__ __launch_bounds__(kThreads) void norm_back_kernel(const NormBackArgs 
         widen_row<E, VEC>(rg, ga, gb);
         float ss = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
+        for (int i = 0; i < 8; ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
         ss = group_sum(ss, 1 << lg);
-        const float rs = 1.0f / sqrtf(ss / static_cast<float>(D) + p.eps);
+        const float rs = rsqrtf(ss * p.inv_dim + p.eps);
         turn<LAYOUT, VEC>(ga, gb, g, lane, D, rot, sl);
         float inner = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             xa[i] *= rs;
             xb[i] *= rs;
-            da[i] += ga[i] * xa[i];
-            db[i] += gb[i] * xb[i];
+            da[i] = fmaf(ga[i], xa[i], da[i]);
+            db[i] = fmaf(gb[i], xb[i], db[i]);
             ga[i] *= wa[i];
             gb[i] *= wb[i];
-            inner += ga[i] * xa[i] + gb[i] * xb[i];
+            inner = fmaf(ga[i], xa[i], fmaf(gb[i], xb[i], inner));
         }
-        inner = group_sum(inner, 1 << lg) / static_cast<float>(D);
+        inner = group_sum(inner, 1 << lg) * p.inv_dim;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             xa[i] = rs * (ga[i] - xa[i] * inner);
@@ -458,7 +471,16 @@ __global__ __launch_bounds__(kGradCols* kGradSplits) void norm_weight_grad_kerne
     const int lo = blockIdx.y == 0 ? 0 : first, hi = blockIdx.y == 0 ? first : total;
     float sum = 0.0f;
     if (e < D)
-        for (int i = lo + r; i < hi; i += kGradSplits) sum += partial[static_cast<int64_t>(i) * D + e];
+        for (int i = lo + r; i < hi; i += 8 * kGradSplits) {  // eight loads on their way at a time
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int row = i + j * kGradSplits;
+                v[j] = row < hi ? partial[static_cast<int64_t>(row) * D + e] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += v[j];
+        }
     red[r][c] = sum;
     __syncthreads();
     for (int s = kGradSplits / 2; s > 0; s >>= 1) {
@@ -487,6 +509,7 @@ __global__ __launch_bounds__(kThreads) void rope_table_kernel(const double* __re
 template <class E, int LAYOUT, bool NORM, bool PAGED, bool VEC, int R>
 int launch_heads_r(HeadsArgs& p, int64_t batch, void* stream) {
     for (auto& s : p.set) s.units = (s.heads + R - 1) / R;
+    p.tokens_first = p.set[0].in_s < p.set[0].in_h;
     const int lg = VEC ? p.log2_lanes : 6;
     p.units = static_cast<uint32_t>(p.tokens * (p.set[0].units + p.set[1].units));
     unsigned grid = (p.units + (kThreads >> lg) - 1) / (kThreads >> lg);
@@ -499,6 +522,15 @@ int launch_heads_r(HeadsArgs& p, int64_t batch, void* stream) {
 template <class E, int LAYOUT, bool NORM, bool PAGED>
 int launch_heads_l(HeadsArgs& p, int64_t batch, bool vec, void* stream) {
     if (!vec) return launch_heads_r<E, LAYOUT, NORM, PAGED, false, 1>(p, batch, stream);
+    // Several heads a lane group once the groups fill the device all the same
+    // (8 workgroups a compute unit), else one.  8192 tokens, heads of 128 in
+    // 16 bits, R = 1 / 2 / 4 / 8: rotation of 32 heads 26.6 / 24.7 / 25.8 / 29.7
+    // us, norm of 40 heads 47.8 / 38.0 / 34.9 / 36.2, append of 8 heads 14.1 /
+    // 14.3 / 12.9 / 12.7.
+    constexpr int R = NORM || PAGED ? 4 : 2;
+    const int64_t units = p.tokens * ((p.set[0].heads + R - 1) / R + (p.set[1].heads + R - 1) / R) * batch;
+    if ((units << p.log2_lanes) >= static_cast<int64_t>(device_cu_count()) * 8 * kThreads)
+        return launch_heads_r<E, LAYOUT, NORM, PAGED, true, R>(p, batch, stream);
     return launch_heads_r<E, LAYOUT, NORM, PAGED, true, 1>(p, batch, stream);
 }
 
@@ -518,19 +550,21 @@ int launch_heads_e(HeadsArgs& p, int64_t batch, HeadsKind kind, int layout, bool
     }
 }
 
-template <class E, int LAYOUT, bool VEC>
-int launch_back_v(const NormBackArgs& p, int grid, void* stream) {
-    hipLaunchKernelGGL((norm_back_kernel<E, LAYOUT, VEC>), dim3(grid), dim3(kThreads), 0,
-                       static_cast<hipStream_t>(stream), p);
+template <class E, int LAYOUT>
+int launch_back_l(const NormBackArgs& p, bool vec, int grid, void* stream) {
+    if (vec)
+        hipLaunchKernelGGL((norm_back_kernel<E, LAYOUT, true>), dim3(grid), dim3(kThreads), 0,
+                           static_cast<hipStream_t>(stream), p);
+    else
+        hipLaunchKernelGGL((norm_back_kernel<E, LAYOUT, false>), dim3(grid), dim3(kThreads), 0,
+                           static_cast<hipStream_t>(stream), p);
     return static_cast<int>(hipGetLastError());
 }
 
 template <class E>
 int launch_back_e(const NormBackArgs& p, int layout, bool vec, int grid, void* stream) {
-    if (layout == kHalf)
-        return vec ? launch_back_v<E, kHalf, true>(p, grid, stream) : launch_back_v<E, kHalf, false>(p, grid, stream);
-    return vec ? launch_back_v<E, kInterleaved, true>(p, grid, stream)
-               : launch_back_v<E, kInterleaved, false>(p, grid, stream);
+    return layout == kHalf ? launch_back_l<E, kHalf>(p, vec, grid, stream)
+                           : launch_back_l<E, kInterleaved>(p, vec, grid, stream);
 }
 
 }  // namespace
@@ -544,17 +578,15 @@ int launch_heads(Dtype t, HeadsArgs& p, int64_t batch, HeadsKind kind, int layou
 }
 
 int launch_norm_back(Dtype t, NormBackArgs& p, int layout, bool vec, float* d0, float* d1, void* stream) {
-    const int lg = vec ? p.log2_lanes : 6;
-    const int groups = kThreads >> lg;
+    const int groups = kThreads >> (vec ? p.log2_lanes : 6);
     // Workgroups in the proportion of the two sets' rows, at least one each
     // (a set without rows has its weight gradient written as zeros).
-    const int64_t n0 = (p.set[0].rows + groups - 1) / groups, n1 = (p.set[1].rows + groups - 1) / groups;
-    int64_t cap = kNormBackGroups;
-    int64_t g0 = n0, g1 = n1;
-    if (n0 + n1 > cap) {
-        g0 = n0 * cap / (n0 + n1);
-        g1 = cap - g0;
-        if (g1 > n1) g1 = n1;
+    int64_t n[2];
+    for (int i = 0; i < 2; ++i) n[i] = (static_cast<int64_t>(p.set[i].rows) + groups - 1) / groups;
+    int64_t g0 = n[0], g1 = n[1];
+    if (n[0] + n[1] > kNormBackGroups) {
+        g0 = n[0] * kNormBackGroups / (n[0] + n[1]);
+        g1 = kNormBackGroups - g0;
     }
     if (g0 < 1) g0 = 1;
     if (g1 < 1) g1 = 1;

@@ -3,8 +3,8 @@
 // epilogue.
 //
 //   codes    amax = max |x| over the row, scale = RN(amax / 127),
-//            q = rint(RN(x * RN(127 / amax))), half to even; |q| <= 127.
-//            A row below 2^-100 throughout (127 / amax would leave the fp32
+//            q = rint(RN(x * RN(127 * RN(1 / amax)))), half to even; |q| <= 127.
+//            A row below 2^-100 throughout (1 / amax could leave the fp32
 //            range) gets scale 0 and codes 0; a row with a NaN or an
 //            infinity gets scale NaN and codes 0, so that its outputs are NaN.
 //   product  acc[m][n] = sum over k of x[m][k] * w[n][k], exact in int32,
@@ -78,12 +78,12 @@ __device__ __forceinline__ uint32_t pack_codes(const float* x, float inv) {
     return r;
 }
 
-// The row's scale and 127 / amax from the bits of its largest magnitude
+// The row's scale and 127 (1 / amax) from the bits of its largest magnitude
 // (ordered like the magnitudes, with NaN above infinity above the rest).
 __device__ __forceinline__ void row_scale(uint32_t amax_bits, float& scale, float& inv) {
     const float amax = __uint_as_float(amax_bits);
     scale = amax / 127.0f;
-    inv = 127.0f / amax;
+    inv = 127.0f * (1.0f / amax);
     if (amax_bits < 0x0D800000u) scale = inv = 0.0f;  // below 2^-100
     if (amax_bits >= 0x7F800000u) {
         scale = __uint_as_float(0x7FC00000u);

@@ -220,6 +220,7 @@ int do_norm(Dtype t, View q, View k, View qo, View ko, int64_t B, int64_t S, int
     a.max_pos = max_pos;
     a.sign = 1.0f;
     a.eps = eps;
+    a.inv_dim = 1.0f / static_cast<float>(D);
     a.weight_fp32 = weight_fp32 != 0 || t == Dtype::fp32;
     a.log2_lanes = lanes_log2(D, rot, layout);
     const bool vec = vec_sizes(D, rot, layout) && vec_view(q, B, S, Hq, es) && vec_view(k, B, S, Hk, es) &&
@@ -262,6 +263,7 @@ int do_norm_back(Dtype t, View gq, View gk, View q, View k, View dq, View dk, in
     a.dim = D;
     a.rot = rot;
     a.eps = eps;
+    a.inv_dim = 1.0f / static_cast<float>(D);
     a.weight_fp32 = weight_fp32 != 0 || t == Dtype::fp32;
     a.log2_lanes = lanes_log2(D, rot, layout);
     const bool vec = vec_sizes(D, rot, layout) && vec_view(gq, B, S, Hq, es) && vec_view(gk, B, S, Hk, es) &&

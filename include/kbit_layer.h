@@ -24,7 +24,7 @@ extern "C" {
  * int8 linear layer.
  *
  * Codes of a row x of d values, one fp32 scale a row:
- *   amax = max |x|, scale = RN(amax / 127), q = rint(RN(x * RN(127 / amax)))
+ *   amax = max |x|, scale = RN(amax / 127), q = rint(RN(x * RN(127 * RN(1 / amax))))
  *   (half to even), |q| <= 127.  amax < 2^-100: scale 0 and codes 0.  A row
  *   with a NaN or an infinity: scale NaN and codes 0 (its outputs are NaN).
  * codes: row r starts at codes + r * ldc, 16-byte aligned (ldc a multiple of

@@ -74,7 +74,7 @@ def quantize_rows(x32):
     with np.errstate(all="ignore"):
         amax = np.abs(x).max(axis=1)  # NaN if any
         scale = (amax / np.float32(127)).astype(np.float32)
-        inv = (np.float32(127) / amax).astype(np.float32)
+        inv = (np.float32(127) * (np.float32(1) / amax).astype(np.float32)).astype(np.float32)
         tiny = amax < np.float32(2.0 ** -100)
         scale[tiny] = inv[tiny] = 0
         bad = ~np.isfinite(amax)
