@@ -6,15 +6,18 @@ HIP translation units are compiled for gfx950 only, with IEEE binary32
 division and square root, no contraction of multiply-add, denormals kept and
 packed fp32 instructions disabled; host-only C++ files are compiled as plain
 C++.  Objects go to ``_build/`` next to the package; the shared library
-lands in the package directory.
+lands in the package directory, and beside it _layer.so, the torch binding of
+the layer operators (plain C++ against torch's headers).
 """
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkbit.so")
+BINDING = os.path.join(PKG, "_layer.so")
 
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
@@ -102,7 +106,26 @@ def build(verbose=False, jobs=None):
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     shutil.move(tmp, LIB)
+    _build_binding(verbose)
     return LIB
+
+
+def _build_binding(verbose):
+    """_layer.so: csrc/layer_bind.cpp against torch's and Python's headers."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    include = os.path.join(torch, "include")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-I", INCLUDE, "-I", os.path.join(ROCM, "include"), "-I", include,
+           "-I", os.path.join(include, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "layer_bind.cpp"), "-o", tmp, "-L", PKG, "-l:libkbit.so",
+           "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for layer_bind.cpp:\n" + r.stdout + r.stderr)
+    shutil.move(tmp, BINDING)
 
 
 def main(argv=None):
