@@ -330,12 +330,12 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_few_rows_kernel(const Int8P
     static_assert(BM * kPitch * 4 <= WAVES * kStep, "the sums fit over the operands");
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, q = lane >> 4;
-    // Workgroups id, id + 8, ... run on one XCD: the m tiles of a block of
-    // channels follow each other there and share its weights in that L2.
-    const int id = blockIdx.x, turn = id >> 3;
-    const int n_tile = (turn / m_tiles) * 8 + (id & 7);
-    const int64_t m0 = static_cast<int64_t>(turn % m_tiles) * BM;
-    const int n0 = n_tile * BN;
+    // Workgroups id, id + 8, ... run on one XCD: it takes a run of tiles with
+    // the m tiles of a block of channels after each other, so that they share
+    // its weights in that L2.
+    const int per = gridDim.x >> 3, t = static_cast<int>(blockIdx.x & 7) * per + static_cast<int>(blockIdx.x >> 3);
+    const int n0 = t / m_tiles * BN;
+    const int64_t m0 = static_cast<int64_t>(t % m_tiles) * BM;
     if (n0 >= p.N) return;
     const int rows = static_cast<int>(min<int64_t>(p.M - m0, BM)), cols = min(p.N - n0, BN);
     const int8_t* xb = p.x + m0 * p.ldx;
@@ -660,8 +660,8 @@ __device__ __forceinline__ void store_tile(const Int8Product& p, uint8_t* region
     }
 }
 
-template <class E, int KG, int WM, int WN, int TM>
-__global__ __launch_bounds__(KG* WM* WN* kWave) void int8_tile_kernel(const Int8Product p, int m_tiles, int n_tiles,
+template <class E, int WM, int WN, int TM>
+__global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Product p, int m_tiles, int n_tiles,
                                                                   bool packed) {
     constexpr int TN = 4, kT = WM * WN * kWave;
     constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
@@ -670,12 +670,8 @@ __global__ __launch_bounds__(KG* WM* WN* kWave) void int8_tile_kernel(const Int8
     // Four arrays by name, and code that names the one it means: the compiler
     // then sees that the operands it reads are not those on their way, and
     // puts no wait for the loads before the reads.
-    __shared__ __align__(1024) uint8_t x_even_all[KG * BM * kDepth], x_odd_all[KG * BM * kDepth],
-        w_even_all[KG * BN * kDepth], w_odd_all[KG * BN * kDepth];
-    const int lane = __lane_id(), wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int part = KG == 1 ? 0 : wave_id / (WM * WN), wave = KG == 1 ? wave_id : wave_id % (WM * WN);
-    uint8_t *const x_even = x_even_all + part * BM * kDepth, *const x_odd = x_odd_all + part * BM * kDepth;
-    uint8_t *const w_even = w_even_all + part * BN * kDepth, *const w_odd = w_odd_all + part * BN * kDepth;
+    __shared__ __align__(1024) uint8_t x_even[BM * kDepth], x_odd[BM * kDepth], w_even[BN * kDepth], w_odd[BN * kDepth];
+    const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, q = lane >> 4;
     const int wm = (wave % WM) * TM * 16, wn = (wave / WM) * TN * 16;
 
@@ -773,9 +769,9 @@ __global__ __launch_bounds__(KG* WM* WN* kWave) void int8_tile_kernel(const Int8
     // The pipeline takes pairs of steps.  What the depth has beyond them comes
     // first (the sums are exact in any order), piece by piece through
     // registers, zeros past K.
-    const int pairs = p.K / (2 * kDepth);
+    const int steps = p.K / (2 * kDepth) * 2;
 #pragma clang loop unroll(disable)
-    for (int k = pairs * 2 * kDepth; k < p.K; k += kDepth) {
+    for (int k = steps * kDepth; k < p.K; k += kDepth) {
 #pragma clang loop unroll(disable)
         for (int i = 0; i < kXLoads + kWLoads; ++i) {
             const bool w = i >= kXLoads;
@@ -783,33 +779,28 @@ __global__ __launch_bounds__(KG* WM* WN* kWave) void int8_tile_kernel(const Int8
             const int key = w ? key_w<TN>(row) : key_x(row);
             const int8_t* from = w ? wb + static_cast<int64_t>(row) * ldw : xb + static_cast<int64_t>(row) * ldx;
             uint8_t* to = (w ? w_even : x_even) + row * kDepth + piece0 * 16;
-            if (part == 0) *reinterpret_cast<u32x4*>(to) = load_codes<true>(from, k + 16 * (piece0 ^ key), p.K);
+            *reinterpret_cast<u32x4*>(to) = load_codes<true>(from, k + 16 * (piece0 ^ key), p.K);
         }
         __syncthreads();
-        if (part == 0) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                read(x_even, w_even, h, w0);
-                multiply_all(w0);
-            }
+        for (int h = 0; h < 2; ++h) {
+            read(x_even, w_even, h, w0);
+            multiply_all(w0);
         }
         __syncthreads();
     }
-    // This part's pairs; all parts go through the most that one has.
-    const int most = 2 * ((pairs + KG - 1) / KG);
-    const int first = 2 * (pairs * part / KG), steps = 2 * (pairs * (part + 1) / KG) - first;
     // One step from (xd, wd), the next one's first half from (xn, wn).
     auto step = [&](int s, uint8_t* xd, uint8_t* wd, const uint8_t* xn, const uint8_t* wn) {
-        if (KG == 1 || s < steps) multiply(w0, xd, wd, 1, w1);
+        multiply(w0, xd, wd, 1, w1);
         arrive();
-        fetch((first + s + 2) * kDepth, xd, wd, s + 2 < steps);
-        if (KG == 1 || s < steps) multiply(w1, xn, wn, 0, w0);
+        fetch((s + 2) * kDepth, xd, wd, s + 2 < steps);
+        multiply(w1, xn, wn, 0, w0);
     };
-    fetch(first * kDepth, x_even, w_even, steps > 0);
-    fetch((first + 1) * kDepth, x_odd, w_odd, steps > 0);
+    fetch(0, x_even, w_even, steps > 0);
+    fetch(kDepth, x_odd, w_odd, steps > 0);
     arrive();
     read(x_even, w_even, 0, w0);
-    for (int s = 0; s < most; s += 2) {  // past the last step it reads operands that nobody multiplies
+    for (int s = 0; s < steps; s += 2) {  // past the last step it reads operands that nobody multiplies
         step(s, x_even, w_even, x_odd, w_odd);
         step(s + 1, x_odd, w_odd, x_even, w_even);
     }
@@ -818,58 +809,33 @@ __global__ __launch_bounds__(KG* WM* WN* kWave) void int8_tile_kernel(const Int8
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
     arrive();  // the operands are read, and the empty loads of the last steps are done
-    if constexpr (KG > 1) {
-        // The second part's sums go to the first through LDS, over the
-        // operands, half of a lane's rows at a time.
-        static_assert(KG == 2 && TM % 2 == 0, "two parts, halves of their rows");
-        constexpr int kHalfRows = TM / 2;
-        i32x4* pass = reinterpret_cast<i32x4*>(wave % 2 == 0 ? x_even_all : w_even_all) +
-                      (wave / 2) * (kHalfRows * TN * kWave);
-        static_assert(WM * WN / 2 * kHalfRows * TN * kWave * 16 <= KG * BM * kDepth && BM <= BN, "the sums fit");
-#pragma unroll
-        for (int i0 = 0; i0 < TM; i0 += kHalfRows) {
-#pragma unroll
-            for (int i = 0; i < kHalfRows; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    if (part == 1) pass[(i * TN + j) * kWave + (tid & 63)] = acc[i0 + i][j];
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kHalfRows; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    if (part == 0) acc[i0 + i][j] += pass[(i * TN + j) * kWave + (tid & 63)];
-            __syncthreads();
-        }
-        if (part == 1) return;
-    }
     // A region for each wave, in the array that has room for it.
-    constexpr int kPart = (BM < BN ? BM : BN) >= 256 ? 16384 : 8192;
+    constexpr int kPart = (BM < BN ? BM : BN) >= 256 ? 16384 : (BM < BN ? BM : BN) >= 64 ? 8192 : 4096;
     static_assert(kPart <= BM * kDepth && kPart <= BN * kDepth, "a region fits into either array");
     constexpr int kInX = BM * kDepth / kPart, kInW = BN * kDepth / kPart;
     static_assert(2 * kInX + 2 * kInW >= WM * WN, "a region for every wave");
-    uint8_t* region = wave < kInX ? x_even_all + wave * kPart
-                      : wave < 2 * kInX ? x_odd_all + (wave - kInX) * kPart
-                      : wave < 2 * kInX + kInW ? w_even_all + (wave - 2 * kInX) * kPart
-                                               : w_odd_all + (wave - 2 * kInX - kInW) * kPart;
+    uint8_t* region = wave < kInX ? x_even + wave * kPart
+                      : wave < 2 * kInX ? x_odd + (wave - kInX) * kPart
+                      : wave < 2 * kInX + kInW ? w_even + (wave - 2 * kInX) * kPart
+                                               : w_odd + (wave - 2 * kInX - kInW) * kPart;
     store_tile<E, TM, kPart>(p, region, tid & 63, m0 + wm, n0 + wn, acc, packed && (n0 * sizeof(typename E::T)) % 16 == 0);
 }
 
 template <class E, int MT, int TN, int WAVES>
 int launch_few(const Int8Product& p, void* stream) {
     const int m_tiles = static_cast<int>((p.M + MT * 16 - 1) / (MT * 16)), n_tiles = (p.N + TN * 16 - 1) / (TN * 16);
-    const unsigned grid = static_cast<unsigned>((n_tiles + 7) / 8 * 8 * m_tiles);
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
     hipLaunchKernelGGL((int8_few_rows_kernel<E, MT, TN, WAVES>), dim3(grid), dim3(WAVES * kWave), 0,
                        static_cast<hipStream_t>(stream), p, m_tiles, out_aligned(p, sizeof(typename E::T), 4 * sizeof(typename E::T)));
     return static_cast<int>(hipGetLastError());
 }
 
-template <class E, int KG, int WM, int WN, int TM>
+template <class E, int WM, int WN, int TM>
 int launch_tile(const Int8Product& p, void* stream) {
     constexpr int BM = WM * TM * 16, BN = WN * 64;
     const int m_tiles = static_cast<int>((p.M + BM - 1) / BM), n_tiles = (p.N + BN - 1) / BN;
     const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
-    hipLaunchKernelGGL((int8_tile_kernel<E, KG, WM, WN, TM>), dim3(grid), dim3(KG * WM * WN * kWave), 0,
+    hipLaunchKernelGGL((int8_tile_kernel<E, WM, WN, TM>), dim3(grid), dim3(WM * WN * kWave), 0,
                        static_cast<hipStream_t>(stream), p, m_tiles, n_tiles, out_aligned(p, sizeof(typename E::T), 16));
     return static_cast<int>(hipGetLastError());
 }
@@ -881,68 +847,80 @@ int launch_generic(const Int8Product& p, void* stream) {
     return static_cast<int>(hipGetLastError());
 }
 
-// Which kernel and tile: the least estimated time in microseconds, from what
-// the variants measured over M = 1 .. 8192, N = 512 .. 11008, K = 4096 with
-// operands from memory (256 compute units).  A round is one workgroup on every
-// compute unit.  Few-rows tiles: 4 us + rounds * (bytes of a workgroup's
-// operands) / 45 GB/s, and 0.4 us a 16 rows for a depth that
-// ends inside a step (1 x 4096: 7.1 us, 77 x 11008: 17.9 us, 256 x 4096: 14.9
-// us with 64 x 64 tiles, against 23.0 for the best of the others).  Tiles
-// through LDS, per step of 128: 64 x 128 in two parts 0.62 us a round (512 x
-// 4096: 23.8 us; 26.6 for few rows), 128 x 128 in two parts 0.80 us a round
-// (1024 x 4096: 29.7 us; 33.3 in one part), 128 x 128 in one part, two
-// workgroups a compute unit, 0.90 us or 0.59 a round (2048 x 4096: 41.4 us; 56.7
-// in two parts), 256 x 256 1.55 us and 9 us a round (4096 x 4096: 60.8 us; 75.9
-// with 128 x 128).
-enum class Int8Form { few, tile2_64, tile2_128, tile_128, tile_256 };
-
-struct Int8Choice {
-    Int8Form form;
+// Which kernel and tile: the least of estimated times, in microseconds.  The
+// estimates were fitted to 1800 measurements, every variant at 110 shapes
+// spread over M = 1 .. 8192 and N, K = 64 .. 16384 with operands from memory:
+// what the rule picks is 0.6% slower than the fastest variant on average, 10%
+// at most.  `rounds` counts workgroups on every compute unit, `bytes` a
+// workgroup's operands.  Both sides of it, for example: 77 x 11008 x 4096 18.3
+// us in 80 x 48 and 19.7 us in 80 x 64 pieces of few rows, 26.7 in tiles of 32
+// x 128; 500 x 4099 x 3840 25.2 in those, 27.3 in tiles of 64 x 128, 30.1 in 80
+// x 64 pieces; 2048 x 4096 x 4096 41.4 in tiles of 128 x 128, 51 in 256 x 256;
+// 4096 x 4096 x 4096 75.9 and 60.8.
+struct Int8Few {
     int mt, tn;
 };
+struct Int8Tile {
+    int bm, bn;
+    double least, step, round, tail, operands;  // us: a step alone, a step a round, a round, a partial step, 10 MB
+};
+constexpr Int8Few kFew[] = {{1, 1}, {1, 2}, {1, 3}, {1, 4}, {2, 2}, {2, 4}, {3, 2}, {3, 4}, {4, 4}, {5, 3}, {5, 4}};
+constexpr Int8Tile kTiles[] = {{32, 128, 0.455, 0.152, 1.47, 4.70, 3.97},
+                               {64, 128, 0.629, 0.271, 2.39, 3.11, 2.45},
+                               {128, 128, 0.761, 0.452, 4.01, 3.82, 1.79},
+                               {256, 256, 1.491, 1.551, 6.64, 6.14, 0.27}};
 
-constexpr int kFewTiles[][2] = {{1, 1}, {1, 3}, {1, 4}, {2, 1}, {2, 2}, {2, 4}, {3, 2}, {3, 4}, {4, 2}, {4, 4}, {5, 3}, {5, 4}};
+struct Int8Choice {
+    Int8Few few;  // or
+    int bm;       // tiles of bm rows, where not 0
+};
 
 Int8Choice choose_form(int64_t M, int N, int K) {
-    const double cus = device_cu_count(), steps = (K + kDepth - 1) / kDepth;
+    const int64_t cus = device_cu_count();
     auto rounds = [&](int bm, int bn) {
-        const double tiles = static_cast<double>((M + bm - 1) / bm) * ((N + bn - 1) / bn);
-        const int64_t r = static_cast<int64_t>((tiles + cus - 1) / cus);
-        return static_cast<double>(r);
+        const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+        return static_cast<double>((tiles + cus - 1) / cus);
     };
+    const double operands = 1e-7 * (static_cast<double>(M) + N) * K;
     Int8Choice best{};
     double least = 1e30;
-    auto consider = [&](double us, Int8Form form, int mt, int tn) {
+    for (const Int8Few& f : kFew) {
+        const double bytes = 16.0 * (f.mt + f.tn) * K;
+        const double us = 1.23 + operands + rounds(16 * f.mt, 16 * f.tn) *
+                                                (2.21 + 0.161 * f.mt * f.tn + 1.216e-5 * bytes +
+                                                 (K % kDepth ? 0.433 * (f.mt + f.tn) : 0.0));
         if (us < least) {
             least = us;
-            best = Int8Choice{form, mt, tn};
+            best = Int8Choice{f, 0};
         }
-    };
-    for (const auto& t : kFewTiles)
-        consider(4.0 + rounds(16 * t[0], 16 * t[1]) * (t[0] + t[1]) * (16.0 * K / 45e3 + (K % kDepth ? 0.4 : 0.0)),
-                 Int8Form::few, t[0], t[1]);
-    if (M >= 64 && N >= 128) consider(4.0 + rounds(64, 128) * steps * 0.62, Int8Form::tile2_64, 0, 0);
-    if (M >= 128 && N >= 128) {
-        const double r = rounds(128, 128);
-        consider(4.0 + r * steps * 0.80, Int8Form::tile2_128, 0, 0);
-        consider(4.0 + steps * (0.59 * r > 0.90 ? 0.59 * r : 0.90), Int8Form::tile_128, 0, 0);
     }
-    if (M >= 256 && N >= 256) consider(rounds(256, 256) * (9.0 + steps * 1.55), Int8Form::tile_256, 0, 0);
+    const int rest = K % (2 * kDepth);
+    const double steps = K / (2 * kDepth) * 2 + (rest > 0 ? 1 : 0) + (rest > kDepth ? 1 : 0);
+    for (const Int8Tile& t : kTiles) {
+        if (M < t.bm || N < t.bn) continue;
+        const double r = rounds(t.bm, t.bn);
+        const double us = (t.step * r > t.least ? t.step * r : t.least) * steps + t.round * r + (rest ? t.tail : 0.0) +
+                          t.operands * operands;
+        if (us < least) {
+            least = us;
+            best = Int8Choice{{}, t.bm};
+        }
+    }
     return best;
 }
 
+// The waves that split the depth: as many as their operands fit into LDS.
 template <class E>
-int launch_few_tile(const Int8Product& p, int mt, int tn, void* stream) {
-    switch (10 * mt + tn) {
+int launch_few_tile(const Int8Product& p, Int8Few f, void* stream) {
+    switch (10 * f.mt + f.tn) {
         case 11: return launch_few<E, 1, 1, 16>(p, stream);
+        case 12: return launch_few<E, 1, 2, 8>(p, stream);
         case 13: return launch_few<E, 1, 3, 8>(p, stream);
         case 14: return launch_few<E, 1, 4, 7>(p, stream);
-        case 21: return launch_few<E, 2, 1, 12>(p, stream);
         case 22: return launch_few<E, 2, 2, 8>(p, stream);
         case 24: return launch_few<E, 2, 4, 6>(p, stream);
         case 32: return launch_few<E, 3, 2, 6>(p, stream);
         case 34: return launch_few<E, 3, 4, 5>(p, stream);
-        case 42: return launch_few<E, 4, 2, 6>(p, stream);
         case 44: return launch_few<E, 4, 4, 4>(p, stream);
         case 53: return launch_few<E, 5, 3, 4>(p, stream);
         default: return launch_few<E, 5, 4, 4>(p, stream);
@@ -965,12 +943,12 @@ int launch_product_e(const Int8Product& whole, bool aligned, void* stream) {
             e = launch_generic<E>(p, stream);
         } else {
             const Int8Choice c = choose_form(p.M, p.N, p.K);
-            switch (c.form) {
-                case Int8Form::few: e = launch_few_tile<E>(p, c.mt, c.tn, stream); break;
-                case Int8Form::tile2_64: e = launch_tile<E, 2, 2, 2, 2>(p, stream); break;
-                case Int8Form::tile2_128: e = launch_tile<E, 2, 2, 2, 4>(p, stream); break;
-                case Int8Form::tile_128: e = launch_tile<E, 1, 2, 2, 4>(p, stream); break;
-                default: e = launch_tile<E, 1, 2, 4, 8>(p, stream); break;
+            switch (c.bm) {
+                case 0: e = launch_few_tile<E>(p, c.few, stream); break;
+                case 32: e = launch_tile<E, 2, 2, 1>(p, stream); break;
+                case 64: e = launch_tile<E, 2, 2, 2>(p, stream); break;
+                case 128: e = launch_tile<E, 2, 2, 4>(p, stream); break;
+                default: e = launch_tile<E, 2, 4, 8>(p, stream); break;
             }
         }
         if (e != 0) return e;
