@@ -597,8 +597,10 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Pro
 // so that a row leaves as one run of 64 channels: a lane's 16 channels alone
 // are 32 bytes of a line, and writing those cost 36 us a tile of 256 x 256.
 // The 16-byte pieces of a row are xor-ed with the row like the operands'.
+// NT, stores that do not stay in L2: 8192 x 11008 x 4096 380 -> 368 us in tiles
+// of 256 rows, 435 -> 408 us in 128, but 75.0 -> 80.3 us (1000 x 11008) in 64.
 // m, n: the wave's first row and channel.
-template <class E, int TM, int kRegion>
+template <class E, int TM, int kRegion, bool NT>
 __device__ __forceinline__ void store_tile(const Int8Product& p, uint8_t* region, int lane, int64_t m, int n,
                                            const i32x4 (&acc)[TM][4], bool packed) {
     using T = typename E::T;
@@ -648,7 +650,7 @@ __device__ __forceinline__ void store_tile(const Int8Product& p, uint8_t* region
             for (int r0 = 0; r0 < kPass * 16; r0 += kRows) {
                 const int row = r0 + lane / kPieces, piece = lane % kPieces;
                 const u32x4 d = *reinterpret_cast<const u32x4*>(region + row * kRow + 16 * (piece ^ (row & 7)));
-                store16<false>(out + (16 * i0 + row) * p.ldo + piece * (16 / kSize), d);
+                store16<NT>(out + (16 * i0 + row) * p.ldo + piece * (16 / kSize), d);
             }
         } else {
             for (int row = 0; row < kPass * 16; ++row) {
@@ -818,7 +820,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
                       : wave < 2 * kInX ? x_odd + (wave - kInX) * kPart
                       : wave < 2 * kInX + kInW ? w_even + (wave - 2 * kInX) * kPart
                                                : w_odd + (wave - 2 * kInX - kInW) * kPart;
-    store_tile<E, TM, kPart>(p, region, tid & 63, m0 + wm, n0 + wn, acc, packed && (n0 * sizeof(typename E::T)) % 16 == 0);
+    store_tile<E, TM, kPart, (BM >= 128)>(p, region, tid & 63, m0 + wm, n0 + wn, acc, packed && (n0 * sizeof(typename E::T)) % 16 == 0);
 }
 
 template <class E, int MT, int TN, int WAVES>
@@ -848,63 +850,60 @@ int launch_generic(const Int8Product& p, void* stream) {
 }
 
 // Which kernel and tile: the least of estimated times, in microseconds.  The
-// estimates were fitted to 1800 measurements, every variant at 110 shapes
+// estimates were fitted to 1100 measurements, every variant at 130 shapes
 // spread over M = 1 .. 8192 and N, K = 64 .. 16384 with operands from memory:
-// what the rule picks is 0.6% slower than the fastest variant on average, 10%
-// at most.  `rounds` counts workgroups on every compute unit, `bytes` a
-// workgroup's operands.  Both sides of it, for example: 77 x 11008 x 4096 18.3
-// us in 80 x 48 and 19.7 us in 80 x 64 pieces of few rows, 26.7 in tiles of 32
-// x 128; 500 x 4099 x 3840 25.2 in those, 27.3 in tiles of 64 x 128, 30.1 in 80
-// x 64 pieces; 2048 x 4096 x 4096 41.4 in tiles of 128 x 128, 51 in 256 x 256;
-// 4096 x 4096 x 4096 75.9 and 60.8.
+// what the rule picks is 2% slower than the fastest variant on average, and
+// over 20% at 2 of them.  `rounds` counts workgroups on every compute unit.
+// Both sides of it, for example: 77 x 11008 x 4096 18.3 us in 80 x 48 and 19.7
+// us in 80 x 64 pieces of few rows, 26.7 in tiles of 32 x 128; 500 x 4099 x
+// 3840 27.1 in tiles of 64 x 128, 27.3 in 32 x 128, 30.1 in 80 x 64 pieces, 31.7
+// in 128 x 128; 4096 x 4096 x 4096 58.8 in 256 x 256, 71.5 in 128 x 128.
 struct Int8Few {
     int mt, tn;
 };
 struct Int8Tile {
     int bm, bn;
-    double least, step, round, tail, operands;  // us: a step alone, a step a round, a round, a partial step, 10 MB
+    // us: a launch, a step alone, a step a round, a round, a partial step, 10 MB of operands
+    double base, least, step, round, tail, operands;
 };
 constexpr Int8Few kFew[] = {{1, 1}, {1, 2}, {1, 3}, {1, 4}, {2, 2}, {2, 4}, {3, 2}, {3, 4}, {4, 4}, {5, 3}, {5, 4}};
-constexpr Int8Tile kTiles[] = {{32, 128, 0.455, 0.152, 1.47, 4.70, 3.97},
-                               {64, 128, 0.629, 0.271, 2.39, 3.11, 2.45},
-                               {128, 128, 0.761, 0.452, 4.01, 3.82, 1.79},
-                               {256, 256, 1.491, 1.551, 6.64, 6.14, 0.27}};
+constexpr Int8Tile kTiles[] = {{32, 128, 0.6, 0.615, 0.287, 1.18, 2.54, 1.75},
+                               {64, 128, 0.0, 0.709, 0.379, 2.11, 2.92, 1.26},
+                               {128, 128, 0.0, 0.899, 0.584, 3.77, 2.74, 0.11},
+                               {256, 256, 0.0, 1.418, 1.456, 8.36, 3.15, 1.65}};
 
 struct Int8Choice {
     Int8Few few;  // or
     int bm;       // tiles of bm rows, where not 0
+    double us;
 };
 
-Int8Choice choose_form(int64_t M, int N, int K) {
-    const int64_t cus = device_cu_count();
-    auto rounds = [&](int bm, int bn) {
-        const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
-        return static_cast<double>((tiles + cus - 1) / cus);
-    };
-    const double operands = 1e-7 * (static_cast<double>(M) + N) * K;
-    Int8Choice best{};
-    double least = 1e30;
-    for (const Int8Few& f : kFew) {
-        const double bytes = 16.0 * (f.mt + f.tn) * K;
-        const double us = 1.23 + operands + rounds(16 * f.mt, 16 * f.tn) *
-                                                (2.21 + 0.161 * f.mt * f.tn + 1.216e-5 * bytes +
-                                                 (K % kDepth ? 0.433 * (f.mt + f.tn) : 0.0));
-        if (us < least) {
-            least = us;
-            best = Int8Choice{f, 0};
-        }
-    }
+double rounds_of(int64_t M, int64_t N, int bm, int bn, int64_t cus) {
+    const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+    return static_cast<double>((tiles + cus - 1) / cus);
+}
+
+double tile_us(const Int8Tile& t, double rounds, int64_t M, int N, int K) {
     const int rest = K % (2 * kDepth);
     const double steps = K / (2 * kDepth) * 2 + (rest > 0 ? 1 : 0) + (rest > kDepth ? 1 : 0);
+    return t.base + (t.step * rounds > t.least ? t.step * rounds : t.least) * steps + t.round * rounds + (rest ? t.tail : 0.0) +
+           t.operands * 1e-7 * (static_cast<double>(M) + N) * K;
+}
+
+Int8Choice choose_form(int64_t M, int N, int K, int64_t cus) {
+    Int8Choice best{};
+    best.us = 1e30;
+    for (const Int8Few& f : kFew) {
+        const double us = 1.14 + 0.88e-7 * (static_cast<double>(M) + N) * K +
+                          rounds_of(M, N, 16 * f.mt, 16 * f.tn, cus) *
+                              (2.02 + 0.172 * f.mt * f.tn + 1.34e-5 * 16.0 * (f.mt + f.tn) * K +
+                               (K % kDepth ? 0.414 * (f.mt + f.tn) : 0.0));
+        if (us < best.us) best = Int8Choice{f, 0, us};
+    }
     for (const Int8Tile& t : kTiles) {
         if (M < t.bm || N < t.bn) continue;
-        const double r = rounds(t.bm, t.bn);
-        const double us = (t.step * r > t.least ? t.step * r : t.least) * steps + t.round * r + (rest ? t.tail : 0.0) +
-                          t.operands * operands;
-        if (us < least) {
-            least = us;
-            best = Int8Choice{{}, t.bm};
-        }
+        const double us = tile_us(t, rounds_of(M, N, t.bm, t.bn, cus), M, N, K);
+        if (us < best.us) best = Int8Choice{{}, t.bm, us};
     }
     return best;
 }
@@ -928,7 +927,20 @@ int launch_few_tile(const Int8Product& p, Int8Few f, void* stream) {
 }
 
 template <class E>
+int launch_form(const Int8Product& p, const Int8Choice& c, void* stream) {
+    switch (c.bm) {
+        case 0: return launch_few_tile<E>(p, c.few, stream);
+        case 32: return launch_tile<E, 2, 2, 1>(p, stream);
+        case 64: return launch_tile<E, 2, 2, 2>(p, stream);
+        case 128: return launch_tile<E, 2, 2, 4>(p, stream);
+        default: return launch_tile<E, 2, 4, 8>(p, stream);
+    }
+}
+
+template <class E>
 int launch_product_e(const Int8Product& whole, bool aligned, void* stream) {
+    using T = typename E::T;
+    const int64_t cus = device_cu_count();
     // Row blocks keep the grids (below 2^32 threads) and the kernels' 32-bit
     // offsets in range.
     constexpr int64_t kRowBlock = int64_t(1) << 15;
@@ -937,20 +949,14 @@ int launch_product_e(const Int8Product& whole, bool aligned, void* stream) {
         p.M = whole.M - m < kRowBlock ? whole.M - m : kRowBlock;
         p.x += m * p.ldx;
         p.xs += m;
-        p.out = static_cast<typename E::T*>(p.out) + m * p.ldo;
+        p.out = static_cast<T*>(p.out) + m * p.ldo;
         int e;
         if (!aligned || p.ldx >= (1 << 22) || p.ldw >= (1 << 22)) {
             e = launch_generic<E>(p, stream);
-        } else {
-            const Int8Choice c = choose_form(p.M, p.N, p.K);
-            switch (c.bm) {
-                case 0: e = launch_few_tile<E>(p, c.few, stream); break;
-                case 32: e = launch_tile<E, 2, 2, 1>(p, stream); break;
-                case 64: e = launch_tile<E, 2, 2, 2>(p, stream); break;
-                case 128: e = launch_tile<E, 2, 2, 4>(p, stream); break;
-                default: e = launch_tile<E, 2, 4, 8>(p, stream); break;
-            }
+            if (e != 0) return e;
+            continue;
         }
+        e = launch_form<E>(p, choose_form(p.M, p.N, p.K, cus), stream);
         if (e != 0) return e;
     }
     return 0;
