@@ -850,60 +850,67 @@ int launch_generic(const Int8Product& p, void* stream) {
 }
 
 // Which kernel and tile: the least of estimated times, in microseconds.  The
-// estimates were fitted to 1100 measurements, every variant at 130 shapes
-// spread over M = 1 .. 8192 and N, K = 64 .. 16384 with operands from memory:
-// what the rule picks is 2% slower than the fastest variant on average, and
-// over 20% at 2 of them.  `rounds` counts workgroups on every compute unit.
-// Both sides of it, for example: 77 x 11008 x 4096 18.3 us in 80 x 48 and 19.7
-// us in 80 x 64 pieces of few rows, 26.7 in tiles of 32 x 128; 500 x 4099 x
-// 3840 27.1 in tiles of 64 x 128, 27.3 in 32 x 128, 30.1 in 80 x 64 pieces, 31.7
-// in 128 x 128; 4096 x 4096 x 4096 58.8 in 256 x 256, 71.5 in 128 x 128.
+// estimates were fitted to 2100 measurements, every variant at 130 shapes
+// spread over M = 1 .. 8192 and N, K = 64 .. 16384 with operands from memory
+// and from cache: what the rule picks is 0.7% slower than the fastest variant
+// on average, 11% at most.  Both sides of it, for example (operands from
+// memory): 77 x 11008 x 4096 18.3 us in 80 x 48 and 19.7 us in 80 x 64 pieces of
+// few rows, 26.7 in tiles of 32 x 128; 500 x 4099 x 3840 27.1 in tiles of 64 x
+// 128, 27.3 in 32 x 128, 30.1 in 80 x 64 pieces, 31.7 in 128 x 128; 4096 x 4096 x
+// 4096 58.8 in 256 x 256, 71.5 in 128 x 128.
 struct Int8Few {
     int mt, tn;
 };
 struct Int8Tile {
     int bm, bn;
-    // us: a launch, a step alone, a step a round, a round, a partial step, 10 MB of operands
-    double base, least, step, round, tail, operands;
+    // us: a launch, a step alone, a step a round, a round, a partial step, 10
+    // MB of operands; the weight of whole rounds against parts of one
+    double base, least, step, round, tail, operands, whole;
 };
 constexpr Int8Few kFew[] = {{1, 1}, {1, 2}, {1, 3}, {1, 4}, {2, 2}, {2, 4}, {3, 2}, {3, 4}, {4, 4}, {5, 3}, {5, 4}};
-constexpr Int8Tile kTiles[] = {{32, 128, 0.6, 0.615, 0.287, 1.18, 2.54, 1.75},
-                               {64, 128, 0.0, 0.709, 0.379, 2.11, 2.92, 1.26},
-                               {128, 128, 0.0, 0.899, 0.584, 3.77, 2.74, 0.11},
-                               {256, 256, 0.0, 1.418, 1.456, 8.36, 3.15, 1.65}};
+constexpr Int8Tile kTiles[] = {{32, 128, 0.84, 0.497, 0.253, 1.08, 2.32, 1.29, 0.255},
+                               {64, 128, 0.0, 0.572, 0.382, 1.85, 3.01, 1.07, 0.454},
+                               {128, 128, 0.0, 0.799, 0.544, 2.70, 3.31, 0.11, 0.742},
+                               {256, 256, 0.0, 1.189, 1.386, 7.47, 2.93, 0.83, 1.0}};
 
 struct Int8Choice {
     Int8Few few;  // or
     int bm;       // tiles of bm rows, where not 0
-    double us;
 };
 
-double rounds_of(int64_t M, int64_t N, int bm, int bn, int64_t cus) {
+// Workgroups a compute unit: a part of a round is cheaper than a whole one
+// where several workgroups fit a compute unit (whole < 1).
+double rounds_of(int64_t M, int64_t N, int bm, int bn, int64_t cus, double whole) {
     const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
-    return static_cast<double>((tiles + cus - 1) / cus);
-}
-
-double tile_us(const Int8Tile& t, double rounds, int64_t M, int N, int K) {
-    const int rest = K % (2 * kDepth);
-    const double steps = K / (2 * kDepth) * 2 + (rest > 0 ? 1 : 0) + (rest > kDepth ? 1 : 0);
-    return t.base + (t.step * rounds > t.least ? t.step * rounds : t.least) * steps + t.round * rounds + (rest ? t.tail : 0.0) +
-           t.operands * 1e-7 * (static_cast<double>(M) + N) * K;
+    const double r = whole * static_cast<double>((tiles + cus - 1) / cus) + (1.0 - whole) * tiles / cus;
+    return r < 1.0 ? 1.0 : r;
 }
 
 Int8Choice choose_form(int64_t M, int N, int K, int64_t cus) {
     Int8Choice best{};
-    best.us = 1e30;
+    double least = 1e30;
+    const double operands = 1e-7 * (static_cast<double>(M) + N) * K;
     for (const Int8Few& f : kFew) {
-        const double us = 1.14 + 0.88e-7 * (static_cast<double>(M) + N) * K +
-                          rounds_of(M, N, 16 * f.mt, 16 * f.tn, cus) *
-                              (2.02 + 0.172 * f.mt * f.tn + 1.34e-5 * 16.0 * (f.mt + f.tn) * K +
-                               (K % kDepth ? 0.414 * (f.mt + f.tn) : 0.0));
-        if (us < best.us) best = Int8Choice{f, 0, us};
+        const double us = 1.34 + 0.68 * operands +
+                          rounds_of(M, N, 16 * f.mt, 16 * f.tn, cus, 1.0) *
+                              (1.783 + 0.204 * f.mt * f.tn + 1.297e-5 * 16.0 * (f.mt + f.tn) * K +
+                               (K % kDepth ? 0.286 * (f.mt + f.tn) : 0.0));
+        if (us < least) {
+            least = us;
+            best = Int8Choice{f, 0};
+        }
     }
+    const int rest = K % (2 * kDepth);
+    const double steps = K / (2 * kDepth) * 2 + (rest > 0 ? 1 : 0) + (rest > kDepth ? 1 : 0);
     for (const Int8Tile& t : kTiles) {
         if (M < t.bm || N < t.bn) continue;
-        const double us = tile_us(t, rounds_of(M, N, t.bm, t.bn, cus), M, N, K);
-        if (us < best.us) best = Int8Choice{{}, t.bm, us};
+        const double r = rounds_of(M, N, t.bm, t.bn, cus, t.whole);
+        const double us = t.base + (t.step * r > t.least ? t.step * r : t.least) * steps + t.round * r +
+                          (rest ? t.tail : 0.0) + t.operands * operands;
+        if (us < least) {
+            least = us;
+            best = Int8Choice{{}, t.bm};
+        }
     }
     return best;
 }
