@@ -140,17 +140,22 @@ __device__ __forceinline__ void element_pair(int p, int D, int rot, int& ea, int
     if (eb >= D) eb = -1;
 }
 
-// The 16 raw elements of a lane before widening.
-template <class E, bool VEC>
+// How a lane holds its elements: the vector form (kVector), 8 + 8 in two
+// pieces, or the element form with 1 or 8 pairs a lane, as the row needs.
+constexpr int kVector = 0;
+constexpr int count_of(int form) { return form == kVector ? 8 : form; }
+
+// A lane's raw elements before widening.
+template <class E, int FORM>
 struct Raw {
-    u32x4 v[VEC ? 2 * E::kVec : 1];
-    typename E::T s[VEC ? 1 : 16];
+    u32x4 v[FORM == kVector ? 2 * E::kVec : 1];
+    typename E::T s[FORM == kVector ? 1 : 2 * FORM];
 };
 
-template <class E, int LAYOUT, bool VEC>
+template <class E, int LAYOUT, int FORM>
 __device__ __forceinline__ void load_row(const typename E::T* p, int lane, int D, int rot, const Slots& sl,
-                                         Raw<E, VEC>& r) {
-    if constexpr (VEC) {
+                                         Raw<E, FORM>& r) {
+    if constexpr (FORM == kVector) {
         constexpr int V = E::kVec;
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) r.v[i] = u32x4{0u, 0u, 0u, 0u};
@@ -164,39 +169,40 @@ __device__ __forceinline__ void load_row(const typename E::T* p, int lane, int D
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < FORM; ++i) {
             int ea, eb;
             bool turned;
             element_pair<LAYOUT>(lane + kWave * i, D, rot, ea, eb, turned);
             r.s[i] = ea >= 0 ? p[ea] : typename E::T(0);
-            r.s[8 + i] = eb >= 0 ? p[eb] : typename E::T(0);
+            r.s[FORM + i] = eb >= 0 ? p[eb] : typename E::T(0);
         }
     }
 }
 
-template <class E, bool VEC>
-__device__ __forceinline__ void widen_row(const Raw<E, VEC>& r, float (&a)[8], float (&b)[8]) {
-    if constexpr (VEC) {
+template <class E, int FORM>
+__device__ __forceinline__ void widen_row(const Raw<E, FORM>& r, float (&a)[count_of(FORM)],
+                                          float (&b)[count_of(FORM)]) {
+    if constexpr (FORM == kVector) {
         E::widen(r.v, a);
         E::widen(r.v + E::kVec, b);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < FORM; ++i) {
             a[i] = E::one(r.s[i]);
-            b[i] = E::one(r.s[8 + i]);
+            b[i] = E::one(r.s[FORM + i]);
         }
     }
 }
 
-template <class E, int LAYOUT, bool VEC>
+template <class E, int LAYOUT, int FORM>
 __device__ __forceinline__ void store_row(typename E::T* p, int lane, int D, int rot, const Slots& sl,
-                                          const float (&a)[8], const float (&b)[8]) {
-    if constexpr (VEC) {
+                                          const float (&a)[count_of(FORM)], const float (&b)[count_of(FORM)]) {
+    if constexpr (FORM == kVector) {
         if (sl.a >= 0) E::store8(p + sl.a, a);
         if (sl.b >= 0) E::store8(p + sl.b, b);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < FORM; ++i) {
             int ea, eb;
             bool turned;
             element_pair<LAYOUT>(lane + kWave * i, D, rot, ea, eb, turned);
@@ -209,18 +215,19 @@ __device__ __forceinline__ void store_row(typename E::T* p, int lane, int D, int
 // The lane's 8 cosines and sines (1 and 0 where nothing is rotated, so that
 // the rotation leaves those elements as they are: x * 1 - y * 0 is x for
 // finite y only, hence turn() skips them instead).
+template <int FORM>
 struct Angles {
-    float c[8], s[8];
+    float c[count_of(FORM)], s[count_of(FORM)];
 };
 
-template <int LAYOUT, bool VEC>
+template <int LAYOUT, int FORM>
 __device__ __forceinline__ void load_angles(const float* table, int64_t pos, int64_t max_pos, int lane, int D, int rot,
-                                            const Slots& sl, float sign, Angles& g) {
+                                            const Slots& sl, float sign, Angles<FORM>& g) {
     // A position outside the table poisons the rotated elements.
     const bool ok = pos >= 0 && pos < max_pos;
     const float* row = table + (ok ? pos : 0) * rot;
     const float bad = __uint_as_float(0x7FC00000u);
-    if constexpr (VEC) {
+    if constexpr (FORM == kVector) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const bool live = LAYOUT == kHalf ? sl.ra : (h == 0 ? sl.ra : sl.rb);
@@ -238,7 +245,7 @@ __device__ __forceinline__ void load_angles(const float* table, int64_t pos, int
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < FORM; ++i) {
             const int p = lane + kWave * i;
             const bool live = p < (rot >> 1);
             g.c[i] = ok ? (live ? row[p] : 1.0f) : bad;
@@ -253,12 +260,12 @@ __device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s, 
     y = on ? ny : y;
 }
 
-template <int LAYOUT, bool VEC>
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const Angles& g, int lane, int D, int rot,
+template <int LAYOUT, int FORM>
+__device__ __forceinline__ void turn(float (&a)[count_of(FORM)], float (&b)[count_of(FORM)], const Angles<FORM>& g, int lane, int D, int rot,
                                      const Slots& sl) {
-    if constexpr (!VEC) {
+    if constexpr (FORM != kVector) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn_pair(a[i], b[i], g.c[i], g.s[i], lane + kWave * i < (rot >> 1));
+        for (int i = 0; i < FORM; ++i) turn_pair(a[i], b[i], g.c[i], g.s[i], lane + kWave * i < (rot >> 1));
     } else if constexpr (LAYOUT == kHalf) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) turn_pair(a[i], b[i], g.c[i], g.s[i], sl.ra);
@@ -286,27 +293,27 @@ __device__ __forceinline__ int64_t load_index(const void* p, int64_t i, bool wid
     return wide ? static_cast<const int64_t*>(p)[i] : static_cast<const int32_t*>(p)[i];
 }
 
-template <class E, int LAYOUT, bool VEC>
+template <class E, int LAYOUT, int FORM>
 __device__ __forceinline__ void load_weight(const void* w, bool w_fp32, int lane, int D, int rot, const Slots& sl,
-                                            float (&a)[8], float (&b)[8]) {
+                                            float (&a)[count_of(FORM)], float (&b)[count_of(FORM)]) {
     if (w_fp32) {
-        Raw<HF32, VEC> r;
-        load_row<HF32, LAYOUT, VEC>(static_cast<const float*>(w), lane, D, rot, sl, r);
-        widen_row<HF32, VEC>(r, a, b);
+        Raw<HF32, FORM> r;
+        load_row<HF32, LAYOUT, FORM>(static_cast<const float*>(w), lane, D, rot, sl, r);
+        widen_row<HF32, FORM>(r, a, b);
     } else {
-        Raw<E, VEC> r;
-        load_row<E, LAYOUT, VEC>(static_cast<const typename E::T*>(w), lane, D, rot, sl, r);
-        widen_row<E, VEC>(r, a, b);
+        Raw<E, FORM> r;
+        load_row<E, LAYOUT, FORM>(static_cast<const typename E::T*>(w), lane, D, rot, sl, r);
+        widen_row<E, FORM>(r, a, b);
     }
 }
 
 // One pass over up to two sets of heads (queries and keys, or keys and
 // values).  NORM: norm before the rotation.  PAGED: the output row is found
 // through the token's slot; set 1 is copied.
-template <class E, int LAYOUT, bool NORM, bool PAGED, bool VEC, int R>
+template <class E, int LAYOUT, bool NORM, bool PAGED, int FORM, int R>
 __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs p) {
     using T = typename E::T;
-    const int lg = VEC ? p.log2_lanes : 6;
+    const int lg = FORM == kVector ? p.log2_lanes : 6;
     const int lane = threadIdx.x & ((1 << lg) - 1);
     const uint32_t step = gridDim.x * (kThreads >> lg);
     const uint32_t per_token = p.set[0].units + p.set[1].units;
@@ -339,37 +346,37 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs p) {
         }
         T* out = static_cast<T*>(set.out) + at;
         const T* in = static_cast<const T*>(set.in) + b * set.in_b + t * set.in_s;
-        Raw<E, VEC> raw[R];
+        Raw<E, FORM> raw[R];
 #pragma unroll
         for (int r = 0; r < R; ++r)
             if (h0 + r * dh < set.heads)
-                load_row<E, LAYOUT, VEC>(in + (h0 + r * dh) * set.in_h, lane, D, rot, sl, raw[r]);
-        Angles g;
+                load_row<E, LAYOUT, FORM>(in + (h0 + r * dh) * set.in_h, lane, D, rot, sl, raw[r]);
+        Angles<FORM> g;
         if (rot > 0) {
             const int64_t pos = load_index(p.positions, b * p.tokens + t, p.positions_wide);
-            load_angles<LAYOUT, VEC>(p.table, pos, p.max_pos, lane, D, rot, sl, p.sign, g);
+            load_angles<LAYOUT, FORM>(p.table, pos, p.max_pos, lane, D, rot, sl, p.sign, g);
         }
-        float wa[8], wb[8];
-        if constexpr (NORM) load_weight<E, LAYOUT, VEC>(set.weight, p.weight_fp32, lane, D, rot, sl, wa, wb);
+        float wa[count_of(FORM)], wb[count_of(FORM)];
+        if constexpr (NORM) load_weight<E, LAYOUT, FORM>(set.weight, p.weight_fp32, lane, D, rot, sl, wa, wb);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (h0 + r * dh >= set.heads) break;
-            float xa[8], xb[8];
-            widen_row<E, VEC>(raw[r], xa, xb);
+            float xa[count_of(FORM)], xb[count_of(FORM)];
+            widen_row<E, FORM>(raw[r], xa, xb);
             if constexpr (NORM) {
                 float ss = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+                for (int i = 0; i < count_of(FORM); ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
                 ss = group_sum(ss, 1 << lg);
                 const float rs = rsqrtf(ss * p.inv_dim + p.eps);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < count_of(FORM); ++i) {
                     xa[i] = xa[i] * rs * wa[i];
                     xb[i] = xb[i] * rs * wb[i];
                 }
             }
-            if (rot > 0) turn<LAYOUT, VEC>(xa, xb, g, lane, D, rot, sl);
-            store_row<E, LAYOUT, VEC>(out + (h0 + r * dh) * set.out_h, lane, D, rot, sl, xa, xb);
+            if (rot > 0) turn<LAYOUT, FORM>(xa, xb, g, lane, D, rot, sl);
+            store_row<E, LAYOUT, FORM>(out + (h0 + r * dh) * set.out_h, lane, D, rot, sl, xa, xb);
         }
     }
 }
@@ -379,11 +386,11 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs p) {
 // of u * xhat in registers, adds its lane groups in LDS in a fixed order and
 // stores one partial row of D sums, which norm_weight_grad_kernel adds in a
 // fixed order: the result does not depend on scheduling.
-template <class E, int LAYOUT, bool VEC>
+template <class E, int LAYOUT, int FORM>
 __global__ __launch_bounds__(kThreads) void norm_back_kernel(const NormBackArgs p) {
     using T = typename E::T;
     __shared__ float red[kThreads * 16];
-    const int lg = VEC ? p.log2_lanes : 6;
+    const int lg = FORM == kVector ? p.log2_lanes : 6;
     const int groups = kThreads >> lg;
     const int lane = threadIdx.x & ((1 << lg) - 1);
     const int group = threadIdx.x >> lg;
@@ -393,10 +400,10 @@ __global__ __launch_bounds__(kThreads) void norm_back_kernel(const NormBackArgs 
     const int blocks = second ? gridDim.x - p.first_groups : p.first_groups;
     const int D = p.dim, rot = p.rot;
     const Slots sl = vector_slots<LAYOUT>(lane, D, rot);
-    float wa[8], wb[8], da[8], db[8];
-    load_weight<E, LAYOUT, VEC>(set.weight, p.weight_fp32, lane, D, rot, sl, wa, wb);
+    float wa[count_of(FORM)], wb[count_of(FORM)], da[count_of(FORM)], db[count_of(FORM)];
+    load_weight<E, LAYOUT, FORM>(set.weight, p.weight_fp32, lane, D, rot, sl, wa, wb);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) da[i] = db[i] = 0.0f;
+    for (int i = 0; i < count_of(FORM); ++i) da[i] = db[i] = 0.0f;
 
     const uint32_t rows = set.rows;
     for (uint32_t row = block * groups + group; row < rows; row += blocks * groups) {
@@ -407,24 +414,24 @@ __global__ __launch_bounds__(kThreads) void norm_back_kernel(const NormBackArgs 
         const T* x = static_cast<const T*>(set.x) + b * set.x_b + t * set.x_s + h * set.x_h;
         const T* gr = static_cast<const T*>(set.g) + b * set.g_b + t * set.g_s + h * set.g_h;
         T* dx = static_cast<T*>(set.dx) + b * set.dx_b + t * set.dx_s + h * set.dx_h;
-        Raw<E, VEC> rx, rg;
-        load_row<E, LAYOUT, VEC>(x, lane, D, rot, sl, rx);
-        load_row<E, LAYOUT, VEC>(gr, lane, D, rot, sl, rg);
-        Angles g;
+        Raw<E, FORM> rx, rg;
+        load_row<E, LAYOUT, FORM>(x, lane, D, rot, sl, rx);
+        load_row<E, LAYOUT, FORM>(gr, lane, D, rot, sl, rg);
+        Angles<FORM> g;
         const int64_t pos = load_index(p.positions, bt, p.positions_wide);
-        load_angles<LAYOUT, VEC>(p.table, pos, p.max_pos, lane, D, rot, sl, -1.0f, g);
-        float xa[8], xb[8], ga[8], gb[8];
-        widen_row<E, VEC>(rx, xa, xb);
-        widen_row<E, VEC>(rg, ga, gb);
+        load_angles<LAYOUT, FORM>(p.table, pos, p.max_pos, lane, D, rot, sl, -1.0f, g);
+        float xa[count_of(FORM)], xb[count_of(FORM)], ga[count_of(FORM)], gb[count_of(FORM)];
+        widen_row<E, FORM>(rx, xa, xb);
+        widen_row<E, FORM>(rg, ga, gb);
         float ss = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+        for (int i = 0; i < count_of(FORM); ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
         ss = group_sum(ss, 1 << lg);
         const float rs = rsqrtf(ss * p.inv_dim + p.eps);
-        turn<LAYOUT, VEC>(ga, gb, g, lane, D, rot, sl);
+        turn<LAYOUT, FORM>(ga, gb, g, lane, D, rot, sl);
         float inner = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < count_of(FORM); ++i) {
             xa[i] *= rs;
             xb[i] *= rs;
             da[i] = fmaf(ga[i], xa[i], da[i]);
@@ -435,27 +442,28 @@ __global__ __launch_bounds__(kThreads) void norm_back_kernel(const NormBackArgs 
         }
         inner = group_sum(inner, 1 << lg) * p.inv_dim;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < count_of(FORM); ++i) {
             xa[i] = rs * (ga[i] - xa[i] * inner);
             xb[i] = rs * (gb[i] - xb[i] * inner);
         }
-        store_row<E, LAYOUT, VEC>(dx, lane, D, rot, sl, xa, xb);
+        store_row<E, LAYOUT, FORM>(dx, lane, D, rot, sl, xa, xb);
     }
     float* mine = red + group * D;  // groups * D <= kThreads * 16
-    if constexpr (VEC) {
+    if constexpr (FORM == kVector) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (sl.a >= 0) mine[sl.a + i] = da[i];
             if (sl.b >= 0) mine[sl.b + i] = db[i];
         }
     } else {
-        store_row<HF32, LAYOUT, false>(mine, lane, D, rot, sl, da, db);
+        store_row<HF32, LAYOUT, FORM>(mine, lane, D, rot, sl, da, db);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < D; e += kThreads) {
         float sum = red[e];
         for (int q = 1; q < groups; ++q) sum += red[q * D + e];
-        p.partial[static_cast<int64_t>(blockIdx.x) * D + e] = sum;
+        if (p.direct[0] != nullptr) p.direct[second ? 1 : 0][e] = sum;
+        else p.partial[static_cast<int64_t>(blockIdx.x) * D + e] = sum;
     }
 }
 
@@ -506,32 +514,42 @@ __global__ __launch_bounds__(kThreads) void rope_table_kernel(const double* __re
     }
 }
 
-template <class E, int LAYOUT, bool NORM, bool PAGED, bool VEC, int R>
+template <class E, int LAYOUT, bool NORM, bool PAGED, int FORM, int R>
 int launch_heads_r(HeadsArgs& p, int64_t batch, void* stream) {
     for (auto& s : p.set) s.units = (s.heads + R - 1) / R;
     p.tokens_first = p.set[0].in_s < p.set[0].in_h;
-    const int lg = VEC ? p.log2_lanes : 6;
+    const int lg = FORM == kVector ? p.log2_lanes : 6;
     p.units = static_cast<uint32_t>(p.tokens * (p.set[0].units + p.set[1].units));
     unsigned grid = (p.units + (kThreads >> lg) - 1) / (kThreads >> lg);
     if (grid > kMaxHeadsGrid) grid = kMaxHeadsGrid;  // a launch holds fewer than 2^32 threads
-    hipLaunchKernelGGL((heads_kernel<E, LAYOUT, NORM, PAGED, VEC, R>), dim3(grid, static_cast<unsigned>(batch)),
+    hipLaunchKernelGGL((heads_kernel<E, LAYOUT, NORM, PAGED, FORM, R>), dim3(grid, static_cast<unsigned>(batch)),
                        dim3(kThreads), 0, static_cast<hipStream_t>(stream), p);
     return static_cast<int>(hipGetLastError());
 }
 
+// Several heads a lane group once the groups fill the device all the same
+// (4 workgroups a compute unit), else one.  8192 tokens, heads of 128 in 16
+// bits, R = 1 / 2 / 4 / 8: rotation of 32 heads 26.6 / 24.7 / 25.8 / 29.7 us,
+// norm of 40 heads 47.8 / 38.0 / 34.9 / 36.2, append of 8 heads 14.1 / 14.3 /
+// 12.9 / 12.7.
+template <class E, int LAYOUT, bool NORM, bool PAGED, int FORM>
+int launch_heads_f(HeadsArgs& p, int64_t batch, void* stream) {
+    constexpr int R = NORM || PAGED || FORM == 1 ? 4 : 2;
+    const int lg = FORM == kVector ? p.log2_lanes : 6;
+    const int64_t units = p.tokens * ((p.set[0].heads + R - 1) / R + (p.set[1].heads + R - 1) / R) * batch;
+    if ((units << lg) >= static_cast<int64_t>(device_cu_count()) * 4 * kThreads)
+        return launch_heads_r<E, LAYOUT, NORM, PAGED, FORM, R>(p, batch, stream);
+    return launch_heads_r<E, LAYOUT, NORM, PAGED, FORM, 1>(p, batch, stream);
+}
+
+// Pairs a lane in the element form: one a lane covers heads of 128.
+bool one_pair_a_lane(int dim0, int dim1) { return dim0 <= 2 * kWave && dim1 <= 2 * kWave; }
+
 template <class E, int LAYOUT, bool NORM, bool PAGED>
 int launch_heads_l(HeadsArgs& p, int64_t batch, bool vec, void* stream) {
-    if (!vec) return launch_heads_r<E, LAYOUT, NORM, PAGED, false, 1>(p, batch, stream);
-    // Several heads a lane group once the groups fill the device all the same
-    // (8 workgroups a compute unit), else one.  8192 tokens, heads of 128 in
-    // 16 bits, R = 1 / 2 / 4 / 8: rotation of 32 heads 26.6 / 24.7 / 25.8 / 29.7
-    // us, norm of 40 heads 47.8 / 38.0 / 34.9 / 36.2, append of 8 heads 14.1 /
-    // 14.3 / 12.9 / 12.7.
-    constexpr int R = NORM || PAGED ? 4 : 2;
-    const int64_t units = p.tokens * ((p.set[0].heads + R - 1) / R + (p.set[1].heads + R - 1) / R) * batch;
-    if ((units << p.log2_lanes) >= static_cast<int64_t>(device_cu_count()) * 8 * kThreads)
-        return launch_heads_r<E, LAYOUT, NORM, PAGED, true, R>(p, batch, stream);
-    return launch_heads_r<E, LAYOUT, NORM, PAGED, true, 1>(p, batch, stream);
+    if (vec) return launch_heads_f<E, LAYOUT, NORM, PAGED, kVector>(p, batch, stream);
+    if (one_pair_a_lane(p.set[0].dim, p.set[1].dim)) return launch_heads_f<E, LAYOUT, NORM, PAGED, 1>(p, batch, stream);
+    return launch_heads_r<E, LAYOUT, NORM, PAGED, 8, 1>(p, batch, stream);
 }
 
 template <class E>
@@ -550,15 +568,18 @@ int launch_heads_e(HeadsArgs& p, int64_t batch, HeadsKind kind, int layout, bool
     }
 }
 
+template <class E, int LAYOUT, int FORM>
+int launch_back_f(const NormBackArgs& p, int grid, void* stream) {
+    hipLaunchKernelGGL((norm_back_kernel<E, LAYOUT, FORM>), dim3(grid), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), p);
+    return static_cast<int>(hipGetLastError());
+}
+
 template <class E, int LAYOUT>
 int launch_back_l(const NormBackArgs& p, bool vec, int grid, void* stream) {
-    if (vec)
-        hipLaunchKernelGGL((norm_back_kernel<E, LAYOUT, true>), dim3(grid), dim3(kThreads), 0,
-                           static_cast<hipStream_t>(stream), p);
-    else
-        hipLaunchKernelGGL((norm_back_kernel<E, LAYOUT, false>), dim3(grid), dim3(kThreads), 0,
-                           static_cast<hipStream_t>(stream), p);
-    return static_cast<int>(hipGetLastError());
+    if (vec) return launch_back_f<E, LAYOUT, kVector>(p, grid, stream);
+    if (one_pair_a_lane(p.dim, p.dim)) return launch_back_f<E, LAYOUT, 1>(p, grid, stream);
+    return launch_back_f<E, LAYOUT, 8>(p, grid, stream);
 }
 
 template <class E>
@@ -590,6 +611,15 @@ int launch_norm_back(Dtype t, NormBackArgs& p, int layout, bool vec, float* d0, 
     }
     if (g0 < 1) g0 = 1;
     if (g1 < 1) g1 = 1;
+    // Up to four rows a lane group in one workgroup a set: its sums are the
+    // result, and there is no second launch (3 us of host time and 5 us of
+    // latency against three more rows after each other).
+    const bool direct = n[0] <= 4 && n[1] <= 4;
+    if (direct) {
+        g0 = g1 = 1;
+        p.direct[0] = d0;
+        p.direct[1] = d1;
+    }
     p.first_groups = static_cast<int>(g0);
     const int grid = static_cast<int>(g0 + g1);
     int e;
@@ -598,7 +628,7 @@ int launch_norm_back(Dtype t, NormBackArgs& p, int layout, bool vec, float* d0, 
         case Dtype::fp16: e = launch_back_e<HF16>(p, layout, vec, grid, stream); break;
         default: e = launch_back_e<HB16>(p, layout, vec, grid, stream); break;
     }
-    if (e != 0) return e;
+    if (e != 0 || direct) return e;
     hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((p.dim + kGradCols - 1) / kGradCols, 2),
                        dim3(kGradCols * kGradSplits), 0, static_cast<hipStream_t>(stream), p.partial, p.dim,
                        p.first_groups, grid, d0, d1);

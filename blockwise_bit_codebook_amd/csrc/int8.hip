@@ -91,9 +91,52 @@ __device__ __forceinline__ void row_scale(uint32_t amax_bits, float& scale, floa
     }
 }
 
-// One row a workgroup; the first kKeep pieces of each thread stay in
-// registers between the two steps, longer rows are read a second time (from
-// cache).  In a row that is not finite inv is 0 and inf * 0 must not become
+// One row a wave, four a workgroup, no barrier: rows of up to 4096 values stay
+// in registers between the two steps.
+constexpr int kWavePieces = 8;
+template <class E, bool VEC>
+__global__ __launch_bounds__(kThreads) void quantize_rows_wave_kernel(const typename E::T* __restrict__ X, int64_t rows,
+                                                                      int d, int64_t ldx, int8_t* __restrict__ codes,
+                                                                      int64_t ldc, float* __restrict__ scale) {
+    const int lane = __lane_id();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWavesPerGroup + threadIdx.x / kWave;
+    if (row >= rows) return;
+    const typename E::T* x = X + row * ldx;
+    const int end = (d + 15) / 16 * 16;
+    float v[kWavePieces][8];
+#pragma unroll
+    for (int i = 0; i < kWavePieces; ++i) {
+        const int c = (i * kWave + lane) * 8;
+        if (i * kWave * 8 < d && c < d) {
+            load8<E, VEC>(x, c, d, v[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+        }
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kWavePieces; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int s = 1; s < kWave; s <<= 1) m = max(m, shfl_xor_u32(m, s));
+    float sc, inv;
+    row_scale(m, sc, inv);
+    int8_t* out = codes + row * ldc;
+#pragma unroll
+    for (int i = 0; i < kWavePieces; ++i) {
+        const int c = (i * kWave + lane) * 8;
+        uint2 q = make_uint2(pack_codes(v[i], inv), pack_codes(v[i] + 4, inv));
+        if (m >= 0x7F800000u) q = make_uint2(0u, 0u);
+        if (c < end) *reinterpret_cast<uint2*>(out + c) = q;
+    }
+    if (lane == 0) scale[row] = sc;
+}
+
+// One row a workgroup, where rows are few or long; the first kKeep pieces of
+// each thread stay in registers between the two steps, longer rows are read a
+// second time (from cache).  In a row that is not finite inv is 0 and inf * 0 must not become
 // a code, so such rows store zeros outright.
 constexpr int kKeep = 4;
 template <class E, bool VEC>
@@ -993,18 +1036,29 @@ int launch_tokens_e(const Int8Product& p, const void* X, int64_t ldX, bool vec, 
     return launch_tokens_t<E, 4, 8>(p, X, ldX, vec, stream);
 }
 
+template <class E, bool VEC>
+int launch_rows_v(const typename E::T* x, int64_t rows, int d, int64_t ldx, int8_t* codes, int64_t ldc, float* scale,
+                  void* stream) {
+    // A wave a row once that gives every compute unit a workgroup: 8192 rows
+    // of 4096 in bf16 28.2 us with a workgroup a row, 22.7 with a wave (4.4 TB/s).
+    const int64_t groups = (rows + kWavesPerGroup - 1) / kWavesPerGroup;
+    if (groups >= device_cu_count() && groups < (1 << 24) && d <= kWavePieces * kWave * 8) {
+        hipLaunchKernelGGL((quantize_rows_wave_kernel<E, VEC>), dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0,
+                           static_cast<hipStream_t>(stream), x, rows, d, ldx, codes, ldc, scale);
+    } else {
+        const unsigned grid = static_cast<unsigned>(rows < (1 << 20) ? rows : (1 << 20));
+        hipLaunchKernelGGL((quantize_rows_kernel<E, VEC>), dim3(grid), dim3(kThreads), 0,
+                           static_cast<hipStream_t>(stream), x, rows, d, ldx, codes, ldc, scale);
+    }
+    return static_cast<int>(hipGetLastError());
+}
+
 template <class E>
 int launch_rows_e(const void* X, int64_t rows, int d, int64_t ldx, int8_t* codes, int64_t ldc, float* scale, bool vec,
                   void* stream) {
-    const unsigned grid = static_cast<unsigned>(rows < (1 << 20) ? rows : (1 << 20));
     const auto* x = static_cast<const typename E::T*>(X);
-    if (vec)
-        hipLaunchKernelGGL((quantize_rows_kernel<E, true>), dim3(grid), dim3(kThreads), 0,
-                           static_cast<hipStream_t>(stream), x, rows, d, ldx, codes, ldc, scale);
-    else
-        hipLaunchKernelGGL((quantize_rows_kernel<E, false>), dim3(grid), dim3(kThreads), 0,
-                           static_cast<hipStream_t>(stream), x, rows, d, ldx, codes, ldc, scale);
-    return static_cast<int>(hipGetLastError());
+    return vec ? launch_rows_v<E, true>(x, rows, d, ldx, codes, ldc, scale, stream)
+               : launch_rows_v<E, false>(x, rows, d, ldx, codes, ldc, scale, stream);
 }
 
 }  // namespace

@@ -61,7 +61,8 @@ struct NormBackArgs {
     BackSet set[2];
     const void* positions;
     const float* table;
-    float* partial;  // [(kNormBackGroups + 2) * dim]
+    float* partial;    // [(kNormBackGroups + 2) * dim]
+    float* direct[2];  // set by the launcher: where a lone workgroup's sums are the result
     int64_t max_pos;
     int64_t tokens;
     int dim, rot, log2_lanes;
