@@ -542,7 +542,9 @@ int launch_heads_f(HeadsArgs& p, int64_t batch, void* stream) {
     return launch_heads_r<E, LAYOUT, NORM, PAGED, FORM, 1>(p, batch, stream);
 }
 
-// Pairs a lane in the element form: one a lane covers heads of 128.
+// Pairs a lane in the element form: one a lane covers heads of 128.  Rotation
+// of 40 of 72 elements, 8192 tokens x 32 heads: 176 us with room for 8 pairs a
+// lane, 40 with one.
 bool one_pair_a_lane(int dim0, int dim1) { return dim0 <= 2 * kWave && dim1 <= 2 * kWave; }
 
 template <class E, int LAYOUT, bool NORM, bool PAGED>
@@ -611,10 +613,11 @@ int launch_norm_back(Dtype t, NormBackArgs& p, int layout, bool vec, float* d0, 
     }
     if (g0 < 1) g0 = 1;
     if (g1 < 1) g1 = 1;
-    // Up to four rows a lane group in one workgroup a set: its sums are the
-    // result, and there is no second launch (3 us of host time and 5 us of
-    // latency against three more rows after each other).
-    const bool direct = n[0] <= 4 && n[1] <= 4;
+    // Up to two rows a lane group in one workgroup a set: its sums are the
+    // result, and there is no second launch.  Heads of 128 in 16 bits, one
+    // launch and two: 8 tokens x 8 heads (two rows a lane group) 5.6 and 6.6
+    // us, 16 tokens (four) 7.9 and 6.5.
+    const bool direct = n[0] <= 2 && n[1] <= 2;
     if (direct) {
         g0 = g1 = 1;
         p.direct[0] = d0;

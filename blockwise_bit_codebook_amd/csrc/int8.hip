@@ -314,9 +314,17 @@ __device__ __forceinline__ int operand_channel(int j, int i) {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// 16 bytes a lane from memory to LDS: lane l's go to lds + 16 l.
+// 16 bytes a lane from memory to LDS: lane l's go to lds + 16 l.  Counted with
+// the vector loads, in order: landed<N>() waits until at most the last N are
+// still on their way.
 __device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, void* lds, int lane_offset, int offset) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, lane_offset, offset, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void landed() {
+    static_assert(N < 64, "the counter has six bits");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
 }
 
 __device__ __forceinline__ int key_x(int row) { return row & 7; }
@@ -429,11 +437,13 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_few_rows_kernel(const Int8P
     };
     const int steps = p.K / kDepth;
     uint8_t *const e = even + wave * kStep, *const o = odd + wave * kStep;
-    // A step's operands have left LDS (lgkmcnt(0)) before the loads of the
-    // step after the next go over them.  Past the last step everything but
+    // A step's operands have arrived in LDS (of the loads on their way only
+    // the next step's are newer), and have left it (lgkmcnt(0)) before the
+    // loads of the step after the next go over them.  Past the last step everything but
     // the products is done all the same: branches around loads to LDS make
     // the compiler wait for all of them.
     auto turn_step = [&](int s, uint8_t* at) {
+        landed<2 * (MT + TN)>();
         read(at);
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         fetch(s + 2 * WAVES, at, s + 2 * WAVES < steps);
@@ -488,13 +498,16 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_few_rows_kernel(const Int8P
 // ---------------------------------------------------------------------------
 // The few-rows kernel for a few tokens whose codes every workgroup makes for
 // itself, in LDS, while its first weights are on their way: one launch
-// instead of two (one token x 4096: see the layer's table of measurements),
-// for a reading of the tokens from cache by each workgroup.  A wave takes 512
-// values of a row at a time, at most kItems times.
+// instead of two, for a reading of the tokens from cache by each workgroup.
+// bf16, weights from memory, two launches and one: 1 x 4096 x 4096 9.6 and 6.5
+// us (2.6 TB/s; its 16.8 MB alone would take 3.2 us), 1 x 32000 x 4096 35.1 and
+// 32.4 (4.0 TB/s), 8 x 4096 x 2048 8.4 and 7.4, but 4 x 11008 x 4096 15.9 and
+// 16.3.  A wave takes 512 values of a row at a time, at most kItems times.
 constexpr int kItems = 4;
 constexpr int kTokenBytes = 28 * 1024;  // of codes, rows kTokenPad apart from whole steps
 constexpr int kTokenPad = 16;
 constexpr int kMaxTokens = 8;
+constexpr int64_t kMaxChannels = int64_t(1) << 20;  // a launch
 
 template <class E, int TN, int WAVES, bool VEC>
 __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Product p,
@@ -589,6 +602,7 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Pro
                 acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][j], x[h], acc[j], 0, 0, 0);
     };
     auto turn_step = [&](int s, uint8_t* at) {  // as in the few-rows kernel
+        landed<2 * TN>();
         read(at, s);
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         fetch(s + 2 * WAVES, at, s + 2 * WAVES < steps);
@@ -991,23 +1005,25 @@ template <class E>
 int launch_product_e(const Int8Product& whole, bool aligned, void* stream) {
     using T = typename E::T;
     const int64_t cus = device_cu_count();
-    // Row blocks keep the grids (below 2^32 threads) and the kernels' 32-bit
-    // offsets in range.
+    // Blocks of rows and channels keep the grids (below 2^32 threads) and the
+    // kernels' 32-bit offsets in range.
     constexpr int64_t kRowBlock = int64_t(1) << 15;
-    for (int64_t m = 0; m < whole.M; m += kRowBlock) {
-        Int8Product p = whole;
-        p.M = whole.M - m < kRowBlock ? whole.M - m : kRowBlock;
-        p.x += m * p.ldx;
-        p.xs += m;
-        p.out = static_cast<T*>(p.out) + m * p.ldo;
-        int e;
-        if (!aligned || p.ldx >= (1 << 22) || p.ldw >= (1 << 22)) {
-            e = launch_generic<E>(p, stream);
+    for (int64_t n = 0; n < whole.N; n += kMaxChannels) {
+        for (int64_t m = 0; m < whole.M; m += kRowBlock) {
+            Int8Product p = whole;
+            p.M = whole.M - m < kRowBlock ? whole.M - m : kRowBlock;
+            p.N = static_cast<int>(whole.N - n < kMaxChannels ? whole.N - n : kMaxChannels);
+            p.x += m * p.ldx;
+            p.xs += m;
+            p.w += n * p.ldw;
+            p.ws += n;
+            if (p.bias) p.bias = static_cast<const T*>(p.bias) + n;
+            p.out = static_cast<T*>(p.out) + m * p.ldo + n;
+            const int e = !aligned || p.ldx >= (1 << 22) || p.ldw >= (1 << 22)
+                              ? launch_generic<E>(p, stream)
+                              : launch_form<E>(p, choose_form(p.M, p.N, p.K, cus), stream);
             if (e != 0) return e;
-            continue;
         }
-        e = launch_form<E>(p, choose_form(p.M, p.N, p.K, cus), stream);
-        if (e != 0) return e;
     }
     return 0;
 }
@@ -1026,14 +1042,19 @@ int launch_tokens_t(const Int8Product& p, const void* X, int64_t ldX, bool vec, 
     return static_cast<int>(hipGetLastError());
 }
 
-// Channels a workgroup: 16 while those fill the compute units once, else 48
-// or 64, as many rounds less.
+// Channels a workgroup (one fits a compute unit): 16, 48 or 64, whose rounds
+// over the device take about 1 : 2 : 3, the largest of equals.  One token x
+// 4096 in 16 / 48 / 64: 4096 channels 6.5 / 9.4 / 10.8 us, 6000 10.8 / 10.3 / 11.3,
+// 11008 15.9 / 13.6 / 13.8, 14336 20.3 / 20.7 / 15.9, 32000 39.0 / 33.5 / 32.4; two
+// tokens, 20000 x 2048, 22.3 / 14.7 / 16.4.
 template <class E>
 int launch_tokens_e(const Int8Product& p, const void* X, int64_t ldX, bool vec, void* stream) {
     const int cus = device_cu_count();
-    if (p.N <= 16 * cus) return launch_tokens_t<E, 1, 16>(p, X, ldX, vec, stream);
-    if (p.N <= 48 * cus) return launch_tokens_t<E, 3, 8>(p, X, ldX, vec, stream);
-    return launch_tokens_t<E, 4, 8>(p, X, ldX, vec, stream);
+    auto rounds = [&](int channels) { return (p.N + channels * cus - 1) / (channels * cus); };
+    const int c16 = rounds(16), c48 = 2 * rounds(48), c64 = 3 * rounds(64);
+    if (c64 <= c48 && c64 <= c16) return launch_tokens_t<E, 4, 8>(p, X, ldX, vec, stream);
+    if (c48 <= c16) return launch_tokens_t<E, 3, 8>(p, X, ldX, vec, stream);
+    return launch_tokens_t<E, 1, 16>(p, X, ldX, vec, stream);
 }
 
 template <class E, bool VEC>
@@ -1073,7 +1094,7 @@ int launch_quantize_rows(Dtype t, const void* X, int64_t rows, int d, int64_t ld
 }
 
 bool int8_tokens_fit(int64_t M, int N, int K, int64_t ldw) {
-    if (M > kMaxTokens || ldw >= (1 << 22)) return false;
+    if (M > kMaxTokens || N > kMaxChannels || ldw >= (1 << 22)) return false;
     const int64_t per_row = (K + 511) / 512, steps = (K + kDepth - 1) / kDepth;
     return M * (steps * kDepth + kTokenPad) <= kTokenBytes && M * per_row <= 8 * kItems;
 }
@@ -1086,9 +1107,7 @@ int launch_int8_tokens(Dtype t, const Int8Product& p, const void* X, int64_t ldX
     }
 }
 
-int64_t int8_product_workspace(int64_t, int, int) { return 0; }
-
-int launch_int8_product(Dtype t, const Int8Product& p, bool aligned, void*, void* stream) {
+int launch_int8_product(Dtype t, const Int8Product& p, bool aligned, void* stream) {
     switch (t) {
         case Dtype::fp32: return launch_product_e<QF32>(p, aligned, stream);
         case Dtype::fp16: return launch_product_e<QF16>(p, aligned, stream);
