@@ -64,6 +64,7 @@ def _layer_signatures():
     view = [_p, _i64, _i64, _i64]
     turn = [_p, _i32, _p, _i32, _i64, _i32]  # positions, their bytes, table, rot, max_pos, layout
     sig = [
+        ("linear_int8_workspace_bytes", [_i64, _i32, _i32]),
         ("linear_int8_dynamic_workspace_bytes", [_i64, _i32, _i32]),
         ("linear_int8_dynamic_fused", [_i64, _i32, _i32, _i64]),
         ("qk_norm_rope_backward_workspace_bytes", [_i32]),
@@ -73,7 +74,7 @@ def _layer_signatures():
     for t in DTYPES:
         sig += [
             (f"quantize_rows_int8_{t}", [_p, _i64, _i32, _i64, _p, _i64, _p, _p]),
-            (f"linear_int8_{t}", [_p, _p, _i64, _i32, _i64, _p, _p, _i32, _i64, _p, _p, _i64, _p]),
+            (f"linear_int8_{t}", [_p, _p, _i64, _i32, _i64, _p, _p, _i32, _i64, _p, _p, _i64, _p, _i64, _p]),
             (f"linear_int8_dynamic_{t}", [_p, _i64, _i32, _i64, _p, _p, _i32, _i64, _p, _p, _i64, _p, _i64, _p]),
             (f"rope_{t}", view * 2 + [_i64, _i64, _i32, _i32] + turn + [_i32, _p]),
             (f"qk_norm_rope_{t}", view * 4 + [_i64, _i64, _i32, _i32, _i32, _p, _p, _i32, _f32] + turn + [_p]),
@@ -101,6 +102,7 @@ def load(path=LIB_PATH):
                       "kbit_nested_noalloc_scratch_bytes": ct.c_int64,
                       "kbit_quantize_nested_workspace_bytes": ct.c_int64,
                       "kbit_act_tables_bytes": ct.c_int64,
+                      "linear_int8_workspace_bytes": ct.c_int64,
                       "linear_int8_dynamic_workspace_bytes": ct.c_int64,
                       "qk_norm_rope_backward_workspace_bytes": ct.c_int64}.get(name, ct.c_int)
     return lib

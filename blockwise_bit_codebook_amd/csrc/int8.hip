@@ -658,9 +658,10 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Pro
 // of 256 rows, 435 -> 408 us in 128, but 75.0 -> 80.3 us (1000 x 11008) in 64.
 // m, n: the wave's first row and channel.
 template <class E, int TM, int kRegion, bool NT>
-__device__ __forceinline__ void store_tile(const Int8Product& p, uint8_t* region, int lane, int64_t m, int n,
-                                           const i32x4 (&acc)[TM][4], bool packed) {
+__device__ __forceinline__ void store_tile(const Int8Product& p, typename E::T* out, uint8_t* region, int lane,
+                                           int64_t m, int n, const i32x4 (&acc)[TM][4], bool packed) {
     using T = typename E::T;
+    constexpr bool kSums = std::is_same<T, int>::value;  // the sums themselves
     constexpr int kSize = sizeof(T), kRow = 64 * kSize;
     constexpr int kFit = kRegion / (16 * kRow) < TM ? kRegion / (16 * kRow) : TM;
     constexpr int kPass = TM % kFit == 0 ? kFit : 1;  // blocks of 16 rows a pass
@@ -669,23 +670,25 @@ __device__ __forceinline__ void store_tile(const Int8Product& p, uint8_t* region
     float sc[16], bias[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        sc[e] = p.ws[n + 16 * q + e];
+        sc[e] = kSums ? 1.0f : p.ws[n + 16 * q + e];
         bias[e] = 0.0f;
     }
-    if (p.bias) {
+    if constexpr (!kSums) {
+        if (p.bias) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) bias[e] = E::one(static_cast<const T*>(p.bias)[n + 16 * q + e]);
+            for (int e = 0; e < 16; ++e) bias[e] = E::one(static_cast<const T*>(p.bias)[n + 16 * q + e]);
+        }
     }
-    T* out = static_cast<T*>(p.out) + m * p.ldo + n;
+    out += m * p.ldo + n;
 #pragma unroll
     for (int i0 = 0; i0 < TM; i0 += kPass) {
 #pragma unroll
         for (int i = 0; i < kPass; ++i) {
             const int row = 16 * i + l16;
-            const float xs = p.xs[m + 16 * i0 + row];
+            const float xs = kSums ? 1.0f : p.xs[m + 16 * i0 + row];
             float v[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 16 && !kSums; ++e) {
                 v[e] = static_cast<float>(acc[i0 + i][e >> 2][e & 3]) * xs * sc[e];
                 if (p.bias) v[e] = v[e] + bias[e];
             }
@@ -694,7 +697,8 @@ __device__ __forceinline__ void store_tile(const Int8Product& p, uint8_t* region
                 u32x4 d;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    if constexpr (kSize == 4) d[r] = __float_as_uint(v[4 * c + r]);
+                    if constexpr (kSums) d[r] = acc[i0 + i][c][r];
+                    else if constexpr (kSize == 4) d[r] = __float_as_uint(v[4 * c + r]);
                     else d[r] = E::pack(v[8 * c + 2 * r], v[8 * c + 2 * r + 1]);
                 }
                 *reinterpret_cast<u32x4*>(region + row * kRow + 16 * ((q * kSize + c) ^ (row & 7))) = d;
@@ -719,9 +723,19 @@ __device__ __forceinline__ void store_tile(const Int8Product& p, uint8_t* region
     }
 }
 
+// With E = QSums the depth is split as well: workgroups (x, y) take the codes
+// from y part_depth on, at most part_depth (whole pairs of steps), and store
+// their sums as they are, one matrix after the other.
+struct QSums {
+    using T = int;
+    static __device__ T narrow(float);  // unused
+    static __device__ float one(T);
+};
+
 template <class E, int WM, int WN, int TM>
 __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Product p, int m_tiles, int n_tiles,
-                                                                  bool packed) {
+                                                                  int part_depth, bool packed) {
+    constexpr bool kSplit = std::is_same<E, QSums>::value;
     constexpr int TN = 4, kT = WM * WN * kWave;
     constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
     constexpr int kXLoads = BM * 8 / kT, kWLoads = BN * 8 / kT;
@@ -748,8 +762,10 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
     const int64_t m0 = min<int64_t>(static_cast<int64_t>(group * kGroupM + in % gm) * BM, p.M - BM);
     const int n0 = min(in / gm * BN, p.N - BN);
 
-    const int8_t* xb = p.x + m0 * p.ldx;
-    const int8_t* wb = p.w + static_cast<int64_t>(n0) * p.ldw;
+    const int first = kSplit ? static_cast<int>(blockIdx.y) * part_depth : 0;
+    const int K = kSplit ? min(p.K - first, part_depth) : p.K;
+    const int8_t* xb = p.x + m0 * p.ldx + first;
+    const int8_t* wb = p.w + static_cast<int64_t>(n0) * p.ldw + first;
     // A round of loads covers kRound rows; the keys repeat from round to
     // round, but for the weights' where a round is shorter than their period.
     constexpr int kRound = kT / 8;
@@ -828,9 +844,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
     // The pipeline takes pairs of steps.  What the depth has beyond them comes
     // first (the sums are exact in any order), piece by piece through
     // registers, zeros past K.
-    const int steps = p.K / (2 * kDepth) * 2;
+    const int steps = K / (2 * kDepth) * 2;
 #pragma clang loop unroll(disable)
-    for (int k = steps * kDepth; k < p.K; k += kDepth) {
+    for (int k = steps * kDepth; k < K; k += kDepth) {
 #pragma clang loop unroll(disable)
         for (int i = 0; i < kXLoads + kWLoads; ++i) {
             const bool w = i >= kXLoads;
@@ -838,7 +854,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
             const int key = w ? key_w<TN>(row) : key_x(row);
             const int8_t* from = w ? wb + static_cast<int64_t>(row) * ldw : xb + static_cast<int64_t>(row) * ldx;
             uint8_t* to = (w ? w_even : x_even) + row * kDepth + piece0 * 16;
-            *reinterpret_cast<u32x4*>(to) = load_codes<true>(from, k + 16 * (piece0 ^ key), p.K);
+            *reinterpret_cast<u32x4*>(to) = load_codes<true>(from, k + 16 * (piece0 ^ key), K);
         }
         __syncthreads();
 #pragma unroll
@@ -877,7 +893,24 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
                       : wave < 2 * kInX ? x_odd + (wave - kInX) * kPart
                       : wave < 2 * kInX + kInW ? w_even + (wave - 2 * kInX) * kPart
                                                : w_odd + (wave - 2 * kInX - kInW) * kPart;
-    store_tile<E, TM, kPart, (BM >= 128)>(p, region, tid & 63, m0 + wm, n0 + wn, acc, packed && (n0 * sizeof(typename E::T)) % 16 == 0);
+    typename E::T* out = static_cast<typename E::T*>(p.out);
+    if constexpr (kSplit) out += blockIdx.y * p.M * p.ldo;
+    store_tile<E, TM, kPart, (BM >= 128 && !kSplit)>(p, out, region, tid & 63, m0 + wm, n0 + wn, acc,
+                                                     packed && (n0 * sizeof(typename E::T)) % 16 == 0);
+}
+
+// Adds the parts' sums and applies the scales: four channels a thread.
+template <class E>
+__global__ __launch_bounds__(kThreads) void int8_add_parts_kernel(const Int8Product p, const int* __restrict__ sums,
+                                                                  int64_t ld, int parts, bool packed) {
+    const uint32_t pieces = static_cast<uint32_t>(p.N + 3) / 4, at = blockIdx.x * kThreads + threadIdx.x;
+    const uint32_t m = at / pieces;
+    if (m >= p.M) return;
+    const int n = static_cast<int>(at - m * pieces) * 4;
+    const int* s = sums + m * ld + n;
+    i32x4 acc = *reinterpret_cast<const i32x4*>(s);
+    for (int i = 1; i < parts; ++i) acc += *reinterpret_cast<const i32x4*>(s + i * (p.M * ld));
+    store_out4<E>(p, m, n, acc, p.xs[m], packed);
 }
 
 template <class E, int MT, int TN, int WAVES>
@@ -895,7 +928,39 @@ int launch_tile(const Int8Product& p, void* stream) {
     const int m_tiles = static_cast<int>((p.M + BM - 1) / BM), n_tiles = (p.N + BN - 1) / BN;
     const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
     hipLaunchKernelGGL((int8_tile_kernel<E, WM, WN, TM>), dim3(grid), dim3(WM * WN * kWave), 0,
-                       static_cast<hipStream_t>(stream), p, m_tiles, n_tiles, out_aligned(p, sizeof(typename E::T), 16));
+                       static_cast<hipStream_t>(stream), p, m_tiles, n_tiles, 0, out_aligned(p, sizeof(typename E::T), 16));
+    return static_cast<int>(hipGetLastError());
+}
+
+constexpr int kSplitTile = 128;
+
+// Sums of one part: rows of whole 16-byte pieces.
+int64_t sums_ld(int N) { return (static_cast<int64_t>(N) + 3) / 4 * 4; }
+
+// Depth of a part: whole pairs of steps.
+int split_depth(int K, int parts) {
+    const int pairs = (K + 2 * kDepth - 1) / (2 * kDepth);
+    return (pairs + parts - 1) / parts * 2 * kDepth;
+}
+
+// Tiles of 128 x 128 with the depth in parts (as many as split_depth leaves).
+template <class E>
+int launch_split(const Int8Product& p, int parts, void* workspace, void* stream) {
+    const int m_tiles = static_cast<int>((p.M + kSplitTile - 1) / kSplitTile);
+    const int n_tiles = (p.N + kSplitTile - 1) / kSplitTile;
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
+    const int part_depth = split_depth(p.K, parts);
+    Int8Product s = p;
+    s.out = workspace;
+    s.ldo = sums_ld(p.N);
+    hipLaunchKernelGGL((int8_tile_kernel<QSums, 2, 2, 4>), dim3(grid, parts), dim3(4 * kWave), 0,
+                       static_cast<hipStream_t>(stream), s, m_tiles, n_tiles, part_depth, true);
+    const int e = static_cast<int>(hipGetLastError());
+    if (e != 0) return e;
+    const uint32_t pieces = static_cast<uint32_t>(p.M) * (static_cast<uint32_t>(p.N + 3) / 4);
+    hipLaunchKernelGGL((int8_add_parts_kernel<E>), dim3((pieces + kThreads - 1) / kThreads), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), p, static_cast<const int*>(workspace), s.ldo, parts,
+                       out_aligned(p, sizeof(typename E::T), 4 * sizeof(typename E::T)));
     return static_cast<int>(hipGetLastError());
 }
 
@@ -930,15 +995,28 @@ constexpr Int8Tile kTiles[] = {{32, 128, 0.84, 0.497, 0.253, 1.08, 2.32, 1.29, 0
                                {128, 128, 0.0, 0.799, 0.544, 2.70, 3.31, 0.11, 0.742},
                                {256, 256, 0.0, 1.189, 1.386, 7.47, 2.93, 0.83, 1.0}};
 
+// Parts of the depth, in 128 x 128: where the tiles alone leave compute units
+// idle or half a round empty and the depth is long.  us: the second launch, and
+// 10 MB of the parts' sums.  Measured on 70 shapes with 32, 64, 128 and 256
+// rows: 128 alone gives what all of them give within 1%.  Without and with parts
+// (operands from memory): 512 x 4096 x 11008 54.2 and 45.1 us in 4, 1024 x 2048 x
+// 8192 51.5 and 34.1 in 4, 562 x 2432 x 11776 51.5 and 35.2 in 4, but 256 x 4096 x
+// 4096 15.3 and 20.0, 1024 x 1024 x 4096 13.3 and 18.1.  At most as many workgroups
+// as are resident at once, two a compute unit: 4778 x 857 x 13738 would take 126 us
+// without and 146 in 2 parts (532 workgroups).
+constexpr int kParts[] = {2, 3, 4, 8};
+constexpr double kPartsLaunch = 4.5, kPartsSums = 1.5;
+
 struct Int8Choice {
     Int8Few few;  // or
     int bm;       // tiles of bm rows, where not 0
+    int parts;    // of the depth; 1: no split
 };
 
 // Workgroups a compute unit: a part of a round is cheaper than a whole one
 // where several workgroups fit a compute unit (whole < 1).
-double rounds_of(int64_t M, int64_t N, int bm, int bn, int64_t cus, double whole) {
-    const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
+double rounds_of(int64_t tiles, int64_t cus, double whole) {
     const double r = whole * static_cast<double>((tiles + cus - 1) / cus) + (1.0 - whole) * tiles / cus;
     return r < 1.0 ? 1.0 : r;
 }
@@ -949,24 +1027,38 @@ Int8Choice choose_form(int64_t M, int N, int K, int64_t cus) {
     const double operands = 1e-7 * (static_cast<double>(M) + N) * K;
     for (const Int8Few& f : kFew) {
         const double us = 1.34 + 0.68 * operands +
-                          rounds_of(M, N, 16 * f.mt, 16 * f.tn, cus, 1.0) *
+                          rounds_of(tiles_of(M, N, 16 * f.mt, 16 * f.tn), cus, 1.0) *
                               (1.783 + 0.204 * f.mt * f.tn + 1.297e-5 * 16.0 * (f.mt + f.tn) * K +
                                (K % kDepth ? 0.286 * (f.mt + f.tn) : 0.0));
         if (us < least) {
             least = us;
-            best = Int8Choice{f, 0};
+            best = Int8Choice{f, 0, 1};
         }
     }
     const int rest = K % (2 * kDepth);
     const double steps = K / (2 * kDepth) * 2 + (rest > 0 ? 1 : 0) + (rest > kDepth ? 1 : 0);
     for (const Int8Tile& t : kTiles) {
         if (M < t.bm || N < t.bn) continue;
-        const double r = rounds_of(M, N, t.bm, t.bn, cus, t.whole);
+        const int64_t tiles = tiles_of(M, N, t.bm, t.bn);
+        const double r = rounds_of(tiles, cus, t.whole);
         const double us = t.base + (t.step * r > t.least ? t.step * r : t.least) * steps + t.round * r +
                           (rest ? t.tail : 0.0) + t.operands * operands;
         if (us < least) {
             least = us;
-            best = Int8Choice{{}, t.bm};
+            best = Int8Choice{{}, t.bm, 1};
+        }
+        if (t.bm != kSplitTile) continue;
+        for (const int n : kParts) {
+            const int depth = split_depth(K, n), parts = (K + depth - 1) / depth;
+            if (parts < 2 || tiles * parts > 2 * cus) continue;
+            const double rp = rounds_of(tiles * parts, cus, t.whole);
+            const double split = t.base + (t.step * rp > t.least ? t.step * rp : t.least) * (depth / kDepth) +
+                                 t.round * rp + t.operands * operands + kPartsLaunch +
+                                 kPartsSums * 4e-7 * static_cast<double>(parts) * M * N;
+            if (split < 0.95 * least) {  // it takes memory
+                least = split;
+                best = Int8Choice{{}, t.bm, parts};
+            }
         }
     }
     return best;
@@ -991,7 +1083,8 @@ int launch_few_tile(const Int8Product& p, Int8Few f, void* stream) {
 }
 
 template <class E>
-int launch_form(const Int8Product& p, const Int8Choice& c, void* stream) {
+int launch_form(const Int8Product& p, const Int8Choice& c, void* workspace, void* stream) {
+    if (c.parts > 1) return launch_split<E>(p, c.parts, workspace, stream);
     switch (c.bm) {
         case 0: return launch_few_tile<E>(p, c.few, stream);
         case 32: return launch_tile<E, 2, 2, 1>(p, stream);
@@ -1001,13 +1094,14 @@ int launch_form(const Int8Product& p, const Int8Choice& c, void* stream) {
     }
 }
 
+// Blocks of rows and channels keep the grids (below 2^32 threads) and the
+// kernels' 32-bit offsets in range.
+constexpr int64_t kRowBlock = int64_t(1) << 15;
+
 template <class E>
-int launch_product_e(const Int8Product& whole, bool aligned, void* stream) {
+int launch_product_e(const Int8Product& whole, bool aligned, void* workspace, void* stream) {
     using T = typename E::T;
     const int64_t cus = device_cu_count();
-    // Blocks of rows and channels keep the grids (below 2^32 threads) and the
-    // kernels' 32-bit offsets in range.
-    constexpr int64_t kRowBlock = int64_t(1) << 15;
     for (int64_t n = 0; n < whole.N; n += kMaxChannels) {
         for (int64_t m = 0; m < whole.M; m += kRowBlock) {
             Int8Product p = whole;
@@ -1021,7 +1115,7 @@ int launch_product_e(const Int8Product& whole, bool aligned, void* stream) {
             p.out = static_cast<T*>(p.out) + m * p.ldo + n;
             const int e = !aligned || p.ldx >= (1 << 22) || p.ldw >= (1 << 22)
                               ? launch_generic<E>(p, stream)
-                              : launch_form<E>(p, choose_form(p.M, p.N, p.K, cus), stream);
+                              : launch_form<E>(p, choose_form(p.M, p.N, p.K, cus), workspace, stream);
             if (e != 0) return e;
         }
     }
@@ -1107,11 +1201,25 @@ int launch_int8_tokens(Dtype t, const Int8Product& p, const void* X, int64_t ldX
     }
 }
 
-int launch_int8_product(Dtype t, const Int8Product& p, bool aligned, void* stream) {
+int64_t int8_product_workspace(int64_t M, int N, int K) {
+    const int64_t cus = device_cu_count();
+    int64_t most = 0;
+    // the blocks' sizes: whole ones and what is left
+    for (const int64_t m : {M < kRowBlock ? M : kRowBlock, M % kRowBlock})
+        for (const int64_t n : {N < kMaxChannels ? N : kMaxChannels, N % kMaxChannels}) {
+            if (m == 0 || n == 0) continue;
+            const Int8Choice c = choose_form(m, static_cast<int>(n), K, cus);
+            const int64_t need = c.parts > 1 ? c.parts * m * sums_ld(static_cast<int>(n)) * 4 : 0;
+            if (need > most) most = need;
+        }
+    return most;
+}
+
+int launch_int8_product(Dtype t, const Int8Product& p, bool aligned, void* workspace, void* stream) {
     switch (t) {
-        case Dtype::fp32: return launch_product_e<QF32>(p, aligned, stream);
-        case Dtype::fp16: return launch_product_e<QF16>(p, aligned, stream);
-        default: return launch_product_e<QB16>(p, aligned, stream);
+        case Dtype::fp32: return launch_product_e<QF32>(p, aligned, workspace, stream);
+        case Dtype::fp16: return launch_product_e<QF16>(p, aligned, workspace, stream);
+        default: return launch_product_e<QB16>(p, aligned, workspace, stream);
     }
 }
 

@@ -57,26 +57,29 @@ bool product_aligned(const Int8Product& p) {
     return aligned(p.x, 16) && aligned(p.w, 16) && p.ldx % 16 == 0 && p.ldw % 16 == 0;
 }
 
-int do_linear_int8(Dtype t, const Int8Product& p, void* stream) {
+int do_linear_int8(Dtype t, const Int8Product& p, void* workspace, int64_t workspace_bytes, void* stream) {
     const int c = check_product(t, p);
     if (c != 1) return c;
     if (!p.x || !p.xs) return KBIT_EINVAL;
-    if (!aligned(p.xs, 4)) return KBIT_EALIGN;
+    const int64_t need = int8_product_workspace(p.M, p.N, p.K);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return KBIT_EINVAL;
+    if (!aligned(p.xs, 4) || !aligned(workspace, 16)) return KBIT_EALIGN;
     if (!device_usable()) return KBIT_EDEVICE;
-    return map_launch(launch_int8_product(t, p, product_aligned(p), stream));
+    return map_launch(launch_int8_product(t, p, product_aligned(p), workspace, stream));
 }
 
-// Workspace of the dynamic form: the codes and their scales.
+// Workspace of the dynamic form: the codes, their scales, the product's own.
 // Its rows of codes are whole cache lines, so that no step of 128 codes lies
 // across two.
 int64_t dynamic_ld(int32_t K) { return round_up(K, 128); }
 struct DynamicParts {
-    int64_t scale, total;
+    int64_t scale, product, total;
 };
-DynamicParts dynamic_parts(int64_t M, int32_t K) {
+DynamicParts dynamic_parts(int64_t M, int32_t N, int32_t K) {
     DynamicParts w;
     w.scale = M * dynamic_ld(K);
-    w.total = w.scale + round_up(4 * M, 16);
+    w.product = w.scale + round_up(4 * M, 16);
+    w.total = w.product + int8_product_workspace(M, N, K);
     return w;
 }
 
@@ -88,7 +91,7 @@ int do_linear_int8_dynamic(Dtype t, const void* X, int64_t ldX, Int8Product p, v
     if (!X || !rows_shape_ok(p.M, p.K, ldX)) return KBIT_EINVAL;
     if (!aligned(X, elem_size(t)) || !aligned(workspace, 16)) return KBIT_EALIGN;
     const bool one_kernel = aligned(p.w, 16) && linear_int8_dynamic_fused(p.M, p.N, p.K, p.ldw);
-    const DynamicParts w = dynamic_parts(p.M, p.K);
+    const DynamicParts w = dynamic_parts(p.M, p.N, p.K);
     if (!one_kernel && (workspace_bytes < w.total || !workspace)) return KBIT_EINVAL;
     if (!device_usable()) return KBIT_EDEVICE;
     const bool vec = aligned(X, 16) && (p.M == 1 || ldX * elem_size(t) % 16 == 0);
@@ -99,7 +102,7 @@ int do_linear_int8_dynamic(Dtype t, const void* X, int64_t ldX, Int8Product p, v
     if (q != 0) return KBIT_ELAUNCH;
     p.x = codes;
     p.xs = scale;
-    return map_launch(launch_int8_product(t, p, product_aligned(p), stream));
+    return map_launch(launch_int8_product(t, p, product_aligned(p), codes + w.product, stream));
 }
 
 // ---------------------------------------------------------------------------
@@ -313,9 +316,14 @@ using kbit::View;
 
 extern "C" {
 
+int64_t linear_int8_workspace_bytes(int64_t M, int32_t N, int32_t K) {
+    if (M < 0 || M > kbit::kMaxRows || N < 1 || K < 1 || K > kbit::kMaxInt8Depth) return -1;
+    return kbit::int8_product_workspace(M, N, K);
+}
+
 int64_t linear_int8_dynamic_workspace_bytes(int64_t M, int32_t N, int32_t K) {
     if (M < 0 || M > kbit::kMaxRows || N < 1 || K < 1 || K > kbit::kMaxInt8Depth) return -1;
-    return kbit::dynamic_parts(M, K).total;
+    return kbit::dynamic_parts(M, N, K).total;
 }
 
 int linear_int8_dynamic_fused(int64_t M, int32_t N, int32_t K, int64_t ldw) {
@@ -371,10 +379,10 @@ int rope_table(const double* freq, int32_t rot, int64_t max_pos, double amplitud
     }                                                                                                                 \
     int linear_int8_##TNAME(const int8_t* codes, const float* scale, int64_t M, int32_t K, int64_t ldx,               \
                             const int8_t* w_codes, const float* w_scale, int32_t N, int64_t ldw, const CTYPE* bias,   \
-                            CTYPE* out, int64_t ldo, void* stream) {                                                  \
+                            CTYPE* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {        \
         return kbit::do_linear_int8(Dtype::TNAME,                                                                     \
                                     Int8Product{codes, scale, w_codes, w_scale, bias, out, M, ldx, ldw, ldo, N, K},   \
-                                    stream);                                                                          \
+                                    workspace, workspace_bytes, stream);                                              \
     }                                                                                                                 \
     int linear_int8_dynamic_##TNAME(const CTYPE* X, int64_t M, int32_t K, int64_t ldx, const int8_t* w_codes,         \
                                     const float* w_scale, int32_t N, int64_t ldw, const CTYPE* bias, CTYPE* out,      \

@@ -275,7 +275,7 @@ Weight weight(const Tensor& x, PyObject* codes, PyObject* scale, PyObject* bias,
     return w;
 }
 
-PyObject* linear(PyObject* const* a) {  // codes, scale, w_codes, w_scale, bias, dtype, out
+PyObject* linear(PyObject* const* a) {  // codes, scale, w_codes, w_scale, bias, dtype, out, workspace
     const Tensor& x = tensor(a[0], "codes");
     const int64_t ldx = rows_of(x, "codes", x.scalar_type() == at::kChar, "int8"), M = x.size(0);
     if (!THPDtype_Check(a[5])) type_error("dtype must be a torch.dtype");
@@ -283,9 +283,10 @@ PyObject* linear(PyObject* const* a) {  // codes, scale, w_codes, w_scale, bias,
     if (!is_float(type)) type_error(cat("unsupported element dtype ", type));
     const Weight w = weight(x, a[2], a[3], a[4], a[6], type, "codes");
     const float* scale = static_cast<const float*>(vector(a[1], "scale", at::kFloat, M, x));
+    const Space ws = workspace(linear_int8_workspace_bytes(M, w.N, w.K), a[7], "linear_int8", x);
     KBIT_BY_TYPE(type, linear_int8, run("linear_int8", x, [&](void* stream) {
         return fn(static_cast<const int8_t*>(x.data_ptr()), scale, M, w.K, ldx, w.codes, w.scale, w.N, w.ldw,
-                  static_cast<const T*>(w.bias), static_cast<T*>(w.out.data_ptr()), w.ldo, stream);
+                  static_cast<const T*>(w.bias), static_cast<T*>(w.out.data_ptr()), w.ldo, ws.p, ws.bytes, stream);
     }))
     return wrap(w.out);
 }
@@ -535,7 +536,7 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {
     method<quantize_rows, 3>("quantize_rows_int8"),
-    method<linear, 7>("linear_int8"),
+    method<linear, 8>("linear_int8"),
     method<linear_dynamic, 6>("linear_int8_dynamic"),
     method<rope, 6>("rope"),
     method<norm_rope, 10>("qk_norm_rope"),

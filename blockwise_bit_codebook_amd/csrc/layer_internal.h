@@ -90,8 +90,10 @@ struct Int8Product {
     int N, K;
 };
 
-// aligned: both operands' rows start at multiples of 16 bytes.
-int launch_int8_product(Dtype t, const Int8Product& p, bool aligned, void* stream);
+// aligned: both operands' rows start at multiples of 16 bytes.  workspace: of
+// int8_product_workspace bytes on the current device, 16-byte aligned.
+int launch_int8_product(Dtype t, const Int8Product& p, bool aligned, void* workspace, void* stream);
+int64_t int8_product_workspace(int64_t M, int N, int K);
 
 // A few tokens quantized inside the product's kernel (the weights' rows start
 // at multiples of 16 bytes): whether they fit, and the launch (p.x and p.xs

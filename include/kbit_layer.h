@@ -42,15 +42,21 @@ extern "C" {
  * 131071, codes any int8 value).  bias: N values of T, or null.  ldx, ldw,
  * ldo: distance of rows.  Any alignment and any K >= 1 give the same values;
  * rows of codes that all start at multiples of 16 bytes take the fast path.
- * M = 0 is a no-op. */
+ * workspace: at least linear_int8_workspace_bytes(M, N, K) bytes, 16-byte
+ * aligned (may be null where that is 0): where rows and channels are too few
+ * to fill the device and the depth is long, the parts' sums.  M = 0 is a
+ * no-op. */
 #define KBIT_DECLARE_LINEAR_INT8(T, CTYPE)                                                                     \
     int linear_int8_##T(const int8_t* codes, const float* scale, int64_t M, int32_t K, int64_t ldx,              \
                         const int8_t* w_codes, const float* w_scale, int32_t N, int64_t ldw, const CTYPE* bias,  \
-                        CTYPE* out, int64_t ldo, void* stream);
+                        CTYPE* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace on the current device (-1 for arguments out of range). */
+int64_t linear_int8_workspace_bytes(int64_t M, int32_t N, int32_t K);
 
 /* quantize_rows_int8 of X, then linear_int8: the same values as the two
- * calls.  workspace: linear_int8_dynamic_workspace_bytes(M, N, K) bytes (-1
- * for arguments out of range), 16-byte aligned.  A few tokens are quantized inside the product's kernel:
+ * calls.  workspace: linear_int8_dynamic_workspace_bytes(M, N, K) bytes,
+ * 16-byte aligned.  A few tokens are quantized inside the product's kernel:
  * where linear_int8_dynamic_fused(M, N, K, ldw) is 1 and w_codes is 16-byte
  * aligned no workspace is needed and it may be null. */
 #define KBIT_DECLARE_LINEAR_INT8_DYNAMIC(T, CTYPE)                                                             \

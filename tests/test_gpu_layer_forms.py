@@ -37,6 +37,31 @@ def test_product_forms(i, M, N, K):
 
 
 @pytest.mark.parametrize("t", DT)
+@pytest.mark.parametrize("M,N,K", [(202, 4157, 2276), (128, 2802, 8002), (600, 2100, 3840), (640, 2050, 3300)])
+def test_product_with_the_depth_in_parts(t, M, N, K):
+    case(f"linear int8 parts {t} M={M} N={N} K={K}")
+    need = kb.lib().linear_int8_workspace_bytes(M, N, K)
+    assert need > 0 or torch().cuda.get_device_properties(0).multi_processor_count != 256
+    got, want = product_case(M, N, K, t, bias=N % 2 == 0)
+    assert_bits_equal(bits(got), want, f"product {M} {N} {K}")
+    rng = np.random.default_rng(N)
+    a, w = (rng.integers(-128, 128, s).astype(np.int8) for s in ((M, K), (N, K)))
+    sa, sw = (rng.uniform(1e-3, 1e-2, n).astype(np.float32) for n in (M, N))
+    args = codes_dev(a), to_dev(sa), codes_dev(w), to_dev(sw)
+    out = torch().full((M, N + 3), 3.0, dtype=tdt(t), device=dev())
+    ws = torch().full((max(need, 1),), 171, dtype=torch().uint8, device=dev())
+    kb.linear_int8(*args, dtype=tdt(t), out=out[:, 1:N + 1], workspace=ws)
+    assert_bits_equal(bits(out[:, 1:N + 1].contiguous()), layer.round_to(layer.product(a, sa, w, sw), t), "out")
+    assert (out[:, 0] == 3.0).all() and (out[:, N + 1:] == 3.0).all()
+    if need:
+        with pytest.raises(ValueError, match="workspace"):
+            kb.linear_int8(*args, dtype=tdt(t), workspace=ws[:-1])
+    b, x = make(rng, (M, K), t)
+    got = kb.linear_int8_dynamic(upload(b, t), *args[2:])
+    assert_bits_equal(bits(got), layer.round_to(layer.product(*layer.quantize_rows(x), w, sw), t), "dynamic")
+
+
+@pytest.mark.parametrize("t", DT)
 @pytest.mark.parametrize("M,N", [(70, 300), (300, 9000), (600, 9001)])
 def test_product_into_rows_of_odd_distance(t, M, N):
     # outputs whose rows do not start at 16 bytes leave the tiles one by one

@@ -30,7 +30,7 @@ def test_header_compiles_as_c_and_cpp():
 def test_every_declared_symbol_is_exported_and_bound():
     out = subprocess.run(["gcc", "-E", "-P", "-x", "c", HEADER], capture_output=True, text=True, check=True).stdout
     names = sorted(set(re.findall(r"\b(?:int|int64_t)\s+(\w+)\s*\(", out)))
-    assert len(names) == 5 + 3 * 7, names
+    assert len(names) == 6 + 3 * 7, names
     nm = subprocess.run(["nm", "-D", "--defined-only", os.path.join(ROOT, "blockwise_bit_codebook_amd", "libkbit.so")],
                         capture_output=True, text=True, check=True).stdout
     exported = set(l.split()[-1] for l in nm.splitlines() if " T " in l)
@@ -55,18 +55,21 @@ def test_int8_validation_codes():
     assert q(B1, 2, 100, 100, A, 112, A, None) == -3                    # an odd address of 16-bit elements
     assert q(A, 2, 100, 100, A, 112, None, None) == -1
     li = lib.linear_int8_fp16
-    assert lib.linear_int8_dynamic_workspace_bytes(4, 64, 131072) == -1  # the sum could leave int32
-    assert lib.linear_int8_dynamic_workspace_bytes(-1, 64, 64) == -1
-    assert lib.linear_int8_dynamic_workspace_bytes(4, 64, 100) >= 4 * 112 + 16
-    assert li(None, None, 0, 100, 100, None, None, 64, 100, None, None, 64, None) == 0
-    assert li(A, A, 4, 100, 100, A, A, 64, 100, None, None, 64, None) == -1       # no output
-    assert li(A, None, 4, 100, 100, A, A, 64, 100, None, A, 64, None) == -1       # no scale
-    assert li(A, A, 4, 131072, 131072, A, A, 64, 131072, None, A, 64, None) == -1
-    assert li(A, A, 4, 100, 99, A, A, 64, 100, None, A, 64, None) == -1           # rows overlap
-    assert li(A, A, 4, 100, 100, A, A, 64, 99, None, A, 64, None) == -1
-    assert li(A, A, 4, 100, 100, A, A, 64, 100, None, A, 63, None) == -1
-    assert li(A, B1, 4, 100, 100, A, A, 64, 100, None, A, 64, None) == -3
-    assert li(A, A, 4, 100, 100, A, A, 64, 100, B1, A, 64, None) == -3
+    ws = lib.linear_int8_workspace_bytes(4, 64, 100)
+    assert ws >= 0
+    assert lib.linear_int8_workspace_bytes(4, 64, 131072) == -1         # the sum could leave int32
+    assert lib.linear_int8_workspace_bytes(-1, 64, 64) == -1
+    assert lib.linear_int8_dynamic_workspace_bytes(4, 64, 100) >= 4 * 112 + 16 + ws
+    big = 1 << 40
+    assert li(None, None, 0, 100, 100, None, None, 64, 100, None, None, 64, None, 0, None) == 0
+    assert li(A, A, 4, 100, 100, A, A, 64, 100, None, None, 64, A, big, None) == -1       # no output
+    assert li(A, None, 4, 100, 100, A, A, 64, 100, None, A, 64, A, big, None) == -1       # no scale
+    assert li(A, A, 4, 131072, 131072, A, A, 64, 131072, None, A, 64, A, big, None) == -1
+    assert li(A, A, 4, 100, 99, A, A, 64, 100, None, A, 64, A, big, None) == -1           # rows overlap
+    assert li(A, A, 4, 100, 100, A, A, 64, 99, None, A, 64, A, big, None) == -1
+    assert li(A, A, 4, 100, 100, A, A, 64, 100, None, A, 63, A, big, None) == -1
+    assert li(A, B1, 4, 100, 100, A, A, 64, 100, None, A, 64, A, big, None) == -3
+    assert li(A, A, 4, 100, 100, A, A, 64, 100, B1, A, 64, A, big, None) == -3
     dy = lib.linear_int8_dynamic_fp32
     need = lib.linear_int8_dynamic_workspace_bytes(4, 64, 100)
     assert dy(None, 0, 100, 100, None, None, 64, 100, None, None, 64, None, 0, None) == 0
