@@ -333,6 +333,13 @@ __device__ __forceinline__ int key_w(int row) {  // see operand_channel
     return (row & 3) | (row / (4 * TN) & 1) << 2;
 }
 
+// Where a lane's four sums stand in a 1 KB block of 16 rows (l16) and 4 x 4
+// channels (q): the rows of neighbouring pieces c of 4 channels are xor-ed
+// apart, so that neither the lanes that write a block nor the threads that
+// read a row of several blocks meet in a bank.  (Integer atomics into one
+// cleared array met four to a bank: 77 x 11008 x 4096 17.7 us, 16.6 so.)
+__device__ __forceinline__ int sum_place(int l16, int q, int c) { return 16 * (16 * q + (l16 ^ c)); }
+
 // Four neighbouring outputs of a row.
 template <class E>
 __device__ __forceinline__ void store_out4(const Int8Product& p, int64_t m, int n, const i32x4& acc, float xs,
@@ -370,15 +377,14 @@ bool out_aligned(const Int8Product& p, int64_t esize, int64_t bytes) {
 // A workgroup takes 16 MT rows and 16 TN channels.  Its waves split the depth
 // and work alone, each with two steps of both operands in LDS of its own and
 // no barrier: while one step is multiplied the next is on its way.  At the
-// end they add their int32 tiles in LDS with integer additions, whose order
-// does not matter.  The weights are read from memory once; the rows of x come
+// end each leaves its int32 sums where its operands were, and after the one
+// barrier every thread adds four channels of all waves.  The weights are read from memory once; the rows of x come
 // from cache.  Bound by the weights' bytes and, for the smallest, by the
 // latency of one load and the launch.
 template <class E, int MT, int TN, int WAVES>
 __global__ __launch_bounds__(WAVES* kWave) void int8_few_rows_kernel(const Int8Product p, int m_tiles, bool packed) {
-    constexpr int BM = MT * 16, BN = TN * 16, kStep = (BM + BN) * kDepth, kPitch = BN + 4;
+    constexpr int BM = MT * 16, BN = TN * 16, kStep = (BM + BN) * kDepth;
     __shared__ __align__(1024) uint8_t even[WAVES * kStep], odd[WAVES * kStep];
-    static_assert(BM * kPitch * 4 <= WAVES * kStep, "the sums fit over the operands");
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, q = lane >> 4;
     // Workgroups id, id + 8, ... run on one XCD: it takes a run of tiles with
@@ -473,23 +479,27 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_few_rows_kernel(const Int8P
         read(e);
         multiply();
     }
-    __syncthreads();
-    int* sum = reinterpret_cast<int*>(even);  // [BM][kPitch]
-    for (int i = threadIdx.x; i < BM * kPitch; i += WAVES * kWave) sum[i] = 0;
-    __syncthreads();
+    // Block (i, j) of sums: 1 KB of the wave's own operands, whose last reads
+    // are done.
+    constexpr int kFirst = kStep / 1024 < MT * TN ? kStep / 1024 : MT * TN;
+    static_assert(MT * TN - kFirst <= kStep / 1024, "the sums fit over the operands");
+    auto block = [&](int n, int w) {
+        return n < kFirst ? even + w * kStep + n * 1024 : odd + w * kStep + (n - kFirst) * 1024;
+    };
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                __hip_atomic_fetch_add(sum + (16 * i + l16) * kPitch + 4 * TN * q + 4 * j + r, acc[i][j][r],
-                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            *reinterpret_cast<i32x4*>(block(i * TN + j, wave) + sum_place(l16, q, TN * q + j)) = acc[i][j];
     __syncthreads();
-    for (int i = threadIdx.x; i < BM * BN / 4; i += WAVES * kWave) {
-        const int r = i / (BN / 4), c = (i % (BN / 4)) * 4;
-        if (r < rows && c < cols)
-            store_out4<E>(p, m0 + r, n0 + c, *reinterpret_cast<const i32x4*>(sum + r * kPitch + c), p.xs[m0 + r], packed);
+    for (int t = threadIdx.x; t < BM * BN / 4; t += WAVES * kWave) {
+        const int r = t / (BN / 4), c = t % (BN / 4);
+        if (r >= rows || 4 * c >= cols) continue;
+        const int n = (r >> 4) * TN + c % TN, at = sum_place(r & 15, c / TN, c);
+        i32x4 sum = *reinterpret_cast<const i32x4*>(block(n, 0) + at);
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) sum += *reinterpret_cast<const i32x4*>(block(n, w) + at);
+        store_out4<E>(p, m0 + r, n0 + 4 * c, sum, p.xs[m0 + r], packed);
     }
 }
 
@@ -513,12 +523,12 @@ template <class E, int TN, int WAVES, bool VEC>
 __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Product p,
                                                                    const typename E::T* __restrict__ X, int64_t ldX,
                                                                    bool packed) {
-    constexpr int BN = TN * 16, kStep = BN * kDepth, kPitch = BN + 4;
+    constexpr int BN = TN * 16, kStep = BN * kDepth;
     __shared__ __align__(1024) uint8_t even[WAVES * kStep], odd[WAVES * kStep];
     __shared__ __align__(16) int8_t codes[kTokenBytes];
     __shared__ uint32_t amax[WAVES * kItems];
     __shared__ float scale[kMaxTokens];
-    static_assert(16 * kPitch * 4 <= WAVES * kStep, "the sums fit over the operands");
+    static_assert(TN * 1024 <= kStep, "the sums fit over the operands");
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, q = lane >> 4;
     const int rows = static_cast<int>(p.M), n0 = blockIdx.x * BN, cols = min(p.N - n0, BN);
@@ -624,23 +634,18 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Pro
         read(e, steps);
         multiply();
     }
-    __syncthreads();
-    int* sum = reinterpret_cast<int*>(even);  // [rows][kPitch]
-    for (int i = threadIdx.x; i < rows * kPitch; i += WAVES * kWave) sum[i] = 0;
-    __syncthreads();
-    if (l16 < rows) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                __hip_atomic_fetch_add(sum + l16 * kPitch + 4 * TN * q + 4 * j + r, acc[j][r], __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_WORKGROUP);
-    }
+    for (int j = 0; j < TN; ++j)
+        *reinterpret_cast<i32x4*>(e + j * 1024 + sum_place(l16, q, TN * q + j)) = acc[j];
     __syncthreads();
-    for (int i = threadIdx.x; i < rows * BN / 4; i += WAVES * kWave) {
-        const int r = i / (BN / 4), c = (i % (BN / 4)) * 4;
-        if (c < cols)
-            store_out4<E>(p, r, n0 + c, *reinterpret_cast<const i32x4*>(sum + r * kPitch + c), scale[r], packed);
+    for (int t = threadIdx.x; t < rows * BN / 4; t += WAVES * kWave) {
+        const int r = t / (BN / 4), c = t % (BN / 4);
+        if (4 * c >= cols) continue;
+        const uint8_t* at = even + c % TN * 1024 + sum_place(r, c / TN, c);
+        i32x4 sum = *reinterpret_cast<const i32x4*>(at);
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) sum += *reinterpret_cast<const i32x4*>(at + w * kStep);
+        store_out4<E>(p, r, n0 + 4 * c, sum, scale[r], packed);
     }
 }
 
