@@ -982,7 +982,8 @@ int launch_generic(const Int8Product& p, void* stream) {
 // and from cache: what the rule picks is 0.7% slower than the fastest variant
 // on average, 11% at most.  Both sides of it, for example (operands from
 // memory): 77 x 11008 x 4096 18.3 us in 80 x 48 and 19.7 us in 80 x 64 pieces of
-// few rows, 26.7 in tiles of 32 x 128; 500 x 4099 x 3840 27.1 in tiles of 64 x
+// few rows, 26.7 in tiles of 32 x 128; 112 x 11008 x 4096 20.6 in 112 x 48 pieces,
+// 25.5 in 80 x 48 and 29.4 in tiles; 500 x 4099 x 3840 27.1 in tiles of 64 x
 // 128, 27.3 in 32 x 128, 30.1 in 80 x 64 pieces, 31.7 in 128 x 128; 4096 x 4096 x
 // 4096 58.8 in 256 x 256, 71.5 in 128 x 128.
 struct Int8Few {
@@ -994,7 +995,8 @@ struct Int8Tile {
     // MB of operands; the weight of whole rounds against parts of one
     double base, least, step, round, tail, operands, whole;
 };
-constexpr Int8Few kFew[] = {{1, 1}, {1, 2}, {1, 3}, {1, 4}, {2, 2}, {2, 4}, {3, 2}, {3, 4}, {4, 4}, {5, 3}, {5, 4}};
+constexpr Int8Few kFew[] = {{1, 1}, {1, 2}, {1, 3}, {1, 4}, {2, 2}, {2, 4}, {3, 2}, {3, 4}, {4, 4},
+                             {5, 3}, {5, 4}, {7, 3}, {8, 3}};
 constexpr Int8Tile kTiles[] = {{32, 128, 0.84, 0.497, 0.253, 1.08, 2.32, 1.29, 0.255},
                                {64, 128, 0.0, 0.572, 0.382, 1.85, 3.01, 1.07, 0.454},
                                {128, 128, 0.0, 0.799, 0.544, 2.70, 3.31, 0.11, 0.742},
@@ -1031,6 +1033,7 @@ Int8Choice choose_form(int64_t M, int N, int K, int64_t cus) {
     double least = 1e30;
     const double operands = 1e-7 * (static_cast<double>(M) + N) * K;
     for (const Int8Few& f : kFew) {
+        if (f.mt > 5 && M > 16 * f.mt) continue;  // made to read the weights once
         const double us = 1.34 + 0.68 * operands +
                           rounds_of(tiles_of(M, N, 16 * f.mt, 16 * f.tn), cus, 1.0) *
                               (1.783 + 0.204 * f.mt * f.tn + 1.297e-5 * 16.0 * (f.mt + f.tn) * K +
@@ -1083,7 +1086,9 @@ int launch_few_tile(const Int8Product& p, Int8Few f, void* stream) {
         case 34: return launch_few<E, 3, 4, 5>(p, stream);
         case 44: return launch_few<E, 4, 4, 4>(p, stream);
         case 53: return launch_few<E, 5, 3, 4>(p, stream);
-        default: return launch_few<E, 5, 4, 4>(p, stream);
+        case 54: return launch_few<E, 5, 4, 4>(p, stream);
+        case 73: return launch_few<E, 7, 3, 4>(p, stream);
+        default: return launch_few<E, 8, 3, 3>(p, stream);
     }
 }
 

@@ -19,13 +19,13 @@ pytestmark = pytest.mark.gpu
 
 # On 256 compute units, in this order: few rows in pieces of 16 x 16, 32, 48
 # and 64, 32 x 32 and 64, 48 x 32 and 64, 64 x 64, 80 x 48 and 64 (rows x
-# channels), tiles of 32, 64 and 128 x 128 and of 256 x 256; each with the
-# last piece of the depth partial and, in the second list, whole.
+# channels), tiles of 32, 64 and 128 x 128 and of 256 x 256, pieces of 112 and
+# 128 x 48; each with the last piece of the depth partial and, in the second list, whole.
 FORMS = [(1, 7, 20), (1, 4287, 20), (1, 8197, 20), (1, 12393, 20), (17, 6689, 21), (17, 8529, 20), (106, 2351, 128),
          (38, 9511, 640), (49, 12905, 1609), (50, 8657, 1556), (67, 12875, 1982), (36, 152, 256), (139, 10040, 20),
-         (321, 8117, 20), (428, 18432, 20)]
+         (321, 8117, 20), (428, 18432, 20), (89, 9166, 2483), (125, 11500, 3001)]
 WHOLE = [(2, 4300, 256), (3, 8200, 384), (5, 12400, 512), (20, 6700, 256), (20, 8600, 384), (40, 160, 1024),
-         (150, 10040, 512), (333, 8120, 384), (515, 16400, 512), (700, 9000, 640)]
+         (150, 10040, 512), (333, 8120, 384), (515, 16400, 512), (700, 9000, 640), (110, 11008, 2560), (118, 11659, 2176)]
 
 
 @pytest.mark.parametrize("i,M,N,K", [(i, *s) for i, s in enumerate(FORMS + WHOLE)])
