@@ -224,10 +224,13 @@ __device__ __forceinline__ u32x4 load_codes(const int8_t* row, int k, int K) {
             if ((n & 3) && i == n >> 2) r[i] = last;
         }
     } else {
+        typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+        if (k + 16 <= K) return *reinterpret_cast<const u32x4_any*>(p);
+        for (int i = 0; i < K - k; ++i) {
+            const uint32_t v = static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i & 3));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t v = static_cast<uint8_t>(p[min(i, K - 1 - k)]);
-            r[i >> 2] |= (i < K - k ? v : 0u) << (8 * (i & 3));
+            for (int j = 0; j < 4; ++j)
+                if (i >> 2 == j) r[j] |= v;
         }
     }
     return r;
@@ -241,47 +244,64 @@ __device__ __forceinline__ void store_out(const Int8Product& p, int64_t m, int n
     static_cast<typename E::T*>(p.out)[m * p.ldo + n] = E::narrow(v);
 }
 
-// Any shape and alignment: a 64 x 64 tile a workgroup, four waves of 32 x 32,
-// 64 codes deep a step through LDS (rows 80 bytes apart, so that the 16 rows
-// of a fragment start in different banks).
-constexpr int kGenTile = 64, kGenStep = 64, kGenPitch = 80;
-template <class E>
+// Any shape and alignment: a tile of 32 B x 32 B a workgroup, four waves of
+// half its side, 128 codes deep a step through LDS (rows 144 bytes apart, so
+// that the 16 rows of a fragment start in different banks).  The loads need no
+// alignment and go through registers: those of the next step are on their way
+// while a step is multiplied.  For rows that do not all start at 16 bytes, which
+// the kernels below need: 8192 x 11008 x 4096 698 us against their 301, 77 x
+// 11008 x 4096 33 against 13, 500 x 4099 x 3840 39.5 against 19.3.
+constexpr int kGenStep = 128, kGenPitch = 144;
+template <class E, int B>
 __global__ __launch_bounds__(kThreads) void int8_generic_kernel(const Int8Product p) {
-    __shared__ __align__(16) uint8_t lds[2][kGenTile * kGenPitch];
+    constexpr int kTile = 32 * B, kLoads = kTile * 8 / kThreads;
+    __shared__ __align__(16) uint8_t lds[2][kTile * kGenPitch];
     const int lane = __lane_id(), wave = threadIdx.x / kWave;
     const int l16 = lane & 15, q = lane >> 4;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kGenTile;
-    const int n0 = blockIdx.x * kGenTile;
-    const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
-    const int row = threadIdx.x >> 2, piece = (threadIdx.x & 3) * 16;
-    const bool x_ok = m0 + row < p.M, w_ok = n0 + row < p.N;
-    const int8_t* xr = p.x + (m0 + row) * p.ldx;
-    const int8_t* wr = p.w + static_cast<int64_t>(n0 + row) * p.ldw;
-    i32x4 acc[2][2] = {};
-    for (int k = 0; k < p.K; k += kGenStep) {
-        const u32x4 xv = x_ok ? load_codes<false>(xr, k + piece, p.K) : u32x4{0u, 0u, 0u, 0u};
-        const u32x4 wv = w_ok ? load_codes<false>(wr, k + piece, p.K) : u32x4{0u, 0u, 0u, 0u};
-        __syncthreads();
-        *reinterpret_cast<u32x4*>(&lds[0][row * kGenPitch + piece]) = xv;
-        *reinterpret_cast<u32x4*>(&lds[1][row * kGenPitch + piece]) = wv;
-        __syncthreads();
-        i32x4 a[2], b[2];
+    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile;
+    const int n0 = blockIdx.x * kTile;
+    const int wm = (wave & 1) * 16 * B, wn = (wave >> 1) * 16 * B;
+    const int row0 = threadIdx.x >> 3, piece = (threadIdx.x & 7) * 16;
+    u32x4 xv[kLoads], wv[kLoads];
+    auto load = [&](int k) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            a[i] = *reinterpret_cast<const i32x4*>(&lds[0][(wm + 16 * i + l16) * kGenPitch + 16 * q]);
-            b[i] = *reinterpret_cast<const i32x4*>(&lds[1][(wn + 16 * i + l16) * kGenPitch + 16 * q]);
+        for (int i = 0; i < kLoads; ++i) {  // rows past the matrix repeat its last one: they are not stored
+            const int row = row0 + 32 * i;
+            xv[i] = load_codes<false>(p.x + min<int64_t>(m0 + row, p.M - 1) * p.ldx, k + piece, p.K);
+            wv[i] = load_codes<false>(p.w + static_cast<int64_t>(min(n0 + row, p.N - 1)) * p.ldw, k + piece, p.K);
         }
+    };
+    i32x4 acc[B][B] = {};
+    load(0);
+    for (int k = 0; k < p.K; k += kGenStep) {
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < kLoads; ++i) {
+            *reinterpret_cast<u32x4*>(&lds[0][(row0 + 32 * i) * kGenPitch + piece]) = xv[i];
+            *reinterpret_cast<u32x4*>(&lds[1][(row0 + 32 * i) * kGenPitch + piece]) = wv[i];
+        }
+        __syncthreads();
+        if (k + kGenStep < p.K) load(k + kGenStep);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+        for (int h = 0; h < 2; ++h) {
+            i32x4 a[B], b[B];
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                a[i] = *reinterpret_cast<const i32x4*>(&lds[0][(wm + 16 * i + l16) * kGenPitch + 64 * h + 16 * q]);
+                b[i] = *reinterpret_cast<const i32x4*>(&lds[1][(wn + 16 * i + l16) * kGenPitch + 64 * h + 16 * q]);
+            }
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+        }
     }
     // lane l holds rows 4q + r, column l % 16 of each 16 x 16 block
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < B; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < B; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int64_t m = m0 + wm + 16 * i + 4 * q + r;
@@ -971,8 +991,14 @@ int launch_split(const Int8Product& p, int parts, void* workspace, void* stream)
 
 template <class E>
 int launch_generic(const Int8Product& p, void* stream) {
-    const dim3 grid((p.N + kGenTile - 1) / kGenTile, static_cast<unsigned>((p.M + kGenTile - 1) / kGenTile));
-    hipLaunchKernelGGL((int8_generic_kernel<E>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream), p);
+    const auto grid = [&](int tile) {
+        return dim3((p.N + tile - 1) / tile, static_cast<unsigned>((p.M + tile - 1) / tile));
+    };
+    const dim3 large = grid(128);  // half the operands' traffic, once its tiles fill the device
+    if (static_cast<int64_t>(large.x) * large.y >= device_cu_count())
+        hipLaunchKernelGGL((int8_generic_kernel<E, 4>), large, dim3(kThreads), 0, static_cast<hipStream_t>(stream), p);
+    else
+        hipLaunchKernelGGL((int8_generic_kernel<E, 2>), grid(64), dim3(kThreads), 0, static_cast<hipStream_t>(stream), p);
     return static_cast<int>(hipGetLastError());
 }
 

@@ -75,6 +75,15 @@ def test_product_into_rows_of_odd_distance(t, M, N):
     assert (out[:, 0] == 3.0).all() and (out[:, N + 1:] == 3.0).all()
 
 
+@pytest.mark.parametrize("M,N,K,px,pw", [(2050, 2049, 131, 131, 133), (2100, 2500, 400, 401, 400), (300, 300, 128, 129, 129),
+                                         (70, 200, 2000, 2001, 2003), (1, 5000, 127, 127, 127), (2200, 2300, 17, 17, 17)])
+def test_unaligned_rows_in_both_tiles(M, N, K, px, pw):
+    for t in DT:
+        case(f"linear int8 unaligned {t} M={M} N={N} K={K} strides {px} {pw}")
+        got, want = product_case(M, N, K, t, pitches=(px, pw))
+        assert_bits_equal(bits(got), want, f"unaligned {t}")
+
+
 @pytest.mark.parametrize("M,N,K", [(40000, 64, 48), (32769, 300, 20), (70000, 5, 33)])
 def test_more_rows_than_a_launch(M, N, K):
     case(f"linear int8 many rows M={M} N={N} K={K}")
