@@ -399,8 +399,8 @@ bool out_aligned(const Int8Product& p, int64_t esize, int64_t bytes) {
 // no barrier: while one step is multiplied the next is on its way.  At the
 // end each leaves its int32 sums where its operands were, and after the one
 // barrier every thread adds four channels of all waves.  The weights are read from memory once; the rows of x come
-// from cache.  Bound by the weights' bytes and, for the smallest, by the
-// latency of one load and the launch.
+// from cache.  Bound by the weights' bytes (77 x 11008 x 4096 in 13.3 us, 3.4
+// TB/s) and, for the smallest, by the latency of a few loads and the launch.
 template <class E, int MT, int TN, int WAVES>
 __global__ __launch_bounds__(WAVES* kWave) void int8_few_rows_kernel(const Int8Product p, int m_tiles, bool packed) {
     constexpr int BM = MT * 16, BN = TN * 16, kStep = (BM + BN) * kDepth;
@@ -674,7 +674,17 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Pro
 // ---------------------------------------------------------------------------
 // A workgroup of WM x WN waves takes a tile of 16 TM WM rows and 64 WN
 // channels, two steps of both operands in LDS: while the matrix cores work on
-// one, the loads of the next go into the other.
+// one, the loads of the next go into the other.  Tiles of 256 x 256 on 8 waves
+// need 1/256 byte of operands an operation, half of what 128 x 128 needs, and
+// run 8192 x 11008 x 4096 in 300 us with its scales (2.46 POP/s; the library's
+// product into int32, without scales, took 350); the smaller ones are for what
+// would not fill the device (choose_form).  The matrix pipes are busy for 52%
+// of the kernel's cycles, without one bank conflict: what is lost goes to the
+// step's barrier, to the rounds' ends (7.5 us each: one workgroup fits a
+// compute unit) and to the last, partly filled round.  Not kept, 4096^3 in 61 us:
+// fetching the next operands into L2 first 68, steps of 64 codes in a ring of
+// four 67.5, a second launch for the last round no gain.
+//
 // A wave's 16 TM x 64 outputs, through a region of LDS that is the wave's own,
 // so that a row leaves as one run of 64 channels: a lane's 16 channels alone
 // are 32 bytes of a line, and writing those cost 36 us a tile of 256 x 256.
