@@ -680,8 +680,9 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Pro
 // product into int32, without scales, took 350); the smaller ones are for what
 // would not fill the device (choose_form).  The matrix pipes are busy for 52%
 // of the kernel's cycles, without one bank conflict: what is lost goes to the
-// step's barrier, to the rounds' ends (7.5 us each: one workgroup fits a
-// compute unit) and to the last, partly filled round.  Not kept, 4096^3 in 61 us:
+// step's barrier, to the rounds' ends (one workgroup fits a compute unit: 7.5
+// us each, 5 where a workgroup stays, see below) and to the last, partly filled
+// round.  Not kept, 4096^3 in 61 us:
 // fetching the next operands into L2 first 68, steps of 64 codes in a ring of
 // four 67.5, a second launch for the last round no gain.
 //
@@ -692,47 +693,59 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Pro
 // NT, stores that do not stay in L2: 8192 x 11008 x 4096 380 -> 368 us in tiles
 // of 256 rows, 435 -> 408 us in 128, but 75.0 -> 80.3 us (1000 x 11008) in 64.
 // m, n: the wave's first row and channel.
+template <class E>
+constexpr bool kSums = std::is_same<typename E::T, int>::value;  // the sums themselves, no scales
+
+template <int TM>
+struct Scales {  // of a lane's 16 channels and TM rows
+    float w[16], bias[16], x[TM];
+};
+template <class E, int TM>
+__device__ __forceinline__ void load_scales(const Int8Product& p, int lane, int64_t m, int n, Scales<TM>& s) {
+    const int l16 = lane & 15, q = lane >> 4;
+    if constexpr (!kSums<E>) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            s.w[e] = p.ws[n + 16 * q + e];
+            s.bias[e] = 0.0f;
+        }
+        if (p.bias) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s.bias[e] = E::one(static_cast<const typename E::T*>(p.bias)[n + 16 * q + e]);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) s.x[i] = p.xs[m + 16 * i + l16];
+    }
+}
+
 template <class E, int TM, int kRegion, bool NT>
 __device__ __forceinline__ void store_tile(const Int8Product& p, typename E::T* out, uint8_t* region, int lane,
-                                           int64_t m, int n, const i32x4 (&acc)[TM][4], bool packed) {
+                                           int64_t m, int n, const i32x4 (&acc)[TM][4], const Scales<TM>& s,
+                                           bool packed) {
     using T = typename E::T;
-    constexpr bool kSums = std::is_same<T, int>::value;  // the sums themselves
     constexpr int kSize = sizeof(T), kRow = 64 * kSize;
     constexpr int kFit = kRegion / (16 * kRow) < TM ? kRegion / (16 * kRow) : TM;
     constexpr int kPass = TM % kFit == 0 ? kFit : 1;  // blocks of 16 rows a pass
     static_assert(kFit >= 1, "a block fits");
     const int l16 = lane & 15, q = lane >> 4;
-    float sc[16], bias[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        sc[e] = kSums ? 1.0f : p.ws[n + 16 * q + e];
-        bias[e] = 0.0f;
-    }
-    if constexpr (!kSums) {
-        if (p.bias) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) bias[e] = E::one(static_cast<const T*>(p.bias)[n + 16 * q + e]);
-        }
-    }
     out += m * p.ldo + n;
 #pragma unroll
     for (int i0 = 0; i0 < TM; i0 += kPass) {
 #pragma unroll
         for (int i = 0; i < kPass; ++i) {
             const int row = 16 * i + l16;
-            const float xs = kSums ? 1.0f : p.xs[m + 16 * i0 + row];
             float v[16];
 #pragma unroll
-            for (int e = 0; e < 16 && !kSums; ++e) {
-                v[e] = static_cast<float>(acc[i0 + i][e >> 2][e & 3]) * xs * sc[e];
-                if (p.bias) v[e] = v[e] + bias[e];
+            for (int e = 0; e < 16 && !kSums<E>; ++e) {
+                v[e] = static_cast<float>(acc[i0 + i][e >> 2][e & 3]) * s.x[i0 + i] * s.w[e];
+                if (p.bias) v[e] = v[e] + s.bias[e];
             }
 #pragma unroll
             for (int c = 0; c < kSize; ++c) {  // the lane's 16 kSize bytes
                 u32x4 d;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    if constexpr (kSums) d[r] = acc[i0 + i][c][r];
+                    if constexpr (kSums<E>) d[r] = acc[i0 + i][c][r];
                     else if constexpr (kSize == 4) d[r] = __float_as_uint(v[4 * c + r]);
                     else d[r] = E::pack(v[8 * c + 2 * r], v[8 * c + 2 * r + 1]);
                 }
@@ -767,10 +780,17 @@ struct QSums {
     static __device__ float one(T);
 };
 
-template <class E, int WM, int WN, int TM>
+// With STAY a workgroup takes one tile after the other: the first two steps of
+// the next are on their way while the outputs of one leave, through LDS of
+// their own, and the next one's products do not wait for those stores.  For
+// whole pairs of steps and outputs of whole 16-byte pieces.  8192 x 11008 x 1024
+// 126.9 us without, 112.7 with; 6000 x 6000 x 2048 106 and 101, 4096^3 59.8 and
+// 58.2, no difference from 8192 x 8192 x 8192 on.
+template <class E, int WM, int WN, int TM, bool STAY>
 __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Product p, int m_tiles, int n_tiles,
                                                                   int part_depth, bool packed) {
-    constexpr bool kSplit = std::is_same<E, QSums>::value;
+    using T = typename E::T;
+    constexpr bool kSplit = kSums<E>;
     constexpr int TN = 4, kT = WM * WN * kWave;
     constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
     constexpr int kXLoads = BM * 8 / kT, kWLoads = BN * 8 / kT;
@@ -779,6 +799,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
     // then sees that the operands it reads are not those on their way, and
     // puts no wait for the loads before the reads.
     __shared__ __align__(1024) uint8_t x_even[BM * kDepth], x_odd[BM * kDepth], w_even[BN * kDepth], w_odd[BN * kDepth];
+    constexpr int kPassing = 1024 * sizeof(T);  // 16 rows of outputs a wave
+    __shared__ __align__(1024) uint8_t passing[STAY ? WM * WN * kPassing : 16];
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, q = lane >> 4;
     const int wm = (wave % WM) * TM * 16, wn = (wave / WM) * TN * 16;
@@ -787,20 +809,26 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
     // of tiles, so that its L2 holds the operands its workgroups share.
     const int tiles = m_tiles * n_tiles;
     const int per = (tiles + 7) / 8;
-    const int t = static_cast<int>(blockIdx.x & 7) * per + static_cast<int>(blockIdx.x >> 3);
-    if (t >= tiles || static_cast<int>(blockIdx.x >> 3) >= per) return;
-    constexpr int kGroupM = 8;
-    const int group = t / (kGroupM * n_tiles), in = t - group * kGroupM * n_tiles;
-    const int gm = min(kGroupM, m_tiles - group * kGroupM);
-    // The last tiles of a row or column are moved inside the matrix (M >= BM,
-    // N >= BN): outputs computed twice get the same values twice.
-    const int64_t m0 = min<int64_t>(static_cast<int64_t>(group * kGroupM + in % gm) * BM, p.M - BM);
-    const int n0 = min(in / gm * BN, p.N - BN);
-
+    const int end = min(static_cast<int>(blockIdx.x & 7) * per + per, tiles);
+    int t = static_cast<int>(blockIdx.x & 7) * per + static_cast<int>(blockIdx.x >> 3);
+    if (t >= end) return;
     const int first = kSplit ? static_cast<int>(blockIdx.y) * part_depth : 0;
     const int K = kSplit ? min(p.K - first, part_depth) : p.K;
-    const int8_t* xb = p.x + m0 * p.ldx + first;
-    const int8_t* wb = p.w + static_cast<int64_t>(n0) * p.ldw + first;
+    int64_t m0;
+    int n0;
+    const int8_t *xb, *wb;
+    auto to_tile = [&] {
+        constexpr int kGroupM = 8;
+        const int group = t / (kGroupM * n_tiles), in = t - group * kGroupM * n_tiles;
+        const int gm = min(kGroupM, m_tiles - group * kGroupM);
+        // The last tiles of a row or column are moved inside the matrix (M >=
+        // BM, N >= BN): outputs computed twice get the same values twice.
+        m0 = min<int64_t>(static_cast<int64_t>(group * kGroupM + in % gm) * BM, p.M - BM);
+        n0 = min(in / gm * BN, p.N - BN);
+        xb = p.x + m0 * p.ldx + first;
+        wb = p.w + static_cast<int64_t>(n0) * p.ldw + first;
+    };
+    to_tile();
     // A round of loads covers kRound rows; the keys repeat from round to
     // round, but for the weights' where a round is shorter than their period.
     constexpr int kRound = kT / 8;
@@ -829,7 +857,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
     const int xp[2] = {(wm + l16) * kDepth + 16 * (q ^ key_x(l16)), (wm + l16) * kDepth + 16 * ((4 + q) ^ key_x(l16))};
     const int wp[2] = {(wn + w_row) * kDepth + 16 * (q ^ key_w<TN>(w_row)),
                        (wn + w_row) * kDepth + 16 * ((4 + q) ^ key_w<TN>(w_row))};
-    i32x4 acc[TM][TN] = {};
+    i32x4 acc[TM][TN];
     i32x4 x[TM], w0[TN], w1[TN];
     auto read_x = [&](const uint8_t* xd, int h, int i) {
         x[i] = *reinterpret_cast<const i32x4*>(xd + xp[h] + 16 * i * kDepth);
@@ -876,29 +904,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
         __builtin_amdgcn_s_waitcnt(0);  // loads to LDS are counted with the vector loads: a barrier does not wait for them
         __syncthreads();
     };
-    // The pipeline takes pairs of steps.  What the depth has beyond them comes
-    // first (the sums are exact in any order), piece by piece through
-    // registers, zeros past K.
     const int steps = K / (2 * kDepth) * 2;
-#pragma clang loop unroll(disable)
-    for (int k = steps * kDepth; k < K; k += kDepth) {
-#pragma clang loop unroll(disable)
-        for (int i = 0; i < kXLoads + kWLoads; ++i) {
-            const bool w = i >= kXLoads;
-            const int row = (w ? i - kXLoads : i) * kRound + row0;
-            const int key = w ? key_w<TN>(row) : key_x(row);
-            const int8_t* from = w ? wb + static_cast<int64_t>(row) * ldw : xb + static_cast<int64_t>(row) * ldx;
-            uint8_t* to = (w ? w_even : x_even) + row * kDepth + piece0 * 16;
-            *reinterpret_cast<u32x4*>(to) = load_codes<true>(from, k + 16 * (piece0 ^ key), K);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            read(x_even, w_even, h, w0);
-            multiply_all(w0);
-        }
-        __syncthreads();
-    }
     // One step from (xd, wd), the next one's first half from (xn, wn).
     auto step = [&](int s, uint8_t* xd, uint8_t* wd, const uint8_t* xn, const uint8_t* wn) {
         multiply(w0, xd, wd, 1, w1);
@@ -906,32 +912,86 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
         fetch((s + 2) * kDepth, xd, wd, s + 2 < steps);
         multiply(w1, xn, wn, 0, w0);
     };
-    fetch(0, x_even, w_even, steps > 0);
-    fetch(kDepth, x_odd, w_odd, steps > 0);
-    arrive();
-    read(x_even, w_even, 0, w0);
-    for (int s = 0; s < steps; s += 2) {  // past the last step it reads operands that nobody multiplies
-        step(s, x_even, w_even, x_odd, w_odd);
-        step(s + 1, x_odd, w_odd, x_even, w_even);
+    constexpr int kStores = TM * sizeof(T);  // a wave's stores of a tile
+    bool fetched = false;
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+        // The pipeline takes pairs of steps.  What the depth has beyond them comes
+        // first (the sums are exact in any order), piece by piece through
+        // registers, zeros past K.
+        if constexpr (!STAY) {
+#pragma clang loop unroll(disable)
+            for (int k = steps * kDepth; k < K; k += kDepth) {
+#pragma clang loop unroll(disable)
+                for (int i = 0; i < kXLoads + kWLoads; ++i) {
+                    const bool w = i >= kXLoads;
+                    const int row = (w ? i - kXLoads : i) * kRound + row0;
+                    const int key = w ? key_w<TN>(row) : key_x(row);
+                    const int8_t* from = w ? wb + static_cast<int64_t>(row) * ldw : xb + static_cast<int64_t>(row) * ldx;
+                    uint8_t* to = (w ? w_even : x_even) + row * kDepth + piece0 * 16;
+                    *reinterpret_cast<u32x4*>(to) = load_codes<true>(from, k + 16 * (piece0 ^ key), K);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    read(x_even, w_even, h, w0);
+                    multiply_all(w0);
+                }
+                __syncthreads();
+            }
+        }
+        if (STAY && fetched) {
+            landed<kStores>();  // the operands are older than the last tile's stores
+            __syncthreads();
+        } else {
+            fetch(0, x_even, w_even, steps > 0);
+            fetch(kDepth, x_odd, w_odd, steps > 0);
+            arrive();
+        }
+        read(x_even, w_even, 0, w0);
+        for (int s = 0; s < steps; s += 2) {  // past the last step it reads operands that nobody multiplies
+            step(s, x_even, w_even, x_odd, w_odd);
+            step(s + 1, x_odd, w_odd, x_even, w_even);
+        }
+        // What follows runs once a tile: its addresses are made anew from the
+        // thread's number, so that the loop above keeps no registers for them.
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        T* out = static_cast<T*>(p.out);
+        if constexpr (kSplit) out += blockIdx.y * p.M * p.ldo;
+        const int64_t m = m0 + wm;
+        const int n = n0 + wn;
+        Scales<TM> scales;
+        load_scales<E, TM>(p, tid & 63, m, n, scales);
+        arrive();  // the operands are read, and the empty loads of the last steps are done
+        if constexpr (STAY) {
+            t += static_cast<int>(gridDim.x >> 3);
+            fetched = t < end;
+            if (fetched) {
+                to_tile();
+                fetch(0, x_even, w_even, true);
+                fetch(kDepth, x_odd, w_odd, true);
+            }
+            store_tile<E, TM, kPassing, true>(p, out, passing + wave * kPassing, tid & 63, m, n, acc, scales, true);
+            if (!fetched) return;
+        } else {
+            // A region for each wave, in the array that has room for it.
+            constexpr int kPart = (BM < BN ? BM : BN) >= 256 ? 16384 : (BM < BN ? BM : BN) >= 64 ? 8192 : 4096;
+            static_assert(kPart <= BM * kDepth && kPart <= BN * kDepth, "a region fits into either array");
+            constexpr int kInX = BM * kDepth / kPart, kInW = BN * kDepth / kPart;
+            static_assert(2 * kInX + 2 * kInW >= WM * WN, "a region for every wave");
+            uint8_t* region = wave < kInX ? x_even + wave * kPart
+                              : wave < 2 * kInX ? x_odd + (wave - kInX) * kPart
+                              : wave < 2 * kInX + kInW ? w_even + (wave - 2 * kInX) * kPart
+                                                       : w_odd + (wave - 2 * kInX - kInW) * kPart;
+            store_tile<E, TM, kPart, (BM >= 128 && !kSplit)>(p, out, region, tid & 63, m, n, acc, scales,
+                                                             packed && (n0 * sizeof(T)) % 16 == 0);
+            return;
+        }
     }
-    // What follows runs once: its addresses are made anew from the thread's
-    // number, so that the loop above keeps no registers for them.
-    int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));
-    arrive();  // the operands are read, and the empty loads of the last steps are done
-    // A region for each wave, in the array that has room for it.
-    constexpr int kPart = (BM < BN ? BM : BN) >= 256 ? 16384 : (BM < BN ? BM : BN) >= 64 ? 8192 : 4096;
-    static_assert(kPart <= BM * kDepth && kPart <= BN * kDepth, "a region fits into either array");
-    constexpr int kInX = BM * kDepth / kPart, kInW = BN * kDepth / kPart;
-    static_assert(2 * kInX + 2 * kInW >= WM * WN, "a region for every wave");
-    uint8_t* region = wave < kInX ? x_even + wave * kPart
-                      : wave < 2 * kInX ? x_odd + (wave - kInX) * kPart
-                      : wave < 2 * kInX + kInW ? w_even + (wave - 2 * kInX) * kPart
-                                               : w_odd + (wave - 2 * kInX - kInW) * kPart;
-    typename E::T* out = static_cast<typename E::T*>(p.out);
-    if constexpr (kSplit) out += blockIdx.y * p.M * p.ldo;
-    store_tile<E, TM, kPart, (BM >= 128 && !kSplit)>(p, out, region, tid & 63, m0 + wm, n0 + wn, acc,
-                                                     packed && (n0 * sizeof(typename E::T)) % 16 == 0);
 }
 
 // Adds the parts' sums and applies the scales: four channels a thread.
@@ -957,12 +1017,16 @@ int launch_few(const Int8Product& p, void* stream) {
     return static_cast<int>(hipGetLastError());
 }
 
-template <class E, int WM, int WN, int TM>
+template <class E, int WM, int WN, int TM, bool STAY>
 int launch_tile(const Int8Product& p, void* stream) {
     constexpr int BM = WM * TM * 16, BN = WN * 64;
     const int m_tiles = static_cast<int>((p.M + BM - 1) / BM), n_tiles = (p.N + BN - 1) / BN;
-    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
-    hipLaunchKernelGGL((int8_tile_kernel<E, WM, WN, TM>), dim3(grid), dim3(WM * WN * kWave), 0,
+    unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
+    if (STAY) {  // one workgroup a compute unit, the same number on each XCD
+        const unsigned resident = device_cu_count() < 8 ? 8u : static_cast<unsigned>(device_cu_count()) / 8 * 8;
+        if (grid > resident) grid = resident;
+    }
+    hipLaunchKernelGGL((int8_tile_kernel<E, WM, WN, TM, STAY>), dim3(grid), dim3(WM * WN * kWave), 0,
                        static_cast<hipStream_t>(stream), p, m_tiles, n_tiles, 0, out_aligned(p, sizeof(typename E::T), 16));
     return static_cast<int>(hipGetLastError());
 }
@@ -988,7 +1052,7 @@ int launch_split(const Int8Product& p, int parts, void* workspace, void* stream)
     Int8Product s = p;
     s.out = workspace;
     s.ldo = sums_ld(p.N);
-    hipLaunchKernelGGL((int8_tile_kernel<QSums, 2, 2, 4>), dim3(grid, parts), dim3(4 * kWave), 0,
+    hipLaunchKernelGGL((int8_tile_kernel<QSums, 2, 2, 4, false>), dim3(grid, parts), dim3(4 * kWave), 0,
                        static_cast<hipStream_t>(stream), s, m_tiles, n_tiles, part_depth, true);
     const int e = static_cast<int>(hipGetLastError());
     if (e != 0) return e;
@@ -1133,11 +1197,15 @@ int launch_form(const Int8Product& p, const Int8Choice& c, void* workspace, void
     if (c.parts > 1) return launch_split<E>(p, c.parts, workspace, stream);
     switch (c.bm) {
         case 0: return launch_few_tile<E>(p, c.few, stream);
-        case 32: return launch_tile<E, 2, 2, 1>(p, stream);
-        case 64: return launch_tile<E, 2, 2, 2>(p, stream);
-        case 128: return launch_tile<E, 2, 2, 4>(p, stream);
-        default: return launch_tile<E, 2, 4, 8>(p, stream);
+        case 32: return launch_tile<E, 2, 2, 1, false>(p, stream);
+        case 64: return launch_tile<E, 2, 2, 2, false>(p, stream);
+        case 128: return launch_tile<E, 2, 2, 4, false>(p, stream);
+        default: break;
     }
+    constexpr int kSize = sizeof(typename E::T);
+    return p.K % (2 * kDepth) == 0 && p.N * kSize % 16 == 0 && out_aligned(p, kSize, 16)
+               ? launch_tile<E, 2, 4, 8, true>(p, stream)
+               : launch_tile<E, 2, 4, 8, false>(p, stream);
 }
 
 // Blocks of rows and channels keep the grids (below 2^32 threads) and the

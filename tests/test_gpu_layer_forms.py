@@ -75,6 +75,16 @@ def test_product_into_rows_of_odd_distance(t, M, N):
     assert (out[:, 0] == 3.0).all() and (out[:, N + 1:] == 3.0).all()
 
 
+@pytest.mark.parametrize("t", DT)
+@pytest.mark.parametrize("M,N,K", [(4360, 4352, 256), (8200, 2600, 512), (4400, 4362, 256), (2700, 8200, 768), (4360, 4352, 300)])
+def test_workgroups_that_take_several_tiles(t, M, N, K):
+    # more tiles of 256 x 256 than compute units; odd channels and a depth of
+    # no whole pair of steps take the other way
+    case(f"linear int8 several tiles {t} M={M} N={N} K={K}")
+    got, want = product_case(M, N, K, t, bias=M % 100 != 0)
+    assert_bits_equal(bits(got), want, f"product {M} {N} {K}")
+
+
 @pytest.mark.parametrize("M,N,K,px,pw", [(2050, 2049, 131, 131, 133), (2100, 2500, 400, 401, 400), (300, 300, 128, 129, 129),
                                          (70, 200, 2000, 2001, 2003), (1, 5000, 127, 127, 127), (2200, 2300, 17, 17, 17)])
 def test_unaligned_rows_in_both_tiles(M, N, K, px, pw):
