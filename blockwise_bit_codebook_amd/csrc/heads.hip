@@ -393,12 +393,12 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(const HeadsArgs p) {
 // of u * xhat in registers, adds its lane groups in LDS in a fixed order and
 // stores one partial row of D sums, which norm_weight_grad_kernel adds in a
 // fixed order: the result does not depend on scheduling.
-template <class E, int LAYOUT, int FORM>
-__global__ __launch_bounds__(kThreads) void norm_back_kernel(const NormBackArgs p) {
+template <class E, int LAYOUT, int FORM, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_back_kernel(const NormBackArgs p) {
     using T = typename E::T;
-    __shared__ __align__(16) float red[kThreads * 16];
+    __shared__ __align__(16) float red[THREADS * 16];
     const int lg = FORM == kVector ? p.log2_lanes : 6;
-    const int groups = kThreads >> lg;
+    const int groups = THREADS >> lg;
     const int lane = threadIdx.x & ((1 << lg) - 1);
     const int group = threadIdx.x >> lg;
     const bool second = blockIdx.x >= static_cast<unsigned>(p.first_groups);
@@ -455,7 +455,7 @@ __global__ __launch_bounds__(kThreads) void norm_back_kernel(const NormBackArgs 
         }
         store_row<E, LAYOUT, FORM>(dx, lane, D, rot, sl, xa, xb);
     }
-    float* mine = red + group * D;  // groups * D <= kThreads * 16
+    float* mine = red + group * D;  // groups * D <= THREADS * 16
     if constexpr (FORM == kVector) {
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {  // D is a multiple of 8: 16-byte pieces
@@ -466,11 +466,18 @@ __global__ __launch_bounds__(kThreads) void norm_back_kernel(const NormBackArgs 
         store_row<HF32, LAYOUT, FORM>(mine, lane, D, rot, sl, da, db);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < D; e += kThreads) {
-        float sum = red[e];
-        for (int q = 1; q < groups; ++q) sum += red[q * D + e];
-        if (p.direct[0] != nullptr) p.direct[second ? 1 : 0][e] = sum;
-        else p.partial[static_cast<int64_t>(blockIdx.x) * D + e] = sum;
+    if constexpr (THREADS == kThreads) {
+        for (int e = threadIdx.x; e < D; e += THREADS) {
+            float sum = red[e];
+            for (int q = 1; q < groups; ++q) sum += red[q * D + e];
+            p.partial[static_cast<int64_t>(blockIdx.x) * D + e] = sum;
+        }
+    } else {  // up to 1024 lane groups, and nobody else at work: halves added to halves
+        for (int s = groups >> 1; s >= 1; s >>= 1) {
+            for (int i = threadIdx.x; i < s * D; i += THREADS) red[i] += red[i + s * D];
+            __syncthreads();
+        }
+        for (int e = threadIdx.x; e < D; e += THREADS) p.direct[second ? 1 : 0][e] = red[e];
     }
 }
 
@@ -577,10 +584,18 @@ int launch_heads_e(HeadsArgs& p, int64_t batch, HeadsKind kind, int layout, bool
     }
 }
 
+// Threads of a workgroup that makes a whole weight gradient: as many as its
+// registers allow.
+constexpr int direct_threads(int form) { return form <= 1 ? 1024 : 512; }
+
 template <class E, int LAYOUT, int FORM>
 int launch_back_f(const NormBackArgs& p, int grid, void* stream) {
-    hipLaunchKernelGGL((norm_back_kernel<E, LAYOUT, FORM>), dim3(grid), dim3(kThreads), 0,
-                       static_cast<hipStream_t>(stream), p);
+    if (p.direct[0] != nullptr)
+        hipLaunchKernelGGL((norm_back_kernel<E, LAYOUT, FORM, direct_threads(FORM)>), dim3(grid),
+                           dim3(direct_threads(FORM)), 0, static_cast<hipStream_t>(stream), p);
+    else
+        hipLaunchKernelGGL((norm_back_kernel<E, LAYOUT, FORM, kThreads>), dim3(grid), dim3(kThreads), 0,
+                           static_cast<hipStream_t>(stream), p);
     return static_cast<int>(hipGetLastError());
 }
 
@@ -620,11 +635,15 @@ int launch_norm_back(Dtype t, NormBackArgs& p, int layout, bool vec, float* d0, 
     }
     if (g0 < 1) g0 = 1;
     if (g1 < 1) g1 = 1;
-    // Up to two rows a lane group in one workgroup a set: its sums are the
-    // result, and there is no second launch.  Heads of 128 in 16 bits, one
-    // launch and two: 8 tokens x 8 heads (two rows a lane group) 5.6 and 6.6
-    // us, 16 tokens (four) 7.9 and 6.5.
-    const bool direct = n[0] <= 2 && n[1] <= 2;
+    // Up to a row a lane group in one large workgroup a set: its sums are the
+    // result, and there is no second launch.  Heads of 128 in 16 bits, in a
+    // graph (and called from Python): 16 tokens x 8 heads, a row a lane group,
+    // 6.3 us (6.7) against 6.3 (7.9) in two launches; 32 tokens, two rows, 8.7
+    // (9.0) against 6.4 (7.9); 1 token 5.3 (5.8) against 6.3 (8.0).
+    const int direct_groups =
+        direct_threads(vec ? kVector : one_pair_a_lane(p.dim, p.dim) ? 1 : 8) >> (vec ? p.log2_lanes : 6);
+    const bool direct = p.set[0].rows <= static_cast<uint32_t>(direct_groups) &&
+                        p.set[1].rows <= static_cast<uint32_t>(direct_groups);
     if (direct) {
         g0 = g1 = 1;
         p.direct[0] = d0;

@@ -221,10 +221,10 @@ def test_norm_and_gradient_large(t, layout, T, H, D, rot):
         assert_close(bits(back[2 + i]), "fp32", dw, dwb, f"d{n}_weight")
 
 
-@pytest.mark.parametrize("rows", [15, 16, 17, 63, 64, 65, 66, 200])
+@pytest.mark.parametrize("rows", [15, 16, 17, 31, 32, 33, 63, 64, 65, 66, 127, 128, 129, 200])
 def test_norm_gradient_with_and_without_the_second_kernel(rows):
-    # heads of 128 in 16 bits: 8 lanes a row, 32 rows a workgroup; up to four
-    # times that a set the sums are stored directly
+    # heads of 128 in 16 bits: 8 lanes a row, 32 rows a workgroup, or 128 in one
+    # large workgroup a set, which stores its sums directly
     for H, Hk in ((4, 1), (2, 2), (1, 3)):
         case(f"norm gradient rows={rows} heads={H},{Hk}")
         rng = np.random.default_rng(rows + H)
