@@ -86,7 +86,8 @@ def quantize_rows(x32):
 
 def product(codes, scale, w_codes, w_scale, bias=None):
     """fp32 values before the rounding to T."""
-    acc = codes.astype(np.int64) @ w_codes.astype(np.int64).T
+    # integers below 2^31 in every partial sum: exact in fp64, in any order
+    acc = codes.astype(np.float64) @ w_codes.astype(np.float64).T
     with np.errstate(all="ignore"):
         v = (acc.astype(np.float32) * scale[:, None]).astype(np.float32)
         v = (v * w_scale[None, :]).astype(np.float32)
