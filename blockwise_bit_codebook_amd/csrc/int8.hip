@@ -919,12 +919,26 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-        // The pipeline takes pairs of steps.  What the depth has beyond them comes
-        // first (the sums are exact in any order), piece by piece through
-        // registers, zeros past K.
+        // The pipeline takes pairs of steps.  What the depth has beyond them
+        // comes first (the sums are exact in any order): a whole step like the
+        // others, a partial one piece by piece through registers, zeros past K.
         if constexpr (!STAY) {
-#pragma clang loop unroll(disable)
-            for (int k = steps * kDepth; k < K; k += kDepth) {
+            auto alone = [&] {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    read(x_even, w_even, h, w0);
+                    multiply_all(w0);
+                }
+                __syncthreads();
+            };
+            int k = steps * kDepth;
+            if (k + kDepth <= K) {
+                fetch(k, x_even, w_even, true);
+                arrive();
+                alone();
+                k += kDepth;
+            }
+            if (k < K) {
 #pragma clang loop unroll(disable)
                 for (int i = 0; i < kXLoads + kWLoads; ++i) {
                     const bool w = i >= kXLoads;
@@ -935,12 +949,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
                     *reinterpret_cast<u32x4*>(to) = load_codes<true>(from, k + 16 * (piece0 ^ key), K);
                 }
                 __syncthreads();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    read(x_even, w_even, h, w0);
-                    multiply_all(w0);
-                }
-                __syncthreads();
+                alone();
             }
         }
         if (STAY && fetched) {
@@ -1150,7 +1159,7 @@ Int8Choice choose_form(int64_t M, int N, int K, int64_t cus) {
         const int64_t tiles = tiles_of(M, N, t.bm, t.bn);
         const double r = rounds_of(tiles, cus, t.whole);
         const double us = t.base + (t.step * r > t.least ? t.step * r : t.least) * steps + t.round * r +
-                          (rest ? t.tail : 0.0) + t.operands * operands;
+                          (K % kDepth ? t.tail : 0.0) + t.operands * operands;
         if (us < least) {
             least = us;
             best = Int8Choice{{}, t.bm, 1};
