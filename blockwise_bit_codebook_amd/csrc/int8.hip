@@ -771,6 +771,63 @@ __device__ __forceinline__ void store_tile(const Int8Product& p, typename E::T* 
     }
 }
 
+// The partial step of an operand to LDS: rows row0, row0 + ROUND, ... from
+// column 0 of `from`, `left` codes each, zeros past them (nothing else is
+// read).  The loads of all rows are on their way together.
+template <int LOADS, int ROUND, class Key>
+__device__ __forceinline__ void store_partial(const int8_t* from, int64_t ld, int left, uint8_t* to, int row0, int piece0,
+                                              const Key& key) {
+    const int full = left >> 4, n = left & 15;  // whole pieces, codes of the one after them
+    const int8_t* row[LOADS];
+    int piece[LOADS];
+    u32x4 d[LOADS];
+    uint2 b8[LOADS];
+    uint32_t b4[LOADS], b2[LOADS], b1[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        row[i] = from + (row0 + i * ROUND) * ld;
+        piece[i] = piece0 ^ key(row0 + i * ROUND);
+        d[i] = u32x4{0u, 0u, 0u, 0u};
+        b8[i] = make_uint2(0u, 0u);
+        b4[i] = b2[i] = b1[i] = 0u;
+        if (piece[i] < full) d[i] = load16<false>(row[i] + 16 * piece[i]);
+        row[i] += 16 * full;
+    }
+    if (n & 8) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            if (piece[i] == full) b8[i] = *reinterpret_cast<const uint2*>(row[i]);
+    }
+    if (n & 4) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            if (piece[i] == full) b4[i] = *reinterpret_cast<const uint32_t*>(row[i] + (n & 8));
+    }
+    if (n & 2) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            if (piece[i] == full) b2[i] = *reinterpret_cast<const uint16_t*>(row[i] + (n & 12));
+    }
+    if (n & 1) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            if (piece[i] == full) b1[i] = static_cast<uint8_t>(row[i][n & 14]);
+    }
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        if (piece[i] == full) {
+            const uint32_t last = b2[i] | b1[i] << (8 * (n & 2));
+            d[i] = u32x4{b8[i].x, b8[i].y, 0u, 0u};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if ((n & 4) && w == (n & 8) >> 2) d[i][w] = b4[i];
+                if ((n & 3) && w == n >> 2) d[i][w] = last;
+            }
+        }
+        *reinterpret_cast<u32x4*>(to + (row0 + i * ROUND) * kDepth + 16 * piece0) = d[i];
+    }
+}
+
 // With E = QSums the depth is split as well: workgroups (x, y) take the codes
 // from y part_depth on, at most part_depth (whole pairs of steps), and store
 // their sums as they are, one matrix after the other.
@@ -939,15 +996,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(const Int8Prod
                 k += kDepth;
             }
             if (k < K) {
-#pragma clang loop unroll(disable)
-                for (int i = 0; i < kXLoads + kWLoads; ++i) {
-                    const bool w = i >= kXLoads;
-                    const int row = (w ? i - kXLoads : i) * kRound + row0;
-                    const int key = w ? key_w<TN>(row) : key_x(row);
-                    const int8_t* from = w ? wb + static_cast<int64_t>(row) * ldw : xb + static_cast<int64_t>(row) * ldx;
-                    uint8_t* to = (w ? w_even : x_even) + row * kDepth + piece0 * 16;
-                    *reinterpret_cast<u32x4*>(to) = load_codes<true>(from, k + 16 * (piece0 ^ key), K);
-                }
+                store_partial<kXLoads, kRound>(xb + k, ldx, K - k, x_even, row0, piece0, [](int row) { return key_x(row); });
+                store_partial<kWLoads, kRound>(wb + k, ldw, K - k, w_even, row0, piece0,
+                                               [](int row) { return key_w<TN>(row); });
                 __syncthreads();
                 alone();
             }
