@@ -1139,9 +1139,11 @@ int launch_generic(const Int8Product& p, void* stream) {
 // Which kernel and tile: the least of estimated times, in microseconds.  The
 // estimates were fitted to 2100 measurements, every variant at 130 shapes
 // spread over M = 1 .. 8192 and N, K = 64 .. 16384 with operands from memory
-// and from cache: what the rule picks is 0.7% slower than the fastest variant
-// on average, 11% at most.  Both sides of it, for example (operands from
-// memory): 77 x 11008 x 4096 18.3 us in 80 x 48 and 19.7 us in 80 x 64 pieces of
+// and from cache: what the rule picked was 0.7% slower than the fastest variant
+// on average, 11% at most.  (Since then few rows join 1 us faster, the ends of
+// 256 x 256 rounds and partial steps 1 to 3 us; measured again over 140 shapes
+// the rule is within 4% on average, 23% at most.)  Both sides of it, as fitted
+// (operands from memory): 77 x 11008 x 4096 18.3 us in 80 x 48 and 19.7 us in 80 x 64 pieces of
 // few rows, 26.7 in tiles of 32 x 128; 112 x 11008 x 4096 20.6 in 112 x 48 pieces,
 // 25.5 in 80 x 48 and 29.4 in tiles; 500 x 4099 x 3840 27.1 in tiles of 64 x
 // 128, 27.3 in 32 x 128, 30.1 in 80 x 64 pieces, 31.7 in 128 x 128; 4096 x 4096 x
@@ -1232,11 +1234,15 @@ Int8Choice choose_form(int64_t M, int N, int K, int64_t cus) {
     return best;
 }
 
-// The waves that split the depth: as many as their operands fit into LDS.
+// The waves that split the depth: as many as their operands fit into LDS, but
+// for the smallest pieces, several of which share a compute unit.  16 x 16, in 4 /
+// 8 / 16 waves with operands from memory: 6 x 1216 x 768 3.1 / 3.6 / 4.1 us, 16 x
+// 4096 x 2048 4.6 / 4.7 / 5.6, 16 x 4096 x 4096 6.4 / 6.6 / 6.9, 16 x 1024 x 8192
+// 7.6 / 7.4 / 7.7.
 template <class E>
 int launch_few_tile(const Int8Product& p, Int8Few f, void* stream) {
     switch (10 * f.mt + f.tn) {
-        case 11: return launch_few<E, 1, 1, 16>(p, stream);
+        case 11: return p.K <= 4096 ? launch_few<E, 1, 1, 4>(p, stream) : launch_few<E, 1, 1, 8>(p, stream);
         case 12: return launch_few<E, 1, 2, 8>(p, stream);
         case 13: return launch_few<E, 1, 3, 8>(p, stream);
         case 14: return launch_few<E, 1, 4, 7>(p, stream);
@@ -1314,7 +1320,8 @@ int launch_tokens_t(const Int8Product& p, const void* X, int64_t ldX, bool vec, 
 // over the device take about 1 : 2 : 3, the largest of equals.  One token x
 // 4096 in 16 / 48 / 64: 4096 channels 6.5 / 9.4 / 10.8 us, 6000 10.8 / 10.3 / 11.3,
 // 11008 15.9 / 13.6 / 13.8, 14336 20.3 / 20.7 / 15.9, 32000 39.0 / 33.5 / 32.4; two
-// tokens, 20000 x 2048, 22.3 / 14.7 / 16.4.
+// tokens, 20000 x 2048, 22.3 / 14.7 / 16.4.  Pieces of 16 in 16 waves, not 8: 1 x
+// 4096 x 4096 6.5 against 8.5 us, 1 x 4096 x 1024 4.4 against 4.2.
 template <class E>
 int launch_tokens_e(const Int8Product& p, const void* X, int64_t ldX, bool vec, void* stream) {
     const int cus = device_cu_count();

@@ -7,8 +7,10 @@ the C entry points (``include/kbit_layer.h``) are in ``_layer``
 (``csrc/layer_bind.cpp``), whose host time is a fraction of what they cost
 here.  Calls run on torch's current stream of the inputs' device.  Tensors
 may be strided; the last axis has to be contiguous where it is a row of codes,
-of a matrix or of a head.  If ``_layer`` was not built the import raises:
-there is no other path.
+of a matrix or of a head.  Nothing is recorded for autograd: gradients are
+calls of their own (``rope(..., inverse=True)``, ``qk_norm_rope_backward``), to
+be put into a ``torch.autograd.Function`` where a model is trained that way.
+If ``_layer`` was not built the import raises: there is no other path.
 """
 
 import ctypes as ct
