@@ -1277,11 +1277,14 @@ int launch_form(const Int8Product& p, const Int8Choice& c, void* workspace, void
 // Blocks of rows and channels keep the grids (below 2^32 threads) and the
 // kernels' 32-bit offsets in range.
 constexpr int64_t kRowBlock = int64_t(1) << 15;
+constexpr int64_t kFarRows = int64_t(1) << 22;  // bytes between rows
 
 template <class E>
 int launch_product_e(const Int8Product& whole, bool aligned, void* workspace, void* stream) {
     using T = typename E::T;
     const int64_t cus = device_cu_count();
+    // The other kernels' offsets inside a tile are 32 bits wide.
+    const bool far = (whole.M > 1 && whole.ldx >= kFarRows) || (whole.N > 1 && whole.ldw >= kFarRows);
     for (int64_t n = 0; n < whole.N; n += kMaxChannels) {
         for (int64_t m = 0; m < whole.M; m += kRowBlock) {
             Int8Product p = whole;
@@ -1293,7 +1296,7 @@ int launch_product_e(const Int8Product& whole, bool aligned, void* workspace, vo
             p.ws += n;
             if (p.bias) p.bias = static_cast<const T*>(p.bias) + n;
             p.out = static_cast<T*>(p.out) + m * p.ldo + n;
-            const int e = !aligned || p.ldx >= (1 << 22) || p.ldw >= (1 << 22)
+            const int e = !aligned || far
                               ? launch_generic<E>(p, stream)
                               : launch_form<E>(p, choose_form(p.M, p.N, p.K, cus), workspace, stream);
             if (e != 0) return e;
@@ -1369,7 +1372,7 @@ int launch_quantize_rows(Dtype t, const void* X, int64_t rows, int d, int64_t ld
 }
 
 bool int8_tokens_fit(int64_t M, int N, int K, int64_t ldw) {
-    if (M > kMaxTokens || N > kMaxChannels || ldw >= (1 << 22)) return false;
+    if (M > kMaxTokens || N > kMaxChannels || (N > 1 && ldw >= kFarRows)) return false;
     const int64_t per_row = (K + 511) / 512, steps = (K + kDepth - 1) / kDepth;
     return M * (steps * kDepth + kTokenPad) <= kTokenBytes && M * per_row <= 8 * kItems;
 }

@@ -52,9 +52,10 @@ int check_product(Dtype t, const Int8Product& p) {
     return 1;
 }
 
-// Both operands' rows start at multiples of 16 bytes.
+// Both operands' rows start at multiples of 16 bytes (a single row has no
+// second one to reach, whatever its distance).
 bool product_aligned(const Int8Product& p) {
-    return aligned(p.x, 16) && aligned(p.w, 16) && p.ldx % 16 == 0 && p.ldw % 16 == 0;
+    return aligned(p.x, 16) && aligned(p.w, 16) && (p.M == 1 || p.ldx % 16 == 0) && (p.N == 1 || p.ldw % 16 == 0);
 }
 
 int do_linear_int8(Dtype t, const Int8Product& p, void* workspace, int64_t workspace_bytes, void* stream) {
@@ -327,8 +328,8 @@ int64_t linear_int8_dynamic_workspace_bytes(int64_t M, int32_t N, int32_t K) {
 }
 
 int linear_int8_dynamic_fused(int64_t M, int32_t N, int32_t K, int64_t ldw) {
-    return M >= 1 && M <= kbit::kMaxRows && N >= 1 && K >= 1 && K <= kbit::kMaxInt8Depth && ldw % 16 == 0 &&
-           kbit::int8_tokens_fit(M, N, K, ldw);
+    return M >= 1 && M <= kbit::kMaxRows && N >= 1 && K >= 1 && K <= kbit::kMaxInt8Depth &&
+           (N == 1 || ldw % 16 == 0) && kbit::int8_tokens_fit(M, N, K, ldw);
 }
 
 int64_t qk_norm_rope_backward_workspace_bytes(int32_t D) {
