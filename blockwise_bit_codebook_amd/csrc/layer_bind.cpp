@@ -8,13 +8,19 @@
 // Every function checks all it passes on (the C ABI sees raw addresses):
 // types and shapes raise TypeError and ValueError, a status of the library
 // KbitError.  No C++ exception leaves a function.
+//
+// Nothing is recorded for autograd, but it is not left in the dark: whatever
+// was written counts as modified in place, and a call that cuts a gradient
+// off says so.
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 
+#include <initializer_list>
 #include <sstream>
 #include <string>
 
@@ -132,9 +138,16 @@ struct On {
     }
 };
 
-// f(stream) without the interpreter's lock.
+// A tensor that a call wrote through its address: autograd then refuses a
+// backward pass that saved the old values, as for any in-place operation.
+// (Inference tensors have no version.)
+void written(const Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+// f(stream) without the interpreter's lock; `outputs` are what it writes.
 template <class F>
-void run(const char* name, const Tensor& ref, F f) {
+void run(const char* name, const Tensor& ref, std::initializer_list<const Tensor*> outputs, F f) {
     int status;
     {
         On on(ref);
@@ -143,6 +156,7 @@ void run(const char* name, const Tensor& ref, F f) {
         PyEval_RestoreThread(save);
     }
     if (status != 0) status_error(name, status);
+    for (const Tensor* t : outputs) written(*t);
 }
 
 // The entry point of a type (data arguments are passed as that type).
@@ -232,7 +246,7 @@ PyObject* quantize_rows(PyObject* const* a) {
     if (a[2] == Py_None) scale = at::empty({rows}, X.options().dtype(at::kFloat));
     else vector(a[2], "scale", at::kFloat, rows, X), scale = THPVariable_Unpack(a[2]);
     const int di = fits_int(d, "the number of columns");
-    KBIT_BY_TYPE(X.scalar_type(), quantize_rows_int8, run("quantize_rows_int8", X, [&](void* stream) {
+    KBIT_BY_TYPE(X.scalar_type(), quantize_rows_int8, run("quantize_rows_int8", X, {&codes, &scale}, [&](void* stream) {
         return fn(static_cast<const T*>(X.data_ptr()), rows, di, ldx, static_cast<int8_t*>(codes.data_ptr()), ldc,
                   static_cast<float*>(scale.data_ptr()), stream);
     }))
@@ -284,7 +298,7 @@ PyObject* linear(PyObject* const* a) {  // codes, scale, w_codes, w_scale, bias,
     const Weight w = weight(x, a[2], a[3], a[4], a[6], type, "codes");
     const float* scale = static_cast<const float*>(vector(a[1], "scale", at::kFloat, M, x));
     const Space ws = workspace(linear_int8_workspace_bytes(M, w.N, w.K), a[7], "linear_int8", x);
-    KBIT_BY_TYPE(type, linear_int8, run("linear_int8", x, [&](void* stream) {
+    KBIT_BY_TYPE(type, linear_int8, run("linear_int8", x, {&w.out}, [&](void* stream) {
         return fn(static_cast<const int8_t*>(x.data_ptr()), scale, M, w.K, ldx, w.codes, w.scale, w.N, w.ldw,
                   static_cast<const T*>(w.bias), static_cast<T*>(w.out.data_ptr()), w.ldo, ws.p, ws.bytes, stream);
     }))
@@ -299,7 +313,7 @@ PyObject* linear_dynamic(PyObject* const* a) {  // X, w_codes, w_scale, bias, ou
     if (M == 0) return wrap(w.out);
     const bool fused = reinterpret_cast<uintptr_t>(w.codes) % 16 == 0 && linear_int8_dynamic_fused(M, w.N, w.K, w.ldw);
     const Space ws = workspace(fused ? 0 : linear_int8_dynamic_workspace_bytes(M, w.N, w.K), a[5], "linear_int8_dynamic", x);
-    KBIT_BY_TYPE(type, linear_int8_dynamic, run("linear_int8_dynamic", x, [&](void* stream) {
+    KBIT_BY_TYPE(type, linear_int8_dynamic, run("linear_int8_dynamic", x, {&w.out}, [&](void* stream) {
         return fn(static_cast<const T*>(x.data_ptr()), M, w.K, ldx, w.codes, w.scale, w.N, w.ldw,
                   static_cast<const T*>(w.bias), static_cast<T*>(w.out.data_ptr()), w.ldo, ws.p, ws.bytes, stream);
     }))
@@ -402,7 +416,7 @@ PyObject* rope(PyObject* const* a) {  // x, positions, table, layout, inverse, o
     const View vx = view(x), vo = view(out);
     const int64_t batch = x.dim() == 4 ? x.size(0) : 1, tokens = x.size(-3);
     const int h = fits_int(x.size(-2), "the number of heads"), dim = fits_int(x.size(-1), "the head's size");
-    KBIT_BY_TYPE(x.scalar_type(), rope, run("rope", x, [&](void* stream) {
+    KBIT_BY_TYPE(x.scalar_type(), rope, run("rope", x, {&out}, [&](void* stream) {
         return fn(KBIT_VIEW(const T, vx), KBIT_VIEW(T, vo), batch, tokens, h, dim, t.positions.p, t.positions.bytes,
                   t.table, t.rot, t.max_pos, t.layout, inverse, stream);
     }))
@@ -449,7 +463,7 @@ PyObject* norm_rope(PyObject* const* a) {  // q, k, q_weight, k_weight, position
     const float eps = number(a[6], "eps");
     const Tensor qo = out_like(n.q, a[8], "q_out"), ko = out_like(n.k, a[9], "k_out");
     const View vq = view(n.q), vk = view(n.k), vqo = view(qo), vko = view(ko);
-    KBIT_BY_TYPE(n.q.scalar_type(), qk_norm_rope, run("qk_norm_rope", n.q, [&](void* stream) {
+    KBIT_BY_TYPE(n.q.scalar_type(), qk_norm_rope, run("qk_norm_rope", n.q, {&qo, &ko}, [&](void* stream) {
         return fn(KBIT_VIEW(const T, vq), KBIT_VIEW(const T, vk), KBIT_VIEW(T, vqo), KBIT_VIEW(T, vko), n.batch, n.tokens,
                   n.q_heads, n.k_heads, n.dim, n.qw, n.kw, n.weight_fp32, eps, t.positions.p, t.positions.bytes, t.table,
                   t.rot, t.max_pos, t.layout, stream);
@@ -470,7 +484,7 @@ PyObject* norm_rope_backward(PyObject* const* a) {
     const Tensor dqw = at::empty({n.dim}, n.q.options().dtype(at::kFloat)), dkw = at::empty_like(dqw);
     const Space ws = workspace(qk_norm_rope_backward_workspace_bytes(n.dim), a[12], "qk_norm_rope_backward", n.q);
     const View vgq = view(gq), vgk = view(gk), vq = view(n.q), vk = view(n.k), vdq = view(dq), vdk = view(dk);
-    KBIT_BY_TYPE(n.q.scalar_type(), qk_norm_rope_backward, run("qk_norm_rope_backward", n.q, [&](void* stream) {
+    KBIT_BY_TYPE(n.q.scalar_type(), qk_norm_rope_backward, run("qk_norm_rope_backward", n.q, {&dq, &dk}, [&](void* stream) {
         return fn(KBIT_VIEW(const T, vgq), KBIT_VIEW(const T, vgk), KBIT_VIEW(const T, vq), KBIT_VIEW(const T, vk),
                   KBIT_VIEW(T, vdq), KBIT_VIEW(T, vdk), n.batch, n.tokens, n.q_heads, n.k_heads, n.dim, n.qw, n.kw,
                   n.weight_fp32, static_cast<float*>(dqw.data_ptr()), static_cast<float*>(dkw.data_ptr()), eps,
@@ -499,7 +513,7 @@ PyObject* append(PyObject* const* a) {  // k, v, slots, k_cache, v_cache, positi
     const int h = fits_int(k.size(1), "the number of heads"), dim = fits_int(k.size(2), "the head's size"),
               v_dim = fits_int(v.size(2), "the head's size"), page = fits_int(kc.size(1), "page_size");
     const View vk = view(k), vv = view(v), ck = view(kc), cv = view(vc);
-    KBIT_BY_TYPE(k.scalar_type(), append_kv_paged, run("append_kv_paged", k, [&](void* stream) {
+    KBIT_BY_TYPE(k.scalar_type(), append_kv_paged, run("append_kv_paged", k, {&kc, &vc}, [&](void* stream) {
         return fn(static_cast<const T*>(vk.p), vk.token, vk.head, static_cast<const T*>(vv.p), vv.token, vv.head,
                   k.size(0), h, dim, v_dim, slots.p, slots.bytes, KBIT_VIEW(T, ck), KBIT_VIEW(T, cv), kc.size(0), page,
                   t.positions.p, t.positions.bytes, t.table, t.rot, t.max_pos, t.layout, stream);
@@ -510,6 +524,15 @@ PyObject* append(PyObject* const* a) {  // k, v, slots, k_cache, v_cache, positi
 // ---------------------------------------------------------------------------
 // module
 // ---------------------------------------------------------------------------
+// Whether autograd expects a gradient through one of the arguments.
+bool gradient_wanted(PyObject* const* args, int n) {
+    if (!c10::GradMode::is_enabled()) return false;
+    auto* tensors = reinterpret_cast<PyTypeObject*>(THPVariableClass);
+    for (int i = 0; i < n; ++i)
+        if (PyType_IsSubtype(Py_TYPE(args[i]), tensors) && THPVariable_Unpack(args[i]).requires_grad()) return true;
+    return false;
+}
+
 template <PyObject* (*F)(PyObject* const*), int kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (n != kArgs) {
@@ -517,6 +540,14 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
         return nullptr;
     }
     try {
+        // 2: the line that called the function of layer.py
+        if (gradient_wanted(args, kArgs) &&
+            PyErr_WarnEx(PyExc_UserWarning,
+                         "an argument requires a gradient, but nothing is recorded for autograd: the outputs are cut off "
+                         "from it (call this under torch.no_grad(), or in a torch.autograd.Function with the gradient's "
+                         "own call)",
+                         2) != 0)
+            return nullptr;
         return F(args);
     } catch (const Raise& r) {
         if (r.type != nullptr) PyErr_SetString(r.type, r.text.c_str());

@@ -10,6 +10,8 @@ may be strided; the last axis has to be contiguous where it is a row of codes,
 of a matrix or of a head.  Nothing is recorded for autograd: gradients are
 calls of their own (``rope(..., inverse=True)``, ``qk_norm_rope_backward``), to
 be put into a ``torch.autograd.Function`` where a model is trained that way.
+An argument that requires a gradient while gradients are recorded gives a
+UserWarning, and given outputs count as modified in place.
 If ``_layer`` was not built the import raises: there is no other path.
 """
 
@@ -101,6 +103,8 @@ def rope_table(freq, max_pos, amplitude=1.0, device="cuda", out=None):
     with torch.cuda.device(f.device):
         _check("rope_table", _lib.rope_table(f.data_ptr(), rot, max_pos, amplitude, out.data_ptr(),
                                              torch.cuda.current_stream(f.device).cuda_stream))
+    if not out.is_inference():
+        torch.autograd.graph.increment_version(out)
     return out
 
 
