@@ -112,6 +112,15 @@ void* vector(PyObject* o, const char* what, at::ScalarType type, int64_t count, 
     return t.data_ptr();
 }
 
+// One value for each of the channels, no more: a longer vector belongs to
+// another layer.
+void* channel_vector(PyObject* o, const char* what, at::ScalarType type, int64_t channels, const Tensor& ref) {
+    void* p = vector(o, what, type, channels, ref);
+    const int64_t n = THPVariable_Unpack(o).numel();
+    if (n != channels) value_error(cat(what, ": ", n, " elements for ", channels, " channels"));
+    return p;
+}
+
 int fits_int(int64_t n, const char* what) {
     if (n < 0 || n > INT32_MAX) value_error(cat(what, " is out of range"));
     return static_cast<int>(n);
@@ -275,8 +284,8 @@ Weight weight(const Tensor& x, PyObject* codes, PyObject* scale, PyObject* bias,
     w.N = fits_int(N, "the number of output channels");
     w.K = fits_int(K, "the depth");
     w.codes = static_cast<const int8_t*>(c.data_ptr());
-    w.scale = static_cast<const float*>(vector(scale, "w_scale", at::kFloat, N, x));
-    w.bias = bias == Py_None ? nullptr : vector(bias, "bias", type, N, x);
+    w.scale = static_cast<const float*>(channel_vector(scale, "w_scale", at::kFloat, N, x));
+    w.bias = bias == Py_None ? nullptr : channel_vector(bias, "bias", type, N, x);
     if (out == Py_None) {
         w.out = at::empty({M, N}, x.options().dtype(type));
         w.ldo = N;

@@ -54,8 +54,9 @@ def quantize_rows_int8(X, codes=None, scale=None):
 def linear_int8(codes, scale, w_codes, w_scale, bias=None, dtype=torch.bfloat16, out=None, workspace=None):
     """out[M, N] = (codes[M, K] @ w_codes[N, K]^T) * scale[:, None] * w_scale + bias.
 
-    codes, w_codes: int8, exact sums; scale, w_scale: fp32, one a row; bias: N
-    values of ``dtype`` (fp32/fp16/bf16), the output's type.  The workspace
+    codes, w_codes: int8, exact sums; scale: fp32, one a row (it may be longer,
+    like the one ``quantize_rows_int8`` was given); w_scale: N fp32 values;
+    bias: N values of ``dtype`` (fp32/fp16/bf16), the output's type.  The workspace
     (uint8, ``linear_int8_workspace_bytes``) is allocated here unless given."""
     return _layer.linear_int8(codes, scale, w_codes, w_scale, bias, dtype, out, workspace)
 
