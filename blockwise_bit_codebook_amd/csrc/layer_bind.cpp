@@ -20,9 +20,11 @@
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <sstream>
 #include <string>
+#include <utility>
 
 #include "kbit.h"
 #include "kbit_layer.h"
@@ -124,6 +126,93 @@ void* channel_vector(PyObject* o, const char* what, at::ScalarType type, int64_t
 int fits_int(int64_t n, const char* what) {
     if (n < 0 || n > INT32_MAX) value_error(cat(what, " is out of range"));
     return static_cast<int>(n);
+}
+
+// ---------------------------------------------------------------------------
+// outputs that overlap
+// ---------------------------------------------------------------------------
+// Rows of `length` neighbouring elements, counted by up to three axes (strides
+// are not negative).
+struct Rows {
+    int64_t size[3], stride[3], length, last;  // last: the last row's first element
+};
+
+Rows rows_in(const Tensor& t) {
+    Rows r{{1, 1, 1}, {0, 0, 0}, t.size(-1), 0};
+    for (int64_t i = 0; i + 1 < t.dim(); ++i) {
+        r.size[i] = t.size(i);
+        r.stride[i] = t.size(i) > 1 ? t.stride(i) : 0;
+        r.last += (r.size[i] - 1) * r.stride[i];
+    }
+    return r;
+}
+
+// Steps lo .. hi of one stride; `reach`: how far the axes after it go down and up.
+struct Axis {
+    int64_t stride, lo, hi, down, up;
+};
+
+// Whether steps along the axes (largest stride first) take v to a value in
+// (low, high).  `moved`: some step was not zero, which is asked for.  Each axis
+// leaves one or two candidates where the strides are nested, as those of views
+// are; `budget` ends the search in any other layout, which then counts as apart.
+bool reaches(int64_t v, const Axis* a, int n, int64_t low, int64_t high, bool moved, int& budget) {
+    if (n == 0) return moved && v > low && v < high;
+    if (--budget < 0) return false;
+    const int64_t from = low - a->up - v, to = high - a->down - v;  // of stride * step, both ends open
+    int64_t lo = a->lo, hi = a->hi;
+    if (a->stride == 0) {
+        if (from >= 0 || to <= 0) return false;
+    } else {
+        const auto below = [](int64_t x, int64_t s) { return x >= 0 ? x / s : -((-x + s - 1) / s); };  // floor(x / s)
+        lo = std::max(lo, below(from, a->stride) + 1);
+        hi = std::min(hi, -below(-to, a->stride) - 1);
+    }
+    for (int64_t d = lo; d <= hi && budget >= 0; ++d)
+        if (reaches(v + d * a->stride, a + 1, n - 1, low, high, moved || d != 0, budget)) return true;
+    return false;
+}
+
+// Whether a row of x and a row of y, whose first elements are `apart` elements
+// apart, have an element in common; with `self` two different rows of x.
+bool rows_meet(const Rows& x, const Rows& y, int64_t apart, bool self) {
+    if (apart + y.last + y.length <= 0 || apart >= x.last + x.length) return false;
+    Axis axes[6];
+    int n = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t sx = x.size[i] > 1 ? x.stride[i] : y.stride[i], sy = y.size[i] > 1 ? y.stride[i] : sx;
+        if (sx == sy) {
+            if (x.size[i] > 1 || y.size[i] > 1) axes[n++] = Axis{sx, 1 - x.size[i], y.size[i] - 1, 0, 0};
+        } else {
+            axes[n++] = Axis{sx, 1 - x.size[i], 0, 0, 0};
+            axes[n++] = Axis{sy, 0, y.size[i] - 1, 0, 0};
+        }
+    }
+    std::sort(axes, axes + n, [](const Axis& a, const Axis& b) { return a.stride > b.stride; });
+    for (int i = n - 1; i > 0; --i) {
+        axes[i - 1].down = axes[i].down + axes[i].lo * axes[i].stride;
+        axes[i - 1].up = axes[i].up + axes[i].hi * axes[i].stride;
+    }
+    int budget = 4096;
+    return reaches(apart, axes, n, -y.length, x.length, !self, budget);
+}
+
+// Refuses an output two rows of which share elements.
+void no_overlap(const Tensor& out, const char* what) {
+    if (out.numel() == 0 || out.is_non_overlapping_and_dense()) return;
+    const Rows r = rows_in(out);
+    if (rows_meet(r, r, 0, true)) value_error(cat(what, ": elements overlap"));
+}
+
+// Refuses an output that shares elements with another tensor of its type, but
+// for `same`: the very same view, each row of which is read before it is written.
+void no_overlap(const Tensor& out, const char* what, const Tensor& other, const char* name, bool same) {
+    if (!out.is_alias_of(other) || out.numel() == 0 || other.numel() == 0) return;
+    const int64_t bytes = static_cast<char*>(other.data_ptr()) - static_cast<char*>(out.data_ptr());
+    if (same && bytes == 0 && out.sizes() == other.sizes() && out.strides() == other.strides()) return;
+    const int64_t size = static_cast<int64_t>(out.element_size());
+    if (bytes % size != 0 || rows_meet(rows_in(out), rows_in(other), bytes / size, false))
+        value_error(cat(what, " overlaps ", name));
 }
 
 // ---------------------------------------------------------------------------
@@ -319,6 +408,7 @@ PyObject* linear_dynamic(PyObject* const* a) {  // X, w_codes, w_scale, bias, ou
     const at::ScalarType type = x.scalar_type();
     const int64_t ldx = rows_of(x, "X", is_float(type), kFloats), M = x.size(0);
     const Weight w = weight(x, a[1], a[2], a[3], a[4], type, "X");
+    no_overlap(w.out, "out", x, "X", false);
     if (M == 0) return wrap(w.out);
     const bool fused = reinterpret_cast<uintptr_t>(w.codes) % 16 == 0 && linear_int8_dynamic_fused(M, w.N, w.K, w.ldw);
     const Space ws = workspace(fused ? 0 : linear_int8_dynamic_workspace_bytes(M, w.N, w.K), a[5], "linear_int8_dynamic", x);
@@ -356,8 +446,9 @@ const Tensor& heads(PyObject* o, const char* what, const Tensor* like) {
     return t;
 }
 
-// An output shaped like x: new, in x's layout where that is dense, or given.
-Tensor out_like(const Tensor& x, PyObject* given, const char* what) {
+// An output shaped like x: new, in x's layout where that is dense, or given
+// (it may be x).
+Tensor out_like(const Tensor& x, PyObject* given, const char* what, const char* name) {
     if (given == Py_None) {
         Tensor out = at::empty_like(x);
         if (out.size(-1) > 1 && out.stride(-1) != 1) out = at::empty(x.sizes(), x.options());
@@ -365,8 +456,8 @@ Tensor out_like(const Tensor& x, PyObject* given, const char* what) {
     }
     const Tensor& out = heads(given, what, &x);
     same_shape(out, what, x.sizes());
-    for (int64_t i = 0; i < out.dim(); ++i)
-        if (out.size(i) > 1 && out.stride(i) == 0) value_error(cat(what, ": elements overlap"));
+    no_overlap(out, what);
+    no_overlap(out, what, x, name, true);
     return out;
 }
 
@@ -421,7 +512,7 @@ PyObject* rope(PyObject* const* a) {  // x, positions, table, layout, inverse, o
     const Turn t = turn(a[1], a[2], a[3], x);
     const int inverse = PyObject_IsTrue(a[4]);
     if (inverse < 0) throw Raise{nullptr, ""};
-    const Tensor out = out_like(x, a[5], "out");
+    const Tensor out = out_like(x, a[5], "out", "x");
     const View vx = view(x), vo = view(out);
     const int64_t batch = x.dim() == 4 ? x.size(0) : 1, tokens = x.size(-3);
     const int h = fits_int(x.size(-2), "the number of heads"), dim = fits_int(x.size(-1), "the head's size");
@@ -470,7 +561,10 @@ PyObject* norm_rope(PyObject* const* a) {  // q, k, q_weight, k_weight, position
     const Norm n = norm_inputs(a[0], a[1], a[2], a[3]);
     const Turn t = turn(a[4], a[5], a[7], n.q);
     const float eps = number(a[6], "eps");
-    const Tensor qo = out_like(n.q, a[8], "q_out"), ko = out_like(n.k, a[9], "k_out");
+    const Tensor qo = out_like(n.q, a[8], "q_out", "q"), ko = out_like(n.k, a[9], "k_out", "k");
+    no_overlap(qo, "q_out", n.k, "k", false);
+    no_overlap(ko, "k_out", n.q, "q", false);
+    no_overlap(qo, "q_out", ko, "k_out", false);
     const View vq = view(n.q), vk = view(n.k), vqo = view(qo), vko = view(ko);
     KBIT_BY_TYPE(n.q.scalar_type(), qk_norm_rope, run("qk_norm_rope", n.q, {&qo, &ko}, [&](void* stream) {
         return fn(KBIT_VIEW(const T, vq), KBIT_VIEW(const T, vk), KBIT_VIEW(T, vqo), KBIT_VIEW(T, vko), n.batch, n.tokens,
@@ -489,7 +583,13 @@ PyObject* norm_rope_backward(PyObject* const* a) {
     const Tensor& gk = heads(a[1], "dk_out", &n.q);
     same_shape(gq, "dq_out", n.q.sizes());
     same_shape(gk, "dk_out", n.k.sizes());
-    const Tensor dq = out_like(n.q, a[10], "dq"), dk = out_like(n.k, a[11], "dk");
+    const Tensor dq = out_like(n.q, a[10], "dq", "q"), dk = out_like(n.k, a[11], "dk", "k");
+    no_overlap(dq, "dq", gq, "dq_out", true);
+    no_overlap(dk, "dk", gk, "dk_out", true);
+    for (const auto& [t, name] : {std::pair<const Tensor&, const char*>{n.k, "k"}, {gk, "dk_out"}, {dk, "dk"}})
+        no_overlap(dq, "dq", t, name, false);
+    no_overlap(dk, "dk", n.q, "q", false);
+    no_overlap(dk, "dk", gq, "dq_out", false);
     const Tensor dqw = at::empty({n.dim}, n.q.options().dtype(at::kFloat)), dkw = at::empty_like(dqw);
     const Space ws = workspace(qk_norm_rope_backward_workspace_bytes(n.dim), a[12], "qk_norm_rope_backward", n.q);
     const View vgq = view(gq), vgk = view(gk), vq = view(n.q), vk = view(n.k), vdq = view(dq), vdk = view(dk);

@@ -7,7 +7,9 @@ the C entry points (``include/kbit_layer.h``) are in ``_layer``
 (``csrc/layer_bind.cpp``), whose host time is a fraction of what they cost
 here.  Calls run on torch's current stream of the inputs' device.  Tensors
 may be strided; the last axis has to be contiguous where it is a row of codes,
-of a matrix or of a head.  Nothing is recorded for autograd: gradients are
+of a matrix or of a head.  A given output may be the input where that is said;
+one that overlaps itself or another operand's heads or rows is refused (the
+caches of ``append_kv_paged`` apart, whose slots are the caller's).  Nothing is recorded for autograd: gradients are
 calls of their own (``rope(..., inverse=True)``, ``qk_norm_rope_backward``), to
 be put into a ``torch.autograd.Function`` where a model is trained that way.
 An argument that requires a gradient while gradients are recorded gives a

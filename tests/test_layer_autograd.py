@@ -66,7 +66,7 @@ def test_written_tensors_count_as_modified():
             assert (t._version > v) == any(t is o for o in written), i
     before = h._version  # a refused call writes nothing
     with pytest.raises(kb.KbitError):
-        kb.qk_norm_rope(h, h, w, w, pos, table, eps=-1.0, q_out=h, k_out=h)
+        kb.qk_norm_rope(h, k, w, w, pos, table, eps=-1.0, q_out=h, k_out=k)
     assert h._version == before
     with torch.inference_mode():
         inside = torch.randn(6, 2, 64, device=dev)
