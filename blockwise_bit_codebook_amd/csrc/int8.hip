@@ -10,6 +10,7 @@
 //   product  acc[m][n] = sum over k of x[m][k] * w[n][k], exact in int32,
 //            out = RN_T(RN(RN(RN(acc) * xs[m]) * ws[n]) + bias[n]).
 #include "device.h"
+#include "int8_choice.h"
 #include "kbit_internal.h"
 #include "launch.h"
 #include "layer_internal.h"
@@ -313,7 +314,7 @@ __global__ __launch_bounds__(kThreads) void int8_generic_kernel(const Int8Produc
 // ---------------------------------------------------------------------------
 // What the two product kernels share
 // ---------------------------------------------------------------------------
-// Operands reach the matrix cores through LDS, 128 codes of a row a step: one
+// Operands reach the matrix cores through LDS, kDepth = 128 codes of a row a step: one
 // cache line, and all banks of the LDS.  A lane needs 16 codes of row
 // lane % 16, so reading them from memory directly would touch 16 rows with
 // every 16 lanes (measured: 38 GB/s a CU against 115 for whole lines).  The
@@ -325,8 +326,6 @@ __global__ __launch_bounds__(kThreads) void int8_generic_kernel(const Int8Produc
 // The weight is the first matrix operand, so that lane l holds channels
 // 4 (l / 16) .. + 3 of row l % 16; channel 4 TN (i / 4) + 4 j + i % 4 sits in
 // row i of operand j, which makes a lane's 4 TN channels neighbours.
-constexpr int kDepth = 128;
-
 template <int TN>
 __device__ __forceinline__ int operand_channel(int j, int i) {
     return 4 * TN * (i >> 2) + 4 * j + (i & 3);
@@ -532,13 +531,7 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_few_rows_kernel(const Int8P
 // bf16, weights from memory, two launches and one: 1 x 4096 x 4096 9.6 and 6.5
 // us (2.6 TB/s; its 16.8 MB alone would take 3.2 us), 1 x 32000 x 4096 35.1 and
 // 32.4 (4.0 TB/s), 8 x 4096 x 2048 8.4 and 7.4, but 4 x 11008 x 4096 15.9 and
-// 16.3.  A wave takes 512 values of a row at a time, at most kItems times.
-constexpr int kItems = 4;
-constexpr int kTokenBytes = 28 * 1024;  // of codes, rows kTokenPad apart from whole steps
-constexpr int kTokenPad = 16;
-constexpr int kMaxTokens = 8;
-constexpr int64_t kMaxChannels = int64_t(1) << 20;  // a launch
-
+// 16.3.
 template <class E, int TN, int WAVES, bool VEC>
 __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Product p,
                                                                    const typename E::T* __restrict__ X, int64_t ldX,
@@ -1091,17 +1084,6 @@ int launch_tile(const Int8Product& p, void* stream) {
     return static_cast<int>(hipGetLastError());
 }
 
-constexpr int kSplitTile = 128;
-
-// Sums of one part: rows of whole 16-byte pieces.
-int64_t sums_ld(int N) { return (static_cast<int64_t>(N) + 3) / 4 * 4; }
-
-// Depth of a part: whole pairs of steps.
-int split_depth(int K, int parts) {
-    const int pairs = (K + 2 * kDepth - 1) / (2 * kDepth);
-    return (pairs + parts - 1) / parts * 2 * kDepth;
-}
-
 // Tiles of 128 x 128 with the depth in parts (as many as split_depth leaves).
 template <class E>
 int launch_split(const Int8Product& p, int parts, void* workspace, void* stream) {
@@ -1134,104 +1116,6 @@ int launch_generic(const Int8Product& p, void* stream) {
     else
         hipLaunchKernelGGL((int8_generic_kernel<E, 2>), grid(64), dim3(kThreads), 0, static_cast<hipStream_t>(stream), p);
     return static_cast<int>(hipGetLastError());
-}
-
-// Which kernel and tile: the least of estimated times, in microseconds.  The
-// estimates were fitted to 2100 measurements, every variant at 130 shapes
-// spread over M = 1 .. 8192 and N, K = 64 .. 16384 with operands from memory
-// and from cache: what the rule picked was 0.7% slower than the fastest variant
-// on average, 11% at most.  (Since then few rows join 1 us faster, the ends of
-// 256 x 256 rounds and partial steps 1 to 3 us; measured again over 140 shapes
-// the rule is within 4% on average, 23% at most.)  Both sides of it, as fitted
-// (operands from memory): 77 x 11008 x 4096 18.3 us in 80 x 48 and 19.7 us in 80 x 64 pieces of
-// few rows, 26.7 in tiles of 32 x 128; 112 x 11008 x 4096 20.6 in 112 x 48 pieces,
-// 25.5 in 80 x 48 and 29.4 in tiles; 500 x 4099 x 3840 27.1 in tiles of 64 x
-// 128, 27.3 in 32 x 128, 30.1 in 80 x 64 pieces, 31.7 in 128 x 128; 4096 x 4096 x
-// 4096 58.8 in 256 x 256, 71.5 in 128 x 128.
-struct Int8Few {
-    int mt, tn;
-};
-struct Int8Tile {
-    int bm, bn;
-    // us: a launch, a step alone, a step a round, a round, a partial step, 10
-    // MB of operands; the weight of whole rounds against parts of one
-    double base, least, step, round, tail, operands, whole;
-};
-constexpr Int8Few kFew[] = {{1, 1}, {1, 2}, {1, 3}, {1, 4}, {2, 2}, {2, 4}, {3, 2}, {3, 4}, {4, 4},
-                             {5, 3}, {5, 4}, {7, 3}, {8, 3}};
-constexpr Int8Tile kTiles[] = {{32, 128, 0.84, 0.497, 0.253, 1.08, 2.32, 1.29, 0.255},
-                               {64, 128, 0.0, 0.572, 0.382, 1.85, 3.01, 1.07, 0.454},
-                               {128, 128, 0.0, 0.799, 0.544, 2.70, 3.31, 0.11, 0.742},
-                               {256, 256, 0.0, 1.189, 1.386, 7.47, 2.93, 0.83, 1.0}};
-
-// Parts of the depth, in 128 x 128: where the tiles alone leave compute units
-// idle or half a round empty and the depth is long.  us: the second launch, and
-// 10 MB of the parts' sums.  Measured on 70 shapes with 32, 64, 128 and 256
-// rows: 128 alone gives what all of them give within 1%.  Without and with parts
-// (operands from memory): 512 x 4096 x 11008 54.2 and 45.1 us in 4, 1024 x 2048 x
-// 8192 51.5 and 34.1 in 4, 562 x 2432 x 11776 51.5 and 35.2 in 4, but 256 x 4096 x
-// 4096 15.3 and 20.0, 1024 x 1024 x 4096 13.3 and 18.1.  At most as many workgroups
-// as are resident at once, two a compute unit: 4778 x 857 x 13738 would take 126 us
-// without and 146 in 2 parts (532 workgroups).
-constexpr int kParts[] = {2, 3, 4, 8};
-constexpr double kPartsLaunch = 4.5, kPartsSums = 1.5;
-
-struct Int8Choice {
-    Int8Few few;  // or
-    int bm;       // tiles of bm rows, where not 0
-    int parts;    // of the depth; 1: no split
-};
-
-// Workgroups a compute unit: a part of a round is cheaper than a whole one
-// where several workgroups fit a compute unit (whole < 1).
-int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
-double rounds_of(int64_t tiles, int64_t cus, double whole) {
-    const double r = whole * static_cast<double>((tiles + cus - 1) / cus) + (1.0 - whole) * tiles / cus;
-    return r < 1.0 ? 1.0 : r;
-}
-
-Int8Choice choose_form(int64_t M, int N, int K, int64_t cus) {
-    Int8Choice best{};
-    double least = 1e30;
-    const double operands = 1e-7 * (static_cast<double>(M) + N) * K;
-    for (const Int8Few& f : kFew) {
-        if (f.mt > 5 && M > 16 * f.mt) continue;  // made to read the weights once
-        const double us = 1.34 + 0.68 * operands +
-                          rounds_of(tiles_of(M, N, 16 * f.mt, 16 * f.tn), cus, 1.0) *
-                              (1.783 + 0.204 * f.mt * f.tn + 1.297e-5 * 16.0 * (f.mt + f.tn) * K +
-                               (K % kDepth ? 0.286 * (f.mt + f.tn) : 0.0));
-        if (us < least) {
-            least = us;
-            best = Int8Choice{f, 0, 1};
-        }
-    }
-    const int rest = K % (2 * kDepth);
-    const double steps = K / (2 * kDepth) * 2 + (rest > 0 ? 1 : 0) + (rest > kDepth ? 1 : 0);
-    for (const Int8Tile& t : kTiles) {
-        if (M < t.bm || N < t.bn) continue;
-        const int64_t tiles = tiles_of(M, N, t.bm, t.bn);
-        const double r = rounds_of(tiles, cus, t.whole);
-        const double us = t.base + (t.step * r > t.least ? t.step * r : t.least) * steps + t.round * r +
-                          (K % kDepth ? t.tail : 0.0) + t.operands * operands;
-        if (us < least) {
-            least = us;
-            best = Int8Choice{{}, t.bm, 1};
-        }
-        if (t.bm != kSplitTile) continue;
-        for (const int n : kParts) {
-            const int depth = split_depth(K, n), parts = (K + depth - 1) / depth;
-            if (parts < 2 || tiles * parts > 2 * cus) continue;
-            const double rp = rounds_of(tiles * parts, cus, t.whole);
-            const double split = t.base + (t.step * rp > t.least ? t.step * rp : t.least) * (depth / kDepth) +
-                                 t.round * rp + t.operands * operands + kPartsLaunch +
-                                 kPartsSums * 4e-7 * static_cast<double>(parts) * M * N;
-            if (split < 0.95 * least) {  // it takes memory
-                least = split;
-                best = Int8Choice{{}, t.bm, parts};
-            }
-        }
-    }
-    return best;
 }
 
 // The waves that split the depth: as many as their operands fit into LDS, but
@@ -1273,11 +1157,6 @@ int launch_form(const Int8Product& p, const Int8Choice& c, void* workspace, void
                ? launch_tile<E, 2, 4, 8, true>(p, stream)
                : launch_tile<E, 2, 4, 8, false>(p, stream);
 }
-
-// Blocks of rows and channels keep the grids (below 2^32 threads) and the
-// kernels' 32-bit offsets in range.
-constexpr int64_t kRowBlock = int64_t(1) << 15;
-constexpr int64_t kFarRows = int64_t(1) << 22;  // bytes between rows
 
 template <class E>
 int launch_product_e(const Int8Product& whole, bool aligned, void* workspace, void* stream) {
@@ -1371,32 +1250,12 @@ int launch_quantize_rows(Dtype t, const void* X, int64_t rows, int d, int64_t ld
     }
 }
 
-bool int8_tokens_fit(int64_t M, int N, int K, int64_t ldw) {
-    if (M > kMaxTokens || N > kMaxChannels || (N > 1 && ldw >= kFarRows)) return false;
-    const int64_t per_row = (K + 511) / 512, steps = (K + kDepth - 1) / kDepth;
-    return M * (steps * kDepth + kTokenPad) <= kTokenBytes && M * per_row <= 8 * kItems;
-}
-
 int launch_int8_tokens(Dtype t, const Int8Product& p, const void* X, int64_t ldX, bool vec, void* stream) {
     switch (t) {
         case Dtype::fp32: return launch_tokens_e<QF32>(p, X, ldX, vec, stream);
         case Dtype::fp16: return launch_tokens_e<QF16>(p, X, ldX, vec, stream);
         default: return launch_tokens_e<QB16>(p, X, ldX, vec, stream);
     }
-}
-
-int64_t int8_product_workspace(int64_t M, int N, int K) {
-    const int64_t cus = device_cu_count();
-    int64_t most = 0;
-    // the blocks' sizes: whole ones and what is left
-    for (const int64_t m : {M < kRowBlock ? M : kRowBlock, M % kRowBlock})
-        for (const int64_t n : {N < kMaxChannels ? N : kMaxChannels, N % kMaxChannels}) {
-            if (m == 0 || n == 0) continue;
-            const Int8Choice c = choose_form(m, static_cast<int>(n), K, cus);
-            const int64_t need = c.parts > 1 ? c.parts * m * sums_ld(static_cast<int>(n)) * 4 : 0;
-            if (need > most) most = need;
-        }
-    return most;
 }
 
 int launch_int8_product(Dtype t, const Int8Product& p, bool aligned, void* workspace, void* stream) {

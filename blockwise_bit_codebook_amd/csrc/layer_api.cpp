@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "int8_choice.h"
 #include "kbit.h"
 #include "kbit_layer.h"
 #include "layer_internal.h"

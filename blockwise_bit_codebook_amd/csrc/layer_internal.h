@@ -93,12 +93,10 @@ struct Int8Product {
 // aligned: both operands' rows start at multiples of 16 bytes.  workspace: of
 // int8_product_workspace bytes on the current device, 16-byte aligned.
 int launch_int8_product(Dtype t, const Int8Product& p, bool aligned, void* workspace, void* stream);
-int64_t int8_product_workspace(int64_t M, int N, int K);
 
-// A few tokens quantized inside the product's kernel (the weights' rows start
-// at multiples of 16 bytes): whether they fit, and the launch (p.x and p.xs
-// are not looked at).
-bool int8_tokens_fit(int64_t M, int N, int K, int64_t ldw);
+// A few tokens quantized inside the product's kernel, where int8_tokens_fit
+// (the weights' rows start at multiples of 16 bytes; p.x and p.xs are not
+// looked at).
 int launch_int8_tokens(Dtype t, const Int8Product& p, const void* X, int64_t ldX, bool vec, void* stream);
 
 }  // namespace kbit

@@ -1,6 +1,7 @@
 // Stands in for the HIP launchers behind csrc/layer_api.cpp: each records what
 // it was given, so that a test sees on the host which way an entry point sends
 // a call.  Nothing is dereferenced.
+#include "int8_choice.h"
 #include "layer_internal.h"
 
 namespace kbit {
@@ -22,12 +23,20 @@ int launch_int8_product(Dtype, const Int8Product& p, bool aligned, void*, void*)
     ++product_launches;
     return 0;
 }
-int64_t int8_product_workspace(int64_t, int, int) { return 0; }
-bool int8_tokens_fit(int64_t, int, int, int64_t) { return true; }
 int launch_int8_tokens(Dtype, const Int8Product&, const void*, int64_t, bool, void*) { return 0; }
 }  // namespace kbit
 
 extern "C" {
 int stub_product_launches() { return kbit::product_launches; }
 int stub_product_on_fast_path() { return kbit::product_on_fast_path; }
+
+// The form of a product on `cus` compute units: rows of the tile, or 0 and the
+// pieces of few rows in 16 x 16; parts of the depth.
+void stub_form(int64_t M, int N, int K, int64_t cus, int* bm, int* mt, int* tn, int* parts) {
+    const kbit::Int8Choice c = kbit::choose_form(M, N, K, cus);
+    *bm = c.bm;
+    *mt = c.few.mt;
+    *tn = c.few.tn;
+    *parts = c.parts;
+}
 }

@@ -9,7 +9,7 @@ import subprocess
 import pytest
 
 kb = pytest.importorskip("blockwise_bit_codebook_amd")
-from blockwise_bit_codebook_amd import _lib as L  # noqa: E402
+pytest.importorskip("torch")
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "blockwise_bit_codebook_amd", "csrc")
@@ -23,6 +23,7 @@ def stub(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
                     os.path.join(CSRC, "layer_api.cpp"), os.path.join(ROOT, "tests", "host", "layer_stub.cpp"), "-o", so],
                    check=True)
+    from blockwise_bit_codebook_amd import _lib as L
     lib = ct.CDLL(so)
     for name, args in L.LAYER_SIGNATURES:
         getattr(lib, name).argtypes = args
