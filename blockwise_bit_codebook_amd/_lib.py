@@ -5,7 +5,9 @@ module raises, so no caller can silently fall back to another path.
 """
 
 import ctypes as ct
+import importlib.util
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkbit.so")
@@ -89,11 +91,30 @@ def _layer_signatures():
 LAYER_SIGNATURES = _layer_signatures()
 
 
+def _share_torch_runtime():
+    """torch ships a HIP runtime of its own.  Loaded first it serves libkbit.so
+    too, which asks for the same soname; the other way round the process would
+    hold two runtimes, and the second to touch the GPU fails.  So where torch is
+    installed and not imported yet, its runtime (not torch) is loaded here."""
+    if "torch" in sys.modules:
+        return
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return
+    path = os.path.join(os.path.dirname(spec.origin), "lib", "libamdhip64.so")
+    if os.path.exists(path):
+        try:
+            ct.CDLL(path)
+        except OSError:
+            pass  # a torch that cannot be imported here either
+
+
 def load(path=LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
             f"libkbit.so not found at {path}; build it with "
             "`python -m blockwise_bit_codebook_amd.build` (hipcc, gfx950)")
+    _share_torch_runtime()
     lib = ct.CDLL(path)
     for name, args in SIGNATURES + LAYER_SIGNATURES:
         fn = getattr(lib, name)
