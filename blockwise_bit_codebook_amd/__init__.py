@@ -18,7 +18,9 @@ block (uint8 tensor).
 """
 
 import ctypes as ct
+import importlib.util
 import operator
+import os
 
 import numpy as np
 
@@ -479,10 +481,19 @@ def _install_named():
 _install_named()
 
 # The operators around a quantized layer need torch at import; they are bound
-# on first use, so that the host-only functions stay usable without it.
+# on first use, so that the host-only functions stay usable without it.  "import
+# *" binds every name of __all__ at once: they are in it where they can be.
 _LAYER = ("quantize_rows_int8", "linear_int8", "linear_int8_dynamic", "rope_frequencies", "rope_table", "rope",
           "qk_norm_rope", "qk_norm_rope_backward", "append_kv_paged")
-__all__ += _LAYER
+
+
+def _layer_usable():
+    return (importlib.util.find_spec("torch") is not None
+            and os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_layer.so")))
+
+
+if _layer_usable():
+    __all__ += _LAYER
 
 
 def __getattr__(name):
