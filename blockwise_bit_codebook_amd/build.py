@@ -6,8 +6,9 @@ HIP translation units are compiled for gfx950 only, with IEEE binary32
 division and square root, no contraction of multiply-add, denormals kept and
 packed fp32 instructions disabled; host-only C++ files are compiled as plain
 C++.  Objects go to ``_build/`` next to the package; the shared library
-lands in the package directory, and beside it _layer.so, the torch binding of
-the layer operators (plain C++ against torch's headers).
+lands in the package directory, and beside it, where torch is installed,
+_layer.so, the torch binding of the layer operators (plain C++ against torch's
+headers).
 """
 
 import argparse
@@ -111,8 +112,14 @@ def build(verbose=False, jobs=None):
 
 
 def _build_binding(verbose):
-    """_layer.so: csrc/layer_bind.cpp against torch's and Python's headers."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """_layer.so: csrc/layer_bind.cpp against torch's and Python's headers.
+    Without torch there is nothing to bind to: libkbit.so alone serves the C
+    ABI and the host-only functions."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        print("torch is not installed: _layer.so, its binding of the layer operators, is not built", flush=True)
+        return
+    torch = os.path.dirname(spec.origin)
     include = os.path.join(torch, "include")
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
