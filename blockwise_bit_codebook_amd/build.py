@@ -123,7 +123,7 @@ def _build_binding(verbose):
     include = os.path.join(torch, "include")
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
-           "-I", INCLUDE, "-I", os.path.join(ROCM, "include"), "-I", include,
+           "-I", INCLUDE, "-I", CSRC, "-I", os.path.join(ROCM, "include"), "-I", include,
            "-I", os.path.join(include, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
            os.path.join(CSRC, "layer_bind.cpp"), "-o", tmp, "-L", PKG, "-l:libkbit.so",
            "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]

@@ -83,6 +83,7 @@ constexpr Int8Tile kTiles[] = {{32, 128, 0.84, 0.497, 0.253, 1.08, 2.32, 1.29, 0
 // as are resident at once, two a compute unit: 4778 x 857 x 13738 would take 126 us
 // without and 146 in 2 parts (532 workgroups).
 constexpr int kParts[] = {2, 3, 4, 8};
+constexpr int64_t kMostParts = 8;
 constexpr double kPartsLaunch = 4.5, kPartsSums = 1.5;
 
 struct Int8Choice {
@@ -156,6 +157,37 @@ inline int64_t int8_product_workspace(int64_t M, int N, int K) {
             if (need > most) most = need;
         }
     return most;
+}
+
+// No less than that for any number of rows up to M, and never less for more
+// rows, so that one buffer serves all batches: at most two workgroups a compute
+// unit, each with the sums of one tile (64 KB).
+inline int64_t int8_product_workspace_up_to(int64_t M, int N, int K) {
+    const int64_t cus = device_cu_count(), pairs = (static_cast<int64_t>(K) + 2 * kDepth - 1) / (2 * kDepth);
+    if (M < kSplitTile || pairs < 2) return 0;
+    const int64_t rows = M < kRowBlock ? M : kRowBlock, parts = pairs < kMostParts ? pairs : kMostParts;
+    int64_t most = 0;
+    for (const int64_t n : {N < kMaxChannels ? N : kMaxChannels, N % kMaxChannels}) {
+        if (n < kSplitTile || (n + kSplitTile - 1) / kSplitTile > cus) continue;  // too many for two parts of one row of tiles
+        const int64_t all = parts * rows * sums_ld(static_cast<int>(n)), tiles = 2 * cus * kSplitTile * kSplitTile;
+        const int64_t need = 4 * (all < tiles ? all : tiles);
+        if (need > most) most = need;
+    }
+    return most;
+}
+
+// Workspace of the dynamic form: the codes, their scales, the product's own.
+// Its rows of codes are whole cache lines, so that no step of 128 codes lies
+// across two.
+inline int64_t dynamic_ld(int32_t K) { return (static_cast<int64_t>(K) + kDepth - 1) / kDepth * kDepth; }
+struct DynamicParts {
+    int64_t scale, product;  // where they start
+};
+inline DynamicParts dynamic_parts(int64_t M, int32_t K) {
+    DynamicParts w;
+    w.scale = M * dynamic_ld(K);
+    w.product = w.scale + (4 * M + 15) / 16 * 16;
+    return w;
 }
 
 }  // namespace kbit

@@ -70,21 +70,6 @@ int do_linear_int8(Dtype t, const Int8Product& p, void* workspace, int64_t works
     return map_launch(launch_int8_product(t, p, product_aligned(p), workspace, stream));
 }
 
-// Workspace of the dynamic form: the codes, their scales, the product's own.
-// Its rows of codes are whole cache lines, so that no step of 128 codes lies
-// across two.
-int64_t dynamic_ld(int32_t K) { return round_up(K, 128); }
-struct DynamicParts {
-    int64_t scale, product, total;
-};
-DynamicParts dynamic_parts(int64_t M, int32_t N, int32_t K) {
-    DynamicParts w;
-    w.scale = M * dynamic_ld(K);
-    w.product = w.scale + round_up(4 * M, 16);
-    w.total = w.product + int8_product_workspace(M, N, K);
-    return w;
-}
-
 int do_linear_int8_dynamic(Dtype t, const void* X, int64_t ldX, Int8Product p, void* workspace,
                            int64_t workspace_bytes, void* stream) {
     p.ldx = p.K >= 1 ? dynamic_ld(p.K) : 0;
@@ -93,8 +78,9 @@ int do_linear_int8_dynamic(Dtype t, const void* X, int64_t ldX, Int8Product p, v
     if (!X || !rows_shape_ok(p.M, p.K, ldX)) return KBIT_EINVAL;
     if (!aligned(X, elem_size(t)) || !aligned(workspace, 16)) return KBIT_EALIGN;
     const bool one_kernel = aligned(p.w, 16) && linear_int8_dynamic_fused(p.M, p.N, p.K, p.ldw);
-    const DynamicParts w = dynamic_parts(p.M, p.N, p.K);
-    if (!one_kernel && (workspace_bytes < w.total || !workspace)) return KBIT_EINVAL;
+    const DynamicParts w = dynamic_parts(p.M, p.K);
+    if (!one_kernel && (!workspace || workspace_bytes < w.product + int8_product_workspace(p.M, p.N, p.K)))
+        return KBIT_EINVAL;
     if (!device_usable()) return KBIT_EDEVICE;
     const bool vec = aligned(X, 16) && (p.M == 1 || ldX * elem_size(t) % 16 == 0);
     if (one_kernel) return map_launch(launch_int8_tokens(t, p, X, ldX, vec, stream));
@@ -320,12 +306,12 @@ extern "C" {
 
 int64_t linear_int8_workspace_bytes(int64_t M, int32_t N, int32_t K) {
     if (M < 0 || M > kbit::kMaxRows || N < 1 || K < 1 || K > kbit::kMaxInt8Depth) return -1;
-    return kbit::int8_product_workspace(M, N, K);
+    return kbit::int8_product_workspace_up_to(M, N, K);
 }
 
 int64_t linear_int8_dynamic_workspace_bytes(int64_t M, int32_t N, int32_t K) {
     if (M < 0 || M > kbit::kMaxRows || N < 1 || K < 1 || K > kbit::kMaxInt8Depth) return -1;
-    return kbit::dynamic_parts(M, N, K).total;
+    return kbit::dynamic_parts(M, K).product + kbit::int8_product_workspace_up_to(M, N, K);
 }
 
 int linear_int8_dynamic_fused(int64_t M, int32_t N, int32_t K, int64_t ldw) {

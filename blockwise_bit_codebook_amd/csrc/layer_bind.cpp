@@ -26,6 +26,7 @@
 #include <string>
 #include <utility>
 
+#include "int8_choice.h"
 #include "kbit.h"
 #include "kbit_layer.h"
 
@@ -286,16 +287,18 @@ struct Space {
     int64_t bytes = 0;
 };
 
-Space workspace(int64_t need, PyObject* given, const char* name, const Tensor& ref) {
+// `need`: what a given workspace has to hold; `take`: what is allocated else,
+// which may be less (this call's own need).
+Space workspace(int64_t need, int64_t take, PyObject* given, const char* name, const Tensor& ref) {
     if (need < 0) status_error(name, KBIT_EINVAL);
     Space s;
     if (given != Py_None) {
         s.p = vector(given, "workspace", at::kByte, need, ref);
         s.bytes = THPVariable_Unpack(given).numel();
-    } else if (need > 0) {
-        s.keep = at::empty({need}, ref.options().dtype(at::kByte));
+    } else if (take > 0) {
+        s.keep = at::empty({take}, ref.options().dtype(at::kByte));
         s.p = s.keep.data_ptr();
-        s.bytes = need;
+        s.bytes = take;
     }
     return s;
 }
@@ -395,7 +398,8 @@ PyObject* linear(PyObject* const* a) {  // codes, scale, w_codes, w_scale, bias,
     if (!is_float(type)) type_error(cat("unsupported element dtype ", type));
     const Weight w = weight(x, a[2], a[3], a[4], a[6], type, "codes");
     const float* scale = static_cast<const float*>(vector(a[1], "scale", at::kFloat, M, x));
-    const Space ws = workspace(linear_int8_workspace_bytes(M, w.N, w.K), a[7], "linear_int8", x);
+    const int64_t need = linear_int8_workspace_bytes(M, w.N, w.K);
+    const Space ws = workspace(need, need > 0 ? kbit::int8_product_workspace(M, w.N, w.K) : 0, a[7], "linear_int8", x);
     KBIT_BY_TYPE(type, linear_int8, run("linear_int8", x, {&w.out}, [&](void* stream) {
         return fn(static_cast<const int8_t*>(x.data_ptr()), scale, M, w.K, ldx, w.codes, w.scale, w.N, w.ldw,
                   static_cast<const T*>(w.bias), static_cast<T*>(w.out.data_ptr()), w.ldo, ws.p, ws.bytes, stream);
@@ -411,7 +415,9 @@ PyObject* linear_dynamic(PyObject* const* a) {  // X, w_codes, w_scale, bias, ou
     no_overlap(w.out, "out", x, "X", false);
     if (M == 0) return wrap(w.out);
     const bool fused = reinterpret_cast<uintptr_t>(w.codes) % 16 == 0 && linear_int8_dynamic_fused(M, w.N, w.K, w.ldw);
-    const Space ws = workspace(fused ? 0 : linear_int8_dynamic_workspace_bytes(M, w.N, w.K), a[5], "linear_int8_dynamic", x);
+    const int64_t need = fused ? 0 : linear_int8_dynamic_workspace_bytes(M, w.N, w.K);
+    const int64_t take = need <= 0 ? 0 : kbit::dynamic_parts(M, w.K).product + kbit::int8_product_workspace(M, w.N, w.K);
+    const Space ws = workspace(need, take, a[5], "linear_int8_dynamic", x);
     KBIT_BY_TYPE(type, linear_int8_dynamic, run("linear_int8_dynamic", x, {&w.out}, [&](void* stream) {
         return fn(static_cast<const T*>(x.data_ptr()), M, w.K, ldx, w.codes, w.scale, w.N, w.ldw,
                   static_cast<const T*>(w.bias), static_cast<T*>(w.out.data_ptr()), w.ldo, ws.p, ws.bytes, stream);
@@ -591,7 +597,8 @@ PyObject* norm_rope_backward(PyObject* const* a) {
     no_overlap(dk, "dk", n.q, "q", false);
     no_overlap(dk, "dk", gq, "dq_out", false);
     const Tensor dqw = at::empty({n.dim}, n.q.options().dtype(at::kFloat)), dkw = at::empty_like(dqw);
-    const Space ws = workspace(qk_norm_rope_backward_workspace_bytes(n.dim), a[12], "qk_norm_rope_backward", n.q);
+    const int64_t need = qk_norm_rope_backward_workspace_bytes(n.dim);
+    const Space ws = workspace(need, need, a[12], "qk_norm_rope_backward", n.q);
     const View vgq = view(gq), vgk = view(gk), vq = view(n.q), vk = view(n.k), vdq = view(dq), vdk = view(dk);
     KBIT_BY_TYPE(n.q.scalar_type(), qk_norm_rope_backward, run("qk_norm_rope_backward", n.q, {&dq, &dk}, [&](void* stream) {
         return fn(KBIT_VIEW(const T, vgq), KBIT_VIEW(const T, vgk), KBIT_VIEW(const T, vq), KBIT_VIEW(const T, vk),

@@ -59,14 +59,16 @@ def linear_int8(codes, scale, w_codes, w_scale, bias=None, dtype=torch.bfloat16,
     codes, w_codes: int8, exact sums; scale: fp32, one a row (it may be longer,
     like the one ``quantize_rows_int8`` was given); w_scale: N fp32 values;
     bias: N values of ``dtype`` (fp32/fp16/bf16), the output's type.  The workspace
-    (uint8, ``linear_int8_workspace_bytes``) is allocated here unless given."""
+    (uint8, ``lib().linear_int8_workspace_bytes(M, N, K)`` bytes, which serve any
+    fewer rows as well) is allocated here unless given."""
     return _layer.linear_int8(codes, scale, w_codes, w_scale, bias, dtype, out, workspace)
 
 
 def linear_int8_dynamic(X, w_codes, w_scale, bias=None, out=None, workspace=None):
     """linear_int8 of X [M, K] (fp32/fp16/bf16) quantized on the way, the
     output in X's type: the values of ``quantize_rows_int8`` followed by
-    ``linear_int8``."""
+    ``linear_int8``.  workspace: as there, of
+    ``lib().linear_int8_dynamic_workspace_bytes(M, N, K)`` bytes."""
     return _layer.linear_int8_dynamic(X, w_codes, w_scale, bias, out, workspace)
 
 

@@ -51,12 +51,14 @@ extern "C" {
                         const int8_t* w_codes, const float* w_scale, int32_t N, int64_t ldw, const CTYPE* bias,  \
                         CTYPE* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace on the current device (-1 for arguments out of range). */
+/* Bytes of workspace on the current device (-1 for arguments out of range).
+ * It does not fall with M: one workspace for the largest batch serves every
+ * smaller one.  At most 128 KB a compute unit. */
 int64_t linear_int8_workspace_bytes(int64_t M, int32_t N, int32_t K);
 
 /* quantize_rows_int8 of X, then linear_int8: the same values as the two
- * calls.  workspace: linear_int8_dynamic_workspace_bytes(M, N, K) bytes,
- * 16-byte aligned.  A few tokens are quantized inside the product's kernel:
+ * calls.  workspace: linear_int8_dynamic_workspace_bytes(M, N, K) bytes (again
+ * not falling with M), 16-byte aligned.  A few tokens are quantized inside the product's kernel:
  * where linear_int8_dynamic_fused(M, N, K, ldw) is 1 and w_codes is 16-byte
  * aligned no workspace is needed and it may be null. */
 #define KBIT_DECLARE_LINEAR_INT8_DYNAMIC(T, CTYPE)                                                             \

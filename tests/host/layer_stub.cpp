@@ -30,6 +30,9 @@ extern "C" {
 int stub_product_launches() { return kbit::product_launches; }
 int stub_product_on_fast_path() { return kbit::product_on_fast_path; }
 
+// What one product needs, in bytes.
+int64_t stub_product_workspace(int64_t M, int N, int K) { return kbit::int8_product_workspace(M, N, K); }
+
 // The form of a product on `cus` compute units: rows of the tile, or 0 and the
 // pieces of few rows in 16 x 16; parts of the depth.
 void stub_form(int64_t M, int N, int K, int64_t cus, int* bm, int* mt, int* tn, int* parts) {

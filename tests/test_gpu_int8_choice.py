@@ -50,3 +50,23 @@ def test_large_tiles_into_rows_of_odd_distance(t):
     kb.linear_int8(codes_dev(a), to_dev(sa), codes_dev(w), to_dev(sw), dtype=tdt(t), out=out[:, 1:N + 1])
     assert_bits_equal(bits(out[:, 1:N + 1].contiguous()), layer.round_to(layer.product(a, sa, w, sw), t), "out")
     assert (out[:, 0] == 3.0).all() and (out[:, N + 1:] == 3.0).all()
+
+
+def test_one_workspace_for_every_batch():
+    # 171 x 5815 x 4096 puts its depth in parts, the others do not
+    N, K = PARTS[2][2:]
+    t = torch()
+    ws = t.empty(kb.lib().linear_int8_workspace_bytes(2048, N, K), dtype=t.uint8, device=dev())
+    wd = t.empty(kb.lib().linear_int8_dynamic_workspace_bytes(2048, N, K), dtype=t.uint8, device=dev())
+    rng = np.random.default_rng(3)
+    w = rng.integers(-127, 128, (N, K)).astype(np.int8)
+    sw = rng.uniform(1e-3, 1e-2, N).astype(np.float32)
+    x = rng.standard_normal((600, K)).astype(np.float32)
+    W, S, X = codes_dev(w), to_dev(sw), to_dev(x)
+    q, s = layer.quantize_rows(x)
+    Q, SX = codes_dev(q), to_dev(s)
+    want = layer.product(q, s, w, sw).view(np.uint32)
+    for M in (600, 171, 256, 64, 1):
+        case(f"linear int8 one workspace M={M}")
+        assert_bits_equal(bits(kb.linear_int8(Q[:M], SX[:M], W, S, dtype=t.float32, workspace=ws)), want[:M], "codes")
+        assert_bits_equal(bits(kb.linear_int8_dynamic(X[:M], W, S, workspace=wd)), want[:M], "values")

@@ -53,3 +53,23 @@ def test_tokens_on_a_single_channel_need_no_distance_to_the_next():
     fused = kb.lib().linear_int8_dynamic_fused
     assert fused(1, 1, 100, 100) == 1 and fused(1, 1, 100, 1 << 22) == 1
     assert fused(1, 2, 100, 100) == 0 and fused(1, 2, 100, 1 << 22) == 0
+
+
+def test_a_workspace_for_the_largest_batch_serves_every_smaller_one(stub):
+    # on 256 compute units a product of 128 rows puts its depth in parts, one of 256 does not
+    size, dynamic = stub.linear_int8_workspace_bytes, stub.linear_int8_dynamic_workspace_bytes
+    size.restype = dynamic.restype = stub.stub_product_workspace.restype = ct.c_int64
+    stub.stub_product_workspace.argtypes = [ct.c_int64, ct.c_int, ct.c_int]
+    for N, K in ((4096, 11008), (4096, 4096), (1000, 3000), (130, 16384), (20000, 8192), (40000, 4096), (130, 256), (127, 9999),
+                 ((1 << 20) + 4096, 11008)):
+        before = before_dynamic = 0
+        for M in sorted([*range(1, 700, 7), 128, 256, 512, 1024, 2048, 4096, 8192, 32768, 32769, 33000, 65536, 100000]):
+            now, now_dynamic = size(M, N, K), dynamic(M, N, K)
+            assert now >= before and now_dynamic >= before_dynamic, (M, N, K)
+            assert now <= 256 * 2 * 65536
+            # what the call itself asks for is no more than that
+            assert stub.linear_int8_bf16(A, A, M, K, 1 << 15, A, A, N, 1 << 15, None, A, N, A, now, None) == 0, (M, N, K)
+            assert stub.linear_int8_dynamic_bf16(A, M, K, K, A, A, N, 1 << 15, None, A, N, A, now_dynamic, None) == 0
+            before, before_dynamic = now, now_dynamic
+    needs = [stub.stub_product_workspace(M, 4096, 11008) for M in (64, 128, 256, 512, 2048)]
+    assert 0 < needs[1] < needs[3] and needs[0] == needs[2] == needs[4] == 0
