@@ -346,6 +346,15 @@ __device__ __forceinline__ void landed() {
     __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
 }
 
+// Between LDS accesses of one wave whose lanes read what other lanes wrote, or
+// write over what other lanes read, without a barrier: the hardware executes a
+// wave's LDS accesses in order, and this holds the compiler to it as well.  No
+// instruction comes of it.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 __device__ __forceinline__ int key_x(int row) { return row & 7; }
 template <int TN>
 __device__ __forceinline__ int key_w(int row) {  // see operand_channel
@@ -495,9 +504,11 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_few_rows_kernel(const Int8P
             *reinterpret_cast<u32x4*>(e + (BM + 8 * i) * kDepth + lane * 16) = load_codes<true>(
                 wb + static_cast<int64_t>(min(row, cols - 1)) * ldw, k + 16 * (piece0 ^ key_w<TN>(row)), p.K);
         }
+        wave_order();
         read(e);
         multiply();
     }
+    wave_order();
     // Block (i, j) of sums: 1 KB of the wave's own operands, whose last reads
     // are done.
     constexpr int kFirst = kStep / 1024 < MT * TN ? kStep / 1024 : MT * TN;
@@ -644,9 +655,11 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Pro
             *reinterpret_cast<u32x4*>(e + 8 * i * kDepth + lane * 16) = load_codes<true>(
                 wb + static_cast<int64_t>(min(row, cols - 1)) * ldw, k + 16 * (piece0 ^ key_w<TN>(row)), p.K);
         }
+        wave_order();
         read(e, steps);
         multiply();
     }
+    wave_order();
 #pragma unroll
     for (int j = 0; j < TN; ++j)
         *reinterpret_cast<i32x4*>(e + j * 1024 + sum_place(l16, q, TN * q + j)) = acc[j];
@@ -745,7 +758,7 @@ __device__ __forceinline__ void store_tile(const Int8Product& p, typename E::T* 
                 *reinterpret_cast<u32x4*>(region + row * kRow + 16 * ((q * kSize + c) ^ (row & 7))) = d;
             }
         }
-        // One wave's LDS accesses are executed in order: no barrier.
+        wave_order();
         if (packed) {
             constexpr int kPieces = kRow / 16, kRows = kWave / kPieces;  // rows a store instruction
 #pragma unroll
@@ -761,6 +774,7 @@ __device__ __forceinline__ void store_tile(const Int8Product& p, typename E::T* 
                     region + row * kRow + 16 * (piece ^ (row & 7)))[at];
             }
         }
+        if (i0 + kPass < TM) wave_order();  // the next pass goes over the region
     }
 }
 
