@@ -31,8 +31,12 @@ bool rows_shape_ok(int64_t rows, int64_t d, int64_t ld) {
     return rows >= 0 && d >= 1 && ld >= d && ld <= kMaxElems && rows <= kMaxElems / ld;
 }
 
+// Longest row of codes: rounded up to 16 it still counts in 32 bits.
+constexpr int32_t kMaxCodes = INT32_MAX - 15;
+
 int do_quantize_rows(Dtype t, const void* X, int64_t rows, int32_t d, int64_t ldx, int8_t* codes, int64_t ldc,
                      float* scale, void* stream) {
+    if (d > kMaxCodes) return KBIT_EINVAL;
     if (!rows_shape_ok(rows, d, ldx) || ldc < round_up(d, 16) || !rows_shape_ok(rows, d, ldc)) return KBIT_EINVAL;
     if (rows == 0) return KBIT_OK;
     if (!X || !codes || !scale) return KBIT_EINVAL;

@@ -31,7 +31,7 @@ extern "C" {
  *   16, at least d rounded up to 16); the bytes from d up to that multiple of
  *   16 are set to zero, any further ones are left alone.
  * Used for activations (a row is a token) and for weights (a row is an output
- * channel).  rows = 0 is a no-op.
+ * channel).  d is at most 2^31 - 16.  rows = 0 is a no-op.
  * --------------------------------------------------------------------- */
 #define KBIT_DECLARE_QUANTIZE_ROWS(T, CTYPE)                                                                   \
     int quantize_rows_int8_##T(const CTYPE* X, int64_t rows, int32_t d, int64_t ldx, int8_t* codes, int64_t ldc, \

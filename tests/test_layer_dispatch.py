@@ -73,3 +73,11 @@ def test_a_workspace_for_the_largest_batch_serves_every_smaller_one(stub):
             before, before_dynamic = now, now_dynamic
     needs = [stub.stub_product_workspace(M, 4096, 11008) for M in (64, 128, 256, 512, 2048)]
     assert 0 < needs[1] < needs[3] and needs[0] == needs[2] == needs[4] == 0
+
+
+def test_the_longest_row_of_codes(stub):
+    # the kernels round a row's length up to 16 in 32 bits
+    def rows(d):
+        return stub.quantize_rows_int8_bf16(A, 1, d, d, A, 1 << 31, A, None)
+    assert rows((1 << 31) - 16) == 0
+    assert [rows((1 << 31) - k) for k in (15, 2, 1)] == [-1, -1, -1]
