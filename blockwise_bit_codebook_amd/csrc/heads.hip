@@ -27,11 +27,11 @@
 // element, one wave a row, with the same arithmetic.
 //
 // All passes read and write each element once and are bound by memory from
-// some thousand tokens on (a large copy on this card runs at 5.2 TB/s), by the
+// some thousand tokens on (a large copy on this card runs at 5.8 TB/s), by the
 // launch below that.  Heads of 128 in 16 bits: rotation of 8193 x 32 24.1 us
-// (5.6 TB/s: part of what was written stays in cache), norm of 8191 x 40 32.2
-// (5.3), append of 8179 x 8 14.0 (5.1), gradient of 8192 x 40 52.2 with the
-// addition of the weights' partial sums (4.9).
+// (5.6 TB/s), norm of 8191 x 40 32.4 (5.3), append of 8179 x 8 14.0 (5.1),
+// gradient of 8192 x 40 52.1 with the addition of the weights' partial sums
+// (4.9).
 #include "device.h"
 #include "kbit_internal.h"
 #include "launch.h"

@@ -3,7 +3,9 @@
 // epilogue.
 //
 //   codes    amax = max |x| over the row, scale = RN(amax / 127),
-//            q = rint(RN(x * RN(127 * RN(1 / amax)))), half to even; |q| <= 127.
+//            q = rint(RN(x * RN(127 * RN(1 / amax)))), half to even; |q| <= 127
+//            (two roundings of the step, as in a division through the
+//            reciprocal; RN(127 / amax) differs for 24% of the bf16 amax).
 //            A row below 2^-100 throughout (1 / amax could leave the fp32
 //            range) gets scale 0 and codes 0; a row with a NaN or an
 //            infinity gets scale NaN and codes 0, so that its outputs are NaN.
@@ -250,8 +252,9 @@ __device__ __forceinline__ void store_out(const Int8Product& p, int64_t m, int n
 // that the 16 rows of a fragment start in different banks).  The loads need no
 // alignment and go through registers: those of the next step are on their way
 // while a step is multiplied.  For rows that do not all start at 16 bytes, which
-// the kernels below need: 8192 x 11008 x 4096 698 us against their 301, 77 x
-// 11008 x 4096 33 against 13, 500 x 4099 x 3840 39.5 against 19.3.
+// the kernels below need: 8192 x 11008 x 4096 697 us with one operand 8 bytes
+// off and 735 to 862 with both, against their 328, 77 x 11008 x 4096 32 against
+// 13.3, 500 x 4099 x 3840 40 against 20.
 constexpr int kGenStep = 128, kGenPitch = 144;
 template <class E, int B>
 __global__ __launch_bounds__(kThreads) void int8_generic_kernel(const Int8Product p) {
@@ -682,9 +685,9 @@ __global__ __launch_bounds__(WAVES* kWave) void int8_tokens_kernel(const Int8Pro
 // channels, two steps of both operands in LDS: while the matrix cores work on
 // one, the loads of the next go into the other.  Tiles of 256 x 256 on 8 waves
 // need 1/256 byte of operands an operation, half of what 128 x 128 needs, and
-// run 8192 x 11008 x 4096 in 300 us with its scales (2.46 POP/s; the library's
-// product into int32, without scales, took 350); the smaller ones are for what
-// would not fill the device (choose_form).  The matrix pipes are busy for 52%
+// run 8192 x 11008 x 4096 in 328 us with its scales (2.25 POP/s; the library's
+// product into int32, without scales, takes 334 to 341); the smaller ones are for what
+// would not fill the device (choose_form).  The matrix pipes are busy for 53%
 // of the kernel's cycles, without one bank conflict: what is lost goes to the
 // step's barrier, to the rounds' ends (one workgroup fits a compute unit: 7.5
 // us each, 5 where a workgroup stays, see below) and to the last, partly filled

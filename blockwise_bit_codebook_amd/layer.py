@@ -120,7 +120,9 @@ def rope(x, positions, table, layout="half", inverse=False, out=None):
 
     layout: pairs (i, i + rot/2) ("half") or (2i, 2i + 1) ("interleaved").
     ``inverse=True`` is the transposed rotation: the gradient of x from that of
-    the output.  ``out`` may be x.  A position outside the table gives NaN."""
+    the output (with an amplitude a, R^T R = a^2).  ``out`` may be x.  A position
+    outside the table gives NaN.  More than 65535 batches only where they follow
+    one another in memory like the tokens."""
     return _layer.rope(x, positions, table, layout, inverse, out)
 
 

@@ -9,7 +9,8 @@
  * element type (fp32, fp16, bf16; the 16-bit types are raw bits).  Strides
  * count elements.  No pass writes what it does not own: strided outputs leave
  * the elements between their rows alone.  Outputs may be their input (same
- * address and strides) where that is said; other overlaps are undefined.
+ * address and strides) where that is said; other overlaps are undefined (the
+ * torch binding refuses them).
  */
 #ifndef KBIT_LAYER_H
 #define KBIT_LAYER_H
@@ -25,7 +26,10 @@ extern "C" {
  *
  * Codes of a row x of d values, one fp32 scale a row:
  *   amax = max |x|, scale = RN(amax / 127), q = rint(RN(x * RN(127 * RN(1 / amax))))
- *   (half to even), |q| <= 127.  amax < 2^-100: scale 0 and codes 0.  A row
+ *   (half to even), |q| <= 127.  The step is rounded twice, as where a program
+ *   divides a scalar by a tensor through its reciprocal; RN(127 / amax) would
+ *   give another code, by one, for some values within a rounding of a tie.
+ *   amax < 2^-100: scale 0 and codes 0.  A row
  *   with a NaN or an infinity: scale NaN and codes 0 (its outputs are NaN).
  * codes: row r starts at codes + r * ldc, 16-byte aligned (ldc a multiple of
  *   16, at least d rounded up to 16); the bytes from d up to that multiple of
@@ -104,7 +108,9 @@ int rope_table(const double* freq, int32_t rot, int64_t max_pos, double amplitud
  * positions[batch][tokens] (contiguous, int32 or int64: position_bytes 4 or
  * 8).  A position outside [0, max_pos) gives NaN in the rotated elements.
  * inverse != 0 negates s: the transposed rotation, which takes the output's
- * gradient to the input's.  out may be x. */
+ * gradient to the input's.  out may be x.  batch is at most 65535 unless tokens
+ * is 1 or the batches follow one another at tokens times the tokens' distance
+ * (in x and out), so that they count as one; the same holds for qk_norm_rope. */
 #define KBIT_DECLARE_ROPE(T, CTYPE)                                                                            \
     int rope_##T(const CTYPE* x, int64_t x_batch, int64_t x_token, int64_t x_head, CTYPE* out, int64_t out_batch, \
                  int64_t out_token, int64_t out_head, int64_t batch, int64_t tokens, int32_t heads, int32_t dim, \

@@ -1,6 +1,8 @@
-"""Every kernel form the layer operators choose between, at the sizes where
-the choice turns: the tiles of the int8 product, tokens quantized on the way,
-rows by waves or workgroups, several heads a lane group.  Bars as in
+"""The kernel forms the layer operators choose between, at sizes where
+the choice turned when these were written: the tiles of the int8 product, tokens quantized on the way,
+rows by waves or workgroups, several heads a lane group.  (Which kernel of the
+product a shape reaches is held in test_int8_choice, with shapes for every
+kernel.)  Bars as in
 test_gpu_int8 and test_gpu_heads: bits where every rounding is defined, the
 oracle's derived bounds for norms and their gradients."""
 
@@ -18,9 +20,11 @@ pytestmark = pytest.mark.gpu
 
 
 # On 256 compute units, in this order: few rows in pieces of 16 x 16, 32, 48
-# and 64, 32 x 32 and 64, 48 x 32 and 64, 64 x 64, 80 x 48 and 64 (rows x
-# channels), tiles of 32, 64 and 128 x 128 and of 256 x 256, pieces of 112 and
-# 128 x 48; each with the last piece of the depth partial and, in the second list, whole.
+# and 64, 32 x 32 and 64 (rows x channels), tiles of 64 and 32 x 128, pieces of 64
+# x 64, 80 x 48 and 64, tiles of 32, 64, 128 x 128 and 256 x 256, pieces of 112 and
+# 128 x 48; most with the last piece of the depth partial.  In the second list it
+# is whole: 16 x 32, 48 and 64, 32 x 32 and 64, 16 x 16, tiles of 64, 128, 256 and
+# 128 rows, pieces of 112 x 48, tiles of 32 rows.
 FORMS = [(1, 7, 20), (1, 4287, 20), (1, 8197, 20), (1, 12393, 20), (17, 6689, 21), (17, 8529, 20), (106, 2351, 128),
          (38, 9511, 640), (49, 12905, 1609), (50, 8657, 1556), (67, 12875, 1982), (36, 152, 256), (139, 10040, 20),
          (321, 8117, 20), (428, 18432, 20), (89, 9166, 2483), (125, 11500, 3001)]
@@ -78,8 +82,8 @@ def test_product_into_rows_of_odd_distance(t, M, N):
 @pytest.mark.parametrize("t", DT)
 @pytest.mark.parametrize("M,N,K", [(4360, 4352, 256), (8200, 2600, 512), (4400, 4362, 256), (2700, 8200, 768), (4360, 4352, 300)])
 def test_workgroups_that_take_several_tiles(t, M, N, K):
-    # more tiles of 256 x 256 than compute units; odd channels and a depth of
-    # no whole pair of steps take the other way
+    # the second and fourth: more tiles of 256 x 256 than compute units, whose
+    # workgroups stay; the others run in 128 x 128
     case(f"linear int8 several tiles {t} M={M} N={N} K={K}")
     got, want = product_case(M, N, K, t, bias=M % 100 != 0)
     assert_bits_equal(bits(got), want, f"product {M} {N} {K}")
