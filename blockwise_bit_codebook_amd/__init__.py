@@ -485,6 +485,8 @@ _install_named()
 # *" binds every name of __all__ at once: they are in it where they can be.
 _LAYER = ("quantize_rows_int8", "linear_int8", "linear_int8_dynamic", "rope_frequencies", "rope_table", "rope",
           "qk_norm_rope", "qk_norm_rope_backward", "append_kv_paged")
+_MX = ("quantize_mxfp4", "dequantize_mxfp4", "linear_mxfp4", "linear_mxfp4_dynamic", "linear_mxfp4_backward",
+       "layer_norm", "layer_norm_backward")
 
 
 def _layer_usable():
@@ -493,14 +495,15 @@ def _layer_usable():
 
 
 if _layer_usable():
-    __all__ += _LAYER
+    __all__ += _LAYER + _MX
 
 
 def __getattr__(name):
-    if name not in _LAYER:
+    if name not in _LAYER + _MX:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import layer
+    from . import layer, mx
     g = globals()
-    for n in _LAYER:
-        g[n] = getattr(layer, n)
+    for module, names in ((layer, _LAYER), (mx, _MX)):
+        for n in names:
+            g[n] = getattr(module, n)
     return g[name]

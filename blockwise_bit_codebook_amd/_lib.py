@@ -91,6 +91,36 @@ def _layer_signatures():
 LAYER_SIGNATURES = _layer_signatures()
 
 
+def _mx_signatures():
+    """(name, argtypes) for every C entry point declared in include/kbit_mx.h."""
+    sig = [
+        ("linear_mxfp4_workspace_bytes", [_i64, _i32, _i32]),
+        ("linear_mxfp4_dynamic_workspace_bytes", [_i64, _i32, _i32]),
+        ("linear_mxfp4_dynamic_fused", [_i64, _i32, _i32, _i64, _i64]),
+        ("linear_mxfp4_backward_workspace_bytes", [_i64, _i32, _i32]),
+        ("layer_norm_backward_workspace_bytes", [_i64, _i32]),
+    ]
+    weight = [_p, _p, _i32, _i64, _i64]  # codes, scales, N, their rows' distances
+    end = [_p, _p, _i64, _p, _i64, _p]   # bias, out, ldo, workspace, its bytes, stream
+    for t in DTYPES:
+        sig += [
+            (f"quantize_mxfp4_{t}", [_p, _i64, _i32, _i64, _p, _i64, _p, _i64, _p]),
+            (f"quantize_mxfp4_columns_{t}", [_p, _i64, _i32, _i64, _p, _i64, _p, _i64, _p]),
+            (f"dequantize_mxfp4_{t}", [_p, _i64, _p, _i64, _i64, _i32, _p, _i64, _p]),
+            (f"linear_mxfp4_{t}", [_p, _p, _i64, _i32, _i64, _i64] + weight + end),
+            (f"linear_mxfp4_dynamic_{t}", [_p, _i64, _i32, _i64] + weight + end),
+            (f"linear_mxfp4_backward_{t}",
+             [_p, _i64] * 3 + [_i64, _i32, _i32] + [_p, _i64] * 2 + [_p, _p, _i64, _p]),
+            (f"layer_norm_{t}", [_p, _i64, _i32, _i64, _p, _p, _i32, _f32, _p, _i64, _p]),
+            (f"layer_norm_backward_{t}",
+             [_p, _i64, _p, _i64, _i64, _i32, _p, _i32, _f32, _p, _i64, _p, _p, _p, _i64, _p]),
+        ]
+    return sig
+
+
+MX_SIGNATURES = _mx_signatures()
+
+
 def _share_torch_runtime():
     """torch ships a HIP runtime of its own.  Loaded first it serves libkbit.so
     too, which asks for the same soname; the other way round the process would
@@ -116,7 +146,7 @@ def load(path=LIB_PATH):
             "`python -m blockwise_bit_codebook_amd.build` (hipcc, gfx950)")
     _share_torch_runtime()
     lib = ct.CDLL(path)
-    for name, args in SIGNATURES + LAYER_SIGNATURES:
+    for name, args in SIGNATURES + LAYER_SIGNATURES + MX_SIGNATURES:
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = {"kbit_strerror": ct.c_char_p, "kbit_nested_workspace_bytes": ct.c_int64,
@@ -125,7 +155,11 @@ def load(path=LIB_PATH):
                       "kbit_act_tables_bytes": ct.c_int64,
                       "linear_int8_workspace_bytes": ct.c_int64,
                       "linear_int8_dynamic_workspace_bytes": ct.c_int64,
-                      "qk_norm_rope_backward_workspace_bytes": ct.c_int64}.get(name, ct.c_int)
+                      "qk_norm_rope_backward_workspace_bytes": ct.c_int64,
+                      "linear_mxfp4_workspace_bytes": ct.c_int64,
+                      "linear_mxfp4_dynamic_workspace_bytes": ct.c_int64,
+                      "linear_mxfp4_backward_workspace_bytes": ct.c_int64,
+                      "layer_norm_backward_workspace_bytes": ct.c_int64}.get(name, ct.c_int)
     return lib
 
 

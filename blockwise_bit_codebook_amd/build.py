@@ -32,8 +32,9 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 
 HIP_SOURCES = ["quantize.hip", "dequantize.hip", "nested_encode.hip", "linear.hip", "act_fwht.hip",
-               "act_block.hip", "heads.hip", "int8.hip"]
-CXX_SOURCES = ["api.cpp", "codebook.cpp", "layer_api.cpp"]
+               "act_block.hip", "heads.hip", "int8.hip", "mxfp4.hip", "layer_norm.hip"]
+CXX_SOURCES = ["api.cpp", "codebook.cpp", "layer_api.cpp", "mx_api.cpp"]
+BIND_SOURCES = ["layer_bind.cpp", "mx_bind.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 HIP_FLAGS = [
@@ -112,7 +113,7 @@ def build(verbose=False, jobs=None):
 
 
 def _build_binding(verbose):
-    """_layer.so: csrc/layer_bind.cpp against torch's and Python's headers.
+    """_layer.so: BIND_SOURCES against torch's and Python's headers.
     Without torch there is nothing to bind to: libkbit.so alone serves the C
     ABI and the host-only functions."""
     spec = importlib.util.find_spec("torch")
@@ -125,13 +126,13 @@ def _build_binding(verbose):
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
            "-I", INCLUDE, "-I", CSRC, "-I", os.path.join(ROCM, "include"), "-I", include,
            "-I", os.path.join(include, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "layer_bind.cpp"), "-o", tmp, "-L", PKG, "-l:libkbit.so",
+           *(os.path.join(CSRC, src) for src in BIND_SOURCES), "-o", tmp, "-L", PKG, "-l:libkbit.so",
            "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("g++ failed for layer_bind.cpp:\n" + r.stdout + r.stderr)
+        raise RuntimeError(f"g++ failed for {', '.join(BIND_SOURCES)}:\n" + r.stdout + r.stderr)
     shutil.move(tmp, BINDING)
 
 

@@ -1,0 +1,102 @@
+// What the kernels over rows and the matrix products share: element types,
+// pieces of rows, operands on their way to LDS.
+#pragma once
+
+#include "device.h"
+
+namespace kbit {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------------------
+// element types
+// ---------------------------------------------------------------------------
+struct QF32 {
+    using T = float;
+    static constexpr int kVec = 2;
+    static __device__ float one(T v) { return v; }
+    static __device__ T narrow(float v) { return v; }
+    static __device__ void widen(const u32x4* r, float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = __uint_as_float(r[0][i]);
+            x[4 + i] = __uint_as_float(r[1][i]);
+        }
+    }
+};
+struct QF16 {
+    using T = uint16_t;
+    static constexpr int kVec = 1;
+    static __device__ float one(T v) { return Fp16::h2f(v); }
+    static __device__ T narrow(float v) { return static_cast<T>(pack_f16x2(v, 0.0f) & 0xFFFFu); }
+    static __device__ uint32_t pack(float lo, float hi) { return pack_f16x2(lo, hi); }
+    static __device__ void widen(const u32x4* r, float (&x)[8]) { Fp16::unpack(r, x); }
+};
+struct QB16 {
+    using T = uint16_t;
+    static constexpr int kVec = 1;
+    static __device__ float one(T v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+    static __device__ T narrow(float v) { return static_cast<T>(pack_bf16x2(v, 0.0f) & 0xFFFFu); }
+    static __device__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
+    static __device__ void widen(const u32x4* r, float (&x)[8]) { Bf16::unpack(r, x); }
+};
+
+// 8 elements of a row from column c, 0 beyond d.
+template <class E, bool VEC>
+__device__ __forceinline__ void load8(const typename E::T* row, int c, int d, float (&x)[8]) {
+    if (VEC && c + 8 <= d) {
+        u32x4 r[E::kVec];
+#pragma unroll
+        for (int i = 0; i < E::kVec; ++i) r[i] = load16<false>(row + c + 4 * i);
+        E::widen(r, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = c + i < d ? E::one(row[c + i]) : 0.0f;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// operands in LDS
+// ---------------------------------------------------------------------------
+// A step of an operand's row is 128 bytes in LDS, the 16-byte pieces of which
+// stand at positions xor-ed with a key of the row (key_x, key_w), so that the 8
+// rows which a read touches at a time lie in different banks.  The weight is
+// the first matrix operand, so that lane l holds channels 4 (l / 16) .. + 3 of
+// row l % 16; channel 4 TN (i / 4) + 4 j + i % 4 sits in row i of operand j,
+// which makes a lane's 4 TN channels neighbours.
+template <int TN>
+__device__ __forceinline__ int operand_channel(int j, int i) {
+    return 4 * TN * (i >> 2) + 4 * j + (i & 3);
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 bytes a lane from memory to LDS: lane l's go to lds + 16 l.  Counted with
+// the vector loads, in order: landed<N>() waits until at most the last N are
+// still on their way.
+__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, void* lds, int lane_offset, int offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, lane_offset, offset, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void landed() {
+    static_assert(N < 64, "the counter has six bits");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+}
+
+__device__ __forceinline__ int key_x(int row) { return row & 7; }
+template <int TN>
+__device__ __forceinline__ int key_w(int row) {  // see operand_channel
+    return (row & 3) | (row / (4 * TN) & 1) << 2;
+}
+
+// Where a lane's four sums stand in a 1 KB block of 16 rows (l16) and 4 x 4
+// channels (q): the rows of neighbouring pieces c of 4 channels are xor-ed
+// apart, so that neither the lanes that write a block nor the threads that
+// read a row of several blocks meet in a bank.  (Integer atomics into one
+// cleared array met four to a bank: 77 x 11008 x 4096 17.7 us, 16.6 so.)
+__device__ __forceinline__ int sum_place(int l16, int q, int c) { return 16 * (16 * q + (l16 ^ c)); }
+
+}  // namespace
+}  // namespace kbit

@@ -1,0 +1,147 @@
+// Internal launcher interface of the microscaled 4-bit layers and the layer
+// norm (include/kbit_mx.h), between mx_api.cpp and the HIP translation units.
+// No HIP types cross this boundary; arguments are already validated.
+#pragma once
+
+#include <stdint.h>
+
+#include "int8_choice.h"
+#include "kbit_internal.h"
+
+namespace kbit {
+
+constexpr int kMxBlock = 32;       // values a scale
+constexpr int kMxBlockBytes = 16;  // of codes
+
+// Longest row: its codes' bytes and their steps count in 32 bits.
+constexpr int64_t kMxMaxDepth = int64_t(1) << 26;
+
+inline int64_t mx_blocks(int64_t d) { return (d + kMxBlock - 1) / kMxBlock; }
+
+// Rows of X to codes and scales; vec: 16-byte loads are possible.
+int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx, uint8_t* codes, int64_t ldc,
+                       uint8_t* scales, int64_t lds, bool vec, void* stream);
+
+// Columns of X [rows][cols] to codes and scales, a column a row of both; with
+// codes null neither is written.  sums: null, or mx_sum_groups(rows) rows of
+// cols floats, the columns' sums over kMxSumRows rows each.
+constexpr int64_t kMxSumRows = 256;
+inline int64_t mx_sum_groups(int64_t rows) { return (rows + kMxSumRows - 1) / kMxSumRows; }
+int launch_mx_quantize_columns(Dtype t, const void* X, int64_t rows, int cols, int64_t ldx, uint8_t* codes, int64_t ldc,
+                               uint8_t* scales, int64_t lds, float* sums, void* stream);
+
+// out[c] = sum over groups of sums[group][c], in order.
+int launch_mx_add_sums(const float* sums, int64_t groups, int cols, float* out, void* stream);
+
+// Zeros to rows of cols floats.
+int launch_mx_zero(float* out, int64_t rows, int cols, int64_t ldo, void* stream);
+
+int launch_mx_dequantize(Dtype t, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t rows,
+                         int d, void* out, int64_t ldo, bool vec, void* stream);
+
+struct MxProduct {
+    const uint8_t *x, *xs, *w, *ws;
+    const void* bias;
+    void* out;
+    int64_t M, ldx, ldxs, ldw, ldws, ldo;
+    int N, K;  // K: bytes of a row of codes, a multiple of 16
+};
+
+// workspace: of int8_product_workspace(M, N, K) bytes on the current device
+// (the kernels are those of the int8 product, a byte for a byte), 16-byte
+// aligned.
+int launch_mx_product(Dtype t, const MxProduct& p, void* workspace, void* stream);
+
+// Tokens quantized inside the product's kernel: their codes stay in LDS.
+constexpr int kMxTokenItems = 4;   // pieces of 512 values a wave
+constexpr int kMxTokenBytes = 20 * 1024;
+constexpr int kMxTokenPad = 16;
+constexpr int kMxMaxTokens = 8;
+inline bool mx_tokens_fit(int64_t M, int N, int64_t d, int64_t ldw, int64_t ldws) {
+    if (M > kMxMaxTokens || N > kMaxChannels || (N > 1 && (ldw >= kFarRows || ldws >= kFarRows))) return false;
+    const int64_t per_row = (d + 511) / 512, bytes = mx_blocks(d) * kMxBlockBytes;
+    const int64_t steps = (bytes + kDepth - 1) / kDepth;
+    return M * (steps * kDepth + kMxTokenPad) <= kMxTokenBytes && M * per_row <= 8 * kMxTokenItems;
+}
+
+// Rows of quantized operands in a workspace: their codes start at whole cache
+// lines, so that no step of kDepth bytes lies across two.
+struct MxRows {
+    int64_t ldc, lds, scales, bytes;  // scales: where they start
+};
+inline MxRows mx_rows(int64_t rows, int64_t d) {
+    MxRows r;
+    r.ldc = (mx_blocks(d) * kMxBlockBytes + kDepth - 1) / kDepth * kDepth;
+    r.lds = (mx_blocks(d) + 15) / 16 * 16;
+    r.scales = rows * r.ldc;
+    r.bytes = r.scales + rows * r.lds;
+    return r;
+}
+
+// Bytes of a row of codes.
+inline int mx_depth(int64_t d) { return static_cast<int>(mx_blocks(d) * kMxBlockBytes); }
+
+// Workspace of the backward pass: dout and W along N, dout and X along M, the
+// partial sums of the bias gradient, the products' own.
+struct MxBackParts {
+    MxRows g_rows, w_cols, g_cols, x_cols;
+    int64_t w_at, gc_at, x_at, sums_at, product_at;
+};
+inline MxBackParts mx_back_parts(int64_t M, int N, int K) {
+    MxBackParts b;
+    b.g_rows = mx_rows(M, N);
+    b.w_cols = mx_rows(K, N);
+    b.g_cols = mx_rows(N, M);
+    b.x_cols = mx_rows(K, M);
+    const auto up = [](int64_t n) { return (n + kDepth - 1) / kDepth * kDepth; };
+    b.w_at = up(b.g_rows.bytes);
+    b.gc_at = b.w_at + up(b.w_cols.bytes);
+    b.x_at = b.gc_at + up(b.g_cols.bytes);
+    b.sums_at = b.x_at + up(b.x_cols.bytes);
+    b.product_at = b.sums_at + up(4 * mx_sum_groups(M) * N);
+    return b;
+}
+
+// p.x and p.xs are not looked at.
+int launch_mx_tokens(Dtype t, const MxProduct& p, int d, const void* X, int64_t ldX, bool vec, void* stream);
+
+// ---------------------------------------------------------------------------
+// layer norm
+// ---------------------------------------------------------------------------
+struct LayerNormArgs {
+    const void *x, *weight, *bias;  // bias may be null
+    void* out;
+    int64_t rows, ldx, ldo;
+    int d;
+    float eps;
+    bool weight_fp32;
+};
+
+// vec: rows and weights start at multiples of 16 bytes.
+int launch_layer_norm(Dtype t, const LayerNormArgs& p, bool vec, void* stream);
+
+// Rows of partial sums of the weights' gradients, each 2 d floats.
+constexpr int kLayerNormPartials = 512;
+// Longest row whose sums stay in registers, and the longest one at any
+// alignment; above it the rows' statistics go to the workspace and a second
+// pass sums over rows.
+constexpr int kLayerNormKept = 16384, kLayerNormKeptAny = 8192;
+
+inline int64_t layer_norm_backward_bytes(int64_t rows, int d) {
+    const int64_t groups = rows < kLayerNormPartials ? rows : kLayerNormPartials;
+    return 4 * (groups * 2 * d + (d > kLayerNormKeptAny ? 4 * rows : 0));
+}
+
+struct LayerNormBackArgs {
+    const void *g, *x, *weight;
+    void* dx;
+    float *dweight, *dbias, *workspace;
+    int64_t rows, ldg, ldx, lddx;
+    int d;
+    float eps;
+    bool weight_fp32;
+};
+
+int launch_layer_norm_back(Dtype t, const LayerNormBackArgs& p, bool vec, void* stream);
+
+}  // namespace kbit

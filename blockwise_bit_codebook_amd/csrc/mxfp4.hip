@@ -1,0 +1,1212 @@
+// Microscaled 4-bit floating point (MXFP4) for gfx950: rows and columns to
+// codes, codes to values, and the product of two coded matrices.
+//
+//   block    32 values along a row; e = max(floor(log2(max |x|)) - 2, -127), held
+//            as the byte e + 127; code = x / 2^e rounded to the nearest of 0,
+//            1/2, 1, 3/2, 2, 3, 4, 6 (ties to the even code, at most 6) and a
+//            sign.  A block with a NaN or an infinity has the byte 255, which is
+//            NaN, and codes 0.  Values past a row's end are codes 0.
+//   codes    two a byte, the first in the low half, 16 bytes a block.
+//   product  acc[m][n] = sum over blocks b of 2^(xs + ws) sum over k in b of
+//            x[m][k] w[n][k], in fp32 on the matrix cores, out = RN_T(acc + bias).
+#include "kbit_internal.h"
+#include "launch.h"
+#include "matrix.h"
+#include "mx_internal.h"
+
+#include <type_traits>
+
+namespace kbit {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+
+// ---------------------------------------------------------------------------
+// values to codes
+// ---------------------------------------------------------------------------
+// The scale byte of a block from the bits of its largest magnitude (ordered
+// like the magnitudes, with NaN above infinity above the rest).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+    const uint32_t e = amax_bits >> 23;
+    return e == 255u ? 255u : max(e, 2u) - 2u;
+}
+
+// 8 codes; the converter takes the scale's exponent from a float's bits and
+// rounds half to even, at most 6.
+__device__ __forceinline__ uint32_t pack_codes(const float* x, uint32_t byte) {
+    const float s = __uint_as_float(byte << 23);
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x[0], x[1], s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x[2], x[3], s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x[4], x[5], s, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x[6], x[7], s, 3);
+    return byte == 255u ? 0u : r;
+}
+
+__device__ __forceinline__ uint32_t largest_bits(const float (&x)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+    return m;
+}
+
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+    m = max(m, dpp_u32<kDppXor1>(m));
+    return max(m, dpp_u32<kDppXor2>(m));
+}
+
+// Rows: 8 values a lane, four lanes a block, kRowItems pieces of 512 values a
+// wave on their way together.  Piece i of all rows: row i / per_row.
+constexpr int kRowItems = 4;
+template <class E, bool VEC>
+__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const typename E::T* __restrict__ X, uint32_t items,
+                                                               uint32_t per_row, int d, int64_t ldx,
+                                                               uint8_t* __restrict__ codes, int64_t ldc,
+                                                               uint8_t* __restrict__ scales, int64_t lds) {
+    const int lane = __lane_id();
+    const uint32_t first = (blockIdx.x * kWavesPerGroup + threadIdx.x / kWave) * kRowItems;
+    const int end = (d + kMxBlock - 1) / kMxBlock * kMxBlock;
+    float v[kRowItems][8];
+    uint32_t row = first / per_row;
+    uint32_t at = first - row * per_row;
+    const uint32_t row_first = row, at_first = at;
+#pragma unroll
+    for (int i = 0; i < kRowItems; ++i) {
+        const int64_t c = static_cast<int64_t>(at) * 512 + lane * 8;
+        if (first + i < items && c < end) load8<E, VEC>(X + row * ldx, static_cast<int>(c), d, v[i]);
+        if (++at == per_row) {
+            at = 0;
+            ++row;
+        }
+    }
+    row = row_first;
+    at = at_first;
+#pragma unroll
+    for (int i = 0; i < kRowItems; ++i) {
+        const int64_t c = static_cast<int64_t>(at) * 512 + lane * 8;
+        if (first + i < items && c < end) {  // end is a whole number of blocks: quads stay together
+            const uint32_t byte = scale_byte(quad_max(largest_bits(v[i])));
+            *reinterpret_cast<uint32_t*>(codes + row * ldc + c / 2) = pack_codes(v[i], byte);
+            if ((lane & 3) == 0) scales[row * lds + c / kMxBlock] = static_cast<uint8_t>(byte);
+        }
+        if (++at == per_row) {
+            at = 0;
+            ++row;
+        }
+    }
+}
+
+// Columns: a workgroup takes 8 blocks of 32 rows and 128 columns.  A lane has
+// two columns of a block, so that a block's maximum needs no other lane; the
+// codes cross LDS so that a column's leave as whole cache lines.
+constexpr int kColBlocks = 8, kColCols = 128;
+template <class E, bool PAIRS>
+__global__ __launch_bounds__(kThreads) void mx_quantize_columns_kernel(const typename E::T* __restrict__ X, int64_t rows,
+                                                                       int cols, int64_t ldx,
+                                                                       uint8_t* __restrict__ codes, int64_t ldc,
+                                                                       uint8_t* __restrict__ scales, int64_t lds,
+                                                                       float* __restrict__ sums) {
+    using T = typename E::T;
+    constexpr int kPitch = kColBlocks * kMxBlockBytes + 16;
+    __shared__ __align__(16) uint8_t tile[kColCols * kPitch];
+    __shared__ __align__(8) uint8_t bytes[kColCols * kColBlocks];
+    const int lane = __lane_id(), wave = threadIdx.x / kWave;
+    const int64_t block0 = static_cast<int64_t>(blockIdx.y) * kColBlocks, row_blocks = (rows + kMxBlock - 1) / kMxBlock;
+    const int col0 = blockIdx.x * kColCols, col = col0 + 2 * lane;
+    float total[2] = {0.0f, 0.0f};
+    for (int b = wave; b < kColBlocks; b += kWavesPerGroup) {
+        const int64_t r0 = (block0 + b) * kMxBlock;
+        if (r0 >= rows) break;
+        const int n = static_cast<int>(min<int64_t>(rows - r0, kMxBlock));
+        float v[2][kMxBlock];
+#pragma unroll
+        for (int r = 0; r < kMxBlock; ++r) {
+            v[0][r] = v[1][r] = 0.0f;
+            if (r < n) {
+                const T* p = X + (r0 + r) * ldx + col;
+                if (PAIRS && col + 2 <= cols) {
+                    if constexpr (sizeof(T) == 4) {
+                        const float2 f = *reinterpret_cast<const float2*>(p);
+                        v[0][r] = f.x;
+                        v[1][r] = f.y;
+                    } else {
+                        const uint32_t f = *reinterpret_cast<const uint32_t*>(p);
+                        v[0][r] = E::one(static_cast<T>(f & 0xFFFFu));
+                        v[1][r] = E::one(static_cast<T>(f >> 16));
+                    }
+                } else {
+                    if (col < cols) v[0][r] = E::one(p[0]);
+                    if (col + 1 < cols) v[1][r] = E::one(p[1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int r = 0; r < kMxBlock; ++r) {
+                m = max(m, __float_as_uint(v[c][r]) & 0x7FFFFFFFu);
+                total[c] += v[c][r];
+            }
+            const uint32_t byte = scale_byte(m);
+            const u32x4 q = {pack_codes(v[c], byte), pack_codes(v[c] + 8, byte), pack_codes(v[c] + 16, byte),
+                             pack_codes(v[c] + 24, byte)};
+            *reinterpret_cast<u32x4*>(tile + (2 * lane + c) * kPitch + b * kMxBlockBytes) = q;
+            bytes[(2 * lane + c) * kColBlocks + b] = static_cast<uint8_t>(byte);
+        }
+    }
+    __shared__ float partial[kWavesPerGroup][kColCols];
+    partial[wave][2 * lane] = total[0];
+    partial[wave][2 * lane + 1] = total[1];
+    __syncthreads();
+    if (sums && threadIdx.x < kColCols && col0 + static_cast<int>(threadIdx.x) < cols) {
+        const int c = threadIdx.x;
+        sums[blockIdx.y * static_cast<int64_t>(cols) + col0 + c] =
+            ((partial[0][c] + partial[1][c]) + partial[2][c]) + partial[3][c];
+    }
+    const int live = codes ? static_cast<int>(min<int64_t>(row_blocks - block0, kColBlocks)) : 0;
+    for (int t = threadIdx.x; t < kColCols * kColBlocks; t += kThreads) {
+        const int c = t / kColBlocks, b = t % kColBlocks;
+        if (b < live && col0 + c < cols) {
+            *reinterpret_cast<u32x4*>(codes + (col0 + c) * ldc + (block0 + b) * kMxBlockBytes) =
+                *reinterpret_cast<const u32x4*>(tile + c * kPitch + b * kMxBlockBytes);
+            scales[(col0 + c) * lds + block0 + b] = bytes[t];
+        }
+    }
+}
+
+// A column a thread, all groups in order.
+__global__ __launch_bounds__(kWave) void mx_add_sums_kernel(const float* __restrict__ sums, int64_t groups, int cols,
+                                                            float* __restrict__ out) {
+    const int c = blockIdx.x * kWave + threadIdx.x;
+    if (c >= cols) return;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int64_t g = 0; g < groups; ++g) s += sums[g * cols + c];
+    out[c] = s;
+}
+
+__global__ __launch_bounds__(kThreads) void mx_zero_kernel(float* __restrict__ out, int64_t rows, int cols, int64_t ldo) {
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
+        for (int c = blockIdx.x * kThreads + threadIdx.x; c < cols; c += gridDim.x * kThreads) out[r * ldo + c] = 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// codes to values
+// ---------------------------------------------------------------------------
+// 8 values a lane.  The scale 255 is NaN, which the converter does not know.
+template <class E, bool VEC>
+__global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t* __restrict__ codes, int64_t ldc,
+                                                                 const uint8_t* __restrict__ scales, int64_t lds,
+                                                                 uint32_t items, uint32_t per_row, int d,
+                                                                 typename E::T* __restrict__ out, int64_t ldo) {
+    using T = typename E::T;
+    const int lane = __lane_id();
+    const uint32_t first = (blockIdx.x * kWavesPerGroup + threadIdx.x / kWave) * kRowItems;
+    uint32_t row = first / per_row, at = first - row * per_row;
+    const uint32_t row_first = row, at_first = at;
+    uint32_t q[kRowItems], s[kRowItems];
+#pragma unroll
+    for (int i = 0; i < kRowItems; ++i) {
+        const int64_t c = static_cast<int64_t>(at) * 512 + lane * 8;
+        if (first + i < items && c < d) {
+            q[i] = *reinterpret_cast<const uint32_t*>(codes + row * ldc + c / 2);
+            s[i] = scales[row * lds + c / kMxBlock];
+        }
+        if (++at == per_row) {
+            at = 0;
+            ++row;
+        }
+    }
+    row = row_first;
+    at = at_first;
+#pragma unroll
+    for (int i = 0; i < kRowItems; ++i) {
+        const int64_t c = static_cast<int64_t>(at) * 512 + lane * 8;
+        if (first + i < items && c < d) {
+            const float scale = __uint_as_float(s[i] << 23);
+            float v[8];
+            const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], scale, 0);
+            const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], scale, 1);
+            const auto e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], scale, 2);
+            const auto f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], scale, 3);
+            v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = e[0], v[5] = e[1], v[6] = f[0], v[7] = f[1];
+            if (s[i] == 255u) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(0x7FC00000u);
+            }
+            T* o = out + row * ldo + c;
+            if (VEC && c + 8 <= d) {
+                if constexpr (sizeof(T) == 4) {
+                    store16<false>(o, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+                    store16<false>(o + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
+                } else {
+                    store16<false>(o, u32x4{E::pack(v[0], v[1]), E::pack(v[2], v[3]), E::pack(v[4], v[5]), E::pack(v[6], v[7])});
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < d) o[j] = E::narrow(v[j]);
+            }
+        }
+        if (++at == per_row) {
+            at = 0;
+            ++row;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// What the product kernels share
+// ---------------------------------------------------------------------------
+// A step is kDepth = 128 bytes of a row: 256 codes, 8 scales.  The matrix
+// instruction takes 128 codes of a row, 32 of them (one block, one scale) in
+// each of the four lanes l / 16: half h of a step takes block 2 (l / 16) + h,
+// so that a lane's two scales of a step are neighbours in memory and reach the
+// instruction as bytes of one register.  Which blocks meet in an instruction
+// only changes the order of the sum.
+template <int SEL>
+__device__ __forceinline__ f32x4 mfma(const i32x4& w, const i32x4& x, const f32x4& acc, uint32_t ws, uint32_t xs) {
+    const i32x8 a = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
+    const i32x8 b = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, SEL, static_cast<int>(ws), SEL,
+                                                            static_cast<int>(xs));
+}
+
+// Between LDS accesses of one wave whose lanes read what other lanes wrote, or
+// write over what other lanes read, without a barrier: the hardware executes a
+// wave's LDS accesses in order, and this holds the compiler to it as well.  No
+// instruction comes of it.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Up to 8 scales of a row from block k on, as two words; past the row's end 0,
+// which no code meets (a 255 there would).
+__device__ __forceinline__ uint2 tail_scales(const uint8_t* row, int k, int blocks) {
+    uint32_t r[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (k + i < blocks) r[i >> 2] |= static_cast<uint32_t>(row[k + i]) << (8 * (i & 3));
+    return make_uint2(r[0], r[1]);
+}
+
+// Four neighbouring outputs of a row.
+template <class E>
+__device__ __forceinline__ void store_out4(const MxProduct& p, int64_t m, int n, const f32x4& acc, bool packed) {
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        v[r] = acc[r];
+        if (p.bias) v[r] = v[r] + E::one(static_cast<const typename E::T*>(p.bias)[min(n + r, p.N - 1)]);
+    }
+    typename E::T* out = static_cast<typename E::T*>(p.out) + m * p.ldo + n;
+    if (packed && n + 4 <= p.N) {
+        if constexpr (sizeof(typename E::T) == 4)
+            store16<false>(out, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                      __float_as_uint(v[3])});
+        else
+            *reinterpret_cast<uint2*>(out) = make_uint2(E::pack(v[0], v[1]), E::pack(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (n + r < p.N) out[r] = E::narrow(v[r]);
+    }
+}
+
+// Whether every row of the output starts at a multiple of `bytes`.
+bool out_aligned(const MxProduct& p, int64_t esize, int64_t bytes) {
+    return reinterpret_cast<uintptr_t>(p.out) % bytes == 0 && (p.M == 1 || p.ldo * esize % bytes == 0);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows
+// ---------------------------------------------------------------------------
+// A workgroup takes 16 MT rows and 16 TN channels.  Its waves split the depth
+// and work alone, each with two steps of both operands in LDS of its own and no
+// barrier; a lane's scales of a step go straight to registers.  At the end each
+// wave leaves its sums where its operands were, and after the one barrier every
+// thread adds four channels of all waves, in their order.
+template <class E, int MT, int TN, int WAVES>
+__global__ __launch_bounds__(WAVES* kWave) void mx_few_rows_kernel(const MxProduct p, int m_tiles, bool packed) {
+    constexpr int BM = MT * 16, BN = TN * 16, kStep = (BM + BN) * kDepth;
+    __shared__ __align__(1024) uint8_t even[WAVES * kStep], odd[WAVES * kStep];
+    const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l16 = lane & 15, q = lane >> 4;
+    // Workgroups id, id + 8, ... run on one XCD: it takes a run of tiles with
+    // the m tiles of a block of channels after each other, so that they share
+    // its weights in that L2.
+    const int per = gridDim.x >> 3, t = static_cast<int>(blockIdx.x & 7) * per + static_cast<int>(blockIdx.x >> 3);
+    const int n0 = t / m_tiles * BN;
+    const int64_t m0 = static_cast<int64_t>(t % m_tiles) * BM;
+    if (n0 >= p.N) return;
+    const int rows = static_cast<int>(min<int64_t>(p.M - m0, BM)), cols = min(p.N - n0, BN);
+    const uint8_t* xb = p.x + m0 * p.ldx;
+    const uint8_t* wb = p.w + static_cast<int64_t>(n0) * p.ldw;
+    const uint8_t* xsb = p.xs + m0 * p.ldxs;
+    const uint8_t* wsb = p.ws + static_cast<int64_t>(n0) * p.ldws;
+    const int ldx = static_cast<int>(p.ldx), ldw = static_cast<int>(p.ldw);
+
+    // Load i covers rows 8 i .. 8 i + 7 of a tile; rows past the matrix read
+    // its last row, their outputs are not stored.
+    const int row0 = lane >> 3, piece0 = lane & 7;
+    int xo[2 * MT], wo[2 * TN], xso[MT], wso[TN];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i)
+        xo[i] = min(8 * i + row0, rows - 1) * ldx + 16 * (piece0 ^ key_x(8 * i + row0));
+#pragma unroll
+    for (int i = 0; i < 2 * TN; ++i)
+        wo[i] = min(8 * i + row0, cols - 1) * ldw + 16 * (piece0 ^ key_w<TN>(8 * i + row0));
+#pragma unroll
+    for (int i = 0; i < MT; ++i) xso[i] = min(16 * i + l16, rows - 1) * static_cast<int>(p.ldxs) + 2 * q;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+        wso[j] = min(operand_channel<TN>(j, l16), cols - 1) * static_cast<int>(p.ldws) + 2 * q;
+    struct Scales {
+        uint32_t x[MT], w[TN];
+    };
+    auto fetch = [&](int s, uint8_t* to, Scales& sc, bool live) {
+        const int range = live ? 0x7FFFFFFF : 0;  // not live: issued, but reads nothing
+        const auto xsr = buf_rsrc(xsb, range), wsr = buf_rsrc(wsb, range);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sc.w[j] = __builtin_amdgcn_raw_buffer_load_b16(wsr, wso[j], 8 * s, 0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sc.x[i] = __builtin_amdgcn_raw_buffer_load_b16(xsr, xso[i], 8 * s, 0);
+        const auto xr = buf_rsrc(xb, range), wr = buf_rsrc(wb, range);
+#pragma unroll
+        for (int i = 0; i < 2 * TN; ++i) load16_to_lds(wr, to + (BM + 8 * i) * kDepth, wo[i], s * kDepth);
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) load16_to_lds(xr, to + 8 * i * kDepth, xo[i], s * kDepth);
+    };
+    f32x4 acc[MT][TN] = {};
+    i32x4 x[2][MT], w[2][TN];
+    auto read = [&](const uint8_t* from) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int row = operand_channel<TN>(j, l16);
+                w[h][j] = *reinterpret_cast<const i32x4*>(from + (BM + row) * kDepth + 16 * ((2 * q + h) ^ key_w<TN>(row)));
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                x[h][i] = *reinterpret_cast<const i32x4*>(from + (16 * i + l16) * kDepth + 16 * ((2 * q + h) ^ key_x(l16)));
+        }
+    };
+    auto multiply = [&](const Scales& sc) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<0>(w[0][j], x[0][i], acc[i][j], sc.w[j], sc.x[i]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<1>(w[1][j], x[1][i], acc[i][j], sc.w[j], sc.x[i]);
+    };
+    const int steps = p.K / kDepth;
+    uint8_t *const e = even + wave * kStep, *const o = odd + wave * kStep;
+    Scales se, so;
+    // A step's operands have arrived in LDS (of the loads on their way only
+    // the next step's are newer), and have left it (lgkmcnt(0)) before the
+    // loads of the step after the next go over them.  Past the last step everything but
+    // the products is done all the same: branches around loads to LDS make
+    // the compiler wait for all of them.
+    auto turn_step = [&](int s, uint8_t* at, Scales& sc) {
+        landed<3 * (MT + TN)>();
+        read(at);
+        const Scales now = sc;
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        fetch(s + 2 * WAVES, at, sc, s + 2 * WAVES < steps);
+        if (s < steps) multiply(now);
+    };
+    fetch(wave, e, se, wave < steps);
+    fetch(wave + WAVES, o, so, wave + WAVES < steps);
+    for (int s = wave; s < steps; s += 2 * WAVES) {
+        turn_step(s, e, se);
+        turn_step(s + WAVES, o, so);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    if (steps * kDepth < p.K && steps % WAVES == wave) {  // the depth's partial step, zeros past K
+        const int k = steps * kDepth, blocks = p.K / kMxBlockBytes;
+        const u32x4 none = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            const int row = 8 * i + row0, at = k + 16 * (piece0 ^ key_x(row));
+            *reinterpret_cast<u32x4*>(e + 8 * i * kDepth + lane * 16) =
+                at < p.K ? load16<false>(xb + static_cast<int64_t>(min(row, rows - 1)) * ldx + at) : none;
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * TN; ++i) {
+            const int row = 8 * i + row0, at = k + 16 * (piece0 ^ key_w<TN>(row));
+            *reinterpret_cast<u32x4*>(e + (BM + 8 * i) * kDepth + lane * 16) =
+                at < p.K ? load16<false>(wb + static_cast<int64_t>(min(row, cols - 1)) * ldw + at) : none;
+        }
+        auto two = [&](const uint8_t* from) {  // the lane's scales: blocks 8 steps + 2 q and the one after it
+            const int b = 8 * steps + 2 * q;
+            uint32_t r = b < blocks ? from[8 * steps] : 0u;
+            if (b + 1 < blocks) r |= static_cast<uint32_t>(from[8 * steps + 1]) << 8;
+            return r;
+        };
+#pragma unroll
+        for (int i = 0; i < MT; ++i) se.x[i] = two(xsb + xso[i]);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) se.w[j] = two(wsb + wso[j]);
+        wave_order();
+        read(e);
+        multiply(se);
+    }
+    wave_order();
+    // Block (i, j) of sums: 1 KB of the wave's own operands, whose last reads
+    // are done.
+    constexpr int kFirst = kStep / 1024 < MT * TN ? kStep / 1024 : MT * TN;
+    static_assert(MT * TN - kFirst <= kStep / 1024, "the sums fit over the operands");
+    auto block = [&](int n, int w) {
+        return n < kFirst ? even + w * kStep + n * 1024 : odd + w * kStep + (n - kFirst) * 1024;
+    };
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            *reinterpret_cast<f32x4*>(block(i * TN + j, wave) + sum_place(l16, q, TN * q + j)) = acc[i][j];
+    __syncthreads();
+    for (int t = threadIdx.x; t < BM * BN / 4; t += WAVES * kWave) {
+        const int r = t / (BN / 4), c = t % (BN / 4);
+        if (r >= rows || 4 * c >= cols) continue;
+        const int n = (r >> 4) * TN + c % TN, at = sum_place(r & 15, c / TN, c);
+        f32x4 sum = *reinterpret_cast<const f32x4*>(block(n, 0) + at);
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) sum += *reinterpret_cast<const f32x4*>(block(n, w) + at);
+        store_out4<E>(p, m0 + r, n0 + 4 * c, sum, packed);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A few tokens, quantized on the way
+// ---------------------------------------------------------------------------
+// The few-rows kernel for a few tokens whose codes every workgroup makes for
+// itself, in LDS, while its first weights are on their way: one launch
+// instead of two, for a reading of the tokens from cache by each workgroup.
+template <class E, int TN, int WAVES, bool VEC>
+__global__ __launch_bounds__(WAVES* kWave) void mx_tokens_kernel(const MxProduct p, int d,
+                                                                 const typename E::T* __restrict__ X, int64_t ldX,
+                                                                 bool packed) {
+    constexpr int BN = TN * 16, kStep = BN * kDepth;
+    __shared__ __align__(1024) uint8_t even[WAVES * kStep], odd[WAVES * kStep];
+    __shared__ __align__(16) uint8_t codes[kMxTokenBytes];
+    __shared__ __align__(8) uint8_t bytes[kMxTokenBytes / kMxBlockBytes];
+    static_assert(TN * 1024 <= kStep, "the sums fit over the operands");
+    const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l16 = lane & 15, q = lane >> 4;
+    const int rows = static_cast<int>(p.M), n0 = blockIdx.x * BN, cols = min(p.N - n0, BN);
+    const uint8_t* wb = p.w + static_cast<int64_t>(n0) * p.ldw;
+    const uint8_t* wsb = p.ws + static_cast<int64_t>(n0) * p.ldws;
+    const int ldw = static_cast<int>(p.ldw);
+    const int row0 = lane >> 3, piece0 = lane & 7;
+    int wo[2 * TN], wso[TN];
+#pragma unroll
+    for (int i = 0; i < 2 * TN; ++i)
+        wo[i] = min(8 * i + row0, cols - 1) * ldw + 16 * (piece0 ^ key_w<TN>(8 * i + row0));
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+        wso[j] = min(operand_channel<TN>(j, l16), cols - 1) * static_cast<int>(p.ldws) + 2 * q;
+    struct Scales {
+        uint32_t w[TN];
+    };
+    auto fetch = [&](int s, uint8_t* to, Scales& sc, bool live) {
+        const int range = live ? 0x7FFFFFFF : 0;
+        const auto wr = buf_rsrc(wb, range), wsr = buf_rsrc(wsb, range);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sc.w[j] = __builtin_amdgcn_raw_buffer_load_b16(wsr, wso[j], 8 * s, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * TN; ++i) load16_to_lds(wr, to + 8 * i * kDepth, wo[i], s * kDepth);
+    };
+    const int steps = p.K / kDepth, all_steps = (p.K + kDepth - 1) / kDepth;
+    uint8_t *const e = even + wave * kStep, *const o = odd + wave * kStep;
+    Scales se, so;
+    fetch(wave, e, se, wave < steps);
+    fetch(wave + WAVES, o, so, wave + WAVES < steps);
+
+    // The tokens' codes and scales, zeros from K to a whole step.
+    const int per_row = (all_steps * 256 + 511) / 512, items = rows * per_row;
+    const int pitch = all_steps * kDepth + kMxTokenPad, pitch_s = all_steps * 8;
+    float keep[kMxTokenItems][8];
+#pragma unroll
+    for (int t = 0; t < kMxTokenItems; ++t) {
+        const int item = wave + t * WAVES;
+        if (item < items) {
+            const int r = item / per_row;
+            load8<E, VEC>(X + r * ldX, (item - r * per_row) * 512 + lane * 8, d, keep[t]);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kMxTokenItems; ++t) {
+        const int item = wave + t * WAVES;
+        if (item < items) {
+            const int r = item / per_row, c = (item - r * per_row) * 512 + lane * 8;
+            const uint32_t byte = scale_byte(quad_max(largest_bits(keep[t])));
+            if (c < all_steps * 256) {
+                *reinterpret_cast<uint32_t*>(codes + r * pitch + c / 2) = pack_codes(keep[t], byte);
+                if ((lane & 3) == 0) bytes[r * pitch_s + c / kMxBlock] = static_cast<uint8_t>(byte);
+            }
+        }
+    }
+    __syncthreads();
+
+    f32x4 acc[TN] = {};
+    i32x4 x[2], w[2][TN];
+    uint32_t xs;
+    const uint8_t* mine = codes + min(l16, rows - 1) * pitch + 32 * q;  // rows past the last repeat it
+    const uint8_t* mine_s = bytes + min(l16, rows - 1) * pitch_s + 2 * q;
+    auto read = [&](const uint8_t* from, int s) {
+        const int at = min(s, all_steps - 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int row = operand_channel<TN>(j, l16);
+                w[h][j] = *reinterpret_cast<const i32x4*>(from + row * kDepth + 16 * ((2 * q + h) ^ key_w<TN>(row)));
+            }
+            x[h] = *reinterpret_cast<const i32x4*>(mine + at * kDepth + 16 * h);
+        }
+        xs = *reinterpret_cast<const uint16_t*>(mine_s + 8 * at);
+    };
+    auto multiply = [&](const Scales& sc) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[j] = mfma<0>(w[0][j], x[0], acc[j], sc.w[j], xs);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[j] = mfma<1>(w[1][j], x[1], acc[j], sc.w[j], xs);
+    };
+    auto turn_step = [&](int s, uint8_t* at, Scales& sc) {  // as in the few-rows kernel
+        landed<3 * TN>();
+        read(at, s);
+        const Scales now = sc;
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        fetch(s + 2 * WAVES, at, sc, s + 2 * WAVES < steps);
+        if (s < steps) multiply(now);
+    };
+    for (int s = wave; s < steps; s += 2 * WAVES) {
+        turn_step(s, e, se);
+        turn_step(s + WAVES, o, so);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    if (steps * kDepth < p.K && steps % WAVES == wave) {
+        const int k = steps * kDepth, blocks = p.K / kMxBlockBytes;
+        const u32x4 none = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 2 * TN; ++i) {
+            const int row = 8 * i + row0, at = k + 16 * (piece0 ^ key_w<TN>(row));
+            *reinterpret_cast<u32x4*>(e + 8 * i * kDepth + lane * 16) =
+                at < p.K ? load16<false>(wb + static_cast<int64_t>(min(row, cols - 1)) * ldw + at) : none;
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int b = 8 * steps + 2 * q;
+            const uint8_t* from = wsb + wso[j] + 8 * steps;
+            se.w[j] = b < blocks ? from[0] : 0u;
+            if (b + 1 < blocks) se.w[j] |= static_cast<uint32_t>(from[1]) << 8;
+        }
+        wave_order();
+        read(e, steps);
+        multiply(se);
+    }
+    wave_order();
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+        *reinterpret_cast<f32x4*>(e + j * 1024 + sum_place(l16, q, TN * q + j)) = acc[j];
+    __syncthreads();
+    for (int t = threadIdx.x; t < rows * BN / 4; t += WAVES * kWave) {
+        const int r = t / (BN / 4), c = t % (BN / 4);
+        if (4 * c >= cols) continue;
+        const uint8_t* at = even + c % TN * 1024 + sum_place(r, c / TN, c);
+        f32x4 sum = *reinterpret_cast<const f32x4*>(at);
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) sum += *reinterpret_cast<const f32x4*>(at + w * kStep);
+        store_out4<E>(p, r, n0 + 4 * c, sum, packed);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: tiles through LDS.
+// ---------------------------------------------------------------------------
+// A workgroup of WM x WN waves takes a tile of 16 TM WM rows and 64 WN
+// channels, two steps of both operands in LDS: while the matrix cores work on
+// one, the loads of the next go into the other.
+template <class E>
+constexpr bool kSums = std::is_same<typename E::T, void>::value;  // the sums themselves, no bias
+
+struct MSums {
+    using T = void;
+};
+
+// A wave's 16 TM x 64 outputs, through a region of LDS that is the wave's own,
+// so that a row leaves as one run of 64 channels.  The 16-byte pieces of a row
+// are xor-ed with the row like the operands'.  NT: stores that do not stay in
+// L2.  m, n: the wave's first row and channel.
+template <class E, class T, int TM, int kRegion, bool NT>
+__device__ __forceinline__ void store_tile(const MxProduct& p, T* out, uint8_t* region, int lane, int64_t m, int n,
+                                           const f32x4 (&acc)[TM][4], const float (&bias)[16], bool packed) {
+    constexpr int kSize = sizeof(T), kRow = 64 * kSize;
+    constexpr int kFit = kRegion / (16 * kRow) < TM ? kRegion / (16 * kRow) : TM;
+    constexpr int kPass = TM % kFit == 0 ? kFit : 1;  // blocks of 16 rows a pass
+    static_assert(kFit >= 1, "a block fits");
+    const int l16 = lane & 15, q = lane >> 4;
+    out += m * p.ldo + n;
+#pragma unroll
+    for (int i0 = 0; i0 < TM; i0 += kPass) {
+#pragma unroll
+        for (int i = 0; i < kPass; ++i) {
+            const int row = 16 * i + l16;
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                v[e] = acc[i0 + i][e >> 2][e & 3];
+                if (!kSums<E> && p.bias) v[e] = v[e] + bias[e];
+            }
+#pragma unroll
+            for (int c = 0; c < kSize; ++c) {  // the lane's 16 kSize bytes
+                u32x4 d;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (kSize == 4) d[r] = __float_as_uint(v[4 * c + r]);
+                    else d[r] = E::pack(v[8 * c + 2 * r], v[8 * c + 2 * r + 1]);
+                }
+                *reinterpret_cast<u32x4*>(region + row * kRow + 16 * ((q * kSize + c) ^ (row & 7))) = d;
+            }
+        }
+        wave_order();
+        if (packed) {
+            constexpr int kPieces = kRow / 16, kRows = kWave / kPieces;  // rows a store instruction
+#pragma unroll
+            for (int r0 = 0; r0 < kPass * 16; r0 += kRows) {
+                const int row = r0 + lane / kPieces, piece = lane % kPieces;
+                const u32x4 d = *reinterpret_cast<const u32x4*>(region + row * kRow + 16 * (piece ^ (row & 7)));
+                store16<NT>(out + (16 * i0 + row) * p.ldo + piece * (16 / kSize), d);
+            }
+        } else {
+            for (int row = 0; row < kPass * 16; ++row) {
+                const int piece = lane / (16 / kSize), at = lane % (16 / kSize);
+                out[(16 * i0 + row) * p.ldo + lane] = reinterpret_cast<const T*>(
+                    region + row * kRow + 16 * (piece ^ (row & 7)))[at];
+            }
+        }
+        if (i0 + kPass < TM) wave_order();  // the next pass goes over the region
+    }
+}
+
+// With E = MSums the depth is split as well: workgroups (x, y) take the bytes
+// from y part_depth on, at most part_depth (whole pairs of steps), and store
+// their sums as they are, one matrix after the other.
+//
+// With STAY a workgroup takes one tile after the other: the first two steps of
+// the next are on their way while the outputs of one leave, through LDS of
+// their own, and the next one's products do not wait for those stores.  For
+// whole pairs of steps and outputs of whole 16-byte pieces.
+template <class E, int WM, int WN, int TM, bool STAY>
+__global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct p, int m_tiles, int n_tiles,
+                                                                int part_depth, bool packed) {
+    constexpr bool kSplit = kSums<E>;
+    using T = std::conditional_t<kSplit, float, typename E::T>;
+    constexpr int TN = 4, kT = WM * WN * kWave;
+    constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
+    constexpr int kXLoads = BM * 8 / kT, kWLoads = BN * 8 / kT;
+    static_assert(BM * 8 % kT == 0 && BN * 8 % kT == 0, "whole rounds of loads");
+    static_assert(BM + BN <= kT, "a thread for the scales of every row");
+    // Arrays by name, and code that names the one it means: the compiler then
+    // sees that the operands it reads are not those on their way, and puts no
+    // wait for the loads before the reads.
+    __shared__ __align__(1024) uint8_t x_even[BM * kDepth], x_odd[BM * kDepth], w_even[BN * kDepth], w_odd[BN * kDepth];
+    constexpr int kPassing = 1024 * sizeof(T);  // 16 rows of outputs a wave
+    __shared__ __align__(1024) uint8_t passing[STAY ? WM * WN * kPassing : 16];
+    // The scales of a pair of steps, 16 bytes a row, so that word q of a row
+    // has the four scales of lane group q: halves 0 and 1 of the even step,
+    // then of the odd one.  Threads past the last row carry it once more.
+    __shared__ __align__(16) uint8_t scales[2][kT * 16];
+    const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l16 = lane & 15, q = lane >> 4;
+    const int wm = (wave % WM) * TM * 16, wn = (wave / WM) * TN * 16;
+
+    // Each XCD works through a contiguous range of tiles, in groups of 8 rows
+    // of tiles, so that its L2 holds the operands its workgroups share.
+    const int tiles = m_tiles * n_tiles;
+    const int per = (tiles + 7) / 8;
+    const int end = min(static_cast<int>(blockIdx.x & 7) * per + per, tiles);
+    int t = static_cast<int>(blockIdx.x & 7) * per + static_cast<int>(blockIdx.x >> 3);
+    if (t >= end) return;
+    const int first = kSplit ? static_cast<int>(blockIdx.y) * part_depth : 0;
+    const int K = kSplit ? min(p.K - first, part_depth) : p.K;
+    int64_t m0;
+    int n0;
+    const uint8_t *xb, *wb, *sb;
+    auto to_tile = [&] {
+        constexpr int kGroupM = 8;
+        const int group = t / (kGroupM * n_tiles), in = t - group * kGroupM * n_tiles;
+        const int gm = min(kGroupM, m_tiles - group * kGroupM);
+        // The last tiles of a row or column are moved inside the matrix (M >=
+        // BM, N >= BN): outputs computed twice get the same values twice.
+        m0 = min<int64_t>(static_cast<int64_t>(group * kGroupM + in % gm) * BM, p.M - BM);
+        n0 = min(in / gm * BN, p.N - BN);
+        xb = p.x + m0 * p.ldx + first;
+        wb = p.w + static_cast<int64_t>(n0) * p.ldw + first;
+        // the row whose scales this thread carries
+        const int r = threadIdx.x;
+        sb = r < BM ? p.xs + (m0 + r) * p.ldxs : p.ws + (n0 + min(r - BM, BN - 1)) * p.ldws;
+        sb += first / kMxBlockBytes;
+    };
+    to_tile();
+    // A round of loads covers kRound rows; the keys repeat from round to
+    // round, but for the weights' where a round is shorter than their period.
+    constexpr int kRound = kT / 8;
+    constexpr bool kTwoKeys = kRound % (8 * TN) != 0;
+    const int row0 = (wave * kWave + lane) >> 3, piece0 = lane & 7;
+    const int ldx = static_cast<int>(p.ldx), ldw = static_cast<int>(p.ldw);
+    const int xo = row0 * ldx + 16 * (piece0 ^ key_x(row0));
+    const int wo0 = row0 * ldw + 16 * (piece0 ^ key_w<TN>(row0));
+    const int wo1 = kTwoKeys ? row0 * ldw + 16 * (piece0 ^ key_w<TN>(row0 + kRound)) : wo0;
+    // Loads that are not `live` are issued all the same, to an empty range, and
+    // read no memory: a branch around them would make the compiler wait.
+    auto fetch = [&](int k, uint8_t* xd, uint8_t* wd, bool live) {
+        const int range = live ? 0x7FFFFFFF : 0;
+        const auto xr = buf_rsrc(xb, range), wr = buf_rsrc(wb, range);
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i)
+            load16_to_lds(xr, xd + (i * kT + wave * kWave) * 16, xo, k + i * kRound * ldx);
+#pragma unroll
+        for (int i = 0; i < kWLoads; ++i)
+            load16_to_lds(wr, wd + (i * kT + wave * kWave) * 16, (i & 1) ? wo1 : wo0, k + i * kRound * ldw);
+    };
+    // Scales of a pair of steps, as they stand in memory, to their places.
+    auto put_scales = [&](uint8_t* to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+        *reinterpret_cast<u32x4*>(to + threadIdx.x * 16) =
+            u32x4{__builtin_amdgcn_perm(c, a, 0x05040100u), __builtin_amdgcn_perm(c, a, 0x07060302u),
+                  __builtin_amdgcn_perm(d, b, 0x05040100u), __builtin_amdgcn_perm(d, b, 0x07060302u)};
+    };
+
+    // Half a step's operands (4 blocks) in LDS; the keys do not change with i
+    // and j, 16 and 4 rows on.
+    const int w_row = operand_channel<TN>(0, l16);
+    const int xp[2] = {(wm + l16) * kDepth + 16 * ((2 * q) ^ key_x(l16)),
+                       (wm + l16) * kDepth + 16 * ((2 * q + 1) ^ key_x(l16))};
+    const int wp[2] = {(wn + w_row) * kDepth + 16 * ((2 * q) ^ key_w<TN>(w_row)),
+                       (wn + w_row) * kDepth + 16 * ((2 * q + 1) ^ key_w<TN>(w_row))};
+    const int xsp = (wm + l16) * 16 + 4 * q, wsp = (BM + wn + w_row) * 16 + 4 * q;
+    f32x4 acc[TM][TN];
+    i32x4 x[TM], w0[TN], w1[TN];
+    uint32_t sx[TM], sw[TN];
+    auto read_x = [&](const uint8_t* xd, int h, int i) {
+        x[i] = *reinterpret_cast<const i32x4*>(xd + xp[h] + 16 * i * kDepth);
+    };
+    auto read_w = [&](const uint8_t* wd, int h, int j) {
+        return *reinterpret_cast<const i32x4*>(wd + wp[h] + 4 * j * kDepth);
+    };
+    auto read = [&](const uint8_t* xd, const uint8_t* wd, int h, i32x4 (&w)[TN]) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) w[j] = read_w(wd, h, j);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) read_x(xd, h, i);
+    };
+    auto read_scales = [&](const uint8_t* from) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sx[i] = *reinterpret_cast<const uint32_t*>(from + xsp + 16 * i * 16);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sw[j] = *reinterpret_cast<const uint32_t*>(from + wsp + 4 * j * 16);
+    };
+    // The products of half a step; each operand of x is replaced by half h of
+    // (xn, wn) as soon as its last product is issued, and the next weights are
+    // read on the way.
+    constexpr int kPer = TM < TN ? TN / TM : 1;
+    auto multiply = [&](auto sel, const i32x4 (&w)[TN], const uint8_t* xn, const uint8_t* wn, int h, i32x4 (&w_next)[TN]) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<decltype(sel)::value>(w[j], x[i], acc[i][j], sw[j], sx[i]);
+            read_x(xn, h, i);
+#pragma unroll
+            for (int j = i * kPer; j < (i + 1) * kPer && j < TN; ++j) w_next[j] = read_w(wn, h, j);
+            __builtin_amdgcn_sched_group_barrier(0x008, TN, 0);
+            if (i * kPer < TN) __builtin_amdgcn_sched_group_barrier(0x100, 1 + kPer, 0);
+            else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+    };
+    auto multiply_all = [&](auto sel, const i32x4 (&w)[TN]) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<decltype(sel)::value>(w[j], x[i], acc[i][j], sw[j], sx[i]);
+    };
+    using Sel0 = std::integral_constant<int, 0>;
+    using Sel1 = std::integral_constant<int, 1>;
+    using Sel2 = std::integral_constant<int, 2>;
+    using Sel3 = std::integral_constant<int, 3>;
+
+    // Software pipeline: while half a step is multiplied the next half is read
+    // from LDS, and the step after it is on its way from memory.  The one
+    // barrier of a step stands between its halves: past it every wave's loads
+    // of step s + 1 have arrived and nobody reads step s any more, so that
+    // step s + 2 may be fetched over it.
+    auto arrive = [&] {
+        __builtin_amdgcn_s_waitcnt(0);  // loads to LDS are counted with the vector loads: a barrier does not wait for them
+        __syncthreads();
+    };
+    const int steps = K / (2 * kDepth) * 2, pairs = steps / 2;
+    u32x4 carried = {0u, 0u, 0u, 0u};  // scales of a pair on their way
+    // Past the last pair it is loaded again: a branch in the loop would let the
+    // compiler move the products behind it.
+    auto fetch_scales = [&](int pair) { carried = *reinterpret_cast<const u32x4_any*>(sb + 16 * min(pair, pairs - 1)); };
+    constexpr int kStores = TM * sizeof(T);  // a wave's stores of a tile
+    bool fetched = false;
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // The pipeline takes pairs of steps.  What the depth has beyond them
+        // comes first, a step at a time, zeros past K.
+        if constexpr (!STAY) {
+            for (int k = steps * kDepth; k < K; k += kDepth) {
+                const u32x4 none = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int i = 0; i < kXLoads; ++i) {
+                    const int row = row0 + i * kRound, at = k + 16 * (piece0 ^ key_x(row));
+                    *reinterpret_cast<u32x4*>(x_even + row * kDepth + 16 * piece0) =
+                        at < K ? load16<false>(xb + static_cast<int64_t>(row) * ldx + at) : none;
+                }
+#pragma unroll
+                for (int i = 0; i < kWLoads; ++i) {
+                    const int row = row0 + i * kRound, at = k + 16 * (piece0 ^ key_w<TN>(row));
+                    *reinterpret_cast<u32x4*>(w_even + row * kDepth + 16 * piece0) =
+                        at < K ? load16<false>(wb + static_cast<int64_t>(row) * ldw + at) : none;
+                }
+                const uint2 s = tail_scales(sb, k / kMxBlockBytes, K / kMxBlockBytes);
+                put_scales(scales[0], s.x, s.y, 0u, 0u);
+                __syncthreads();
+                read_scales(scales[0]);
+                read(x_even, w_even, 0, w0);
+                multiply_all(Sel0{}, w0);
+                read(x_even, w_even, 1, w0);
+                multiply_all(Sel1{}, w0);
+                __syncthreads();
+            }
+        }
+        if (pairs > 0) fetch_scales(0);
+        if (STAY && fetched) {
+            landed<kStores>();  // the operands are older than the last tile's stores
+        } else {
+            fetch(0, x_even, w_even, steps > 0);
+            fetch(kDepth, x_odd, w_odd, steps > 0);
+            __builtin_amdgcn_s_waitcnt(0);
+        }
+        put_scales(scales[0], carried[0], carried[1], carried[2], carried[3]);
+        __syncthreads();
+        read(x_even, w_even, 0, w0);
+        for (int s = 0; s < steps; s += 2) {  // past the last step it reads operands that nobody multiplies
+            read_scales(scales[(s >> 1) & 1]);
+            multiply(Sel0{}, w0, x_even, w_even, 1, w1);
+            arrive();
+            fetch((s + 2) * kDepth, x_even, w_even, s + 2 < steps);
+            fetch_scales((s >> 1) + 1);
+            multiply(Sel1{}, w1, x_odd, w_odd, 0, w0);
+            multiply(Sel2{}, w0, x_odd, w_odd, 1, w1);
+            __builtin_amdgcn_s_waitcnt(0);
+            put_scales(scales[((s >> 1) + 1) & 1], carried[0], carried[1], carried[2], carried[3]);
+            __syncthreads();
+            fetch((s + 3) * kDepth, x_odd, w_odd, s + 3 < steps);
+            multiply(Sel3{}, w1, x_even, w_even, 0, w0);
+        }
+        // What follows runs once a tile: its addresses are made anew from the
+        // thread's number, so that the loop above keeps no registers for them.
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        T* out = static_cast<T*>(p.out);
+        if constexpr (kSplit) out += blockIdx.y * p.M * p.ldo;
+        const int64_t m = m0 + wm;
+        const int n = n0 + wn;
+        float bias[16];
+        if constexpr (!kSplit) {
+            if (p.bias) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) bias[e] = E::one(static_cast<const T*>(p.bias)[n + 16 * ((tid & 63) >> 4) + e]);
+            }
+        }
+        arrive();  // the operands are read, and the empty loads of the last steps are done
+        if constexpr (STAY) {
+            t += static_cast<int>(gridDim.x >> 3);
+            fetched = t < end;
+            if (fetched) {
+                to_tile();
+                fetch(0, x_even, w_even, true);
+                fetch(kDepth, x_odd, w_odd, true);
+            }
+            store_tile<E, T, TM, kPassing, true>(p, out, passing + wave * kPassing, tid & 63, m, n, acc, bias, true);
+            if (!fetched) return;
+        } else {
+            // A region for each wave, in the array that has room for it.
+            constexpr int kPart = (BM < BN ? BM : BN) >= 256 ? 16384 : (BM < BN ? BM : BN) >= 64 ? 8192 : 4096;
+            static_assert(kPart <= BM * kDepth && kPart <= BN * kDepth, "a region fits into either array");
+            constexpr int kInX = BM * kDepth / kPart, kInW = BN * kDepth / kPart;
+            static_assert(2 * kInX + 2 * kInW >= WM * WN, "a region for every wave");
+            uint8_t* region = wave < kInX ? x_even + wave * kPart
+                              : wave < 2 * kInX ? x_odd + (wave - kInX) * kPart
+                              : wave < 2 * kInX + kInW ? w_even + (wave - 2 * kInX) * kPart
+                                                       : w_odd + (wave - 2 * kInX - kInW) * kPart;
+            store_tile<E, T, TM, kPart, (BM >= 128 && !kSplit)>(p, out, region, tid & 63, m, n, acc, bias,
+                                                                packed && (n0 * sizeof(T)) % 16 == 0);
+            return;
+        }
+    }
+}
+
+// Adds the parts' sums and the bias: four channels a thread.
+template <class E>
+__global__ __launch_bounds__(kThreads) void mx_add_parts_kernel(const MxProduct p, const float* __restrict__ sums,
+                                                                int64_t ld, int parts, bool packed) {
+    const uint32_t pieces = static_cast<uint32_t>(p.N + 3) / 4, at = blockIdx.x * kThreads + threadIdx.x;
+    const uint32_t m = at / pieces;
+    if (m >= p.M) return;
+    const int n = static_cast<int>(at - m * pieces) * 4;
+    const float* s = sums + m * ld + n;
+    f32x4 acc = *reinterpret_cast<const f32x4*>(s);
+    for (int i = 1; i < parts; ++i) acc += *reinterpret_cast<const f32x4*>(s + i * (p.M * ld));
+    store_out4<E>(p, m, n, acc, packed);
+}
+
+template <class E, int MT, int TN, int WAVES>
+int launch_few(const MxProduct& p, void* stream) {
+    const int m_tiles = static_cast<int>((p.M + MT * 16 - 1) / (MT * 16)), n_tiles = (p.N + TN * 16 - 1) / (TN * 16);
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
+    hipLaunchKernelGGL((mx_few_rows_kernel<E, MT, TN, WAVES>), dim3(grid), dim3(WAVES * kWave), 0,
+                       static_cast<hipStream_t>(stream), p, m_tiles, out_aligned(p, sizeof(typename E::T), 4 * sizeof(typename E::T)));
+    return static_cast<int>(hipGetLastError());
+}
+
+template <class E, int WM, int WN, int TM, bool STAY>
+int launch_tile(const MxProduct& p, void* stream) {
+    constexpr int BM = WM * TM * 16, BN = WN * 64;
+    const int m_tiles = static_cast<int>((p.M + BM - 1) / BM), n_tiles = (p.N + BN - 1) / BN;
+    unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
+    if (STAY) {  // one workgroup a compute unit, the same number on each XCD
+        const unsigned resident = device_cu_count() < 8 ? 8u : static_cast<unsigned>(device_cu_count()) / 8 * 8;
+        if (grid > resident) grid = resident;
+    }
+    hipLaunchKernelGGL((mx_tile_kernel<E, WM, WN, TM, STAY>), dim3(grid), dim3(WM * WN * kWave), 0,
+                       static_cast<hipStream_t>(stream), p, m_tiles, n_tiles, 0, out_aligned(p, sizeof(typename E::T), 16));
+    return static_cast<int>(hipGetLastError());
+}
+
+// Tiles of 128 x 128 with the depth in parts (as many as split_depth leaves).
+template <class E>
+int launch_split(const MxProduct& p, int parts, void* workspace, void* stream) {
+    const int m_tiles = static_cast<int>((p.M + kSplitTile - 1) / kSplitTile);
+    const int n_tiles = (p.N + kSplitTile - 1) / kSplitTile;
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
+    const int part_depth = split_depth(p.K, parts);
+    MxProduct s = p;
+    s.out = workspace;
+    s.ldo = sums_ld(p.N);
+    hipLaunchKernelGGL((mx_tile_kernel<MSums, 2, 2, 4, false>), dim3(grid, parts), dim3(4 * kWave), 0,
+                       static_cast<hipStream_t>(stream), s, m_tiles, n_tiles, part_depth, true);
+    const int e = static_cast<int>(hipGetLastError());
+    if (e != 0) return e;
+    const uint32_t pieces = static_cast<uint32_t>(p.M) * (static_cast<uint32_t>(p.N + 3) / 4);
+    hipLaunchKernelGGL((mx_add_parts_kernel<E>), dim3((pieces + kThreads - 1) / kThreads), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), p, static_cast<const float*>(workspace), s.ldo, parts,
+                       out_aligned(p, sizeof(typename E::T), 4 * sizeof(typename E::T)));
+    return static_cast<int>(hipGetLastError());
+}
+
+template <class E>
+int launch_few_tile(const MxProduct& p, Int8Few f, void* stream) {
+    switch (10 * f.mt + f.tn) {
+        case 11: return p.K <= 4096 ? launch_few<E, 1, 1, 4>(p, stream) : launch_few<E, 1, 1, 8>(p, stream);
+        case 12: return launch_few<E, 1, 2, 8>(p, stream);
+        case 13: return launch_few<E, 1, 3, 8>(p, stream);
+        case 14: return launch_few<E, 1, 4, 7>(p, stream);
+        case 22: return launch_few<E, 2, 2, 8>(p, stream);
+        case 24: return launch_few<E, 2, 4, 6>(p, stream);
+        case 32: return launch_few<E, 3, 2, 6>(p, stream);
+        case 34: return launch_few<E, 3, 4, 5>(p, stream);
+        case 44: return launch_few<E, 4, 4, 4>(p, stream);
+        case 53: return launch_few<E, 5, 3, 4>(p, stream);
+        case 54: return launch_few<E, 5, 4, 4>(p, stream);
+        case 73: return launch_few<E, 7, 3, 4>(p, stream);
+        default: return launch_few<E, 8, 3, 3>(p, stream);
+    }
+}
+
+template <class E>
+int launch_form(const MxProduct& p, const Int8Choice& c, void* workspace, void* stream) {
+    if (c.parts > 1) return launch_split<E>(p, c.parts, workspace, stream);
+    switch (c.bm) {
+        case 0: return launch_few_tile<E>(p, c.few, stream);
+        case 32: return launch_tile<E, 2, 2, 1, false>(p, stream);
+        case 64: return launch_tile<E, 2, 2, 2, false>(p, stream);
+        case 128: return launch_tile<E, 2, 2, 4, false>(p, stream);
+        default: break;
+    }
+    return launch_tile<E, 2, 4, 8, false>(p, stream);
+}
+
+template <class E>
+int launch_product_e(const MxProduct& whole, void* workspace, void* stream) {
+    using T = typename E::T;
+    const int64_t cus = device_cu_count();
+    for (int64_t n = 0; n < whole.N; n += kMaxChannels) {
+        for (int64_t m = 0; m < whole.M; m += kRowBlock) {
+            MxProduct p = whole;
+            p.M = whole.M - m < kRowBlock ? whole.M - m : kRowBlock;
+            p.N = static_cast<int>(whole.N - n < kMaxChannels ? whole.N - n : kMaxChannels);
+            p.x += m * p.ldx;
+            p.xs += m * p.ldxs;
+            p.w += n * p.ldw;
+            p.ws += n * p.ldws;
+            if (p.bias) p.bias = static_cast<const T*>(p.bias) + n;
+            p.out = static_cast<T*>(p.out) + m * p.ldo + n;
+            const int e = launch_form<E>(p, choose_form(p.M, p.N, p.K, cus), workspace, stream);
+            if (e != 0) return e;
+        }
+    }
+    return 0;
+}
+
+template <class E, int TN, int WAVES>
+int launch_tokens_t(const MxProduct& p, int d, const void* X, int64_t ldX, bool vec, void* stream) {
+    const dim3 grid((p.N + TN * 16 - 1) / (TN * 16)), block(WAVES * kWave);
+    const auto* x = static_cast<const typename E::T*>(X);
+    const bool packed = out_aligned(p, sizeof(typename E::T), 4 * sizeof(typename E::T));
+    if (vec)
+        hipLaunchKernelGGL((mx_tokens_kernel<E, TN, WAVES, true>), grid, block, 0, static_cast<hipStream_t>(stream), p, d,
+                           x, ldX, packed);
+    else
+        hipLaunchKernelGGL((mx_tokens_kernel<E, TN, WAVES, false>), grid, block, 0, static_cast<hipStream_t>(stream), p, d,
+                           x, ldX, packed);
+    return static_cast<int>(hipGetLastError());
+}
+
+template <class E>
+int launch_tokens_e(const MxProduct& p, int d, const void* X, int64_t ldX, bool vec, void* stream) {
+    const int cus = device_cu_count();
+    auto rounds = [&](int channels) { return (p.N + channels * cus - 1) / (channels * cus); };
+    const int c16 = rounds(16), c48 = 2 * rounds(48), c64 = 3 * rounds(64);
+    if (c64 <= c48 && c64 <= c16) return launch_tokens_t<E, 4, 8>(p, d, X, ldX, vec, stream);
+    if (c48 <= c16) return launch_tokens_t<E, 3, 8>(p, d, X, ldX, vec, stream);
+    return launch_tokens_t<E, 1, 16>(p, d, X, ldX, vec, stream);
+}
+
+// Rows of a launch: their pieces of 512 values count in 32 bits.
+int64_t rows_a_launch(int64_t per_row) { return (int64_t(1) << 30) / per_row; }
+
+template <class E>
+int launch_quantize_e(const void* X, int64_t rows, int d, int64_t ldx, uint8_t* codes, int64_t ldc, uint8_t* scales,
+                      int64_t lds, bool vec, void* stream) {
+    const uint32_t per_row = static_cast<uint32_t>((d + 511) / 512);
+    const int64_t most = rows_a_launch(per_row);
+    for (int64_t r = 0; r < rows; r += most) {
+        const uint32_t items = static_cast<uint32_t>((rows - r < most ? rows - r : most) * per_row);
+        const dim3 grid((items + kWavesPerGroup * kRowItems - 1) / (kWavesPerGroup * kRowItems));
+        const auto* x = static_cast<const typename E::T*>(X) + r * ldx;
+        if (vec)
+            hipLaunchKernelGGL((mx_quantize_kernel<E, true>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream), x,
+                               items, per_row, d, ldx, codes + r * ldc, ldc, scales + r * lds, lds);
+        else
+            hipLaunchKernelGGL((mx_quantize_kernel<E, false>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream), x,
+                               items, per_row, d, ldx, codes + r * ldc, ldc, scales + r * lds, lds);
+        const int e = static_cast<int>(hipGetLastError());
+        if (e != 0) return e;
+    }
+    return 0;
+}
+
+template <class E>
+int launch_columns_e(const void* X, int64_t rows, int cols, int64_t ldx, uint8_t* codes, int64_t ldc, uint8_t* scales,
+                     int64_t lds, float* sums, void* stream) {
+    using T = typename E::T;
+    static_assert(kMxSumRows == int64_t(kMxBlock) * kColBlocks, "a row of sums a row of workgroups");
+    constexpr int64_t kRows = int64_t(kMxBlock) * kColBlocks * 32768;  // of a launch: its grid's second axis
+    const bool pairs = reinterpret_cast<uintptr_t>(X) % (2 * sizeof(T)) == 0 && (rows == 1 || ldx % 2 == 0);
+    for (int64_t r = 0; r < rows; r += kRows) {
+        const int64_t n = rows - r < kRows ? rows - r : kRows;
+        const dim3 grid((cols + kColCols - 1) / kColCols,
+                        static_cast<unsigned>((n + kMxBlock * kColBlocks - 1) / (kMxBlock * kColBlocks)));
+        const T* x = static_cast<const T*>(X) + r * ldx;
+        uint8_t *c = codes ? codes + r / 2 : nullptr, *s = scales ? scales + r / kMxBlock : nullptr;
+        float* f = sums ? sums + r / kMxSumRows * cols : nullptr;
+        if (pairs)
+            hipLaunchKernelGGL((mx_quantize_columns_kernel<E, true>), grid, dim3(kThreads), 0,
+                               static_cast<hipStream_t>(stream), x, n, cols, ldx, c, ldc, s, lds, f);
+        else
+            hipLaunchKernelGGL((mx_quantize_columns_kernel<E, false>), grid, dim3(kThreads), 0,
+                               static_cast<hipStream_t>(stream), x, n, cols, ldx, c, ldc, s, lds, f);
+        const int e = static_cast<int>(hipGetLastError());
+        if (e != 0) return e;
+    }
+    return 0;
+}
+
+template <class E>
+int launch_dequantize_e(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t rows, int d,
+                        void* out, int64_t ldo, bool vec, void* stream) {
+    const uint32_t per_row = static_cast<uint32_t>((d + 511) / 512);
+    const int64_t most = rows_a_launch(per_row);
+    for (int64_t r = 0; r < rows; r += most) {
+        const uint32_t items = static_cast<uint32_t>((rows - r < most ? rows - r : most) * per_row);
+        const dim3 grid((items + kWavesPerGroup * kRowItems - 1) / (kWavesPerGroup * kRowItems));
+        auto* o = static_cast<typename E::T*>(out) + r * ldo;
+        if (vec)
+            hipLaunchKernelGGL((mx_dequantize_kernel<E, true>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream),
+                               codes + r * ldc, ldc, scales + r * lds, lds, items, per_row, d, o, ldo);
+        else
+            hipLaunchKernelGGL((mx_dequantize_kernel<E, false>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream),
+                               codes + r * ldc, ldc, scales + r * lds, lds, items, per_row, d, o, ldo);
+        const int e = static_cast<int>(hipGetLastError());
+        if (e != 0) return e;
+    }
+    return 0;
+}
+
+}  // namespace
+
+#define KBIT_BY_DTYPE(F, ...)                       \
+    switch (t) {                                    \
+        case Dtype::fp32: return F<QF32>(__VA_ARGS__); \
+        case Dtype::fp16: return F<QF16>(__VA_ARGS__); \
+        default: return F<QB16>(__VA_ARGS__);       \
+    }
+
+int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx, uint8_t* codes, int64_t ldc,
+                       uint8_t* scales, int64_t lds, bool vec, void* stream) {
+    KBIT_BY_DTYPE(launch_quantize_e, X, rows, d, ldx, codes, ldc, scales, lds, vec, stream)
+}
+
+int launch_mx_quantize_columns(Dtype t, const void* X, int64_t rows, int cols, int64_t ldx, uint8_t* codes, int64_t ldc,
+                               uint8_t* scales, int64_t lds, float* sums, void* stream) {
+    KBIT_BY_DTYPE(launch_columns_e, X, rows, cols, ldx, codes, ldc, scales, lds, sums, stream)
+}
+
+int launch_mx_add_sums(const float* sums, int64_t groups, int cols, float* out, void* stream) {
+    hipLaunchKernelGGL(mx_add_sums_kernel, dim3((cols + kWave - 1) / kWave), dim3(kWave), 0,
+                       static_cast<hipStream_t>(stream), sums, groups, cols, out);
+    return static_cast<int>(hipGetLastError());
+}
+
+int launch_mx_zero(float* out, int64_t rows, int cols, int64_t ldo, void* stream) {
+    const dim3 grid(cols < 16 * kThreads ? (cols + kThreads - 1) / kThreads : 16, static_cast<unsigned>(rows < 4096 ? rows : 4096));
+    hipLaunchKernelGGL(mx_zero_kernel, grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream), out, rows, cols, ldo);
+    return static_cast<int>(hipGetLastError());
+}
+
+int launch_mx_dequantize(Dtype t, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t rows,
+                         int d, void* out, int64_t ldo, bool vec, void* stream) {
+    KBIT_BY_DTYPE(launch_dequantize_e, codes, ldc, scales, lds, rows, d, out, ldo, vec, stream)
+}
+
+int launch_mx_product(Dtype t, const MxProduct& p, void* workspace, void* stream) {
+    KBIT_BY_DTYPE(launch_product_e, p, workspace, stream)
+}
+
+int launch_mx_tokens(Dtype t, const MxProduct& p, int d, const void* X, int64_t ldX, bool vec, void* stream) {
+    KBIT_BY_DTYPE(launch_tokens_e, p, d, X, ldX, vec, stream)
+}
+
+}  // namespace kbit
