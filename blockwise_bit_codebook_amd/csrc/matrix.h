@@ -56,6 +56,49 @@ __device__ __forceinline__ void load8(const typename E::T* row, int c, int d, fl
     }
 }
 
+// 16 and 8 bytes at any address of an element: the memory unit takes them.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+__device__ __forceinline__ u32x4 load16_any(const void* p) { return *reinterpret_cast<const u32x4_any*>(p); }
+__device__ __forceinline__ void store16_any(void* p, const u32x4& v) { *reinterpret_cast<u32x4_any*>(p) = v; }
+
+// 8 elements of a row from column c at any alignment, as they stand, 0 beyond d.
+template <class E>
+__device__ __forceinline__ void load8_raw(const typename E::T* row, int c, int d, u32x4 (&r)[E::kVec]) {
+    if (c + 8 <= d) {
+#pragma unroll
+        for (int i = 0; i < E::kVec; ++i) r[i] = load16_any(row + c + 4 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E::kVec; ++i) r[i] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (c + e >= d) continue;
+            if constexpr (sizeof(typename E::T) == 4) r[e / 4][e % 4] = __float_as_uint(row[c + e]);
+            else r[0][e / 2] |= static_cast<uint32_t>(row[c + e]) << (16 * (e & 1));
+        }
+    }
+}
+
+// 8 values to a row from column c at any alignment, none beyond d.
+template <class E>
+__device__ __forceinline__ void store8(typename E::T* row, int c, int d, const float (&v)[8]) {
+    if (c + 8 <= d) {
+        if constexpr (sizeof(typename E::T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 4)
+                store16_any(row + c + i, u32x4{__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                                               __float_as_uint(v[i + 3])});
+        } else {
+            store16_any(row + c, u32x4{E::pack(v[0], v[1]), E::pack(v[2], v[3]), E::pack(v[4], v[5]), E::pack(v[6], v[7])});
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < d) row[c + e] = E::narrow(v[e]);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // operands in LDS
 // ---------------------------------------------------------------------------

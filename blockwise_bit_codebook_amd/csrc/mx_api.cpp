@@ -25,9 +25,6 @@ bool rows_ok(int64_t rows, int64_t d, int64_t ld) {
 }
 bool depth_ok(int64_t d) { return d >= 1 && d <= kMxMaxDepth; }
 bool codes_aligned(const void* p, int64_t rows, int64_t ld) { return aligned(p, 16) && (rows <= 1 || ld % 16 == 0); }
-bool vec_rows(const void* p, int64_t rows, int64_t ld, Dtype t) {
-    return aligned(p, 16) && (rows <= 1 || ld * elem_size(t) % 16 == 0);
-}
 
 // Codes and scales of rows of d values.
 bool coded_rows_ok(int64_t rows, int64_t d, int64_t ldc, int64_t lds) {
@@ -41,18 +38,18 @@ int do_quantize(Dtype t, const void* X, int64_t rows, int32_t d, int64_t ldx, ui
     if (!X || !codes || !scales) return KBIT_EINVAL;
     if (!aligned(X, elem_size(t)) || !codes_aligned(codes, rows, ldc)) return KBIT_EALIGN;
     if (!device_usable()) return KBIT_EDEVICE;
-    return map_launch(launch_mx_quantize(t, X, rows, d, ldx, codes, ldc, scales, lds, vec_rows(X, rows, ldx, t), stream));
+    return map_launch(launch_mx_quantize(t, X, rows, d, ldx, MxCoded{codes, scales, ldc, lds}, stream));
 }
 
 int do_quantize_columns(Dtype t, const void* X, int64_t rows, int32_t cols, int64_t ldx, uint8_t* codes, int64_t ldc,
                         uint8_t* scales, int64_t lds, void* stream) {
-    if (!depth_ok(rows) || cols < 0 || (cols > 0 && !rows_ok(rows, cols, ldx)) || !coded_rows_ok(cols, rows, ldc, lds))
+    if (!depth_ok(rows) || cols < 0 || cols > kMxMaxColumns || (cols > 0 && !rows_ok(rows, cols, ldx)) || !coded_rows_ok(cols, rows, ldc, lds))
         return KBIT_EINVAL;
     if (cols == 0) return KBIT_OK;
     if (!X || !codes || !scales) return KBIT_EINVAL;
     if (!aligned(X, elem_size(t)) || !codes_aligned(codes, cols, ldc)) return KBIT_EALIGN;
     if (!device_usable()) return KBIT_EDEVICE;
-    return map_launch(launch_mx_quantize_columns(t, X, rows, cols, ldx, codes, ldc, scales, lds, nullptr, stream));
+    return map_launch(launch_mx_quantize_columns(t, X, rows, cols, ldx, MxCoded{codes, scales, ldc, lds}, MxCoded{}, nullptr, stream));
 }
 
 int do_dequantize(Dtype t, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t rows, int32_t d,
@@ -62,7 +59,7 @@ int do_dequantize(Dtype t, const uint8_t* codes, int64_t ldc, const uint8_t* sca
     if (!out || !codes || !scales) return KBIT_EINVAL;
     if (!aligned(out, elem_size(t)) || !codes_aligned(codes, rows, ldc)) return KBIT_EALIGN;
     if (!device_usable()) return KBIT_EDEVICE;
-    return map_launch(launch_mx_dequantize(t, codes, ldc, scales, lds, rows, d, out, ldo, vec_rows(out, rows, ldo, t), stream));
+    return map_launch(launch_mx_dequantize(t, codes, ldc, scales, lds, rows, d, out, ldo, stream));
 }
 
 // Rows of an operand in reach of the kernels' 32-bit offsets.
@@ -92,6 +89,8 @@ int do_linear(Dtype t, MxProduct p, int64_t d, void* workspace, int64_t workspac
     return map_launch(launch_mx_product(t, p, workspace, stream));
 }
 
+MxCoded coded_in(uint8_t* at, const MxRows& r) { return MxCoded{at, at + r.scales, r.ldc, r.lds}; }
+
 int do_linear_dynamic(Dtype t, const void* X, int64_t ldX, MxProduct p, int64_t d, void* workspace,
                       int64_t workspace_bytes, void* stream) {
     if (!depth_ok(d) || !rows_ok(p.M, d, ldX)) return KBIT_EINVAL;
@@ -103,16 +102,15 @@ int do_linear_dynamic(Dtype t, const void* X, int64_t ldX, MxProduct p, int64_t 
     if (!X) return KBIT_EINVAL;
     if (!aligned(X, elem_size(t)) || !aligned(workspace, 16)) return KBIT_EALIGN;
     p.K = mx_depth(d);
-    const bool vec = vec_rows(X, p.M, ldX, t);
     if (mx_tokens_fit(p.M, p.N, d, p.ldw, p.ldws)) {
         if (!device_usable()) return KBIT_EDEVICE;
-        return map_launch(launch_mx_tokens(t, p, static_cast<int>(d), X, ldX, vec, stream));
+        return map_launch(launch_mx_tokens(t, p, static_cast<int>(d), X, ldX, stream));
     }
     const int64_t at = (r.bytes + 15) / 16 * 16;
     if (!workspace || workspace_bytes < at + int8_product_workspace(p.M, p.N, p.K)) return KBIT_EINVAL;
     if (!device_usable()) return KBIT_EDEVICE;
     uint8_t* w = static_cast<uint8_t*>(workspace);
-    const int e = launch_mx_quantize(t, X, p.M, static_cast<int>(d), ldX, w, r.ldc, w + r.scales, r.lds, vec, stream);
+    const int e = launch_mx_quantize(t, X, p.M, static_cast<int>(d), ldX, coded_in(w, r), stream);
     if (e != 0) return KBIT_ELAUNCH;
     p.x = w;
     p.xs = w + r.scales;
@@ -154,51 +152,37 @@ int do_linear_backward(Dtype t, const void* g, int64_t ldg, const void* X, int64
     }
     uint8_t* w = static_cast<uint8_t*>(workspace);
     float* sums = reinterpret_cast<float*>(w + b.sums_at);
-    if (dX) {
-        if (launch_mx_quantize(t, g, M, N, ldg, w, b.g_rows.ldc, w + b.g_rows.scales, b.g_rows.lds, vec_rows(g, M, ldg, t),
-                               stream) != 0)
-            return KBIT_ELAUNCH;
-        uint8_t* c = w + b.w_at;
-        if (launch_mx_quantize_columns(t, W, N, K, ldw, c, b.w_cols.ldc, c + b.w_cols.scales, b.w_cols.lds, nullptr, stream) != 0)
-            return KBIT_ELAUNCH;
-        if (launch_mx_product(t, product_of(w, b.g_rows, M, c, b.w_cols, K, N, dX, lddx), w + b.product_at, stream) != 0)
-            return KBIT_ELAUNCH;
-    }
-    if (dW || db) {
-        uint8_t* c = w + b.gc_at;
-        if (launch_mx_quantize_columns(t, g, M, N, ldg, dW ? c : nullptr, b.g_cols.ldc, dW ? c + b.g_cols.scales : nullptr,
-                                       b.g_cols.lds, db ? sums : nullptr, stream) != 0)
-            return KBIT_ELAUNCH;
-        if (db && launch_mx_add_sums(sums, mx_sum_groups(M), N, db, stream) != 0) return KBIT_ELAUNCH;
-        if (dW) {
-            uint8_t* x = w + b.x_at;
-            if (launch_mx_quantize_columns(t, X, M, K, ldx, x, b.x_cols.ldc, x + b.x_cols.scales, b.x_cols.lds, nullptr,
-                                           stream) != 0)
-                return KBIT_ELAUNCH;
-            if (launch_mx_product(Dtype::fp32, product_of(c, b.g_cols, N, x, b.x_cols, K, M, dW, lddw), w + b.product_at,
-                                  stream) != 0)
-                return KBIT_ELAUNCH;
-        }
-    }
+    uint8_t *w_cols = w + b.w_at, *g_cols = w + b.gc_at, *x_cols = w + b.x_at;
+    // dout along its rows alone, or its columns with them
+    const int e = dW || db ? launch_mx_quantize_columns(t, g, M, N, ldg, dW ? coded_in(g_cols, b.g_cols) : MxCoded{},
+                                                        dX ? coded_in(w, b.g_rows) : MxCoded{}, db ? sums : nullptr, stream)
+                           : launch_mx_quantize(t, g, M, N, ldg, coded_in(w, b.g_rows), stream);
+    if (e != 0) return KBIT_ELAUNCH;
+    if (db && launch_mx_add_sums(sums, mx_sum_groups(M), N, db, stream) != 0) return KBIT_ELAUNCH;
+    if (dX && (launch_mx_quantize_columns(t, W, N, K, ldw, coded_in(w_cols, b.w_cols), MxCoded{}, nullptr, stream) != 0 ||
+               launch_mx_product(t, product_of(w, b.g_rows, M, w_cols, b.w_cols, K, N, dX, lddx), w + b.product_at, stream) != 0))
+        return KBIT_ELAUNCH;
+    if (dW && (launch_mx_quantize_columns(t, X, M, K, ldx, coded_in(x_cols, b.x_cols), MxCoded{}, nullptr, stream) != 0 ||
+               launch_mx_product(Dtype::fp32, product_of(g_cols, b.g_cols, N, x_cols, b.x_cols, K, M, dW, lddw),
+                                 w + b.product_at, stream) != 0))
+        return KBIT_ELAUNCH;
     return KBIT_OK;
 }
 
 bool eps_ok(float eps) { return eps >= 0.0f && !std::isinf(eps); }
 
 int do_layer_norm(Dtype t, const LayerNormArgs& p, void* stream) {
-    if (p.d < 1 || !rows_ok(p.rows, p.d, p.ldx) || !rows_ok(p.rows, p.d, p.ldo) || !eps_ok(p.eps)) return KBIT_EINVAL;
+    if (p.d < 1 || p.d > kLayerNormMax || !rows_ok(p.rows, p.d, p.ldx) || !rows_ok(p.rows, p.d, p.ldo) || !eps_ok(p.eps)) return KBIT_EINVAL;
     if (p.rows == 0) return KBIT_OK;
     if (!p.x || !p.weight || !p.out) return KBIT_EINVAL;
     const int64_t es = elem_size(t), ws = p.weight_fp32 ? 4 : es;
     if (!aligned(p.x, es) || !aligned(p.out, es) || !aligned(p.weight, ws) || !aligned(p.bias, ws)) return KBIT_EALIGN;
     if (!device_usable()) return KBIT_EDEVICE;
-    const bool vec = vec_rows(p.x, p.rows, p.ldx, t) && vec_rows(p.out, p.rows, p.ldo, t) && aligned(p.weight, 16) &&
-                     aligned(p.bias, 16);
-    return map_launch(launch_layer_norm(t, p, vec, stream));
+    return map_launch(launch_layer_norm(t, p, stream));
 }
 
 int do_layer_norm_backward(Dtype t, const LayerNormBackArgs& p, int64_t workspace_bytes, void* stream) {
-    if (p.d < 1 || !rows_ok(p.rows, p.d, p.ldg) || !rows_ok(p.rows, p.d, p.ldx) || !rows_ok(p.rows, p.d, p.lddx) ||
+    if (p.d < 1 || p.d > kLayerNormMax || !rows_ok(p.rows, p.d, p.ldg) || !rows_ok(p.rows, p.d, p.ldx) || !rows_ok(p.rows, p.d, p.lddx) ||
         !eps_ok(p.eps))
         return KBIT_EINVAL;
     const int64_t need = layer_norm_backward_bytes(p.rows, p.d);
@@ -209,9 +193,7 @@ int do_layer_norm_backward(Dtype t, const LayerNormBackArgs& p, int64_t workspac
         !aligned(p.dbias, 4) || !aligned(p.workspace, 16))
         return KBIT_EALIGN;
     if (!device_usable()) return KBIT_EDEVICE;
-    const bool vec = vec_rows(p.g, p.rows, p.ldg, t) && vec_rows(p.x, p.rows, p.ldx, t) &&
-                     vec_rows(p.dx, p.rows, p.lddx, t) && aligned(p.weight, 16);
-    return map_launch(launch_layer_norm_back(t, p, vec, stream));
+    return map_launch(launch_layer_norm_back(t, p, stream));
 }
 
 bool product_sizes_ok(int64_t M, int32_t N, int32_t K) { return M >= 0 && M <= kMaxRows && N >= 1 && depth_ok(K); }
@@ -249,7 +231,7 @@ int64_t linear_mxfp4_backward_workspace_bytes(int64_t M, int32_t N, int32_t K) {
 }
 
 int64_t layer_norm_backward_workspace_bytes(int64_t rows, int32_t d) {
-    if (rows < 0 || rows > kbit::kMaxRows || d < 1) return -1;
+    if (rows < 0 || rows > kbit::kMaxRows || d < 1 || d > kbit::kLayerNormMax) return -1;
     return kbit::layer_norm_backward_bytes(rows, d);
 }
 

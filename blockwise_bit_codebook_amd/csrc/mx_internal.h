@@ -16,19 +16,27 @@ constexpr int kMxBlockBytes = 16;  // of codes
 // Longest row: its codes' bytes and their steps count in 32 bits.
 constexpr int64_t kMxMaxDepth = int64_t(1) << 26;
 
+// Most columns that are quantized as such: two threads each, counted in 32 bits.
+constexpr int64_t kMxMaxColumns = int64_t(1) << 30;
+
 inline int64_t mx_blocks(int64_t d) { return (d + kMxBlock - 1) / kMxBlock; }
 
-// Rows of X to codes and scales; vec: 16-byte loads are possible.
-int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx, uint8_t* codes, int64_t ldc,
-                       uint8_t* scales, int64_t lds, bool vec, void* stream);
+// Rows of codes and scales.
+struct MxCoded {
+    uint8_t *codes, *scales;  // both or neither null
+    int64_t ldc, lds;
+};
 
-// Columns of X [rows][cols] to codes and scales, a column a row of both; with
-// codes null neither is written.  sums: null, or mx_sum_groups(rows) rows of
-// cols floats, the columns' sums over kMxSumRows rows each.
+int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx, const MxCoded& c, void* stream);
+
+// Columns of X [rows][cols], a column a row of codes, and its rows where
+// by_rows is there, in one reading of X.  sums: null, or mx_sum_groups(rows)
+// rows of cols floats, the columns' sums over kMxSumRows rows each; with
+// columns null they are all that is written.
 constexpr int64_t kMxSumRows = 256;
 inline int64_t mx_sum_groups(int64_t rows) { return (rows + kMxSumRows - 1) / kMxSumRows; }
-int launch_mx_quantize_columns(Dtype t, const void* X, int64_t rows, int cols, int64_t ldx, uint8_t* codes, int64_t ldc,
-                               uint8_t* scales, int64_t lds, float* sums, void* stream);
+int launch_mx_quantize_columns(Dtype t, const void* X, int64_t rows, int cols, int64_t ldx, const MxCoded& columns,
+                               const MxCoded& by_rows, float* sums, void* stream);
 
 // out[c] = sum over groups of sums[group][c], in order.
 int launch_mx_add_sums(const float* sums, int64_t groups, int cols, float* out, void* stream);
@@ -37,7 +45,7 @@ int launch_mx_add_sums(const float* sums, int64_t groups, int cols, float* out, 
 int launch_mx_zero(float* out, int64_t rows, int cols, int64_t ldo, void* stream);
 
 int launch_mx_dequantize(Dtype t, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t rows,
-                         int d, void* out, int64_t ldo, bool vec, void* stream);
+                         int d, void* out, int64_t ldo, void* stream);
 
 struct MxProduct {
     const uint8_t *x, *xs, *w, *ws;
@@ -103,11 +111,14 @@ inline MxBackParts mx_back_parts(int64_t M, int N, int K) {
 }
 
 // p.x and p.xs are not looked at.
-int launch_mx_tokens(Dtype t, const MxProduct& p, int d, const void* X, int64_t ldX, bool vec, void* stream);
+int launch_mx_tokens(Dtype t, const MxProduct& p, int d, const void* X, int64_t ldX, void* stream);
 
 // ---------------------------------------------------------------------------
 // layer norm
 // ---------------------------------------------------------------------------
+// Longest row: 64 threads a column add up the gradients, counted in 32 bits.
+constexpr int kLayerNormMax = 1 << 25;
+
 struct LayerNormArgs {
     const void *x, *weight, *bias;  // bias may be null
     void* out;
@@ -117,19 +128,17 @@ struct LayerNormArgs {
     bool weight_fp32;
 };
 
-// vec: rows and weights start at multiples of 16 bytes.
-int launch_layer_norm(Dtype t, const LayerNormArgs& p, bool vec, void* stream);
+int launch_layer_norm(Dtype t, const LayerNormArgs& p, void* stream);
 
 // Rows of partial sums of the weights' gradients, each 2 d floats.
 constexpr int kLayerNormPartials = 512;
-// Longest row whose sums stay in registers, and the longest one at any
-// alignment; above it the rows' statistics go to the workspace and a second
-// pass sums over rows.
-constexpr int kLayerNormKept = 16384, kLayerNormKeptAny = 8192;
+// Longest row whose sums stay in registers; above it the rows' statistics go
+// to the workspace and a second pass sums over rows.
+constexpr int kLayerNormKept = 16384;
 
 inline int64_t layer_norm_backward_bytes(int64_t rows, int d) {
     const int64_t groups = rows < kLayerNormPartials ? rows : kLayerNormPartials;
-    return 4 * (groups * 2 * d + (d > kLayerNormKeptAny ? 4 * rows : 0));
+    return 4 * (groups * 2 * d + (d > kLayerNormKept ? 4 * rows : 0));
 }
 
 struct LayerNormBackArgs {
@@ -142,6 +151,6 @@ struct LayerNormBackArgs {
     bool weight_fp32;
 };
 
-int launch_layer_norm_back(Dtype t, const LayerNormBackArgs& p, bool vec, void* stream);
+int launch_layer_norm_back(Dtype t, const LayerNormBackArgs& p, void* stream);
 
 }  // namespace kbit

@@ -21,7 +21,6 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 
 // ---------------------------------------------------------------------------
 // values to codes
@@ -33,34 +32,73 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
     return e == 255u ? 255u : max(e, 2u) - 2u;
 }
 
-// 8 codes; the converter takes the scale's exponent from a float's bits and
-// rounds half to even, at most 6.
-__device__ __forceinline__ uint32_t pack_codes(const float* x, uint32_t byte) {
-    const float s = __uint_as_float(byte << 23);
-    uint32_t r = 0;
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x[0], x[1], s, 0);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x[2], x[3], s, 1);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x[4], x[5], s, 2);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, x[6], x[7], s, 3);
-    return byte == 255u ? 0u : r;
+// The converters take the scale's exponent from a float's bits and round half
+// to even, at most 6; PLACE is the byte of the word that two codes go to.
+template <class E, int PLACE>
+__device__ __forceinline__ uint32_t pack2(uint32_t word, uint32_t two, float scale) {
+    if constexpr (std::is_same<E, QB16>::value)
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(word, __builtin_bit_cast(bf16x2, two), scale, PLACE);
+    else
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(word, __builtin_bit_cast(f16x2, two), scale, PLACE);
+}
+template <int PLACE>
+__device__ __forceinline__ uint32_t pack2(uint32_t word, float a, float b, float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, a, b, scale, PLACE);
 }
 
-__device__ __forceinline__ uint32_t largest_bits(const float (&x)[8]) {
-    uint32_t m = 0;
+// Largest magnitudes of both halves of two words of 16-bit values, whose bits
+// are ordered like the magnitudes, with NaN above infinity above the rest.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+constexpr uint32_t kAbs16x2 = 0x7FFF7FFFu, kAbs32 = 0x7FFFFFFFu;
+
+// The bits of a 16-bit magnitude as fp32.
+template <class E>
+__device__ __forceinline__ uint32_t wide_bits(uint32_t half) {
+    return __float_as_uint(E::one(static_cast<uint16_t>(half)));
+}
+
+// The scale byte of a lane's 8 neighbouring values, four lanes a block, and
+// their codes (0 where the block is not finite).
+template <class E>
+__device__ __forceinline__ uint32_t row_byte(const u32x4 (&r)[E::kVec]) {
+    uint32_t m;
+    if constexpr (sizeof(typename E::T) == 4) {
+        m = r[0][0] & kAbs32;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-    return m;
-}
-
-__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+        for (int i = 1; i < 8; ++i) m = max(m, r[i / 4][i % 4] & kAbs32);
+    } else {
+        m = max16x2(max16x2(r[0][0] & kAbs16x2, r[0][1] & kAbs16x2), max16x2(r[0][2] & kAbs16x2, r[0][3] & kAbs16x2));
+        m = wide_bits<E>(max(m & 0xFFFFu, m >> 16));
+    }
     m = max(m, dpp_u32<kDppXor1>(m));
-    return max(m, dpp_u32<kDppXor2>(m));
+    m = max(m, dpp_u32<kDppXor2>(m));
+    return scale_byte(m);
+}
+template <class E>
+__device__ __forceinline__ uint32_t row_codes(const u32x4 (&r)[E::kVec], uint32_t byte) {
+    const float s = __uint_as_float(byte << 23);
+    uint32_t q = 0;
+    if constexpr (sizeof(typename E::T) == 4) {
+        q = pack2<0>(q, __uint_as_float(r[0][0]), __uint_as_float(r[0][1]), s);
+        q = pack2<1>(q, __uint_as_float(r[0][2]), __uint_as_float(r[0][3]), s);
+        q = pack2<2>(q, __uint_as_float(r[1][0]), __uint_as_float(r[1][1]), s);
+        q = pack2<3>(q, __uint_as_float(r[1][2]), __uint_as_float(r[1][3]), s);
+    } else {
+        q = pack2<E, 0>(q, r[0][0], s);
+        q = pack2<E, 1>(q, r[0][1], s);
+        q = pack2<E, 2>(q, r[0][2], s);
+        q = pack2<E, 3>(q, r[0][3], s);
+    }
+    return byte == 255u ? 0u : q;
 }
 
 // Rows: 8 values a lane, four lanes a block, kRowItems pieces of 512 values a
 // wave on their way together.  Piece i of all rows: row i / per_row.
 constexpr int kRowItems = 4;
-template <class E, bool VEC>
+template <class E>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const typename E::T* __restrict__ X, uint32_t items,
                                                                uint32_t per_row, int d, int64_t ldx,
                                                                uint8_t* __restrict__ codes, int64_t ldc,
@@ -68,111 +106,182 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const typename E:
     const int lane = __lane_id();
     const uint32_t first = (blockIdx.x * kWavesPerGroup + threadIdx.x / kWave) * kRowItems;
     const int end = (d + kMxBlock - 1) / kMxBlock * kMxBlock;
-    float v[kRowItems][8];
-    uint32_t row = first / per_row;
-    uint32_t at = first - row * per_row;
-    const uint32_t row_first = row, at_first = at;
+    u32x4 v[kRowItems][E::kVec];
+    uint32_t rows[kRowItems];
+    int cols[kRowItems];
+    uint32_t row = first / per_row, at = first - row * per_row;
 #pragma unroll
     for (int i = 0; i < kRowItems; ++i) {
-        const int64_t c = static_cast<int64_t>(at) * 512 + lane * 8;
-        if (first + i < items && c < end) load8<E, VEC>(X + row * ldx, static_cast<int>(c), d, v[i]);
+        rows[i] = row;
+        cols[i] = first + i < items ? static_cast<int>(at) * 512 + lane * 8 : end;
+        if (cols[i] < end) load8_raw<E>(X + row * ldx, cols[i], d, v[i]);
         if (++at == per_row) {
             at = 0;
             ++row;
         }
     }
-    row = row_first;
-    at = at_first;
 #pragma unroll
     for (int i = 0; i < kRowItems; ++i) {
-        const int64_t c = static_cast<int64_t>(at) * 512 + lane * 8;
-        if (first + i < items && c < end) {  // end is a whole number of blocks: quads stay together
-            const uint32_t byte = scale_byte(quad_max(largest_bits(v[i])));
-            *reinterpret_cast<uint32_t*>(codes + row * ldc + c / 2) = pack_codes(v[i], byte);
-            if ((lane & 3) == 0) scales[row * lds + c / kMxBlock] = static_cast<uint8_t>(byte);
-        }
-        if (++at == per_row) {
-            at = 0;
-            ++row;
+        if (cols[i] < end) {  // end is a whole number of blocks: quads stay together
+            const uint32_t byte = row_byte<E>(v[i]);
+            *reinterpret_cast<uint32_t*>(codes + rows[i] * ldc + cols[i] / 2) = row_codes<E>(v[i], byte);
+            if ((lane & 3) == 0) scales[rows[i] * lds + cols[i] / kMxBlock] = static_cast<uint8_t>(byte);
         }
     }
 }
 
-// Columns: a workgroup takes 8 blocks of 32 rows and 128 columns.  A lane has
-// two columns of a block, so that a block's maximum needs no other lane; the
-// codes cross LDS so that a column's leave as whole cache lines.
-constexpr int kColBlocks = 8, kColCols = 128;
-template <class E, bool PAIRS>
-__global__ __launch_bounds__(kThreads) void mx_quantize_columns_kernel(const typename E::T* __restrict__ X, int64_t rows,
-                                                                       int cols, int64_t ldx,
-                                                                       uint8_t* __restrict__ codes, int64_t ldc,
-                                                                       uint8_t* __restrict__ scales, int64_t lds,
-                                                                       float* __restrict__ sums) {
+// Columns, and rows in the same pass: a workgroup takes 8 blocks of 32 rows, a
+// wave each, and 64 kCols columns.  A lane has kCols columns of its block, 8
+// bytes of a row, so that a column's maximum needs no other lane and a row's a
+// few neighbours; the columns' codes cross LDS so that they leave as whole
+// cache lines.  sums: the columns' sums over the workgroup's rows.
+constexpr int kColBlocks = 8;
+template <class E>
+constexpr int kCols = 8 / sizeof(typename E::T);
+
+template <class E, bool ROWS>
+__global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(
+    const typename E::T* __restrict__ X, int64_t rows, int cols, int64_t ldx, uint8_t* __restrict__ codes, int64_t ldc,
+    uint8_t* __restrict__ scales, int64_t lds, uint8_t* __restrict__ row_codes_out, int64_t ldrc,
+    uint8_t* __restrict__ row_scales_out, int64_t ldrs, float* __restrict__ sums) {
     using T = typename E::T;
-    constexpr int kPitch = kColBlocks * kMxBlockBytes + 16;
-    __shared__ __align__(16) uint8_t tile[kColCols * kPitch];
-    __shared__ __align__(8) uint8_t bytes[kColCols * kColBlocks];
-    const int lane = __lane_id(), wave = threadIdx.x / kWave;
+    constexpr int C = kCols<E>, kTile = kWave * C;
+    constexpr bool kWide = sizeof(T) == 4;
+    __shared__ __align__(16) uint8_t tile[kTile * kColBlocks * kMxBlockBytes];
+    __shared__ __align__(8) uint8_t bytes[kTile * kColBlocks];
+    __shared__ float partial[kColBlocks][kTile];
+    const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t block0 = static_cast<int64_t>(blockIdx.y) * kColBlocks, row_blocks = (rows + kMxBlock - 1) / kMxBlock;
-    const int col0 = blockIdx.x * kColCols, col = col0 + 2 * lane;
-    float total[2] = {0.0f, 0.0f};
-    for (int b = wave; b < kColBlocks; b += kWavesPerGroup) {
-        const int64_t r0 = (block0 + b) * kMxBlock;
-        if (r0 >= rows) break;
+    const int col0 = blockIdx.x * kTile, col = col0 + C * lane;
+    const int64_t r0 = (block0 + wave) * kMxBlock;
+    if (r0 < rows) {
         const int n = static_cast<int>(min<int64_t>(rows - r0, kMxBlock));
-        float v[2][kMxBlock];
+        uint32_t v[kMxBlock][2];
+        const T* x = X + r0 * ldx + col;
 #pragma unroll
-        for (int r = 0; r < kMxBlock; ++r) {
-            v[0][r] = v[1][r] = 0.0f;
-            if (r < n) {
-                const T* p = X + (r0 + r) * ldx + col;
-                if (PAIRS && col + 2 <= cols) {
-                    if constexpr (sizeof(T) == 4) {
-                        const float2 f = *reinterpret_cast<const float2*>(p);
-                        v[0][r] = f.x;
-                        v[1][r] = f.y;
-                    } else {
-                        const uint32_t f = *reinterpret_cast<const uint32_t*>(p);
-                        v[0][r] = E::one(static_cast<T>(f & 0xFFFFu));
-                        v[1][r] = E::one(static_cast<T>(f >> 16));
+        for (int r = 0; r < kMxBlock; ++r) v[r][0] = v[r][1] = 0u;
+        if (n == kMxBlock && col + C <= cols) {
+#pragma unroll
+            for (int r = 0; r < kMxBlock; ++r) {
+                const u32x2_any f = *reinterpret_cast<const u32x2_any*>(x + r * ldx);
+                v[r][0] = f[0];
+                v[r][1] = f[1];
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < kMxBlock; ++r)
+                if (r < n) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        if (col + c >= cols) continue;
+                        if constexpr (kWide) v[r][c] = __float_as_uint(x[r * ldx + c]);
+                        else v[r][c / 2] |= static_cast<uint32_t>(x[r * ldx + c]) << (16 * (c & 1));
                     }
+                }
+        }
+        if (codes) {
+            uint32_t m[2] = {0u, 0u};
+#pragma unroll
+            for (int r = 0; r < kMxBlock; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    m[i] = kWide ? max(m[i], v[r][i] & kAbs32) : max16x2(m[i], v[r][i] & kAbs16x2);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const uint32_t byte = scale_byte(kWide ? m[c % 2] : wide_bits<E>(m[c / 2] >> (16 * (c & 1)) & 0xFFFFu));
+                const float s = __uint_as_float(byte << 23);
+                u32x4 q;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t word = 0;
+                    if constexpr (kWide) {
+                        word = pack2<0>(word, __uint_as_float(v[8 * w][c]), __uint_as_float(v[8 * w + 1][c]), s);
+                        word = pack2<1>(word, __uint_as_float(v[8 * w + 2][c]), __uint_as_float(v[8 * w + 3][c]), s);
+                        word = pack2<2>(word, __uint_as_float(v[8 * w + 4][c]), __uint_as_float(v[8 * w + 5][c]), s);
+                        word = pack2<3>(word, __uint_as_float(v[8 * w + 6][c]), __uint_as_float(v[8 * w + 7][c]), s);
+                    } else {  // the column's values of two rows
+                        constexpr uint32_t kLow = 0x05040100u, kHigh = 0x07060302u;
+                        auto two = [&](int r) {
+                            return __builtin_amdgcn_perm(v[r + 1][c / 2], v[r][c / 2], (c & 1) ? kHigh : kLow);
+                        };
+                        word = pack2<E, 0>(word, two(8 * w), s);
+                        word = pack2<E, 1>(word, two(8 * w + 2), s);
+                        word = pack2<E, 2>(word, two(8 * w + 4), s);
+                        word = pack2<E, 3>(word, two(8 * w + 6), s);
+                    }
+                    q[w] = byte == 255u ? 0u : word;
+                }
+                // a column's blocks are xor-ed with its lane, so that neighbours write different banks
+                *reinterpret_cast<u32x4*>(tile + ((C * lane + c) * kColBlocks + (wave ^ (lane & 7))) * kMxBlockBytes) = q;
+                bytes[(C * lane + c) * kColBlocks + wave] = static_cast<uint8_t>(byte);
+            }
+        }
+        if (sums) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float total = 0.0f;
+#pragma unroll
+                for (int r = 0; r < kMxBlock; ++r)
+                    total += kWide ? __uint_as_float(v[r][c % 2]) : E::one(static_cast<T>(v[r][c / 2] >> (16 * (c & 1)) & 0xFFFFu));
+                partial[wave][C * lane + c] = total;
+            }
+        }
+        if constexpr (ROWS) {  // blocks of 32 columns: 32 / C lanes
+#pragma unroll
+            for (int r = 0; r < kMxBlock; ++r) {
+                uint32_t m = kWide ? max(v[r][0] & kAbs32, v[r][1] & kAbs32)
+                                   : max16x2(v[r][0] & kAbs16x2, v[r][1] & kAbs16x2);
+                if constexpr (!kWide) m = max(m & 0xFFFFu, m >> 16);
+                m = max(m, dpp_u32<kDppXor1>(m));
+                m = max(m, dpp_u32<kDppXor2>(m));
+                m = max(m, dpp_u32<kDppHalfMirror>(m));
+                if (kWide) m = max(m, dpp_u32<kDppMirror>(m));
+                const uint32_t byte = scale_byte(kWide ? m : wide_bits<E>(m));
+                const float s = __uint_as_float(byte << 23);
+                uint32_t q = 0;
+                if constexpr (kWide) {
+                    q = pack2<0>(q, __uint_as_float(v[r][0]), __uint_as_float(v[r][1]), s);
                 } else {
-                    if (col < cols) v[0][r] = E::one(p[0]);
-                    if (col + 1 < cols) v[1][r] = E::one(p[1]);
+                    q = pack2<E, 0>(q, v[r][0], s);
+                    q = pack2<E, 1>(q, v[r][1], s);
+                }
+                if (byte == 255u) q = 0u;
+                const int end = (cols + kMxBlock - 1) / kMxBlock * kMxBlock;
+                if (r < n && col < end) {
+                    uint8_t* to = row_codes_out + (r0 + r) * ldrc + col / 2;
+                    if constexpr (kWide) *to = static_cast<uint8_t>(q);
+                    else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(q);
+                    if (col % kMxBlock == 0) row_scales_out[(r0 + r) * ldrs + col / kMxBlock] = static_cast<uint8_t>(byte);
                 }
             }
         }
+    } else if (sums) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int r = 0; r < kMxBlock; ++r) {
-                m = max(m, __float_as_uint(v[c][r]) & 0x7FFFFFFFu);
-                total[c] += v[c][r];
-            }
-            const uint32_t byte = scale_byte(m);
-            const u32x4 q = {pack_codes(v[c], byte), pack_codes(v[c] + 8, byte), pack_codes(v[c] + 16, byte),
-                             pack_codes(v[c] + 24, byte)};
-            *reinterpret_cast<u32x4*>(tile + (2 * lane + c) * kPitch + b * kMxBlockBytes) = q;
-            bytes[(2 * lane + c) * kColBlocks + b] = static_cast<uint8_t>(byte);
-        }
+        for (int c = 0; c < C; ++c) partial[wave][C * lane + c] = 0.0f;
     }
-    __shared__ float partial[kWavesPerGroup][kColCols];
-    partial[wave][2 * lane] = total[0];
-    partial[wave][2 * lane + 1] = total[1];
     __syncthreads();
-    if (sums && threadIdx.x < kColCols && col0 + static_cast<int>(threadIdx.x) < cols) {
-        const int c = threadIdx.x;
-        sums[blockIdx.y * static_cast<int64_t>(cols) + col0 + c] =
-            ((partial[0][c] + partial[1][c]) + partial[2][c]) + partial[3][c];
+    if (sums && static_cast<int>(threadIdx.x) < kTile && col0 + static_cast<int>(threadIdx.x) < cols) {
+        float total = partial[0][threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < kColBlocks; ++w) total += partial[w][threadIdx.x];
+        sums[blockIdx.y * static_cast<int64_t>(cols) + col0 + threadIdx.x] = total;
     }
-    const int live = codes ? static_cast<int>(min<int64_t>(row_blocks - block0, kColBlocks)) : 0;
-    for (int t = threadIdx.x; t < kColCols * kColBlocks; t += kThreads) {
+    if (!codes) return;
+    const int live = static_cast<int>(min<int64_t>(row_blocks - block0, kColBlocks));
+#pragma unroll
+    for (int t = threadIdx.x; t < kTile * kColBlocks; t += kColBlocks * kWave) {
         const int c = t / kColBlocks, b = t % kColBlocks;
-        if (b < live && col0 + c < cols) {
+        if (b < live && col0 + c < cols)
             *reinterpret_cast<u32x4*>(codes + (col0 + c) * ldc + (block0 + b) * kMxBlockBytes) =
-                *reinterpret_cast<const u32x4*>(tile + c * kPitch + b * kMxBlockBytes);
-            scales[(col0 + c) * lds + block0 + b] = bytes[t];
+                *reinterpret_cast<const u32x4*>(tile + (c * kColBlocks + (b ^ (c / C & 7))) * kMxBlockBytes);
+    }
+    const int c = threadIdx.x;
+    if (c < kTile && col0 + c < cols) {
+        uint8_t* to = scales + (col0 + c) * lds + block0;
+        if (live == kColBlocks) {
+            *reinterpret_cast<u32x2_any*>(to) = *reinterpret_cast<const u32x2_any*>(bytes + c * kColBlocks);
+        } else {
+            for (int b = 0; b < live; ++b) to[b] = bytes[c * kColBlocks + b];
         }
     }
 }
@@ -197,12 +306,11 @@ __global__ __launch_bounds__(kThreads) void mx_zero_kernel(float* __restrict__ o
 // codes to values
 // ---------------------------------------------------------------------------
 // 8 values a lane.  The scale 255 is NaN, which the converter does not know.
-template <class E, bool VEC>
+template <class E>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t* __restrict__ codes, int64_t ldc,
                                                                  const uint8_t* __restrict__ scales, int64_t lds,
                                                                  uint32_t items, uint32_t per_row, int d,
                                                                  typename E::T* __restrict__ out, int64_t ldo) {
-    using T = typename E::T;
     const int lane = __lane_id();
     const uint32_t first = (blockIdx.x * kWavesPerGroup + threadIdx.x / kWave) * kRowItems;
     uint32_t row = first / per_row, at = first - row * per_row;
@@ -237,19 +345,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t* 
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(0x7FC00000u);
             }
-            T* o = out + row * ldo + c;
-            if (VEC && c + 8 <= d) {
-                if constexpr (sizeof(T) == 4) {
-                    store16<false>(o, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
-                    store16<false>(o + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
-                } else {
-                    store16<false>(o, u32x4{E::pack(v[0], v[1]), E::pack(v[2], v[3]), E::pack(v[4], v[5]), E::pack(v[6], v[7])});
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c + j < d) o[j] = E::narrow(v[j]);
-            }
+            store8<E>(out + row * ldo, static_cast<int>(c), d, v);
         }
         if (++at == per_row) {
             at = 0;
@@ -489,7 +585,7 @@ __global__ __launch_bounds__(WAVES* kWave) void mx_few_rows_kernel(const MxProdu
 // The few-rows kernel for a few tokens whose codes every workgroup makes for
 // itself, in LDS, while its first weights are on their way: one launch
 // instead of two, for a reading of the tokens from cache by each workgroup.
-template <class E, int TN, int WAVES, bool VEC>
+template <class E, int TN, int WAVES>
 __global__ __launch_bounds__(WAVES* kWave) void mx_tokens_kernel(const MxProduct p, int d,
                                                                  const typename E::T* __restrict__ X, int64_t ldX,
                                                                  bool packed) {
@@ -532,13 +628,13 @@ __global__ __launch_bounds__(WAVES* kWave) void mx_tokens_kernel(const MxProduct
     // The tokens' codes and scales, zeros from K to a whole step.
     const int per_row = (all_steps * 256 + 511) / 512, items = rows * per_row;
     const int pitch = all_steps * kDepth + kMxTokenPad, pitch_s = all_steps * 8;
-    float keep[kMxTokenItems][8];
+    u32x4 keep[kMxTokenItems][E::kVec];
 #pragma unroll
     for (int t = 0; t < kMxTokenItems; ++t) {
         const int item = wave + t * WAVES;
         if (item < items) {
             const int r = item / per_row;
-            load8<E, VEC>(X + r * ldX, (item - r * per_row) * 512 + lane * 8, d, keep[t]);
+            load8_raw<E>(X + r * ldX, (item - r * per_row) * 512 + lane * 8, d, keep[t]);
         }
     }
 #pragma unroll
@@ -546,9 +642,9 @@ __global__ __launch_bounds__(WAVES* kWave) void mx_tokens_kernel(const MxProduct
         const int item = wave + t * WAVES;
         if (item < items) {
             const int r = item / per_row, c = (item - r * per_row) * 512 + lane * 8;
-            const uint32_t byte = scale_byte(quad_max(largest_bits(keep[t])));
+            const uint32_t byte = row_byte<E>(keep[t]);
             if (c < all_steps * 256) {
-                *reinterpret_cast<uint32_t*>(codes + r * pitch + c / 2) = pack_codes(keep[t], byte);
+                *reinterpret_cast<uint32_t*>(codes + r * pitch + c / 2) = row_codes<E>(keep[t], byte);
                 if ((lane & 3) == 0) bytes[r * pitch_s + c / kMxBlock] = static_cast<uint8_t>(byte);
             }
         }
@@ -1071,47 +1167,38 @@ int launch_product_e(const MxProduct& whole, void* workspace, void* stream) {
 }
 
 template <class E, int TN, int WAVES>
-int launch_tokens_t(const MxProduct& p, int d, const void* X, int64_t ldX, bool vec, void* stream) {
-    const dim3 grid((p.N + TN * 16 - 1) / (TN * 16)), block(WAVES * kWave);
-    const auto* x = static_cast<const typename E::T*>(X);
-    const bool packed = out_aligned(p, sizeof(typename E::T), 4 * sizeof(typename E::T));
-    if (vec)
-        hipLaunchKernelGGL((mx_tokens_kernel<E, TN, WAVES, true>), grid, block, 0, static_cast<hipStream_t>(stream), p, d,
-                           x, ldX, packed);
-    else
-        hipLaunchKernelGGL((mx_tokens_kernel<E, TN, WAVES, false>), grid, block, 0, static_cast<hipStream_t>(stream), p, d,
-                           x, ldX, packed);
+int launch_tokens_t(const MxProduct& p, int d, const void* X, int64_t ldX, void* stream) {
+    hipLaunchKernelGGL((mx_tokens_kernel<E, TN, WAVES>), dim3((p.N + TN * 16 - 1) / (TN * 16)), dim3(WAVES * kWave), 0,
+                       static_cast<hipStream_t>(stream), p, d, static_cast<const typename E::T*>(X), ldX,
+                       out_aligned(p, sizeof(typename E::T), 4 * sizeof(typename E::T)));
     return static_cast<int>(hipGetLastError());
 }
 
 template <class E>
-int launch_tokens_e(const MxProduct& p, int d, const void* X, int64_t ldX, bool vec, void* stream) {
+int launch_tokens_e(const MxProduct& p, int d, const void* X, int64_t ldX, void* stream) {
     const int cus = device_cu_count();
     auto rounds = [&](int channels) { return (p.N + channels * cus - 1) / (channels * cus); };
     const int c16 = rounds(16), c48 = 2 * rounds(48), c64 = 3 * rounds(64);
-    if (c64 <= c48 && c64 <= c16) return launch_tokens_t<E, 4, 8>(p, d, X, ldX, vec, stream);
-    if (c48 <= c16) return launch_tokens_t<E, 3, 8>(p, d, X, ldX, vec, stream);
-    return launch_tokens_t<E, 1, 16>(p, d, X, ldX, vec, stream);
+    if (c64 <= c48 && c64 <= c16) return launch_tokens_t<E, 4, 8>(p, d, X, ldX, stream);
+    if (c48 <= c16) return launch_tokens_t<E, 3, 8>(p, d, X, ldX, stream);
+    return launch_tokens_t<E, 1, 16>(p, d, X, ldX, stream);
 }
 
-// Rows of a launch: their pieces of 512 values count in 32 bits.
-int64_t rows_a_launch(int64_t per_row) { return (int64_t(1) << 30) / per_row; }
+// Rows of a launch: the threads of their pieces of 512 values, 16 a piece,
+// count in 32 bits.
+int64_t rows_a_launch(int64_t per_row) { return (int64_t(1) << 27) / per_row; }
 
 template <class E>
 int launch_quantize_e(const void* X, int64_t rows, int d, int64_t ldx, uint8_t* codes, int64_t ldc, uint8_t* scales,
-                      int64_t lds, bool vec, void* stream) {
+                      int64_t lds, void* stream) {
     const uint32_t per_row = static_cast<uint32_t>((d + 511) / 512);
     const int64_t most = rows_a_launch(per_row);
     for (int64_t r = 0; r < rows; r += most) {
         const uint32_t items = static_cast<uint32_t>((rows - r < most ? rows - r : most) * per_row);
         const dim3 grid((items + kWavesPerGroup * kRowItems - 1) / (kWavesPerGroup * kRowItems));
-        const auto* x = static_cast<const typename E::T*>(X) + r * ldx;
-        if (vec)
-            hipLaunchKernelGGL((mx_quantize_kernel<E, true>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream), x,
-                               items, per_row, d, ldx, codes + r * ldc, ldc, scales + r * lds, lds);
-        else
-            hipLaunchKernelGGL((mx_quantize_kernel<E, false>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream), x,
-                               items, per_row, d, ldx, codes + r * ldc, ldc, scales + r * lds, lds);
+        hipLaunchKernelGGL((mx_quantize_kernel<E>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream),
+                           static_cast<const typename E::T*>(X) + r * ldx, items, per_row, d, ldx, codes + r * ldc, ldc,
+                           scales + r * lds, lds);
         const int e = static_cast<int>(hipGetLastError());
         if (e != 0) return e;
     }
@@ -1119,25 +1206,26 @@ int launch_quantize_e(const void* X, int64_t rows, int d, int64_t ldx, uint8_t* 
 }
 
 template <class E>
-int launch_columns_e(const void* X, int64_t rows, int cols, int64_t ldx, uint8_t* codes, int64_t ldc, uint8_t* scales,
-                     int64_t lds, float* sums, void* stream) {
+int launch_columns_e(const void* X, int64_t rows, int cols, int64_t ldx, const MxCoded& c, const MxCoded& r, float* sums,
+                     void* stream) {
     using T = typename E::T;
     static_assert(kMxSumRows == int64_t(kMxBlock) * kColBlocks, "a row of sums a row of workgroups");
-    constexpr int64_t kRows = int64_t(kMxBlock) * kColBlocks * 32768;  // of a launch: its grid's second axis
-    const bool pairs = reinterpret_cast<uintptr_t>(X) % (2 * sizeof(T)) == 0 && (rows == 1 || ldx % 2 == 0);
-    for (int64_t r = 0; r < rows; r += kRows) {
-        const int64_t n = rows - r < kRows ? rows - r : kRows;
-        const dim3 grid((cols + kColCols - 1) / kColCols,
-                        static_cast<unsigned>((n + kMxBlock * kColBlocks - 1) / (kMxBlock * kColBlocks)));
-        const T* x = static_cast<const T*>(X) + r * ldx;
-        uint8_t *c = codes ? codes + r / 2 : nullptr, *s = scales ? scales + r / kMxBlock : nullptr;
-        float* f = sums ? sums + r / kMxSumRows * cols : nullptr;
-        if (pairs)
-            hipLaunchKernelGGL((mx_quantize_columns_kernel<E, true>), grid, dim3(kThreads), 0,
-                               static_cast<hipStream_t>(stream), x, n, cols, ldx, c, ldc, s, lds, f);
+    constexpr int64_t kRows = kMxSumRows * 32768;  // of a launch: its grid's second axis
+    constexpr int kTile = kWave * kCols<E>;
+    for (int64_t at = 0; at < rows; at += kRows) {
+        const int64_t n = rows - at < kRows ? rows - at : kRows;
+        const dim3 grid((cols + kTile - 1) / kTile, static_cast<unsigned>((n + kMxSumRows - 1) / kMxSumRows));
+        const T* x = static_cast<const T*>(X) + at * ldx;
+        uint8_t *cc = c.codes ? c.codes + at / 2 : nullptr, *cs = c.codes ? c.scales + at / kMxBlock : nullptr;
+        float* f = sums ? sums + at / kMxSumRows * cols : nullptr;
+        if (r.codes)
+            hipLaunchKernelGGL((mx_quantize_columns_kernel<E, true>), grid, dim3(kColBlocks * kWave), 0,
+                               static_cast<hipStream_t>(stream), x, n, cols, ldx, cc, c.ldc, cs, c.lds, r.codes + at * r.ldc,
+                               r.ldc, r.scales + at * r.lds, r.lds, f);
         else
-            hipLaunchKernelGGL((mx_quantize_columns_kernel<E, false>), grid, dim3(kThreads), 0,
-                               static_cast<hipStream_t>(stream), x, n, cols, ldx, c, ldc, s, lds, f);
+            hipLaunchKernelGGL((mx_quantize_columns_kernel<E, false>), grid, dim3(kColBlocks * kWave), 0,
+                               static_cast<hipStream_t>(stream), x, n, cols, ldx, cc, c.ldc, cs, c.lds,
+                               static_cast<uint8_t*>(nullptr), int64_t(0), static_cast<uint8_t*>(nullptr), int64_t(0), f);
         const int e = static_cast<int>(hipGetLastError());
         if (e != 0) return e;
     }
@@ -1146,19 +1234,15 @@ int launch_columns_e(const void* X, int64_t rows, int cols, int64_t ldx, uint8_t
 
 template <class E>
 int launch_dequantize_e(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t rows, int d,
-                        void* out, int64_t ldo, bool vec, void* stream) {
+                        void* out, int64_t ldo, void* stream) {
     const uint32_t per_row = static_cast<uint32_t>((d + 511) / 512);
     const int64_t most = rows_a_launch(per_row);
     for (int64_t r = 0; r < rows; r += most) {
         const uint32_t items = static_cast<uint32_t>((rows - r < most ? rows - r : most) * per_row);
         const dim3 grid((items + kWavesPerGroup * kRowItems - 1) / (kWavesPerGroup * kRowItems));
-        auto* o = static_cast<typename E::T*>(out) + r * ldo;
-        if (vec)
-            hipLaunchKernelGGL((mx_dequantize_kernel<E, true>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream),
-                               codes + r * ldc, ldc, scales + r * lds, lds, items, per_row, d, o, ldo);
-        else
-            hipLaunchKernelGGL((mx_dequantize_kernel<E, false>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream),
-                               codes + r * ldc, ldc, scales + r * lds, lds, items, per_row, d, o, ldo);
+        hipLaunchKernelGGL((mx_dequantize_kernel<E>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream),
+                           codes + r * ldc, ldc, scales + r * lds, lds, items, per_row, d,
+                           static_cast<typename E::T*>(out) + r * ldo, ldo);
         const int e = static_cast<int>(hipGetLastError());
         if (e != 0) return e;
     }
@@ -1174,14 +1258,13 @@ int launch_dequantize_e(const uint8_t* codes, int64_t ldc, const uint8_t* scales
         default: return F<QB16>(__VA_ARGS__);       \
     }
 
-int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx, uint8_t* codes, int64_t ldc,
-                       uint8_t* scales, int64_t lds, bool vec, void* stream) {
-    KBIT_BY_DTYPE(launch_quantize_e, X, rows, d, ldx, codes, ldc, scales, lds, vec, stream)
+int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx, const MxCoded& c, void* stream) {
+    KBIT_BY_DTYPE(launch_quantize_e, X, rows, d, ldx, c.codes, c.ldc, c.scales, c.lds, stream)
 }
 
-int launch_mx_quantize_columns(Dtype t, const void* X, int64_t rows, int cols, int64_t ldx, uint8_t* codes, int64_t ldc,
-                               uint8_t* scales, int64_t lds, float* sums, void* stream) {
-    KBIT_BY_DTYPE(launch_columns_e, X, rows, cols, ldx, codes, ldc, scales, lds, sums, stream)
+int launch_mx_quantize_columns(Dtype t, const void* X, int64_t rows, int cols, int64_t ldx, const MxCoded& columns,
+                               const MxCoded& by_rows, float* sums, void* stream) {
+    KBIT_BY_DTYPE(launch_columns_e, X, rows, cols, ldx, columns, by_rows, sums, stream)
 }
 
 int launch_mx_add_sums(const float* sums, int64_t groups, int cols, float* out, void* stream) {
@@ -1197,16 +1280,16 @@ int launch_mx_zero(float* out, int64_t rows, int cols, int64_t ldo, void* stream
 }
 
 int launch_mx_dequantize(Dtype t, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t rows,
-                         int d, void* out, int64_t ldo, bool vec, void* stream) {
-    KBIT_BY_DTYPE(launch_dequantize_e, codes, ldc, scales, lds, rows, d, out, ldo, vec, stream)
+                         int d, void* out, int64_t ldo, void* stream) {
+    KBIT_BY_DTYPE(launch_dequantize_e, codes, ldc, scales, lds, rows, d, out, ldo, stream)
 }
 
 int launch_mx_product(Dtype t, const MxProduct& p, void* workspace, void* stream) {
     KBIT_BY_DTYPE(launch_product_e, p, workspace, stream)
 }
 
-int launch_mx_tokens(Dtype t, const MxProduct& p, int d, const void* X, int64_t ldX, bool vec, void* stream) {
-    KBIT_BY_DTYPE(launch_tokens_e, p, d, X, ldX, vec, stream)
+int launch_mx_tokens(Dtype t, const MxProduct& p, int d, const void* X, int64_t ldX, void* stream) {
+    KBIT_BY_DTYPE(launch_tokens_e, p, d, X, ldX, stream)
 }
 
 }  // namespace kbit

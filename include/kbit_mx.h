@@ -42,7 +42,7 @@ extern "C" {
 
 /* Columns of X [rows][cols] to codes and scales: row c of both is column c of
  * X, in blocks along its rows (the rows of X transposed, without transposing
- * it).  rows is at most 2^26.  cols = 0 is a no-op. */
+ * it).  rows is at most 2^26, cols at most 2^30.  cols = 0 is a no-op. */
 #define KBIT_DECLARE_QUANTIZE_MXFP4_COLUMNS(T, CTYPE)                                                          \
     int quantize_mxfp4_columns_##T(const CTYPE* X, int64_t rows, int32_t cols, int64_t ldx, uint8_t* codes,      \
                                    int64_t ldc, uint8_t* scales, int64_t lds, void* stream);
@@ -107,7 +107,7 @@ int64_t linear_mxfp4_backward_workspace_bytes(int64_t M, int32_t N, int32_t K);
  * Layer norm of rows of d values: y = (x - mean) / sqrt(var + eps) * weight +
  * bias with var the mean square of x - mean, fp32 inside, one rounding to T.
  * weight, bias: d values of T, or fp32 with weight_fp32 != 0; bias may be null.
- * eps >= 0, finite.  out may be x.  rows = 0 is a no-op.
+ * eps >= 0, finite; d at most 2^25.  out may be x.  rows = 0 is a no-op.
  * --------------------------------------------------------------------- */
 #define KBIT_DECLARE_LAYER_NORM(T, CTYPE)                                                                      \
     int layer_norm_##T(const CTYPE* x, int64_t rows, int32_t d, int64_t ldx, const void* weight,                 \
