@@ -363,6 +363,19 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t* 
 // so that a lane's two scales of a step are neighbours in memory and reach the
 // instruction as bytes of one register.  Which blocks meet in an instruction
 // only changes the order of the sum.
+//
+// LDS serves the 16-byte reads of 8 rows and two neighbouring lane groups at a
+// time, and the rows' parity picks the half of its banks: with pieces 2 (l / 16) +
+// h the lowest bit of a row's key has to stand in bit 1, or the two groups meet
+// (keys as for int8, bit 0: half of the LDS cycles were conflicts, 8192 x 11008 x 4096
+// in 205 us).
+__device__ __forceinline__ int mx_key(int k) { return (k & 4) | (k >> 1 & 1) | (k & 1) << 1; }
+__device__ __forceinline__ int mx_key_x(int row) { return mx_key(key_x(row)); }
+template <int TN>
+__device__ __forceinline__ int mx_key_w(int row) {
+    return mx_key(key_w<TN>(row));
+}
+
 template <int SEL>
 __device__ __forceinline__ f32x4 mfma(const i32x4& w, const i32x4& x, const f32x4& acc, uint32_t ws, uint32_t xs) {
     const i32x8 a = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -452,10 +465,10 @@ __global__ __launch_bounds__(WAVES* kWave) void mx_few_rows_kernel(const MxProdu
     int xo[2 * MT], wo[2 * TN], xso[MT], wso[TN];
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i)
-        xo[i] = min(8 * i + row0, rows - 1) * ldx + 16 * (piece0 ^ key_x(8 * i + row0));
+        xo[i] = min(8 * i + row0, rows - 1) * ldx + 16 * (piece0 ^ mx_key_x(8 * i + row0));
 #pragma unroll
     for (int i = 0; i < 2 * TN; ++i)
-        wo[i] = min(8 * i + row0, cols - 1) * ldw + 16 * (piece0 ^ key_w<TN>(8 * i + row0));
+        wo[i] = min(8 * i + row0, cols - 1) * ldw + 16 * (piece0 ^ mx_key_w<TN>(8 * i + row0));
 #pragma unroll
     for (int i = 0; i < MT; ++i) xso[i] = min(16 * i + l16, rows - 1) * static_cast<int>(p.ldxs) + 2 * q;
 #pragma unroll
@@ -485,11 +498,11 @@ __global__ __launch_bounds__(WAVES* kWave) void mx_few_rows_kernel(const MxProdu
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int row = operand_channel<TN>(j, l16);
-                w[h][j] = *reinterpret_cast<const i32x4*>(from + (BM + row) * kDepth + 16 * ((2 * q + h) ^ key_w<TN>(row)));
+                w[h][j] = *reinterpret_cast<const i32x4*>(from + (BM + row) * kDepth + 16 * ((2 * q + h) ^ mx_key_w<TN>(row)));
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                x[h][i] = *reinterpret_cast<const i32x4*>(from + (16 * i + l16) * kDepth + 16 * ((2 * q + h) ^ key_x(l16)));
+                x[h][i] = *reinterpret_cast<const i32x4*>(from + (16 * i + l16) * kDepth + 16 * ((2 * q + h) ^ mx_key_x(l16)));
         }
     };
     auto multiply = [&](const Scales& sc) {
@@ -530,13 +543,13 @@ __global__ __launch_bounds__(WAVES* kWave) void mx_few_rows_kernel(const MxProdu
         const u32x4 none = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
-            const int row = 8 * i + row0, at = k + 16 * (piece0 ^ key_x(row));
+            const int row = 8 * i + row0, at = k + 16 * (piece0 ^ mx_key_x(row));
             *reinterpret_cast<u32x4*>(e + 8 * i * kDepth + lane * 16) =
                 at < p.K ? load16<false>(xb + static_cast<int64_t>(min(row, rows - 1)) * ldx + at) : none;
         }
 #pragma unroll
         for (int i = 0; i < 2 * TN; ++i) {
-            const int row = 8 * i + row0, at = k + 16 * (piece0 ^ key_w<TN>(row));
+            const int row = 8 * i + row0, at = k + 16 * (piece0 ^ mx_key_w<TN>(row));
             *reinterpret_cast<u32x4*>(e + (BM + 8 * i) * kDepth + lane * 16) =
                 at < p.K ? load16<false>(wb + static_cast<int64_t>(min(row, cols - 1)) * ldw + at) : none;
         }
@@ -604,7 +617,7 @@ __global__ __launch_bounds__(WAVES* kWave) void mx_tokens_kernel(const MxProduct
     int wo[2 * TN], wso[TN];
 #pragma unroll
     for (int i = 0; i < 2 * TN; ++i)
-        wo[i] = min(8 * i + row0, cols - 1) * ldw + 16 * (piece0 ^ key_w<TN>(8 * i + row0));
+        wo[i] = min(8 * i + row0, cols - 1) * ldw + 16 * (piece0 ^ mx_key_w<TN>(8 * i + row0));
 #pragma unroll
     for (int j = 0; j < TN; ++j)
         wso[j] = min(operand_channel<TN>(j, l16), cols - 1) * static_cast<int>(p.ldws) + 2 * q;
@@ -663,7 +676,7 @@ __global__ __launch_bounds__(WAVES* kWave) void mx_tokens_kernel(const MxProduct
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int row = operand_channel<TN>(j, l16);
-                w[h][j] = *reinterpret_cast<const i32x4*>(from + row * kDepth + 16 * ((2 * q + h) ^ key_w<TN>(row)));
+                w[h][j] = *reinterpret_cast<const i32x4*>(from + row * kDepth + 16 * ((2 * q + h) ^ mx_key_w<TN>(row)));
             }
             x[h] = *reinterpret_cast<const i32x4*>(mine + at * kDepth + 16 * h);
         }
@@ -693,7 +706,7 @@ __global__ __launch_bounds__(WAVES* kWave) void mx_tokens_kernel(const MxProduct
         const u32x4 none = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int i = 0; i < 2 * TN; ++i) {
-            const int row = 8 * i + row0, at = k + 16 * (piece0 ^ key_w<TN>(row));
+            const int row = 8 * i + row0, at = k + 16 * (piece0 ^ mx_key_w<TN>(row));
             *reinterpret_cast<u32x4*>(e + 8 * i * kDepth + lane * 16) =
                 at < p.K ? load16<false>(wb + static_cast<int64_t>(min(row, cols - 1)) * ldw + at) : none;
         }
@@ -858,20 +871,24 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
     constexpr bool kTwoKeys = kRound % (8 * TN) != 0;
     const int row0 = (wave * kWave + lane) >> 3, piece0 = lane & 7;
     const int ldx = static_cast<int>(p.ldx), ldw = static_cast<int>(p.ldw);
-    const int xo = row0 * ldx + 16 * (piece0 ^ key_x(row0));
-    const int wo0 = row0 * ldw + 16 * (piece0 ^ key_w<TN>(row0));
-    const int wo1 = kTwoKeys ? row0 * ldw + 16 * (piece0 ^ key_w<TN>(row0 + kRound)) : wo0;
-    // Loads that are not `live` are issued all the same, to an empty range, and
-    // read no memory: a branch around them would make the compiler wait.
-    auto fetch = [&](int k, uint8_t* xd, uint8_t* wd, bool live) {
+    const int xo = row0 * ldx + 16 * (piece0 ^ mx_key_x(row0));
+    const int wo0 = row0 * ldw + 16 * (piece0 ^ mx_key_w<TN>(row0));
+    const int wo1 = kTwoKeys ? row0 * ldw + 16 * (piece0 ^ mx_key_w<TN>(row0 + kRound)) : wo0;
+    // One of the kLoads loads of a step.  Loads that are not `live` are issued all
+    // the same, to an empty range, and read no memory: a branch around them would
+    // make the compiler wait.
+    constexpr int kLoads = kXLoads + kWLoads;
+    auto fetch_one = [&](int n, int k, uint8_t* xd, uint8_t* wd, bool live) {
         const int range = live ? 0x7FFFFFFF : 0;
-        const auto xr = buf_rsrc(xb, range), wr = buf_rsrc(wb, range);
+        const int i = n < kXLoads ? n : n - kXLoads;
+        if (n < kXLoads)
+            load16_to_lds(buf_rsrc(xb, range), xd + (i * kT + wave * kWave) * 16, xo, k + i * kRound * ldx);
+        else
+            load16_to_lds(buf_rsrc(wb, range), wd + (i * kT + wave * kWave) * 16, (i & 1) ? wo1 : wo0, k + i * kRound * ldw);
+    };
+    auto fetch = [&](int k, uint8_t* xd, uint8_t* wd, bool live) {
 #pragma unroll
-        for (int i = 0; i < kXLoads; ++i)
-            load16_to_lds(xr, xd + (i * kT + wave * kWave) * 16, xo, k + i * kRound * ldx);
-#pragma unroll
-        for (int i = 0; i < kWLoads; ++i)
-            load16_to_lds(wr, wd + (i * kT + wave * kWave) * 16, (i & 1) ? wo1 : wo0, k + i * kRound * ldw);
+        for (int n = 0; n < kLoads; ++n) fetch_one(n, k, xd, wd, live);
     };
     // Scales of a pair of steps, as they stand in memory, to their places.
     auto put_scales = [&](uint8_t* to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -883,14 +900,14 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
     // Half a step's operands (4 blocks) in LDS; the keys do not change with i
     // and j, 16 and 4 rows on.
     const int w_row = operand_channel<TN>(0, l16);
-    const int xp[2] = {(wm + l16) * kDepth + 16 * ((2 * q) ^ key_x(l16)),
-                       (wm + l16) * kDepth + 16 * ((2 * q + 1) ^ key_x(l16))};
-    const int wp[2] = {(wn + w_row) * kDepth + 16 * ((2 * q) ^ key_w<TN>(w_row)),
-                       (wn + w_row) * kDepth + 16 * ((2 * q + 1) ^ key_w<TN>(w_row))};
+    const int xp[2] = {(wm + l16) * kDepth + 16 * ((2 * q) ^ mx_key_x(l16)),
+                       (wm + l16) * kDepth + 16 * ((2 * q + 1) ^ mx_key_x(l16))};
+    const int wp[2] = {(wn + w_row) * kDepth + 16 * ((2 * q) ^ mx_key_w<TN>(w_row)),
+                       (wn + w_row) * kDepth + 16 * ((2 * q + 1) ^ mx_key_w<TN>(w_row))};
     const int xsp = (wm + l16) * 16 + 4 * q, wsp = (BM + wn + w_row) * 16 + 4 * q;
     f32x4 acc[TM][TN];
     i32x4 x[TM], w0[TN], w1[TN];
-    uint32_t sx[TM], sw[TN];
+    uint32_t sx[TM], sw[TN], sw_next[TN];
     auto read_x = [&](const uint8_t* xd, int h, int i) {
         x[i] = *reinterpret_cast<const i32x4*>(xd + xp[h] + 16 * i * kDepth);
     };
@@ -903,27 +920,42 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
 #pragma unroll
         for (int i = 0; i < TM; ++i) read_x(xd, h, i);
     };
+    auto read_sx = [&](const uint8_t* from, int i) { return *reinterpret_cast<const uint32_t*>(from + xsp + 16 * i * 16); };
+    auto read_sw = [&](const uint8_t* from, int j) { return *reinterpret_cast<const uint32_t*>(from + wsp + 4 * j * 16); };
     auto read_scales = [&](const uint8_t* from) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) sx[i] = *reinterpret_cast<const uint32_t*>(from + xsp + 16 * i * 16);
+        for (int i = 0; i < TM; ++i) sx[i] = read_sx(from, i);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) sw[j] = *reinterpret_cast<const uint32_t*>(from + wsp + 4 * j * 16);
+        for (int j = 0; j < TN; ++j) sw[j] = read_sw(from, j);
     };
-    // The products of half a step; each operand of x is replaced by half h of
-    // (xn, wn) as soon as its last product is issued, and the next weights are
-    // read on the way.
-    constexpr int kPer = TM < TN ? TN / TM : 1;
-    auto multiply = [&](auto sel, const i32x4 (&w)[TN], const uint8_t* xn, const uint8_t* wn, int h, i32x4 (&w_next)[TN]) {
+    // The products of half a step.  Each operand of x is replaced by half h of (xn,
+    // wn) as soon as its last product is issued, and the next weights are read on
+    // the way; in the last half of a pair (SEL 3) the next pair's scales as well.
+    // Beside them a part of the loads to LDS is issued, load(n).  The order is held
+    // group by group: left to itself the compiler puts reads right before their
+    // use (8192^3 262 us, 8192 x 11008 x 4096 217).
+    constexpr int kPer = TM < TN ? TN / TM : 1, kPerLoads = (kLoads + TM - 1) / TM;
+    auto multiply = [&](auto sel, const i32x4 (&w)[TN], const uint8_t* xn, const uint8_t* wn, int h, i32x4 (&w_next)[TN],
+                        const uint8_t* scales_next, const auto& load) {
+        constexpr int SEL = decltype(sel)::value;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<decltype(sel)::value>(w[j], x[i], acc[i][j], sw[j], sx[i]);
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<SEL>(w[j], x[i], acc[i][j], sw[j], sx[i]);
             read_x(xn, h, i);
 #pragma unroll
-            for (int j = i * kPer; j < (i + 1) * kPer && j < TN; ++j) w_next[j] = read_w(wn, h, j);
-            __builtin_amdgcn_sched_group_barrier(0x008, TN, 0);
-            if (i * kPer < TN) __builtin_amdgcn_sched_group_barrier(0x100, 1 + kPer, 0);
-            else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            for (int j = i * kPer; j < (i + 1) * kPer && j < TN; ++j) {
+                w_next[j] = read_w(wn, h, j);
+                if (SEL == 3) sw_next[j] = read_sw(scales_next, j);
+            }
+            if (SEL == 3) sx[i] = read_sx(scales_next, i);
+#pragma unroll
+            for (int n = i * kPerLoads; n < (i + 1) * kPerLoads && n < kLoads; ++n) load(n);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (SEL == 3) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) sw[j] = sw_next[j];
         }
     };
     auto multiply_all = [&](auto sel, const i32x4 (&w)[TN]) {
@@ -965,13 +997,13 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
                 const u32x4 none = {0u, 0u, 0u, 0u};
 #pragma unroll
                 for (int i = 0; i < kXLoads; ++i) {
-                    const int row = row0 + i * kRound, at = k + 16 * (piece0 ^ key_x(row));
+                    const int row = row0 + i * kRound, at = k + 16 * (piece0 ^ mx_key_x(row));
                     *reinterpret_cast<u32x4*>(x_even + row * kDepth + 16 * piece0) =
                         at < K ? load16<false>(xb + static_cast<int64_t>(row) * ldx + at) : none;
                 }
 #pragma unroll
                 for (int i = 0; i < kWLoads; ++i) {
-                    const int row = row0 + i * kRound, at = k + 16 * (piece0 ^ key_w<TN>(row));
+                    const int row = row0 + i * kRound, at = k + 16 * (piece0 ^ mx_key_w<TN>(row));
                     *reinterpret_cast<u32x4*>(w_even + row * kDepth + 16 * piece0) =
                         at < K ? load16<false>(wb + static_cast<int64_t>(row) * ldw + at) : none;
                 }
@@ -995,21 +1027,23 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
             __builtin_amdgcn_s_waitcnt(0);
         }
         put_scales(scales[0], carried[0], carried[1], carried[2], carried[3]);
+        if (pairs > 0) fetch_scales(1);
         __syncthreads();
         read(x_even, w_even, 0, w0);
+        read_scales(scales[0]);
+        const auto nothing = [](int) {};
         for (int s = 0; s < steps; s += 2) {  // past the last step it reads operands that nobody multiplies
-            read_scales(scales[(s >> 1) & 1]);
-            multiply(Sel0{}, w0, x_even, w_even, 1, w1);
+            uint8_t* const next = scales[(s >> 1) + 1 & 1];
+            multiply(Sel0{}, w0, x_even, w_even, 1, w1, next, nothing);
             arrive();
-            fetch((s + 2) * kDepth, x_even, w_even, s + 2 < steps);
-            fetch_scales((s >> 1) + 1);
-            multiply(Sel1{}, w1, x_odd, w_odd, 0, w0);
-            multiply(Sel2{}, w0, x_odd, w_odd, 1, w1);
-            __builtin_amdgcn_s_waitcnt(0);
-            put_scales(scales[((s >> 1) + 1) & 1], carried[0], carried[1], carried[2], carried[3]);
-            __syncthreads();
-            fetch((s + 3) * kDepth, x_odd, w_odd, s + 3 < steps);
-            multiply(Sel3{}, w1, x_even, w_even, 0, w0);
+            put_scales(next, carried[0], carried[1], carried[2], carried[3]);
+            fetch_scales((s >> 1) + 2);
+            multiply(Sel1{}, w1, x_odd, w_odd, 0, w0, next,
+                     [&](int n) { fetch_one(n, (s + 2) * kDepth, x_even, w_even, s + 2 < steps); });
+            multiply(Sel2{}, w0, x_odd, w_odd, 1, w1, next, nothing);
+            arrive();
+            multiply(Sel3{}, w1, x_even, w_even, 0, w0, next,
+                     [&](int n) { fetch_one(n, (s + 3) * kDepth, x_odd, w_odd, s + 3 < steps); });
         }
         // What follows runs once a tile: its addresses are made anew from the
         // thread's number, so that the loop above keeps no registers for them.
