@@ -38,7 +38,7 @@ int do_quantize(Dtype t, const void* X, int64_t rows, int32_t d, int64_t ldx, ui
     if (!X || !codes || !scales) return KBIT_EINVAL;
     if (!aligned(X, elem_size(t)) || !codes_aligned(codes, rows, ldc)) return KBIT_EALIGN;
     if (!device_usable()) return KBIT_EDEVICE;
-    return map_launch(launch_mx_quantize(t, X, rows, d, ldx, MxCoded{codes, scales, ldc, lds}, stream));
+    return map_launch(launch_mx_quantize(t, X, rows, d, ldx, MxCoded{codes, scales, ldc, lds, false}, stream));
 }
 
 int do_quantize_columns(Dtype t, const void* X, int64_t rows, int32_t cols, int64_t ldx, uint8_t* codes, int64_t ldc,
@@ -49,7 +49,7 @@ int do_quantize_columns(Dtype t, const void* X, int64_t rows, int32_t cols, int6
     if (!X || !codes || !scales) return KBIT_EINVAL;
     if (!aligned(X, elem_size(t)) || !codes_aligned(codes, cols, ldc)) return KBIT_EALIGN;
     if (!device_usable()) return KBIT_EDEVICE;
-    return map_launch(launch_mx_quantize_columns(t, X, rows, cols, ldx, MxCoded{codes, scales, ldc, lds}, MxCoded{}, nullptr, stream));
+    return map_launch(launch_mx_quantize_columns(t, X, rows, cols, ldx, MxCoded{codes, scales, ldc, lds, false}, MxCoded{}, nullptr, stream));
 }
 
 int do_dequantize(Dtype t, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t rows, int32_t d,
@@ -83,13 +83,16 @@ int do_linear(Dtype t, MxProduct p, int64_t d, void* workspace, int64_t workspac
     if (!p.x || !p.xs) return KBIT_EINVAL;
     if (!codes_aligned(p.x, p.M, p.ldx) || !aligned(workspace, 16)) return KBIT_EALIGN;
     p.K = mx_depth(d);
-    const int64_t need = int8_product_workspace(p.M, p.N, p.K);
+    const int64_t need = mx_product_workspace(p.M, p.N, p.K);
     if (workspace_bytes < need || (need > 0 && !workspace)) return KBIT_EINVAL;
     if (!device_usable()) return KBIT_EDEVICE;
     return map_launch(launch_mx_product(t, p, workspace, stream));
 }
 
-MxCoded coded_in(uint8_t* at, const MxRows& r) { return MxCoded{at, at + r.scales, r.ldc, r.lds}; }
+// Rows in a workspace; paired: the order of their scales.
+MxCoded coded_in(uint8_t* at, const MxRows& r, int64_t rows, bool paired) {
+    return MxCoded{at, at + r.scales, r.ldc, paired ? rows * 16 : r.lds, paired};
+}
 
 int do_linear_dynamic(Dtype t, const void* X, int64_t ldX, MxProduct p, int64_t d, void* workspace,
                       int64_t workspace_bytes, void* stream) {
@@ -107,19 +110,21 @@ int do_linear_dynamic(Dtype t, const void* X, int64_t ldX, MxProduct p, int64_t 
         return map_launch(launch_mx_tokens(t, p, static_cast<int>(d), X, ldX, stream));
     }
     const int64_t at = (r.bytes + 15) / 16 * 16;
-    if (!workspace || workspace_bytes < at + int8_product_workspace(p.M, p.N, p.K)) return KBIT_EINVAL;
+    p.x_paired = mx_paired(p.M, p.N, p.K);
+    if (!workspace || workspace_bytes < at + mx_product_workspace(p.M, p.N, p.K, p.x_paired)) return KBIT_EINVAL;
     if (!device_usable()) return KBIT_EDEVICE;
     uint8_t* w = static_cast<uint8_t*>(workspace);
-    const int e = launch_mx_quantize(t, X, p.M, static_cast<int>(d), ldX, coded_in(w, r), stream);
-    if (e != 0) return KBIT_ELAUNCH;
+    const MxCoded c_x = coded_in(w, r, p.M, p.x_paired);
+    if (launch_mx_quantize(t, X, p.M, static_cast<int>(d), ldX, c_x, stream) != 0) return KBIT_ELAUNCH;
     p.x = w;
-    p.xs = w + r.scales;
+    p.xs = c_x.scales;
+    p.ldxs = c_x.lds;
     return map_launch(launch_mx_product(t, p, w + at, stream));
 }
 
-MxProduct product_of(const uint8_t* a, const MxRows& ra, int64_t M, const uint8_t* b, const MxRows& rb, int N, int64_t depth,
-                     void* out, int64_t ldo) {
-    return MxProduct{a, a + ra.scales, b, b + rb.scales, nullptr, out, M, ra.ldc, ra.lds, rb.ldc, rb.lds, ldo, N, mx_depth(depth)};
+MxProduct product_of(const MxCoded& a, int64_t M, const MxCoded& b, int N, int64_t depth, void* out, int64_t ldo) {
+    return MxProduct{a.codes, a.scales, b.codes, b.scales, nullptr, out,           M,       a.ldc,
+                     a.lds,   b.ldc,    b.lds,   ldo,      N,       mx_depth(depth), a.paired, b.paired};
 }
 
 int do_linear_backward(Dtype t, const void* g, int64_t ldg, const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M,
@@ -136,11 +141,7 @@ int do_linear_backward(Dtype t, const void* g, int64_t ldg, const void* X, int64
         !aligned(workspace, 16))
         return KBIT_EALIGN;
     const MxBackParts b = mx_back_parts(M, N, K);
-    const int64_t own = M == 0 ? 0
-                               : int64_t(dX ? int8_product_workspace(M, K, mx_depth(N)) : 0);
-    const int64_t own_w = M == 0 || !dW ? 0 : int8_product_workspace(N, K, mx_depth(M));
-    const int64_t need = b.product_at + (own > own_w ? own : own_w);
-    if (M > 0 && (!workspace || workspace_bytes < need)) return KBIT_EINVAL;
+    if (M > 0 && (!workspace || workspace_bytes < mx_back_workspace(M, N, K, dX != nullptr, dW != nullptr))) return KBIT_EINVAL;
     // the operands' rows in the workspace, as the products need them
     if (M > 0 && ((dX && (!near_rows(M, b.g_rows.ldc) || !near_rows(K, b.w_cols.ldc))) ||
                   (dW && (!near_rows(N, b.g_cols.ldc) || !near_rows(K, b.x_cols.ldc)))))
@@ -152,19 +153,20 @@ int do_linear_backward(Dtype t, const void* g, int64_t ldg, const void* X, int64
     }
     uint8_t* w = static_cast<uint8_t*>(workspace);
     float* sums = reinterpret_cast<float*>(w + b.sums_at);
-    uint8_t *w_cols = w + b.w_at, *g_cols = w + b.gc_at, *x_cols = w + b.x_at;
+    const bool pair_x = dX && mx_paired(M, K, mx_depth(N)), pair_w = dW && mx_paired(N, K, mx_depth(M));
+    const MxCoded g_rows = coded_in(w, b.g_rows, M, pair_x), w_cols = coded_in(w + b.w_at, b.w_cols, K, pair_x),
+                  g_cols = coded_in(w + b.gc_at, b.g_cols, N, pair_w), x_cols = coded_in(w + b.x_at, b.x_cols, K, pair_w);
     // dout along its rows alone, or its columns with them
-    const int e = dW || db ? launch_mx_quantize_columns(t, g, M, N, ldg, dW ? coded_in(g_cols, b.g_cols) : MxCoded{},
-                                                        dX ? coded_in(w, b.g_rows) : MxCoded{}, db ? sums : nullptr, stream)
-                           : launch_mx_quantize(t, g, M, N, ldg, coded_in(w, b.g_rows), stream);
+    const int e = dW || db ? launch_mx_quantize_columns(t, g, M, N, ldg, dW ? g_cols : MxCoded{}, dX ? g_rows : MxCoded{},
+                                                        db ? sums : nullptr, stream)
+                           : launch_mx_quantize(t, g, M, N, ldg, g_rows, stream);
     if (e != 0) return KBIT_ELAUNCH;
     if (db && launch_mx_add_sums(sums, mx_sum_groups(M), N, db, stream) != 0) return KBIT_ELAUNCH;
-    if (dX && (launch_mx_quantize_columns(t, W, N, K, ldw, coded_in(w_cols, b.w_cols), MxCoded{}, nullptr, stream) != 0 ||
-               launch_mx_product(t, product_of(w, b.g_rows, M, w_cols, b.w_cols, K, N, dX, lddx), w + b.product_at, stream) != 0))
+    if (dX && (launch_mx_quantize_columns(t, W, N, K, ldw, w_cols, MxCoded{}, nullptr, stream) != 0 ||
+               launch_mx_product(t, product_of(g_rows, M, w_cols, K, N, dX, lddx), w + b.product_at, stream) != 0))
         return KBIT_ELAUNCH;
-    if (dW && (launch_mx_quantize_columns(t, X, M, K, ldx, coded_in(x_cols, b.x_cols), MxCoded{}, nullptr, stream) != 0 ||
-               launch_mx_product(Dtype::fp32, product_of(g_cols, b.g_cols, N, x_cols, b.x_cols, K, M, dW, lddw),
-                                 w + b.product_at, stream) != 0))
+    if (dW && (launch_mx_quantize_columns(t, X, M, K, ldx, x_cols, MxCoded{}, nullptr, stream) != 0 ||
+               launch_mx_product(Dtype::fp32, product_of(g_cols, N, x_cols, K, M, dW, lddw), w + b.product_at, stream) != 0))
         return KBIT_ELAUNCH;
     return KBIT_OK;
 }
@@ -210,12 +212,12 @@ extern "C" {
 
 int64_t linear_mxfp4_workspace_bytes(int64_t M, int32_t N, int32_t K) {
     if (!kbit::product_sizes_ok(M, N, K)) return -1;
-    return kbit::int8_product_workspace_up_to(M, N, kbit::mx_depth(K));
+    return kbit::mx_product_workspace_up_to(M, N, kbit::mx_depth(K));
 }
 
 int64_t linear_mxfp4_dynamic_workspace_bytes(int64_t M, int32_t N, int32_t K) {
     if (!kbit::product_sizes_ok(M, N, K)) return -1;
-    return (kbit::mx_rows(M, K).bytes + 15) / 16 * 16 + kbit::int8_product_workspace_up_to(M, N, kbit::mx_depth(K));
+    return (kbit::mx_rows(M, K).bytes + 15) / 16 * 16 + kbit::mx_product_workspace_up_to(M, N, kbit::mx_depth(K));
 }
 
 int linear_mxfp4_dynamic_fused(int64_t M, int32_t N, int32_t K, int64_t ldw, int64_t ldws) {
@@ -225,8 +227,8 @@ int linear_mxfp4_dynamic_fused(int64_t M, int32_t N, int32_t K, int64_t ldw, int
 int64_t linear_mxfp4_backward_workspace_bytes(int64_t M, int32_t N, int32_t K) {
     if (M < 0 || M > kbit::kMxMaxDepth || !kbit::depth_ok(N) || !kbit::depth_ok(K)) return -1;
     if (M == 0) return 0;
-    const int64_t a = kbit::int8_product_workspace_up_to(M, K, kbit::mx_depth(N));
-    const int64_t b = kbit::int8_product_workspace_up_to(N, K, kbit::mx_depth(M));
+    const int64_t a = kbit::mx_product_workspace_up_to(M, K, kbit::mx_depth(N));
+    const int64_t b = kbit::mx_product_workspace_up_to(N, K, kbit::mx_depth(M));
     return kbit::mx_back_parts(M, N, K).product_at + (a > b ? a : b);
 }
 
@@ -253,7 +255,7 @@ int64_t layer_norm_backward_workspace_bytes(int64_t rows, int32_t d) {
                              int64_t ldws, const CTYPE* bias, CTYPE* out, int64_t ldo, void* workspace,               \
                              int64_t workspace_bytes, void* stream) {                                                 \
         return kbit::do_linear(Dtype::TNAME,                                                                          \
-                               MxProduct{codes, scales, w_codes, w_scales, bias, out, M, ldx, ldxs, ldw, ldws, ldo, N, 0}, \
+                               MxProduct{codes, scales, w_codes, w_scales, bias, out, M, ldx, ldxs, ldw, ldws, ldo, N, 0, false, false}, \
                                K, workspace, workspace_bytes, stream);                                                \
     }                                                                                                                 \
     int linear_mxfp4_dynamic_##TNAME(const CTYPE* X, int64_t M, int32_t K, int64_t ldx, const uint8_t* w_codes,       \
@@ -261,7 +263,7 @@ int64_t layer_norm_backward_workspace_bytes(int64_t rows, int32_t d) {
                                      const CTYPE* bias, CTYPE* out, int64_t ldo, void* workspace,                     \
                                      int64_t workspace_bytes, void* stream) {                                         \
         return kbit::do_linear_dynamic(                                                                               \
-            Dtype::TNAME, X, ldx, MxProduct{nullptr, nullptr, w_codes, w_scales, bias, out, M, 0, 0, ldw, ldws, ldo, N, 0}, \
+            Dtype::TNAME, X, ldx, MxProduct{nullptr, nullptr, w_codes, w_scales, bias, out, M, 0, 0, ldw, ldws, ldo, N, 0, false, false}, \
             K, workspace, workspace_bytes, stream);                                                                   \
     }                                                                                                                 \
     int linear_mxfp4_backward_##TNAME(const CTYPE* dout, int64_t lddo, const CTYPE* X, int64_t ldx, const CTYPE* W,   \

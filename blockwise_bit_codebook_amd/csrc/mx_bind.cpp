@@ -180,7 +180,7 @@ PyObject* linear(PyObject* const* a) {  // codes, scales, w_codes, w_scales, bia
     apart(w.out.t, "out", x, "codes");
     apart(w.out.t, "out", xs, "scales");
     const int64_t need = linear_mxfp4_workspace_bytes(c.rows, w.N, K);
-    const Space ws = workspace(need, need > 0 ? kbit::int8_product_workspace(c.rows, w.N, kbit::mx_depth(K)) : 0, a[7],
+    const Space ws = workspace(need, need > 0 ? kbit::mx_product_workspace(c.rows, w.N, kbit::mx_depth(K)) : 0, a[7],
                                "linear_mxfp4", x);
     KBIT_BY_TYPE(type, linear_mxfp4, run("linear_mxfp4", x, {&w.out.t}, [&](void* stream) {
         return fn(c.codes, c.scales, c.rows, K, c.ldc, c.lds, w.c.codes, w.c.scales, w.N, w.c.ldc, w.c.lds,
@@ -201,7 +201,8 @@ PyObject* linear_dynamic(PyObject* const* a) {  // X, w_codes, w_scales, bias, o
     const int64_t need = fused ? 0 : linear_mxfp4_dynamic_workspace_bytes(M, w.N, K);
     const int64_t take = need <= 0 ? 0
                                    : (kbit::mx_rows(M, K).bytes + 15) / 16 * 16 +
-                                         kbit::int8_product_workspace(M, w.N, kbit::mx_depth(K));
+                                         kbit::mx_product_workspace(M, w.N, kbit::mx_depth(K),
+                                                                    kbit::mx_paired(M, w.N, kbit::mx_depth(K)));
     const Space ws = workspace(need, take, a[5], "linear_mxfp4_dynamic", x);
     KBIT_BY_TYPE(type, linear_mxfp4_dynamic, run("linear_mxfp4_dynamic", x, {&w.out.t}, [&](void* stream) {
         return fn(static_cast<const T*>(x.data_ptr()), M, K, ldx, w.c.codes, w.c.scales, w.N, w.c.ldc, w.c.lds,
@@ -252,12 +253,7 @@ PyObject* linear_backward(PyObject* const* a) {
     Space ws;
     if (M > 0) {
         const int64_t need = linear_mxfp4_backward_workspace_bytes(M, N, K);
-        int64_t take = need;
-        if (need > 0) {
-            const int64_t p = input ? kbit::int8_product_workspace(M, K, kbit::mx_depth(N)) : 0;
-            const int64_t q = weights ? kbit::int8_product_workspace(N, K, kbit::mx_depth(M)) : 0;
-            take = kbit::mx_back_parts(M, N, K).product_at + std::max(p, q);
-        }
+        const int64_t take = need < 0 ? need : kbit::mx_back_workspace(M, N, K, input, weights);
         ws = workspace(need, take, a[8], "linear_mxfp4_backward", g);
     }
     const auto ptr = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };

@@ -5,6 +5,8 @@
 
 #include <stdint.h>
 
+#include <tuple>
+
 #include "int8_choice.h"
 #include "kbit_internal.h"
 
@@ -21,11 +23,15 @@ constexpr int64_t kMxMaxColumns = int64_t(1) << 30;
 
 inline int64_t mx_blocks(int64_t d) { return (d + kMxBlock - 1) / kMxBlock; }
 
-// Rows of codes and scales.
+// Rows of codes and scales.  paired: the scales stand in the order of pairs of
+// steps of the product, 16 blocks of all rows after each other, lds bytes from
+// pair to pair, 16 bytes a row (pair_place), for tiles of kPairedRows rows.
 struct MxCoded {
     uint8_t *codes, *scales;  // both or neither null
     int64_t ldc, lds;
+    bool paired;
 };
+constexpr int kPairedRows = 256;
 
 int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx, const MxCoded& c, void* stream);
 
@@ -52,12 +58,44 @@ struct MxProduct {
     const void* bias;
     void* out;
     int64_t M, ldx, ldxs, ldw, ldws, ldo;
-    int N, K;  // K: bytes of a row of codes, a multiple of 16
+    int N, K;                 // K: bytes of a row of codes, a multiple of 16
+    bool x_paired, w_paired;  // see MxCoded; only where mx_paired(M, N, K)
 };
 
-// workspace: of int8_product_workspace(M, N, K) bytes on the current device
-// (the kernels are those of the int8 product, a byte for a byte), 16-byte
-// aligned.
+// The kernels are those of the int8 product, a byte for a byte (choose_form).
+// Whether the product takes the scales of both operands paired, which a caller
+// that quantizes them itself may write so.
+inline bool mx_paired(int64_t M, int64_t N, int K) {
+    return M >= 1 && M <= kRowBlock && N <= kMaxChannels &&
+           choose_form(M, static_cast<int>(N), K, device_cu_count()).bm == kPairedRows;
+}
+
+// Bytes of scales in the order of pairs of steps.
+inline int64_t mx_paired_bytes(int64_t rows, int K) { return rows * ((K + 2 * kDepth - 1) / (2 * kDepth)) * 16; }
+
+// Bytes of workspace of a product on the current device: the sums of parts of
+// the depth, or scales that are not paired yet.
+inline int64_t mx_product_workspace(int64_t M, int N, int K, bool x_paired = false, bool w_paired = false) {
+    int64_t most = int8_product_workspace(M, N, K);
+    for (const int64_t m : {M < kRowBlock ? M : kRowBlock, M % kRowBlock})
+        for (const int64_t n : {N < kMaxChannels ? N : kMaxChannels, N % kMaxChannels}) {
+            if (m == 0 || n == 0 || !mx_paired(m, n, K)) continue;
+            const int64_t need = (x_paired ? 0 : mx_paired_bytes(m, K)) + (w_paired ? 0 : mx_paired_bytes(n, K));
+            if (need > most) most = need;
+        }
+    return most;
+}
+
+// No less than that for any number of rows up to M, and never less for more
+// rows.
+inline int64_t mx_product_workspace_up_to(int64_t M, int N, int K) {
+    const int64_t sums = int8_product_workspace_up_to(M, N, K);
+    if (M < kPairedRows || N < kPairedRows) return sums;
+    const int64_t scales = mx_paired_bytes((M < kRowBlock ? M : kRowBlock) + (N < kMaxChannels ? N : kMaxChannels), K);
+    return scales > sums ? scales : sums;
+}
+
+// workspace: of mx_product_workspace bytes, 16-byte aligned.
 int launch_mx_product(Dtype t, const MxProduct& p, void* workspace, void* stream);
 
 // Tokens quantized inside the product's kernel: their codes stay in LDS.
@@ -108,6 +146,18 @@ inline MxBackParts mx_back_parts(int64_t M, int N, int K) {
     b.sums_at = b.x_at + up(b.x_cols.bytes);
     b.product_at = b.sums_at + up(4 * mx_sum_groups(M) * N);
     return b;
+}
+
+// Bytes of it that a call needs.
+inline int64_t mx_back_workspace(int64_t M, int N, int K, bool dX, bool dW) {
+    int64_t own = 0;
+    for (const auto& [rows, depth, wanted] : {std::make_tuple(M, mx_depth(N), dX), std::make_tuple(int64_t(N), mx_depth(M), dW)}) {
+        if (!wanted) continue;
+        const bool paired = mx_paired(rows, K, depth);
+        const int64_t need = mx_product_workspace(rows, K, depth, paired, paired);
+        if (need > own) own = need;
+    }
+    return mx_back_parts(M, N, K).product_at + own;
 }
 
 // p.x and p.xs are not looked at.

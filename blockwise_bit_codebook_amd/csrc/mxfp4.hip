@@ -95,14 +95,22 @@ __device__ __forceinline__ uint32_t row_codes(const u32x4 (&r)[E::kVec], uint32_
     return byte == 255u ? 0u : q;
 }
 
+// Where the scale of a block of a row stands.
+__device__ __forceinline__ int pair_place(int block) {  // of its 16 bytes, see pair_order
+    return 2 * (block & 6) + (block & 8) / 4 + (block & 1);
+}
+__device__ __forceinline__ uint8_t* scale_place(const MxCoded& c, int64_t row, int64_t block) {
+    return c.paired ? c.scales + (block >> 4) * c.lds + row * 16 + pair_place(static_cast<int>(block & 15))
+                    : c.scales + row * c.lds + block;
+}
+
 // Rows: 8 values a lane, four lanes a block, kRowItems pieces of 512 values a
 // wave on their way together.  Piece i of all rows: row i / per_row.
 constexpr int kRowItems = 4;
 template <class E>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const typename E::T* __restrict__ X, uint32_t items,
                                                                uint32_t per_row, int d, int64_t ldx,
-                                                               uint8_t* __restrict__ codes, int64_t ldc,
-                                                               uint8_t* __restrict__ scales, int64_t lds) {
+                                                               const MxCoded out) {
     const int lane = __lane_id();
     const uint32_t first = (blockIdx.x * kWavesPerGroup + threadIdx.x / kWave) * kRowItems;
     const int end = (d + kMxBlock - 1) / kMxBlock * kMxBlock;
@@ -124,8 +132,8 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const typename E:
     for (int i = 0; i < kRowItems; ++i) {
         if (cols[i] < end) {  // end is a whole number of blocks: quads stay together
             const uint32_t byte = row_byte<E>(v[i]);
-            *reinterpret_cast<uint32_t*>(codes + rows[i] * ldc + cols[i] / 2) = row_codes<E>(v[i], byte);
-            if ((lane & 3) == 0) scales[rows[i] * lds + cols[i] / kMxBlock] = static_cast<uint8_t>(byte);
+            *reinterpret_cast<uint32_t*>(out.codes + rows[i] * out.ldc + cols[i] / 2) = row_codes<E>(v[i], byte);
+            if ((lane & 3) == 0) *scale_place(out, rows[i], cols[i] / kMxBlock) = static_cast<uint8_t>(byte);
         }
     }
 }
@@ -141,9 +149,8 @@ constexpr int kCols = 8 / sizeof(typename E::T);
 
 template <class E, bool ROWS>
 __global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(
-    const typename E::T* __restrict__ X, int64_t rows, int cols, int64_t ldx, uint8_t* __restrict__ codes, int64_t ldc,
-    uint8_t* __restrict__ scales, int64_t lds, uint8_t* __restrict__ row_codes_out, int64_t ldrc,
-    uint8_t* __restrict__ row_scales_out, int64_t ldrs, float* __restrict__ sums) {
+    const typename E::T* __restrict__ X, int64_t rows, int cols, int64_t ldx, const MxCoded columns, const MxCoded by_rows,
+    int64_t first_row, float* __restrict__ sums) {
     using T = typename E::T;
     constexpr int C = kCols<E>, kTile = kWave * C;
     constexpr bool kWide = sizeof(T) == 4;
@@ -179,7 +186,7 @@ __global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(
                     }
                 }
         }
-        if (codes) {
+        if (columns.codes) {
             uint32_t m[2] = {0u, 0u};
 #pragma unroll
             for (int r = 0; r < kMxBlock; ++r)
@@ -248,10 +255,11 @@ __global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(
                 if (byte == 255u) q = 0u;
                 const int end = (cols + kMxBlock - 1) / kMxBlock * kMxBlock;
                 if (r < n && col < end) {
-                    uint8_t* to = row_codes_out + (r0 + r) * ldrc + col / 2;
+                    uint8_t* to = by_rows.codes + (first_row + r0 + r) * by_rows.ldc + col / 2;
                     if constexpr (kWide) *to = static_cast<uint8_t>(q);
                     else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(q);
-                    if (col % kMxBlock == 0) row_scales_out[(r0 + r) * ldrs + col / kMxBlock] = static_cast<uint8_t>(byte);
+                    if (col % kMxBlock == 0)
+                        *scale_place(by_rows, first_row + r0 + r, col / kMxBlock) = static_cast<uint8_t>(byte);
                 }
             }
         }
@@ -266,22 +274,23 @@ __global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(
         for (int w = 1; w < kColBlocks; ++w) total += partial[w][threadIdx.x];
         sums[blockIdx.y * static_cast<int64_t>(cols) + col0 + threadIdx.x] = total;
     }
-    if (!codes) return;
+    if (!columns.codes) return;
     const int live = static_cast<int>(min<int64_t>(row_blocks - block0, kColBlocks));
+    const int64_t first_block = first_row / kMxBlock + block0;
 #pragma unroll
     for (int t = threadIdx.x; t < kTile * kColBlocks; t += kColBlocks * kWave) {
         const int c = t / kColBlocks, b = t % kColBlocks;
         if (b < live && col0 + c < cols)
-            *reinterpret_cast<u32x4*>(codes + (col0 + c) * ldc + (block0 + b) * kMxBlockBytes) =
+            *reinterpret_cast<u32x4*>(columns.codes + (col0 + c) * columns.ldc + (first_block + b) * kMxBlockBytes) =
                 *reinterpret_cast<const u32x4*>(tile + (c * kColBlocks + (b ^ (c / C & 7))) * kMxBlockBytes);
     }
     const int c = threadIdx.x;
     if (c < kTile && col0 + c < cols) {
-        uint8_t* to = scales + (col0 + c) * lds + block0;
-        if (live == kColBlocks) {
-            *reinterpret_cast<u32x2_any*>(to) = *reinterpret_cast<const u32x2_any*>(bytes + c * kColBlocks);
+        if (live == kColBlocks && !columns.paired) {
+            *reinterpret_cast<u32x2_any*>(columns.scales + (col0 + c) * columns.lds + first_block) =
+                *reinterpret_cast<const u32x2_any*>(bytes + c * kColBlocks);
         } else {
-            for (int b = 0; b < live; ++b) to[b] = bytes[c * kColBlocks + b];
+            for (int b = 0; b < live; ++b) *scale_place(columns, col0 + c, first_block + b) = bytes[c * kColBlocks + b];
         }
     }
 }
@@ -391,6 +400,13 @@ __device__ __forceinline__ f32x4 mfma(const i32x4& w, const i32x4& x, const f32x
 __device__ __forceinline__ void wave_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+}
+
+// 16 scales of a row in the order of a pair of steps: word q has those of lane
+// group q, halves 0 and 1 of the even step, then of the odd one.
+__device__ __forceinline__ u32x4 pair_order(const u32x4& s) {
+    return u32x4{__builtin_amdgcn_perm(s[2], s[0], 0x05040100u), __builtin_amdgcn_perm(s[2], s[0], 0x07060302u),
+                 __builtin_amdgcn_perm(s[3], s[1], 0x05040100u), __builtin_amdgcn_perm(s[3], s[1], 0x07060302u)};
 }
 
 // Up to 8 scales of a row from block k on, as two words; past the row's end 0,
@@ -813,6 +829,11 @@ __device__ __forceinline__ void store_tile(const MxProduct& p, T* out, uint8_t* 
 // the next are on their way while the outputs of one leave, through LDS of
 // their own, and the next one's products do not wait for those stores.  For
 // whole pairs of steps and outputs of whole 16-byte pieces.
+//
+// Tiles of 256 rows take their scales in the order of a pair of steps
+// (MxScales): 16 bytes of a row a cache line are fetched again for every pair, as
+// much again as half the operands, and cost 11% (8192^3 247 -> 219 us, 8192 x 11008 x
+// 4096 201 -> 179).  They go to LDS like the operands.
 template <class E, int WM, int WN, int TM, bool STAY>
 __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct p, int m_tiles, int n_tiles,
                                                                 int part_depth, bool packed) {
@@ -823,16 +844,18 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
     constexpr int kXLoads = BM * 8 / kT, kWLoads = BN * 8 / kT;
     static_assert(BM * 8 % kT == 0 && BN * 8 % kT == 0, "whole rounds of loads");
     static_assert(BM + BN <= kT, "a thread for the scales of every row");
+    constexpr bool kPaired = BM == kPairedRows;
+    static_assert(!kPaired || (BM + BN == kT && BM % kWave == 0), "whole waves for the scales of either operand");
     // Arrays by name, and code that names the one it means: the compiler then
     // sees that the operands it reads are not those on their way, and puts no
     // wait for the loads before the reads.
     __shared__ __align__(1024) uint8_t x_even[BM * kDepth], x_odd[BM * kDepth], w_even[BN * kDepth], w_odd[BN * kDepth];
     constexpr int kPassing = 1024 * sizeof(T);  // 16 rows of outputs a wave
     __shared__ __align__(1024) uint8_t passing[STAY ? WM * WN * kPassing : 16];
-    // The scales of a pair of steps, 16 bytes a row, so that word q of a row
-    // has the four scales of lane group q: halves 0 and 1 of the even step,
-    // then of the odd one.  Threads past the last row carry it once more.
-    __shared__ __align__(16) uint8_t scales[2][kT * 16];
+    // The scales of a pair of steps, 16 bytes a row, see pair_order.  Threads past
+    // the last row carry it once more.  Its alignment puts it before the other
+    // arrays: the reads' constant offsets, at most 64 KB, reach it from one register.
+    __shared__ __align__(4096) uint8_t scales[2][kT * 16];
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, q = lane >> 4;
     const int wm = (wave % WM) * TM * 16, wn = (wave / WM) * TN * 16;
@@ -859,10 +882,12 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
         n0 = min(in / gm * BN, p.N - BN);
         xb = p.x + m0 * p.ldx + first;
         wb = p.w + static_cast<int64_t>(n0) * p.ldw + first;
-        // the row whose scales this thread carries
-        const int r = threadIdx.x;
-        sb = r < BM ? p.xs + (m0 + r) * p.ldxs : p.ws + (n0 + min(r - BM, BN - 1)) * p.ldws;
-        sb += first / kMxBlockBytes;
+        // the row whose scales this thread carries, or the first row of its wave
+        const int r = kPaired ? wave * kWave : static_cast<int>(threadIdx.x);
+        if constexpr (kPaired)
+            sb = r < BM ? p.xs + (m0 + r) * 16 : p.ws + (n0 + r - BM) * 16;
+        else
+            sb = (r < BM ? p.xs + (m0 + r) * p.ldxs : p.ws + (n0 + min(r - BM, BN - 1)) * p.ldws) + first / kMxBlockBytes;
     };
     to_tile();
     // A round of loads covers kRound rows; the keys repeat from round to
@@ -892,9 +917,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
     };
     // Scales of a pair of steps, as they stand in memory, to their places.
     auto put_scales = [&](uint8_t* to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-        *reinterpret_cast<u32x4*>(to + threadIdx.x * 16) =
-            u32x4{__builtin_amdgcn_perm(c, a, 0x05040100u), __builtin_amdgcn_perm(c, a, 0x07060302u),
-                  __builtin_amdgcn_perm(d, b, 0x05040100u), __builtin_amdgcn_perm(d, b, 0x07060302u)};
+        *reinterpret_cast<u32x4*>(to + threadIdx.x * 16) = pair_order(u32x4{a, b, c, d});
     };
 
     // Half a step's operands (4 blocks) in LDS; the keys do not change with i
@@ -982,7 +1005,11 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
     u32x4 carried = {0u, 0u, 0u, 0u};  // scales of a pair on their way
     // Past the last pair it is loaded again: a branch in the loop would let the
     // compiler move the products behind it.
-    auto fetch_scales = [&](int pair) { carried = *reinterpret_cast<const u32x4_any*>(sb + 16 * min(pair, pairs - 1)); };
+    auto fetch_scales = [&](int pair) { carried = load16_any(sb + 16 * min(pair, pairs - 1)); };
+    const int64_t plane = wave < BM / kWave ? p.ldxs : p.ldws;  // of a pair's scales
+    auto scales_to_lds = [&](int pair, uint8_t* to, bool live) {
+        load16_to_lds(buf_rsrc(sb + pair * plane, live ? 0x7FFFFFFF : 0), to + wave * kWave * 16, 16 * lane, 0);
+    };
     constexpr int kStores = TM * sizeof(T);  // a wave's stores of a tile
     bool fetched = false;
     for (;;) {
@@ -1007,8 +1034,21 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
                     *reinterpret_cast<u32x4*>(w_even + row * kDepth + 16 * piece0) =
                         at < K ? load16<false>(wb + static_cast<int64_t>(row) * ldw + at) : none;
                 }
-                const uint2 s = tail_scales(sb, k / kMxBlockBytes, K / kMxBlockBytes);
-                put_scales(scales[0], s.x, s.y, 0u, 0u);
+                const int block = k / kMxBlockBytes, blocks = K / kMxBlockBytes;
+                if constexpr (kPaired) {
+                    const u32x4 pair = load16<false>(sb + k / (2 * kDepth) * plane + 16 * lane);
+                    u32x4 two;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // blocks 2 i and 2 i + 1 of the step
+                        two[i] = pair[i] >> (k & kDepth ? 16 : 0) & 0xFFFFu;
+                        if (block + 2 * i + 1 >= blocks) two[i] &= 0xFFu;
+                        if (block + 2 * i >= blocks) two[i] = 0u;
+                    }
+                    *reinterpret_cast<u32x4*>(scales[0] + threadIdx.x * 16) = two;
+                } else {
+                    const uint2 s = tail_scales(sb, block, blocks);
+                    put_scales(scales[0], s.x, s.y, 0u, 0u);
+                }
                 __syncthreads();
                 read_scales(scales[0]);
                 read(x_even, w_even, 0, w0);
@@ -1018,16 +1058,19 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
                 __syncthreads();
             }
         }
-        if (pairs > 0) fetch_scales(0);
+        if (!kPaired && pairs > 0) fetch_scales(0);
         if (STAY && fetched) {
             landed<kStores>();  // the operands are older than the last tile's stores
         } else {
             fetch(0, x_even, w_even, steps > 0);
             fetch(kDepth, x_odd, w_odd, steps > 0);
+            if (kPaired) scales_to_lds(0, scales[0], steps > 0);
             __builtin_amdgcn_s_waitcnt(0);
         }
-        put_scales(scales[0], carried[0], carried[1], carried[2], carried[3]);
-        if (pairs > 0) fetch_scales(1);
+        if constexpr (!kPaired) {
+            put_scales(scales[0], carried[0], carried[1], carried[2], carried[3]);
+            if (pairs > 0) fetch_scales(1);
+        }
         __syncthreads();
         read(x_even, w_even, 0, w0);
         read_scales(scales[0]);
@@ -1036,8 +1079,12 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
             uint8_t* const next = scales[(s >> 1) + 1 & 1];
             multiply(Sel0{}, w0, x_even, w_even, 1, w1, next, nothing);
             arrive();
-            put_scales(next, carried[0], carried[1], carried[2], carried[3]);
-            fetch_scales((s >> 1) + 2);
+            if constexpr (kPaired) {
+                scales_to_lds((s >> 1) + 1, next, s + 2 < steps);
+            } else {
+                put_scales(next, carried[0], carried[1], carried[2], carried[3]);
+                fetch_scales((s >> 1) + 2);
+            }
             multiply(Sel1{}, w1, x_odd, w_odd, 0, w0, next,
                      [&](int n) { fetch_one(n, (s + 2) * kDepth, x_even, w_even, s + 2 < steps); });
             multiply(Sel2{}, w0, x_odd, w_odd, 1, w1, next, nothing);
@@ -1054,6 +1101,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
         const int64_t m = m0 + wm;
         const int n = n0 + wn;
         float bias[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) bias[e] = 0.0f;  // nothing of it lives through the loop
         if constexpr (!kSplit) {
             if (p.bias) {
 #pragma unroll
@@ -1068,6 +1117,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
                 to_tile();
                 fetch(0, x_even, w_even, true);
                 fetch(kDepth, x_odd, w_odd, true);
+                scales_to_lds(0, scales[0], true);
             }
             store_tile<E, T, TM, kPassing, true>(p, out, passing + wave * kPassing, tid & 63, m, n, acc, bias, true);
             if (!fetched) return;
@@ -1085,6 +1135,27 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
                                                                 packed && (n0 * sizeof(T)) % 16 == 0);
             return;
         }
+    }
+}
+
+// Scales of rows to the order of pairs of steps: a wave takes 8 pairs of 8 rows,
+// whole cache lines on either side.
+__global__ __launch_bounds__(kThreads) void mx_pair_scales_kernel(const uint8_t* __restrict__ from, int64_t lds, int64_t rows,
+                                                                  int blocks, uint8_t* __restrict__ to, int64_t plane) {
+    const int lane = __lane_id();
+    const int64_t row = (static_cast<int64_t>(blockIdx.x) * kWavesPerGroup + threadIdx.x / kWave) * 8 + lane / 8;
+    if (row >= rows) return;
+    for (int pair = blockIdx.y * 8 + lane % 8; pair * 16 < blocks; pair += gridDim.y * 8) {
+        const uint8_t* at = from + row * lds + pair * 16;
+        u32x4 s = {0u, 0u, 0u, 0u};
+        if (pair * 16 + 16 <= blocks) {
+            s = load16_any(at);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (pair * 16 + i < blocks) s[i / 4] |= static_cast<uint32_t>(at[i]) << (8 * (i % 4));
+        }
+        *reinterpret_cast<u32x4*>(to + pair * plane + row * 16) = pair_order(s);
     }
 }
 
@@ -1178,6 +1249,27 @@ int launch_form(const MxProduct& p, const Int8Choice& c, void* workspace, void* 
     return launch_tile<E, 2, 4, 8, false>(p, stream);
 }
 
+// Scales that are not in the order of pairs of steps yet, to the workspace.
+int pair_scales(MxProduct& p, uint8_t* workspace, void* stream) {
+    auto pair = [&](const uint8_t*& scales, int64_t& ld, int64_t rows, bool& paired) {
+        if (paired) return 0;
+        const int64_t plane = rows * 16;
+        const int eights = (p.K + 16 * kDepth - 1) / (16 * kDepth);
+        constexpr int kRows = 8 * kWavesPerGroup;
+        hipLaunchKernelGGL(mx_pair_scales_kernel,
+                           dim3(static_cast<unsigned>((rows + kRows - 1) / kRows), eights < 4096 ? eights : 4096),
+                           dim3(kThreads), 0, static_cast<hipStream_t>(stream), scales, ld, rows, p.K / kMxBlockBytes, workspace,
+                           plane);
+        scales = workspace;
+        ld = plane;
+        paired = true;
+        workspace += mx_paired_bytes(rows, p.K);
+        return static_cast<int>(hipGetLastError());
+    };
+    const int e = pair(p.xs, p.ldxs, p.M, p.x_paired);
+    return e != 0 ? e : pair(p.ws, p.ldws, p.N, p.w_paired);
+}
+
 template <class E>
 int launch_product_e(const MxProduct& whole, void* workspace, void* stream) {
     using T = typename E::T;
@@ -1188,12 +1280,15 @@ int launch_product_e(const MxProduct& whole, void* workspace, void* stream) {
             p.M = whole.M - m < kRowBlock ? whole.M - m : kRowBlock;
             p.N = static_cast<int>(whole.N - n < kMaxChannels ? whole.N - n : kMaxChannels);
             p.x += m * p.ldx;
-            p.xs += m * p.ldxs;
+            p.xs += m * p.ldxs;  // m = 0 and n = 0 where the scales are paired
             p.w += n * p.ldw;
             p.ws += n * p.ldws;
             if (p.bias) p.bias = static_cast<const T*>(p.bias) + n;
             p.out = static_cast<T*>(p.out) + m * p.ldo + n;
-            const int e = launch_form<E>(p, choose_form(p.M, p.N, p.K, cus), workspace, stream);
+            const Int8Choice c = choose_form(p.M, p.N, p.K, cus);
+            int e = c.bm == kPairedRows ? pair_scales(p, static_cast<uint8_t*>(workspace), stream) : 0;
+            if (e != 0) return e;
+            e = launch_form<E>(p, c, workspace, stream);
             if (e != 0) return e;
         }
     }
@@ -1223,16 +1318,17 @@ int launch_tokens_e(const MxProduct& p, int d, const void* X, int64_t ldX, void*
 int64_t rows_a_launch(int64_t per_row) { return (int64_t(1) << 27) / per_row; }
 
 template <class E>
-int launch_quantize_e(const void* X, int64_t rows, int d, int64_t ldx, uint8_t* codes, int64_t ldc, uint8_t* scales,
-                      int64_t lds, void* stream) {
+int launch_quantize_e(const void* X, int64_t rows, int d, int64_t ldx, const MxCoded& out, void* stream) {
     const uint32_t per_row = static_cast<uint32_t>((d + 511) / 512);
     const int64_t most = rows_a_launch(per_row);
     for (int64_t r = 0; r < rows; r += most) {
         const uint32_t items = static_cast<uint32_t>((rows - r < most ? rows - r : most) * per_row);
         const dim3 grid((items + kWavesPerGroup * kRowItems - 1) / (kWavesPerGroup * kRowItems));
+        MxCoded c = out;
+        c.codes += r * c.ldc;
+        c.scales += r * (c.paired ? 16 : c.lds);
         hipLaunchKernelGGL((mx_quantize_kernel<E>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream),
-                           static_cast<const typename E::T*>(X) + r * ldx, items, per_row, d, ldx, codes + r * ldc, ldc,
-                           scales + r * lds, lds);
+                           static_cast<const typename E::T*>(X) + r * ldx, items, per_row, d, ldx, c);
         const int e = static_cast<int>(hipGetLastError());
         if (e != 0) return e;
     }
@@ -1250,16 +1346,13 @@ int launch_columns_e(const void* X, int64_t rows, int cols, int64_t ldx, const M
         const int64_t n = rows - at < kRows ? rows - at : kRows;
         const dim3 grid((cols + kTile - 1) / kTile, static_cast<unsigned>((n + kMxSumRows - 1) / kMxSumRows));
         const T* x = static_cast<const T*>(X) + at * ldx;
-        uint8_t *cc = c.codes ? c.codes + at / 2 : nullptr, *cs = c.codes ? c.scales + at / kMxBlock : nullptr;
         float* f = sums ? sums + at / kMxSumRows * cols : nullptr;
         if (r.codes)
             hipLaunchKernelGGL((mx_quantize_columns_kernel<E, true>), grid, dim3(kColBlocks * kWave), 0,
-                               static_cast<hipStream_t>(stream), x, n, cols, ldx, cc, c.ldc, cs, c.lds, r.codes + at * r.ldc,
-                               r.ldc, r.scales + at * r.lds, r.lds, f);
+                               static_cast<hipStream_t>(stream), x, n, cols, ldx, c, r, at, f);
         else
             hipLaunchKernelGGL((mx_quantize_columns_kernel<E, false>), grid, dim3(kColBlocks * kWave), 0,
-                               static_cast<hipStream_t>(stream), x, n, cols, ldx, cc, c.ldc, cs, c.lds,
-                               static_cast<uint8_t*>(nullptr), int64_t(0), static_cast<uint8_t*>(nullptr), int64_t(0), f);
+                               static_cast<hipStream_t>(stream), x, n, cols, ldx, c, r, at, f);
         const int e = static_cast<int>(hipGetLastError());
         if (e != 0) return e;
     }
@@ -1293,7 +1386,7 @@ int launch_dequantize_e(const uint8_t* codes, int64_t ldc, const uint8_t* scales
     }
 
 int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx, const MxCoded& c, void* stream) {
-    KBIT_BY_DTYPE(launch_quantize_e, X, rows, d, ldx, c.codes, c.ldc, c.scales, c.lds, stream)
+    KBIT_BY_DTYPE(launch_quantize_e, X, rows, d, ldx, c, stream)
 }
 
 int launch_mx_quantize_columns(Dtype t, const void* X, int64_t rows, int cols, int64_t ldx, const MxCoded& columns,
