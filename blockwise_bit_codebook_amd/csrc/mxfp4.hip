@@ -821,103 +821,78 @@ __device__ __forceinline__ void store_tile(const MxProduct& p, T* out, uint8_t* 
     }
 }
 
-// With E = MSums the depth is split as well: workgroups (x, y) take the bytes
-// from y part_depth on, at most part_depth (whole pairs of steps), and store
-// their sums as they are, one matrix after the other.
+// Tiles of 256 x 256, 2 x 4 waves of 128 rows and 64 channels, two steps of both
+// operands in LDS: while the matrix cores work on one, the loads of the next go
+// into the other.
 //
-// With STAY a workgroup takes one tile after the other: the first two steps of
-// the next are on their way while the outputs of one leave, through LDS of
-// their own, and the next one's products do not wait for those stores.  For
-// whole pairs of steps and outputs of whole 16-byte pieces.
-//
-// Tiles of 256 rows take their scales in the order of a pair of steps
-// (MxScales): 16 bytes of a row a cache line are fetched again for every pair, as
-// much again as half the operands, and cost 11% (8192^3 247 -> 219 us, 8192 x 11008 x
-// 4096 201 -> 179).  They go to LDS like the operands.
-template <class E, int WM, int WN, int TM, bool STAY>
-__global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct p, int m_tiles, int n_tiles,
-                                                                int part_depth, bool packed) {
-    constexpr bool kSplit = kSums<E>;
-    using T = std::conditional_t<kSplit, float, typename E::T>;
-    constexpr int TN = 4, kT = WM * WN * kWave;
-    constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
-    constexpr int kXLoads = BM * 8 / kT, kWLoads = BN * 8 / kT;
-    static_assert(BM * 8 % kT == 0 && BN * 8 % kT == 0, "whole rounds of loads");
-    static_assert(BM + BN <= kT, "a thread for the scales of every row");
-    constexpr bool kPaired = BM == kPairedRows;
-    static_assert(!kPaired || (BM + BN == kT && BM % kWave == 0), "whole waves for the scales of either operand");
+// The scales come in the order of pairs of steps (MxCoded) and go to LDS like the
+// operands: in rows, 16 bytes of a cache line would be fetched again for every
+// pair, as much as half the operands.  What the depth does not fill is fetched
+// from past the operand's range, which leaves zeros.
+constexpr int kNowhere = INT32_MIN;  // an offset past every range
+
+template <class E>
+__global__ __launch_bounds__(8 * kWave) void mx_large_kernel(const MxProduct p, int m_tiles, int n_tiles, bool packed) {
+    using T = typename E::T;
+    constexpr int WM = 2, TM = 8, TN = 4, kT = 8 * kWave, BM = kPairedRows, BN = 256;
+    constexpr int kXLoads = BM * 8 / kT, kLoads = kXLoads + BN * 8 / kT;  // a thread a step
+    constexpr int kRound = kT / 8;                                        // rows a load
+    static_assert(kRound % (8 * TN) == 0, "the keys repeat from load to load");
     // Arrays by name, and code that names the one it means: the compiler then
     // sees that the operands it reads are not those on their way, and puts no
     // wait for the loads before the reads.
     __shared__ __align__(1024) uint8_t x_even[BM * kDepth], x_odd[BM * kDepth], w_even[BN * kDepth], w_odd[BN * kDepth];
-    constexpr int kPassing = 1024 * sizeof(T);  // 16 rows of outputs a wave
-    __shared__ __align__(1024) uint8_t passing[STAY ? WM * WN * kPassing : 16];
-    // The scales of a pair of steps, 16 bytes a row, see pair_order.  Threads past
-    // the last row carry it once more.  Its alignment puts it before the other
-    // arrays: the reads' constant offsets, at most 64 KB, reach it from one register.
-    __shared__ __align__(4096) uint8_t scales[2][kT * 16];
+    // The scales of a pair of steps, 16 bytes a row, see pair_order.  Its alignment
+    // puts it before the other arrays: the reads' constant offsets, at most 64 KB,
+    // reach it from one register.
+    __shared__ __align__(4096) uint8_t scales[2][(BM + BN) * 16];
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, q = lane >> 4;
     const int wm = (wave % WM) * TM * 16, wn = (wave / WM) * TN * 16;
 
     // Each XCD works through a contiguous range of tiles, in groups of 8 rows
     // of tiles, so that its L2 holds the operands its workgroups share.
-    const int tiles = m_tiles * n_tiles;
-    const int per = (tiles + 7) / 8;
-    const int end = min(static_cast<int>(blockIdx.x & 7) * per + per, tiles);
-    int t = static_cast<int>(blockIdx.x & 7) * per + static_cast<int>(blockIdx.x >> 3);
-    if (t >= end) return;
-    const int first = kSplit ? static_cast<int>(blockIdx.y) * part_depth : 0;
-    const int K = kSplit ? min(p.K - first, part_depth) : p.K;
-    int64_t m0;
-    int n0;
-    const uint8_t *xb, *wb, *sb;
-    auto to_tile = [&] {
-        constexpr int kGroupM = 8;
-        const int group = t / (kGroupM * n_tiles), in = t - group * kGroupM * n_tiles;
-        const int gm = min(kGroupM, m_tiles - group * kGroupM);
-        // The last tiles of a row or column are moved inside the matrix (M >=
-        // BM, N >= BN): outputs computed twice get the same values twice.
-        m0 = min<int64_t>(static_cast<int64_t>(group * kGroupM + in % gm) * BM, p.M - BM);
-        n0 = min(in / gm * BN, p.N - BN);
-        xb = p.x + m0 * p.ldx + first;
-        wb = p.w + static_cast<int64_t>(n0) * p.ldw + first;
-        // the row whose scales this thread carries, or the first row of its wave
-        const int r = kPaired ? wave * kWave : static_cast<int>(threadIdx.x);
-        if constexpr (kPaired)
-            sb = r < BM ? p.xs + (m0 + r) * 16 : p.ws + (n0 + r - BM) * 16;
-        else
-            sb = (r < BM ? p.xs + (m0 + r) * p.ldxs : p.ws + (n0 + min(r - BM, BN - 1)) * p.ldws) + first / kMxBlockBytes;
-    };
-    to_tile();
-    // A round of loads covers kRound rows; the keys repeat from round to
-    // round, but for the weights' where a round is shorter than their period.
-    constexpr int kRound = kT / 8;
-    constexpr bool kTwoKeys = kRound % (8 * TN) != 0;
-    const int row0 = (wave * kWave + lane) >> 3, piece0 = lane & 7;
+    const int tiles = m_tiles * n_tiles, per = (tiles + 7) / 8;
+    const int t = static_cast<int>(blockIdx.x & 7) * per + static_cast<int>(blockIdx.x >> 3);
+    if (static_cast<int>(blockIdx.x >> 3) >= per || t >= tiles) return;
+    constexpr int kGroupM = 8;
+    const int group = t / (kGroupM * n_tiles), in = t - group * kGroupM * n_tiles;
+    const int gm = min(kGroupM, m_tiles - group * kGroupM);
+    // The last tiles of a row or column are moved inside the matrix (M >= BM, N >=
+    // BN): outputs computed twice get the same values twice.
+    const int64_t m0 = min<int64_t>(static_cast<int64_t>(group * kGroupM + in % gm) * BM, p.M - BM);
+    const int n0 = min(in / gm * BN, p.N - BN), K = p.K;
+    const uint8_t* xb = p.x + m0 * p.ldx;
+    const uint8_t* wb = p.w + static_cast<int64_t>(n0) * p.ldw;
+    const int row0 = threadIdx.x >> 3, piece0 = lane & 7;
     const int ldx = static_cast<int>(p.ldx), ldw = static_cast<int>(p.ldw);
-    const int xo = row0 * ldx + 16 * (piece0 ^ mx_key_x(row0));
-    const int wo0 = row0 * ldw + 16 * (piece0 ^ mx_key_w<TN>(row0));
-    const int wo1 = kTwoKeys ? row0 * ldw + 16 * (piece0 ^ mx_key_w<TN>(row0 + kRound)) : wo0;
-    // One of the kLoads loads of a step.  Loads that are not `live` are issued all
-    // the same, to an empty range, and read no memory: a branch around them would
-    // make the compiler wait.
-    constexpr int kLoads = kXLoads + kWLoads;
-    auto fetch_one = [&](int n, int k, uint8_t* xd, uint8_t* wd, bool live) {
-        const int range = live ? 0x7FFFFFFF : 0;
-        const int i = n < kXLoads ? n : n - kXLoads;
+    const int xpiece = 16 * (piece0 ^ mx_key_x(row0)), wpiece = 16 * (piece0 ^ mx_key_w<TN>(row0));
+    struct Fetch {  // of a step
+        int k, xo, wo;
+    };
+    auto fetch_of = [&](int s) {
+        const int k = s * kDepth;
+        return Fetch{k, k + xpiece < K ? row0 * ldx + xpiece : kNowhere, k + wpiece < K ? row0 * ldw + wpiece : kNowhere};
+    };
+    auto fetch_one = [&](int n, const Fetch& f, uint8_t* xd, uint8_t* wd) {
         if (n < kXLoads)
-            load16_to_lds(buf_rsrc(xb, range), xd + (i * kT + wave * kWave) * 16, xo, k + i * kRound * ldx);
+            load16_to_lds(buf_rsrc(xb, 0x7FFFFFFF), xd + (n * kT + wave * kWave) * 16, f.xo, f.k + n * kRound * ldx);
         else
-            load16_to_lds(buf_rsrc(wb, range), wd + (i * kT + wave * kWave) * 16, (i & 1) ? wo1 : wo0, k + i * kRound * ldw);
+            load16_to_lds(buf_rsrc(wb, 0x7FFFFFFF), wd + ((n - kXLoads) * kT + wave * kWave) * 16, f.wo,
+                          f.k + (n - kXLoads) * kRound * ldw);
     };
-    auto fetch = [&](int k, uint8_t* xd, uint8_t* wd, bool live) {
+    auto fetch = [&](int s, uint8_t* xd, uint8_t* wd) {
+        const Fetch f = fetch_of(s);
 #pragma unroll
-        for (int n = 0; n < kLoads; ++n) fetch_one(n, k, xd, wd, live);
+        for (int n = 0; n < kLoads; ++n) fetch_one(n, f, xd, wd);
     };
-    // Scales of a pair of steps, as they stand in memory, to their places.
-    auto put_scales = [&](uint8_t* to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-        *reinterpret_cast<u32x4*>(to + threadIdx.x * 16) = pair_order(u32x4{a, b, c, d});
+    // 64 rows' scales a wave.
+    const bool of_x = wave < BM / kWave;
+    const uint8_t* sb = of_x ? p.xs + (m0 + wave * kWave) * 16 : p.ws + (n0 + wave * kWave - BM) * 16;
+    const int64_t plane = of_x ? p.ldxs : p.ldws;
+    const int steps = (K + kDepth - 1) / kDepth;
+    auto fetch_scales = [&](int pair, uint8_t* to) {
+        load16_to_lds(buf_rsrc(sb + pair * plane, 2 * pair < steps ? 0x7FFFFFFF : 0), to + wave * kWave * 16, 16 * lane, 0);
     };
 
     // Half a step's operands (4 blocks) in LDS; the keys do not change with i
@@ -928,7 +903,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
     const int wp[2] = {(wn + w_row) * kDepth + 16 * ((2 * q) ^ mx_key_w<TN>(w_row)),
                        (wn + w_row) * kDepth + 16 * ((2 * q + 1) ^ mx_key_w<TN>(w_row))};
     const int xsp = (wm + l16) * 16 + 4 * q, wsp = (BM + wn + w_row) * 16 + 4 * q;
-    f32x4 acc[TM][TN];
+    f32x4 acc[TM][TN] = {};
     i32x4 x[TM], w0[TN], w1[TN];
     uint32_t sx[TM], sw[TN], sw_next[TN];
     auto read_x = [&](const uint8_t* xd, int h, int i) {
@@ -937,27 +912,14 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
     auto read_w = [&](const uint8_t* wd, int h, int j) {
         return *reinterpret_cast<const i32x4*>(wd + wp[h] + 4 * j * kDepth);
     };
-    auto read = [&](const uint8_t* xd, const uint8_t* wd, int h, i32x4 (&w)[TN]) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j) w[j] = read_w(wd, h, j);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) read_x(xd, h, i);
-    };
     auto read_sx = [&](const uint8_t* from, int i) { return *reinterpret_cast<const uint32_t*>(from + xsp + 16 * i * 16); };
     auto read_sw = [&](const uint8_t* from, int j) { return *reinterpret_cast<const uint32_t*>(from + wsp + 4 * j * 16); };
-    auto read_scales = [&](const uint8_t* from) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i) sx[i] = read_sx(from, i);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) sw[j] = read_sw(from, j);
-    };
     // The products of half a step.  Each operand of x is replaced by half h of (xn,
     // wn) as soon as its last product is issued, and the next weights are read on
     // the way; in the last half of a pair (SEL 3) the next pair's scales as well.
     // Beside them a part of the loads to LDS is issued, load(n).  The order is held
     // group by group: left to itself the compiler puts reads right before their
-    // use (8192^3 262 us, 8192 x 11008 x 4096 217).
-    constexpr int kPer = TM < TN ? TN / TM : 1, kPerLoads = (kLoads + TM - 1) / TM;
+    // use (8192^3 272 -> 258 us, 8192 x 11008 x 4096 234 -> 213).
     auto multiply = [&](auto sel, const i32x4 (&w)[TN], const uint8_t* xn, const uint8_t* wn, int h, i32x4 (&w_next)[TN],
                         const uint8_t* scales_next, const auto& load) {
         constexpr int SEL = decltype(sel)::value;
@@ -966,9 +928,201 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] = mfma<SEL>(w[j], x[i], acc[i][j], sw[j], sx[i]);
             read_x(xn, h, i);
+            if (i < TN) {
+                w_next[i] = read_w(wn, h, i);
+                if (SEL == 3) sw_next[i] = read_sw(scales_next, i);
+            }
+            if (SEL == 3) sx[i] = read_sx(scales_next, i);
+            load(i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (SEL == 3) {
 #pragma unroll
-            for (int j = i * kPer; j < (i + 1) * kPer && j < TN; ++j) {
-                w_next[j] = read_w(wn, h, j);
+            for (int j = 0; j < TN; ++j) sw[j] = sw_next[j];
+        }
+    };
+    static_assert(kLoads == TM, "a load a group");
+
+    // Software pipeline: while half a step is multiplied the next half is read
+    // from LDS, and the step after it is on its way from memory.  The one
+    // barrier of a step stands between its halves: past it every wave's loads
+    // of step s + 1 have arrived and nobody reads step s any more, so that
+    // step s + 2 may be fetched over it.
+    auto arrive = [&] {
+        __builtin_amdgcn_s_waitcnt(0);  // loads to LDS are counted with the vector loads: a barrier does not wait for them
+        __syncthreads();
+    };
+    const auto nothing = [](int) {};
+    fetch(0, x_even, w_even);
+    fetch(1, x_odd, w_odd);
+    fetch_scales(0, scales[0]);
+    arrive();
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+        w0[j] = read_w(w_even, 0, j);
+        sw[j] = read_sw(scales[0], j);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        read_x(x_even, 0, i);
+        sx[i] = read_sx(scales[0], i);
+    }
+    for (int s = 0; s < steps; s += 2) {  // what lies past the last step is zeros
+        uint8_t* const next = scales[(s >> 1) + 1 & 1];
+        multiply(std::integral_constant<int, 0>{}, w0, x_even, w_even, 1, w1, next, nothing);
+        arrive();
+        fetch_scales((s >> 1) + 1, next);
+        const Fetch even = fetch_of(s + 2);
+        multiply(std::integral_constant<int, 1>{}, w1, x_odd, w_odd, 0, w0, next,
+                 [&](int n) { fetch_one(n, even, x_even, w_even); });
+        multiply(std::integral_constant<int, 2>{}, w0, x_odd, w_odd, 1, w1, next, nothing);
+        arrive();
+        const Fetch odd = fetch_of(s + 3);
+        multiply(std::integral_constant<int, 3>{}, w1, x_even, w_even, 0, w0, next,
+                 [&](int n) { fetch_one(n, odd, x_odd, w_odd); });
+    }
+    float bias[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) bias[e] = 0.0f;
+    if (p.bias) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) bias[e] = E::one(static_cast<const T*>(p.bias)[n0 + wn + 16 * q + e]);
+    }
+    arrive();  // the operands are read, and the last loads are done
+    // A region for each wave, in the array that has room for it.
+    constexpr int kPart = 16384, kIn = BM * kDepth / kPart;
+    static_assert(BM == BN && 4 * kIn >= 8, "a region for every wave");
+    uint8_t* region = (wave < 4 ? (wave < kIn ? x_even : x_odd) : (wave - 4 < kIn ? w_even : w_odd)) + wave % kIn * kPart;
+    store_tile<E, T, TM, kPart, true>(p, static_cast<T*>(p.out), region, lane, m0 + wm, n0 + wn, acc, bias,
+                                      packed && (n0 * sizeof(T)) % 16 == 0);
+}
+
+// The smaller tiles, of 32 TM rows and 128 channels, four waves, with a ring of S
+// steps in LDS: a step's loads are issued S - 1 steps ahead, so that their latency
+// is not what a step takes.  What the depth does not fill is fetched from past
+// the operand's range, which leaves zeros.
+//
+// With E = MSums the depth is split as well: workgroups (x, y) take the bytes
+// from y part_depth on, at most part_depth (whole pairs of steps), and store
+// their sums as they are, one matrix after the other.
+// A barrier that waits for the wave's LDS accesses but not for its loads, as
+// __syncthreads would.  The fences emit nothing and hold the compiler to the order.
+__device__ __forceinline__ void barrier_in_flight() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+constexpr int kRingChannels = 128;
+
+template <class E, int TM, int S>
+__global__ __launch_bounds__(kThreads) void mx_ring_kernel(const MxProduct p, int m_tiles, int n_tiles, int part_depth,
+                                                           bool packed) {
+    constexpr bool kSplit = kSums<E>;
+    using T = std::conditional_t<kSplit, float, typename E::T>;
+    constexpr int WM = 2, TN = 4, BM = WM * TM * 16, BN = kRingChannels, kStage = (BM + BN) * kDepth;
+    constexpr int kXLoads = TM, kWLoads = 4, kLoads = kXLoads + kWLoads;  // a thread a step
+    constexpr int kRound = kThreads / 8;                                   // rows a load
+    static_assert(S == 2 || S == 4, "whole pairs of steps, stages with names");
+    // The rows whose scales a thread carries: whole waves for x, then those of w.
+    constexpr int kXWaves = (BM + kWave - 1) / kWave, kWRows = kXWaves * kWave;
+    static_assert(kWRows + BN <= kThreads, "a thread for the scales of every row");
+    // Arrays by name: the compiler then sees that the operands it reads are not
+    // those on their way, and puts no wait for the loads before the reads.
+    __shared__ __align__(1024) uint8_t stage0[kStage], stage1[kStage], stage2[S > 2 ? kStage : 16],
+        stage3[S > 3 ? kStage : 16];
+    __shared__ __align__(4096) uint8_t scales[2][kThreads * 16];  // of a pair of steps, see pair_order
+    const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int l16 = lane & 15, q = lane >> 4;
+    const int wm = (wave % WM) * TM * 16, wn = (wave / WM) * TN * 16;
+    const int tiles = m_tiles * n_tiles, per = (tiles + 7) / 8;
+    const int t = static_cast<int>(blockIdx.x & 7) * per + static_cast<int>(blockIdx.x >> 3);
+    if (static_cast<int>(blockIdx.x >> 3) >= per || t >= tiles) return;
+    const int first = kSplit ? static_cast<int>(blockIdx.y) * part_depth : 0;
+    const int K = kSplit ? min(p.K - first, part_depth) : p.K;
+    // XCDs and the tiles' order: see mx_large_kernel.
+    constexpr int kGroupM = 8;
+    const int group = t / (kGroupM * n_tiles), in = t - group * kGroupM * n_tiles;
+    const int gm = min(kGroupM, m_tiles - group * kGroupM);
+    const int64_t m0 = min<int64_t>(static_cast<int64_t>(group * kGroupM + in % gm) * BM, p.M - BM);
+    const int n0 = min(in / gm * BN, p.N - BN);
+    const uint8_t* xb = p.x + m0 * p.ldx + first;
+    const uint8_t* wb = p.w + static_cast<int64_t>(n0) * p.ldw + first;
+    const uint8_t* sb = (wave < kXWaves ? p.xs + m0 * p.ldxs : p.ws + n0 * p.ldws) + first / kMxBlockBytes;
+    const int so = wave < kXWaves ? min(static_cast<int>(threadIdx.x), BM - 1) * static_cast<int>(p.ldxs)
+                                  : min(static_cast<int>(threadIdx.x) - kWRows, BN - 1) * static_cast<int>(p.ldws);
+
+    const int row0 = threadIdx.x >> 3, piece0 = lane & 7;
+    const int ldx = static_cast<int>(p.ldx), ldw = static_cast<int>(p.ldw);
+    static_assert(kRound % (8 * TN) == 0, "the keys repeat from load to load");
+    const int xpiece = 16 * (piece0 ^ mx_key_x(row0)), wpiece = 16 * (piece0 ^ mx_key_w<TN>(row0));
+    struct Fetch {  // of a step
+        int k, xo, wo;
+    };
+    auto fetch_of = [&](int s) {
+        const int k = s * kDepth;
+        return Fetch{k, k + xpiece < K ? row0 * ldx + xpiece : kNowhere, k + wpiece < K ? row0 * ldw + wpiece : kNowhere};
+    };
+    auto fetch_one = [&](int n, const Fetch& f, uint8_t* to) {
+        if (n < kXLoads)
+            load16_to_lds(buf_rsrc(xb, 0x7FFFFFFF), to + (n * kThreads + wave * kWave) * 16, f.xo, f.k + n * kRound * ldx);
+        else
+            load16_to_lds(buf_rsrc(wb, 0x7FFFFFFF), to + (n * kThreads + wave * kWave) * 16, f.wo,
+                          f.k + (n - kXLoads) * kRound * ldw);
+    };
+    auto fetch = [&](int s, uint8_t* to) {
+        const Fetch f = fetch_of(s);
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) fetch_one(n, f, to);
+    };
+    // Scales of a pair: those of whole pairs from memory, the last, partial one's
+    // fetched byte by byte beforehand, zeros past it.
+    const int blocks = K / kMxBlockBytes, whole = blocks / 16;
+    auto fetch_scales = [&](int pair) -> u32x4 {
+        return __builtin_amdgcn_raw_buffer_load_b128(buf_rsrc(sb, whole > 0 ? 0x7FFFFFFF : 0), so, 16 * min(pair, max(whole - 1, 0)), 0);
+    };
+    u32x4 last = {0u, 0u, 0u, 0u};
+    if (whole * 16 < blocks) {
+        const uint2 a = tail_scales(sb + so, whole * 16, blocks), b = tail_scales(sb + so, whole * 16 + 8, blocks);
+        last = u32x4{a.x, a.y, b.x, b.y};
+    }
+    auto put_scales = [&](int pair, const u32x4& v) {
+        u32x4 s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = pair < whole ? v[i] : pair == whole ? last[i] : 0u;
+        *reinterpret_cast<u32x4*>(scales[pair & 1] + threadIdx.x * 16) = pair_order(s);
+    };
+
+    const int w_row = operand_channel<TN>(0, l16);
+    const int xp = (wm + l16) * kDepth, wp = (BM + wn + w_row) * kDepth;
+    const int xkey = mx_key_x(l16), wkey = mx_key_w<TN>(w_row);
+    const int xsp = (wm + l16) * 16 + 4 * q, wsp = (kWRows + wn + w_row) * 16 + 4 * q;
+    f32x4 acc[TM][TN] = {};
+    i32x4 x[TM], w0[TN], w1[TN];
+    uint32_t sx[TM], sw[TN], sw_next[TN];
+    auto read_x = [&](const uint8_t* from, int h, int i) {
+        x[i] = *reinterpret_cast<const i32x4*>(from + xp + 16 * ((2 * q + h) ^ xkey) + 16 * i * kDepth);
+    };
+    auto read_w = [&](const uint8_t* from, int h, int j) {
+        return *reinterpret_cast<const i32x4*>(from + wp + 16 * ((2 * q + h) ^ wkey) + 4 * j * kDepth);
+    };
+    auto read_sx = [&](const uint8_t* from, int i) { return *reinterpret_cast<const uint32_t*>(from + xsp + 16 * i * 16); };
+    auto read_sw = [&](const uint8_t* from, int j) { return *reinterpret_cast<const uint32_t*>(from + wsp + 4 * j * 16); };
+    // As in mx_large_kernel: half h of `next` is read while half a step is
+    // multiplied, in SEL 3 the next pair's scales with it.
+    constexpr int kPer = TN / TM, kPerLoads = (kLoads + TM - 1) / TM;
+    auto multiply = [&](auto sel, const i32x4 (&w)[TN], const uint8_t* next, int h, i32x4 (&w_next)[TN], const uint8_t* scales_next,
+                        const auto& load) {
+        constexpr int SEL = decltype(sel)::value;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<SEL>(w[j], x[i], acc[i][j], sw[j], sx[i]);
+            read_x(next, h, i);
+#pragma unroll
+            for (int j = i * kPer; j < (i + 1) * kPer; ++j) {
+                w_next[j] = read_w(next, h, j);
                 if (SEL == 3) sw_next[j] = read_sw(scales_next, j);
             }
             if (SEL == 3) sx[i] = read_sx(scales_next, i);
@@ -981,161 +1135,70 @@ __global__ __launch_bounds__(WM* WN* kWave) void mx_tile_kernel(const MxProduct 
             for (int j = 0; j < TN; ++j) sw[j] = sw_next[j];
         }
     };
-    auto multiply_all = [&](auto sel, const i32x4 (&w)[TN]) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<decltype(sel)::value>(w[j], x[i], acc[i][j], sw[j], sx[i]);
+    // A step: its first half's operands are in registers.  Past the barrier the
+    // next step's operands have arrived (of the loads on their way only those of
+    // the steps after it are newer), and nobody reads this step's stage any more,
+    // over which the step S further goes.
+    auto step = [&](auto odd, int s, uint8_t* now, const uint8_t* next, u32x4& carried) {
+        constexpr int SEL = 2 * decltype(odd)::value;
+        uint8_t* const scales_next = scales[(s >> 1) + 1 & 1];
+        multiply(std::integral_constant<int, SEL>{}, w0, now, 1, w1, scales_next, [](int) {});
+        landed<(S - 2) * kLoads>();
+        barrier_in_flight();
+        if constexpr (SEL == 0) {
+            put_scales((s >> 1) + 1, carried);
+            carried = fetch_scales((s >> 1) + 1 + S / 2);
+            __builtin_amdgcn_sched_barrier(0);  // older than the step's loads: to wait for it is not to wait for them
+        }
+        const Fetch f = fetch_of(s + S);
+        multiply(std::integral_constant<int, SEL + 1>{}, w1, next, 0, w0, scales_next, [&](int n) { fetch_one(n, f, now); });
     };
-    using Sel0 = std::integral_constant<int, 0>;
-    using Sel1 = std::integral_constant<int, 1>;
-    using Sel2 = std::integral_constant<int, 2>;
-    using Sel3 = std::integral_constant<int, 3>;
-
-    // Software pipeline: while half a step is multiplied the next half is read
-    // from LDS, and the step after it is on its way from memory.  The one
-    // barrier of a step stands between its halves: past it every wave's loads
-    // of step s + 1 have arrived and nobody reads step s any more, so that
-    // step s + 2 may be fetched over it.
-    auto arrive = [&] {
-        __builtin_amdgcn_s_waitcnt(0);  // loads to LDS are counted with the vector loads: a barrier does not wait for them
-        __syncthreads();
-    };
-    const int steps = K / (2 * kDepth) * 2, pairs = steps / 2;
-    u32x4 carried = {0u, 0u, 0u, 0u};  // scales of a pair on their way
-    // Past the last pair it is loaded again: a branch in the loop would let the
-    // compiler move the products behind it.
-    auto fetch_scales = [&](int pair) { carried = load16_any(sb + 16 * min(pair, pairs - 1)); };
-    const int64_t plane = wave < BM / kWave ? p.ldxs : p.ldws;  // of a pair's scales
-    auto scales_to_lds = [&](int pair, uint8_t* to, bool live) {
-        load16_to_lds(buf_rsrc(sb + pair * plane, live ? 0x7FFFFFFF : 0), to + wave * kWave * 16, 16 * lane, 0);
-    };
-    constexpr int kStores = TM * sizeof(T);  // a wave's stores of a tile
-    bool fetched = false;
-    for (;;) {
+    const int steps = (K + kDepth - 1) / kDepth;
+    const u32x4 scales0 = fetch_scales(0);
+    u32x4 carried[S / 2];
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < S / 2; ++i) carried[i] = fetch_scales(i + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    uint8_t* const stage[4] = {stage0, stage1, stage2, stage3};
 #pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        // The pipeline takes pairs of steps.  What the depth has beyond them
-        // comes first, a step at a time, zeros past K.
-        if constexpr (!STAY) {
-            for (int k = steps * kDepth; k < K; k += kDepth) {
-                const u32x4 none = {0u, 0u, 0u, 0u};
+    for (int i = 0; i < S; ++i) fetch(i, stage[i]);
+    put_scales(0, scales0);
+    landed<(S - 1) * kLoads>();
+    barrier_in_flight();
 #pragma unroll
-                for (int i = 0; i < kXLoads; ++i) {
-                    const int row = row0 + i * kRound, at = k + 16 * (piece0 ^ mx_key_x(row));
-                    *reinterpret_cast<u32x4*>(x_even + row * kDepth + 16 * piece0) =
-                        at < K ? load16<false>(xb + static_cast<int64_t>(row) * ldx + at) : none;
-                }
+    for (int j = 0; j < TN; ++j) {
+        w0[j] = read_w(stage0, 0, j);
+        sw[j] = read_sw(scales[0], j);
+    }
 #pragma unroll
-                for (int i = 0; i < kWLoads; ++i) {
-                    const int row = row0 + i * kRound, at = k + 16 * (piece0 ^ mx_key_w<TN>(row));
-                    *reinterpret_cast<u32x4*>(w_even + row * kDepth + 16 * piece0) =
-                        at < K ? load16<false>(wb + static_cast<int64_t>(row) * ldw + at) : none;
-                }
-                const int block = k / kMxBlockBytes, blocks = K / kMxBlockBytes;
-                if constexpr (kPaired) {
-                    const u32x4 pair = load16<false>(sb + k / (2 * kDepth) * plane + 16 * lane);
-                    u32x4 two;
+    for (int i = 0; i < TM; ++i) {
+        read_x(stage0, 0, i);
+        sx[i] = read_sx(scales[0], i);
+    }
+    for (int s = 0; s < steps; s += S) {  // what lies past the last step is zeros
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // blocks 2 i and 2 i + 1 of the step
-                        two[i] = pair[i] >> (k & kDepth ? 16 : 0) & 0xFFFFu;
-                        if (block + 2 * i + 1 >= blocks) two[i] &= 0xFFu;
-                        if (block + 2 * i >= blocks) two[i] = 0u;
-                    }
-                    *reinterpret_cast<u32x4*>(scales[0] + threadIdx.x * 16) = two;
-                } else {
-                    const uint2 s = tail_scales(sb, block, blocks);
-                    put_scales(scales[0], s.x, s.y, 0u, 0u);
-                }
-                __syncthreads();
-                read_scales(scales[0]);
-                read(x_even, w_even, 0, w0);
-                multiply_all(Sel0{}, w0);
-                read(x_even, w_even, 1, w0);
-                multiply_all(Sel1{}, w0);
-                __syncthreads();
-            }
-        }
-        if (!kPaired && pairs > 0) fetch_scales(0);
-        if (STAY && fetched) {
-            landed<kStores>();  // the operands are older than the last tile's stores
-        } else {
-            fetch(0, x_even, w_even, steps > 0);
-            fetch(kDepth, x_odd, w_odd, steps > 0);
-            if (kPaired) scales_to_lds(0, scales[0], steps > 0);
-            __builtin_amdgcn_s_waitcnt(0);
-        }
-        if constexpr (!kPaired) {
-            put_scales(scales[0], carried[0], carried[1], carried[2], carried[3]);
-            if (pairs > 0) fetch_scales(1);
-        }
-        __syncthreads();
-        read(x_even, w_even, 0, w0);
-        read_scales(scales[0]);
-        const auto nothing = [](int) {};
-        for (int s = 0; s < steps; s += 2) {  // past the last step it reads operands that nobody multiplies
-            uint8_t* const next = scales[(s >> 1) + 1 & 1];
-            multiply(Sel0{}, w0, x_even, w_even, 1, w1, next, nothing);
-            arrive();
-            if constexpr (kPaired) {
-                scales_to_lds((s >> 1) + 1, next, s + 2 < steps);
-            } else {
-                put_scales(next, carried[0], carried[1], carried[2], carried[3]);
-                fetch_scales((s >> 1) + 2);
-            }
-            multiply(Sel1{}, w1, x_odd, w_odd, 0, w0, next,
-                     [&](int n) { fetch_one(n, (s + 2) * kDepth, x_even, w_even, s + 2 < steps); });
-            multiply(Sel2{}, w0, x_odd, w_odd, 1, w1, next, nothing);
-            arrive();
-            multiply(Sel3{}, w1, x_even, w_even, 0, w0, next,
-                     [&](int n) { fetch_one(n, (s + 3) * kDepth, x_odd, w_odd, s + 3 < steps); });
-        }
-        // What follows runs once a tile: its addresses are made anew from the
-        // thread's number, so that the loop above keeps no registers for them.
-        int tid = threadIdx.x;
-        asm volatile("" : "+v"(tid));
-        T* out = static_cast<T*>(p.out);
-        if constexpr (kSplit) out += blockIdx.y * p.M * p.ldo;
-        const int64_t m = m0 + wm;
-        const int n = n0 + wn;
-        float bias[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) bias[e] = 0.0f;  // nothing of it lives through the loop
-        if constexpr (!kSplit) {
-            if (p.bias) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) bias[e] = E::one(static_cast<const T*>(p.bias)[n + 16 * ((tid & 63) >> 4) + e]);
-            }
-        }
-        arrive();  // the operands are read, and the empty loads of the last steps are done
-        if constexpr (STAY) {
-            t += static_cast<int>(gridDim.x >> 3);
-            fetched = t < end;
-            if (fetched) {
-                to_tile();
-                fetch(0, x_even, w_even, true);
-                fetch(kDepth, x_odd, w_odd, true);
-                scales_to_lds(0, scales[0], true);
-            }
-            store_tile<E, T, TM, kPassing, true>(p, out, passing + wave * kPassing, tid & 63, m, n, acc, bias, true);
-            if (!fetched) return;
-        } else {
-            // A region for each wave, in the array that has room for it.
-            constexpr int kPart = (BM < BN ? BM : BN) >= 256 ? 16384 : (BM < BN ? BM : BN) >= 64 ? 8192 : 4096;
-            static_assert(kPart <= BM * kDepth && kPart <= BN * kDepth, "a region fits into either array");
-            constexpr int kInX = BM * kDepth / kPart, kInW = BN * kDepth / kPart;
-            static_assert(2 * kInX + 2 * kInW >= WM * WN, "a region for every wave");
-            uint8_t* region = wave < kInX ? x_even + wave * kPart
-                              : wave < 2 * kInX ? x_odd + (wave - kInX) * kPart
-                              : wave < 2 * kInX + kInW ? w_even + (wave - 2 * kInX) * kPart
-                                                       : w_odd + (wave - 2 * kInX - kInW) * kPart;
-            store_tile<E, T, TM, kPart, (BM >= 128 && !kSplit)>(p, out, region, tid & 63, m, n, acc, bias,
-                                                                packed && (n0 * sizeof(T)) % 16 == 0);
-            return;
+        for (int i = 0; i < S; i += 2) {
+            step(std::integral_constant<int, 0>{}, s + i, stage[i % S], stage[(i + 1) % S], carried[i / 2]);
+            step(std::integral_constant<int, 1>{}, s + i + 1, stage[(i + 1) % S], stage[(i + 2) % S], carried[i / 2]);
         }
     }
+    T* out = static_cast<T*>(p.out);
+    if constexpr (kSplit) out += blockIdx.y * p.M * p.ldo;
+    float bias[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) bias[e] = 0.0f;
+    if constexpr (!kSplit) {
+        if (p.bias) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) bias[e] = E::one(static_cast<const T*>(p.bias)[n0 + wn + 16 * q + e]);
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();  // the operands are read, and the last loads are done
+    constexpr int kPart = BM >= 128 ? 8192 : 4096;  // a region for each wave
+    static_assert(4 * kPart <= kStage, "they fit into a stage");
+    store_tile<E, T, TM, kPart, (BM >= 128 && !kSplit)>(p, out, stage0 + wave * kPart, lane, m0 + wm, n0 + wn, acc, bias,
+                                                        packed && (n0 * sizeof(T)) % 16 == 0);
 }
 
 // Scales of rows to the order of pairs of steps: a wave takes 8 pairs of 8 rows,
@@ -1182,17 +1245,33 @@ int launch_few(const MxProduct& p, void* stream) {
     return static_cast<int>(hipGetLastError());
 }
 
-template <class E, int WM, int WN, int TM, bool STAY>
-int launch_tile(const MxProduct& p, void* stream) {
-    constexpr int BM = WM * TM * 16, BN = WN * 64;
-    const int m_tiles = static_cast<int>((p.M + BM - 1) / BM), n_tiles = (p.N + BN - 1) / BN;
-    unsigned grid = static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8);
-    if (STAY) {  // one workgroup a compute unit, the same number on each XCD
-        const unsigned resident = device_cu_count() < 8 ? 8u : static_cast<unsigned>(device_cu_count()) / 8 * 8;
-        if (grid > resident) grid = resident;
-    }
-    hipLaunchKernelGGL((mx_tile_kernel<E, WM, WN, TM, STAY>), dim3(grid), dim3(WM * WN * kWave), 0,
-                       static_cast<hipStream_t>(stream), p, m_tiles, n_tiles, 0, out_aligned(p, sizeof(typename E::T), 16));
+template <class E>
+int launch_large(const MxProduct& p, void* stream) {
+    const int m_tiles = static_cast<int>((p.M + 255) / 256), n_tiles = (p.N + 255) / 256;
+    hipLaunchKernelGGL((mx_large_kernel<E>), dim3(static_cast<unsigned>((static_cast<int64_t>(m_tiles) * n_tiles + 7) / 8 * 8)),
+                       dim3(8 * kWave), 0, static_cast<hipStream_t>(stream), p, m_tiles, n_tiles,
+                       out_aligned(p, sizeof(typename E::T), 16));
+    return static_cast<int>(hipGetLastError());
+}
+
+// Four steps of the ring where every workgroup has a compute unit of its own, two
+// where several share one and hide each other's latency.  64 x 128, 512 x 4096 x
+// 4096 (256 workgroups): 12.9 us with two, 9.9 with four, but 1024 x 4096 x 4096 16.8
+// and 18.3, 4096 x 4096 x 512 17.0 and 33.0; 128 x 128, 1024 x 4096 x 4096 16.3 and 14.6,
+// 2048 x 4096 x 4096 23.5 and 27.4.
+template <class E, int TM>
+int launch_ring(const MxProduct& p, void* stream) {
+    constexpr int BM = 32 * TM;
+    const int m_tiles = static_cast<int>((p.M + BM - 1) / BM), n_tiles = (p.N + kRingChannels - 1) / kRingChannels;
+    const int64_t tiles = static_cast<int64_t>(m_tiles) * n_tiles;
+    const dim3 grid(static_cast<unsigned>((tiles + 7) / 8 * 8));
+    const bool packed = out_aligned(p, sizeof(typename E::T), 16);
+    if (tiles <= device_cu_count())
+        hipLaunchKernelGGL((mx_ring_kernel<E, TM, 4>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream), p, m_tiles,
+                           n_tiles, 0, packed);
+    else
+        hipLaunchKernelGGL((mx_ring_kernel<E, TM, 2>), grid, dim3(kThreads), 0, static_cast<hipStream_t>(stream), p, m_tiles,
+                           n_tiles, 0, packed);
     return static_cast<int>(hipGetLastError());
 }
 
@@ -1206,8 +1285,12 @@ int launch_split(const MxProduct& p, int parts, void* workspace, void* stream) {
     MxProduct s = p;
     s.out = workspace;
     s.ldo = sums_ld(p.N);
-    hipLaunchKernelGGL((mx_tile_kernel<MSums, 2, 2, 4, false>), dim3(grid, parts), dim3(4 * kWave), 0,
-                       static_cast<hipStream_t>(stream), s, m_tiles, n_tiles, part_depth, true);
+    if (static_cast<int64_t>(m_tiles) * n_tiles * parts <= device_cu_count())
+        hipLaunchKernelGGL((mx_ring_kernel<MSums, 4, 4>), dim3(grid, parts), dim3(kThreads), 0,
+                           static_cast<hipStream_t>(stream), s, m_tiles, n_tiles, part_depth, true);
+    else
+        hipLaunchKernelGGL((mx_ring_kernel<MSums, 4, 2>), dim3(grid, parts), dim3(kThreads), 0,
+                           static_cast<hipStream_t>(stream), s, m_tiles, n_tiles, part_depth, true);
     const int e = static_cast<int>(hipGetLastError());
     if (e != 0) return e;
     const uint32_t pieces = static_cast<uint32_t>(p.M) * (static_cast<uint32_t>(p.N + 3) / 4);
@@ -1241,12 +1324,11 @@ int launch_form(const MxProduct& p, const Int8Choice& c, void* workspace, void* 
     if (c.parts > 1) return launch_split<E>(p, c.parts, workspace, stream);
     switch (c.bm) {
         case 0: return launch_few_tile<E>(p, c.few, stream);
-        case 32: return launch_tile<E, 2, 2, 1, false>(p, stream);
-        case 64: return launch_tile<E, 2, 2, 2, false>(p, stream);
-        case 128: return launch_tile<E, 2, 2, 4, false>(p, stream);
-        default: break;
+        case 32: return launch_ring<E, 1>(p, stream);
+        case 64: return launch_ring<E, 2>(p, stream);
+        case 128: return launch_ring<E, 4>(p, stream);
+        default: return launch_large<E>(p, stream);
     }
-    return launch_tile<E, 2, 4, 8, false>(p, stream);
 }
 
 // Scales that are not in the order of pairs of steps yet, to the workspace.
@@ -1385,12 +1467,24 @@ int launch_dequantize_e(const uint8_t* codes, int64_t ldc, const uint8_t* scales
         default: return F<QB16>(__VA_ARGS__);       \
     }
 
+// The last pair of scales where it is not whole: what no block fills stays zero
+// (a 255 there would make the zeros that stand for its codes NaN).
+int clear_last_pair(const MxCoded& c, int64_t rows, int64_t blocks, void* stream) {
+    if (!c.paired || blocks % 16 == 0) return 0;
+    return launch_mx_zero(reinterpret_cast<float*>(c.scales + blocks / 16 * c.lds), rows, 4, 4, stream);
+}
+
 int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx, const MxCoded& c, void* stream) {
+    const int e = clear_last_pair(c, rows, mx_blocks(d), stream);
+    if (e != 0) return e;
     KBIT_BY_DTYPE(launch_quantize_e, X, rows, d, ldx, c, stream)
 }
 
 int launch_mx_quantize_columns(Dtype t, const void* X, int64_t rows, int cols, int64_t ldx, const MxCoded& columns,
                                const MxCoded& by_rows, float* sums, void* stream) {
+    int e = columns.codes ? clear_last_pair(columns, cols, mx_blocks(rows), stream) : 0;
+    if (e == 0 && by_rows.codes) e = clear_last_pair(by_rows, rows, mx_blocks(cols), stream);
+    if (e != 0) return e;
     KBIT_BY_DTYPE(launch_columns_e, X, rows, cols, ldx, columns, by_rows, sums, stream)
 }
 

@@ -389,3 +389,36 @@ def test_backward_of_values_that_are_not_finite():
     want = np.zeros((N, K), bool)
     want[7] = True
     assert np.array_equal(np.isnan(dw), want) and np.isnan(db).tolist() == [i == 7 for i in range(N)]
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+def test_large_products_of_odd_depth_in_used_workspaces(t):
+    # depths that end inside a pair of steps, in workspaces full of NaN scales
+    T = torch()
+    M, N, K = 4100, 1030, 4104
+    rng = np.random.default_rng(9)
+    grid = np.array([0.5, 1, 1.5, 2, 3, 4, 6, -0.5, -1, -2, -3], np.float32)
+    g, w = (rng.choice(grid, s).astype(np.float32) for s in ((M, N), (N, K)))
+    G, W = (T.from_numpy(v).to(dev()).to(tdt(t)) for v in (g, w))
+    lib = kb.lib()
+
+    def used(n):
+        return T.full((n,), 0xFF, dtype=T.uint8, device=dev())
+    case(f"large dynamic product of odd depth {t}")
+    wt = mx.quantize(np.ascontiguousarray(w.T))
+    want = layer.round_to((mx.rounded(g) @ mx.values(*wt, N).T).astype(np.float32), t)
+    got = kb.linear_mxfp4_dynamic(G, u8(wt[0]), u8(wt[1]), workspace=used(lib.linear_mxfp4_dynamic_workspace_bytes(M, K, N)))
+    assert_bits_equal(bits(got), want, "dynamic")
+    case(f"large product of codes of odd depth {t}")
+    gq = mx.quantize(g)
+    got = kb.linear_mxfp4(u8(gq[0]), u8(gq[1]), u8(wt[0]), u8(wt[1]), dtype=tdt(t),
+                          workspace=used(lib.linear_mxfp4_workspace_bytes(M, K, 32 * wt[1].shape[1])))
+    assert_bits_equal(bits(got), want, "codes")
+    case(f"large gradients of odd depth {t}")
+    x = rng.choice(grid, (M, K)).astype(np.float32)
+    dx, dw, db = kb.linear_mxfp4_backward(G, T.from_numpy(x).to(dev()).to(tdt(t)), W,
+                                          workspace=used(lib.linear_mxfp4_backward_workspace_bytes(M, N, K)))
+    assert_bits_equal(bits(dx), want, "dX")
+    want = mx.rounded(np.ascontiguousarray(g.T)) @ mx.rounded(np.ascontiguousarray(x.T)).T
+    assert_bits_equal(bits(dw), want.astype(np.float32).view(np.uint32), "dW")
+    assert np.array_equal(db.cpu().numpy(), g.sum(0))
