@@ -7,8 +7,8 @@
 
 #include <tuple>
 
-#include "int8_choice.h"
 #include "kbit_internal.h"
+#include "mx_choice.h"
 
 namespace kbit {
 
@@ -31,7 +31,6 @@ struct MxCoded {
     int64_t ldc, lds;
     bool paired;
 };
-constexpr int kPairedRows = 256;
 
 int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx, const MxCoded& c, void* stream);
 
@@ -61,39 +60,6 @@ struct MxProduct {
     int N, K;                 // K: bytes of a row of codes, a multiple of 16
     bool x_paired, w_paired;  // see MxCoded; only where mx_paired(M, N, K)
 };
-
-// The kernels are those of the int8 product, a byte for a byte (choose_form).
-// Whether the product takes the scales of both operands paired, which a caller
-// that quantizes them itself may write so.
-inline bool mx_paired(int64_t M, int64_t N, int K) {
-    return M >= 1 && M <= kRowBlock && N <= kMaxChannels &&
-           choose_form(M, static_cast<int>(N), K, device_cu_count()).bm == kPairedRows;
-}
-
-// Bytes of scales in the order of pairs of steps.
-inline int64_t mx_paired_bytes(int64_t rows, int K) { return rows * ((K + 2 * kDepth - 1) / (2 * kDepth)) * 16; }
-
-// Bytes of workspace of a product on the current device: the sums of parts of
-// the depth, or scales that are not paired yet.
-inline int64_t mx_product_workspace(int64_t M, int N, int K, bool x_paired = false, bool w_paired = false) {
-    int64_t most = int8_product_workspace(M, N, K);
-    for (const int64_t m : {M < kRowBlock ? M : kRowBlock, M % kRowBlock})
-        for (const int64_t n : {N < kMaxChannels ? N : kMaxChannels, N % kMaxChannels}) {
-            if (m == 0 || n == 0 || !mx_paired(m, n, K)) continue;
-            const int64_t need = (x_paired ? 0 : mx_paired_bytes(m, K)) + (w_paired ? 0 : mx_paired_bytes(n, K));
-            if (need > most) most = need;
-        }
-    return most;
-}
-
-// No less than that for any number of rows up to M, and never less for more
-// rows.
-inline int64_t mx_product_workspace_up_to(int64_t M, int N, int K) {
-    const int64_t sums = int8_product_workspace_up_to(M, N, K);
-    if (M < kPairedRows || N < kPairedRows) return sums;
-    const int64_t scales = mx_paired_bytes((M < kRowBlock ? M : kRowBlock) + (N < kMaxChannels ? N : kMaxChannels), K);
-    return scales > sums ? scales : sums;
-}
 
 // workspace: of mx_product_workspace bytes, 16-byte aligned.
 int launch_mx_product(Dtype t, const MxProduct& p, void* workspace, void* stream);

@@ -1367,7 +1367,7 @@ int launch_product_e(const MxProduct& whole, void* workspace, void* stream) {
             p.ws += n * p.ldws;
             if (p.bias) p.bias = static_cast<const T*>(p.bias) + n;
             p.out = static_cast<T*>(p.out) + m * p.ldo + n;
-            const Int8Choice c = choose_form(p.M, p.N, p.K, cus);
+            const Int8Choice c = mx_choose(p.M, p.N, p.K, cus);
             int e = c.bm == kPairedRows ? pair_scales(p, static_cast<uint8_t*>(workspace), stream) : 0;
             if (e != 0) return e;
             e = launch_form<E>(p, c, workspace, stream);
