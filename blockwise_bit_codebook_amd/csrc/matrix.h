@@ -69,14 +69,23 @@ __device__ __forceinline__ void load8_raw(const typename E::T* row, int c, int d
 #pragma unroll
         for (int i = 0; i < E::kVec; ++i) r[i] = load16_any(row + c + 4 * i);
     } else {
+        // the last element stands in for those past it: eight loads without a
+        // branch between them, on their way together
+        typename E::T v[8];
 #pragma unroll
-        for (int i = 0; i < E::kVec; ++i) r[i] = u32x4{0u, 0u, 0u, 0u};
+        for (int e = 0; e < 8; ++e) v[e] = row[min(c + e, d - 1)];
+        uint32_t w[4 * E::kVec];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (c + e >= d) continue;
-            if constexpr (sizeof(typename E::T) == 4) r[e / 4][e % 4] = __float_as_uint(row[c + e]);
-            else r[0][e / 2] |= static_cast<uint32_t>(row[c + e]) << (16 * (e & 1));
+        for (int i = 0; i < 4 * E::kVec; ++i) {
+            if constexpr (sizeof(typename E::T) == 4) {
+                w[i] = c + i < d ? __float_as_uint(v[i]) : 0u;
+            } else {
+                w[i] = c + 2 * i < d ? v[2 * i] : 0u;
+                if (c + 2 * i + 1 < d) w[i] |= static_cast<uint32_t>(v[2 * i + 1]) << 16;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < E::kVec; ++i) r[i] = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
     }
 }
 

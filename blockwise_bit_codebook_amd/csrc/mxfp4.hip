@@ -164,27 +164,38 @@ __global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(
     if (r0 < rows) {
         const int n = static_cast<int>(min<int64_t>(rows - r0, kMxBlock));
         uint32_t v[kMxBlock][2];
-        const T* x = X + r0 * ldx + col;
-#pragma unroll
-        for (int r = 0; r < kMxBlock; ++r) v[r][0] = v[r][1] = 0u;
-        if (n == kMxBlock && col + C <= cols) {
+        const T* x = X + r0 * ldx;
+        if (cols >= C) {
+            // The last columns' lanes read the matrix's last 8 bytes of a row and move
+            // what is theirs down; rows past the last repeat it, and count as zeros.
+            const int from = min(col, cols - C), past = min(col - from, C) * 8 * static_cast<int>(sizeof(T));
 #pragma unroll
             for (int r = 0; r < kMxBlock; ++r) {
-                const u32x2_any f = *reinterpret_cast<const u32x2_any*>(x + r * ldx);
+                const u32x2_any f = *reinterpret_cast<const u32x2_any*>(x + min(r, n - 1) * ldx + from);
                 v[r][0] = f[0];
                 v[r][1] = f[1];
             }
+            if (col0 + kTile > cols || n < kMxBlock) {
+#pragma unroll
+                for (int r = 0; r < kMxBlock; ++r) {
+                    uint64_t f = v[r][0] | static_cast<uint64_t>(v[r][1]) << 32;
+                    f = past < 64 && r < n ? f >> past : 0u;
+                    v[r][0] = static_cast<uint32_t>(f);
+                    v[r][1] = static_cast<uint32_t>(f >> 32);
+                }
+            }
         } else {
 #pragma unroll
-            for (int r = 0; r < kMxBlock; ++r)
-                if (r < n) {
+            for (int r = 0; r < kMxBlock; ++r) {
+                v[r][0] = v[r][1] = 0u;
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        if (col + c >= cols) continue;
-                        if constexpr (kWide) v[r][c] = __float_as_uint(x[r * ldx + c]);
-                        else v[r][c / 2] |= static_cast<uint32_t>(x[r * ldx + c]) << (16 * (c & 1));
-                    }
+                for (int c = 0; c < C; ++c) {
+                    const T f = x[min(r, n - 1) * ldx + min(col + c, cols - 1)];
+                    if (r >= n || col + c >= cols) continue;
+                    if constexpr (kWide) v[r][c] = __float_as_uint(f);
+                    else v[r][c / 2] |= static_cast<uint32_t>(f) << (16 * (c & 1));
                 }
+            }
         }
         if (columns.codes) {
             uint32_t m[2] = {0u, 0u};
@@ -413,9 +424,11 @@ __device__ __forceinline__ u32x4 pair_order(const u32x4& s) {
 // which no code meets (a 255 there would).
 __device__ __forceinline__ uint2 tail_scales(const uint8_t* row, int k, int blocks) {
     uint32_t r[2] = {0u, 0u};
+    uint8_t v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (k + i < blocks) r[i >> 2] |= static_cast<uint32_t>(row[k + i]) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) v[i] = row[min(k + i, blocks - 1)];  // on their way together
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i >> 2] |= k + i < blocks ? static_cast<uint32_t>(v[i]) << (8 * (i & 3)) : 0u;
     return make_uint2(r[0], r[1]);
 }
 
