@@ -1018,15 +1018,6 @@ __global__ __launch_bounds__(8 * kWave) void mx_large_kernel(const MxProduct p, 
 // With E = MSums the depth is split as well: workgroups (x, y) take the bytes
 // from y part_depth on, at most part_depth (whole pairs of steps), and store
 // their sums as they are, one matrix after the other.
-// A barrier that waits for the wave's LDS accesses but not for its loads, as
-// __syncthreads would.  The fences emit nothing and hold the compiler to the order.
-__device__ __forceinline__ void barrier_in_flight() {
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-}
-
 constexpr int kRingChannels = 128;
 
 template <class E, int TM, int S>
