@@ -80,6 +80,30 @@ struct Pieces {
         }
     }
     __device__ __forceinline__ bool counts(int i, int e) const { return TINY ? at[i] + e < d : e >= skip[i]; }
+    // The sum of a piece's values, of their products: only the last lanes of a row
+    // have any that do not count.
+    __device__ __forceinline__ float sum(int i, const float (&v)[8]) const {
+        float s = v[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) s += v[e];
+        if (TINY || skip[i] > 0) {
+            s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += counts(i, e) ? v[e] : 0.0f;
+        }
+        return s;
+    }
+    __device__ __forceinline__ float sum(int i, const float (&a)[8], const float (&b)[8]) const {
+        float s = a[0] * b[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) s = fmaf(a[e], b[e], s);
+        if (TINY || skip[i] > 0) {
+            s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = counts(i, e) ? fmaf(a[e], b[e], s) : s;
+        }
+        return s;
+    }
     template <class F>
     __device__ __forceinline__ void load_raw(const typename F::T* row, int i, u32x4 (&r)[F::kVec]) const {
         if constexpr (TINY) {
@@ -138,15 +162,23 @@ __device__ __forceinline__ void load_weight(const void* w, bool fp32, int c, int
     else load8_any<E>(static_cast<const typename E::T*>(w), c, d, x);
 }
 
-// What a row's sums give.
+// What a row's sums give: (x - m0) r + shift is its normed value.
 struct Stats {
-    float m0, m1, r;
+    float r, shift, m1;
 };
-__device__ __forceinline__ Stats stats_of(float m0, float sum1, float sum2, float inv_d, float eps) {
+// 1 / sqrt(v), within 1 ulp: the instruction's own for all but the smallest v,
+// which it would take for 0.
+__device__ __forceinline__ float reciprocal_root(float v) {
+    const bool small = v < 0x1p-100f;
+    const float r = __builtin_amdgcn_rsqf(small ? v * 0x1p100f : v);
+    return small ? r * 0x1p50f : r;
+}
+__device__ __forceinline__ Stats stats_of(float sum1, float sum2, float inv_d, float eps) {
     const float m1 = sum1 * inv_d;
     const float var = fmaxf(sum2 * inv_d - m1 * m1, 0.0f);
     // fmaxf drops a NaN: a row that has one keeps it
-    return Stats{m0, m1, 1.0f / sqrtf((sum2 != sum2 ? sum2 : var) + eps)};
+    const float r = reciprocal_root((sum2 != sum2 ? sum2 : var) + eps);
+    return Stats{r, -m1 * r, m1};
 }
 
 // ---------------------------------------------------------------------------
@@ -170,23 +202,19 @@ __global__ __launch_bounds__((WAVES < 4 ? 4 : WAVES) * kWave) void layer_norm_ke
     for (int i = 0; i < P; ++i) at.load(x, i, v[i]);
     float s[1] = {0.0f};
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] += at.counts(i, e) ? v[i][e] : 0.0f;
+    for (int i = 0; i < P; ++i) s[0] += at.sum(i, v[i]);
     row_sums<WAVES, 1>(s, red[0] + sub * WAVES, part);
     const float m0 = s[0] * inv_d;
     float s2[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < P; ++i)
+    for (int i = 0; i < P; ++i) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[i][e] = v[i][e] - m0;
-            const float c = at.counts(i, e) ? v[i][e] : 0.0f;
-            s2[0] += c;
-            s2[1] += c * c;
-        }
+        for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] - m0;
+        s2[0] += at.sum(i, v[i]);
+        s2[1] += at.sum(i, v[i], v[i]);
+    }
     row_sums<WAVES, 2>(s2, red[1] + sub * WAVES * 2, part);
-    const Stats st = stats_of(m0, s2[0], s2[1], inv_d, p.eps);
+    const Stats st = stats_of(s2[0], s2[1], inv_d, p.eps);
     T* out = static_cast<T*>(p.out) + row * p.ldo;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -196,8 +224,8 @@ __global__ __launch_bounds__((WAVES < 4 ? 4 : WAVES) * kWave) void layer_norm_ke
         if (p.bias) at.weight(p.bias, p.weight_fp32, i, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            v[i][e] = (v[i][e] - st.m1) * st.r * w[e];
-            if (p.bias) v[i][e] = v[i][e] + b[e];
+            const float xh = fmaf(v[i][e], st.r, st.shift);
+            v[i][e] = p.bias ? fmaf(xh, w[e], b[e]) : xh * w[e];
         }
         at.store(out, i, v[i], streamed);
     }
@@ -208,7 +236,7 @@ __global__ __launch_bounds__((WAVES < 4 ? 4 : WAVES) * kWave) void layer_norm_ke
 constexpr int kLongWaves = 16, kLongLanes = kLongWaves * kWave;
 
 template <class E>
-__device__ __forceinline__ Stats long_stats(const typename E::T* x, int d, float eps, float (*red)[kLongWaves * 2]) {
+__device__ __forceinline__ Stats long_stats(const typename E::T* x, int d, float eps, float (*red)[kLongWaves * 2], float& m0) {
     const int wave = threadIdx.x / kWave, t = threadIdx.x, pieces = (d + kLongLanes * 8 - 1) / (kLongLanes * 8);
     const float inv_d = 1.0f / static_cast<float>(d);
     float s[1] = {0.0f};
@@ -219,7 +247,7 @@ __device__ __forceinline__ Stats long_stats(const typename E::T* x, int d, float
         for (int e = 0; e < 8; ++e) s[0] += v[e];
     }
     row_sums<kLongWaves, 1>(s, red[0], wave);
-    const float m0 = s[0] * inv_d;
+    m0 = s[0] * inv_d;
     float s2[2] = {0.0f, 0.0f};
     for (int i = 0; i < pieces; ++i) {
         float v[8];
@@ -232,7 +260,7 @@ __device__ __forceinline__ Stats long_stats(const typename E::T* x, int d, float
         }
     }
     row_sums<kLongWaves, 2>(s2, red[1], wave);
-    return stats_of(m0, s2[0], s2[1], inv_d, eps);
+    return stats_of(s2[0], s2[1], inv_d, eps);
 }
 
 template <class E>
@@ -241,7 +269,8 @@ __global__ __launch_bounds__(kLongLanes) void layer_norm_long_kernel(const Layer
     __shared__ float red[2][kLongWaves * 2];
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    const Stats st = long_stats<E>(x, p.d, p.eps, red);
+    float m0;
+    const Stats st = long_stats<E>(x, p.d, p.eps, red, m0);
     T* out = static_cast<T*>(p.out) + row * p.ldo;
     const int t = threadIdx.x, pieces = (p.d + kLongLanes * 8 - 1) / (kLongLanes * 8);
     for (int i = 0; i < pieces; ++i) {
@@ -251,8 +280,8 @@ __global__ __launch_bounds__(kLongLanes) void layer_norm_long_kernel(const Layer
         if (p.bias) load_weight<E>(p.bias, p.weight_fp32, column<kLongLanes>(i, t), p.d, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            v[e] = (v[e] - st.m0 - st.m1) * st.r * w[e];
-            if (p.bias) v[e] = v[e] + b[e];
+            const float xh = fmaf(v[e] - m0, st.r, st.shift);
+            v[e] = p.bias ? fmaf(xh, w[e], b[e]) : xh * w[e];
         }
         store8<E>(out, column<kLongLanes>(i, t), p.d, v);
     }
@@ -284,38 +313,33 @@ __global__ __launch_bounds__(WAVES* ROWS* kWave) void layer_norm_back_kernel(con
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.0f;
     }
-    u32x4 xr[P][E::kVec], gr[P][E::kVec];  // the next row, as it stands in memory
+    struct Row {  // as it stands in memory
+        u32x4 x[P][E::kVec], g[P][E::kVec];
+    };
     const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
-    auto fetch = [&](int64_t row) {  // past the last row it is fetched again
+    auto fetch = [&](int64_t row, Row& to) {  // past the last row it is fetched again
         row = min(row, p.rows - 1);
         const T* x = static_cast<const T*>(p.x) + row * p.ldx;
         const T* g = static_cast<const T*>(p.g) + row * p.ldg;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            at.template load_raw<E>(x, i, xr[i]);
-            at.template load_raw<E>(g, i, gr[i]);
+            at.template load_raw<E>(x, i, to.x[i]);
+            at.template load_raw<E>(g, i, to.g[i]);
         }
     };
     int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + sub;
-    if (kAhead) fetch(row);
-    // every row of a workgroup takes part in its barriers
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS; first < p.rows; first += step, row += step) {
+    auto turn = [&](Row& now, Row& next) {
         float v[P][8], h[P][8];
-        if (!kAhead) fetch(row);
+        if (!kAhead) fetch(row, now);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            E::widen(xr[i], v[i]);
-            E::widen(gr[i], h[i]);
+            E::widen(now.x[i], v[i]);
+            E::widen(now.g[i], h[i]);
         }
-        if (kAhead) {
-            __builtin_amdgcn_sched_barrier(0);  // the old values have left their registers
-            fetch(row + step);
-        }
+        if (kAhead) fetch(row + step, next);
         float s[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] += at.counts(i, e) ? v[i][e] : 0.0f;
+        for (int i = 0; i < P; ++i) s[0] += at.sum(i, v[i]);
         row_sums<WAVES, 1>(s, red[0] + sub * WAVES, part);
         const float m0 = s[0] * inv_d;
         const void* weight = p.weight;
@@ -325,35 +349,49 @@ __global__ __launch_bounds__(WAVES* ROWS* kWave) void layer_norm_back_kernel(con
         for (int i = 0; i < P; ++i) {
             const int k = kKeepWeight ? i : 0;
             if (!kKeepWeight) at.weight(weight, p.weight_fp32, i, w[k]);
+            float hw[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 v[i][e] = v[i][e] - m0;
-                const float c = at.counts(i, e) ? v[i][e] : 0.0f, hw = at.counts(i, e) ? h[i][e] * w[k][e] : 0.0f;
-                s4[0] += c;
-                s4[1] += c * c;
-                s4[2] += hw;
-                s4[3] += hw * c;
+                hw[e] = h[i][e] * w[k][e];
             }
+            s4[0] += at.sum(i, v[i]);
+            s4[1] += at.sum(i, v[i], v[i]);
+            s4[2] += at.sum(i, hw);
+            s4[3] += at.sum(i, hw, v[i]);
         }
         row_sums<WAVES, 4>(s4, red[1] + sub * WAVES * 4, part);
-        const Stats st = stats_of(m0, s4[0], s4[1], inv_d, p.eps);
+        const Stats st = stats_of(s4[0], s4[1], inv_d, p.eps);
         const float mh = s4[2] * inv_d, mhx = st.r * (s4[3] - st.m1 * s4[2]) * inv_d;
-        if (row < p.rows) {
+        if (ROWS == 1 || row < p.rows) {
             T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+            const float down = -st.r * mh, along = -st.r * mhx;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int k = kKeepWeight ? i : 0;
                 if (!kKeepWeight) at.weight(weight, p.weight_fp32, i, w[k]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float xh = (v[i][e] - st.m1) * st.r;
-                    dw[i][e] += h[i][e] * xh;
+                    const float xh = fmaf(v[i][e], st.r, st.shift);
+                    dw[i][e] = fmaf(h[i][e], xh, dw[i][e]);
                     db[i][e] += h[i][e];
-                    v[i][e] = st.r * (h[i][e] * w[k][e] - mh - xh * mhx);
+                    v[i][e] = fmaf(xh, along, fmaf(h[i][e] * w[k][e], st.r, down));
                 }
                 at.store(dx, i, v[i], streamed);
             }
         }
+        row += step;
+    };
+    // Two rows by name, as a copy of one that is on its way would wait for it.
+    // Every row of a workgroup takes part in its barriers.
+    Row even, odd;
+    if (kAhead) fetch(row, even);
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS; first < p.rows;) {
+        turn(even, odd);
+        first += step;
+        if (first >= p.rows) break;
+        turn(odd, even);
+        first += step;
     }
     if constexpr (ROWS > 1) {  // the workgroup's rows, in their order
         __shared__ float sums[ROWS - 1][2][P * 8 * LANES];
@@ -405,7 +443,8 @@ __global__ __launch_bounds__(kLongLanes) void layer_norm_back_long_kernel(const 
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
     const T* g = static_cast<const T*>(p.g) + row * p.ldg;
-    const Stats st = long_stats<E>(x, p.d, p.eps, red);
+    float m0;
+    const Stats st = long_stats<E>(x, p.d, p.eps, red, m0);
     const int t = threadIdx.x, wave = threadIdx.x / kWave, pieces = (p.d + kLongLanes * 8 - 1) / (kLongLanes * 8);
     const float inv_d = 1.0f / static_cast<float>(p.d);
     float s[2] = {0.0f, 0.0f};
@@ -417,15 +456,15 @@ __global__ __launch_bounds__(kLongLanes) void layer_norm_back_long_kernel(const 
 #pragma unroll
         for (int e = 0; e < 8; ++e) {  // past the row h is 0
             s[0] += h[e] * w[e];
-            s[1] += h[e] * w[e] * ((v[e] - st.m0 - st.m1) * st.r);
+            s[1] = fmaf(h[e] * w[e], fmaf(v[e] - m0, st.r, st.shift), s[1]);
         }
     }
     row_sums<kLongWaves, 2>(s, red[2], wave);
     const float mh = s[0] * inv_d, mhx = s[1] * inv_d;
     if (t == 0) {
-        stats[row * 4] = st.m0;
-        stats[row * 4 + 1] = st.m1;
-        stats[row * 4 + 2] = st.r;
+        stats[row * 4] = m0;
+        stats[row * 4 + 1] = st.r;
+        stats[row * 4 + 2] = st.shift;
     }
     T* dx = static_cast<T*>(p.dx) + row * p.lddx;
     for (int i = 0; i < pieces; ++i) {
@@ -434,7 +473,7 @@ __global__ __launch_bounds__(kLongLanes) void layer_norm_back_long_kernel(const 
         load8_any<E>(g, column<kLongLanes>(i, t), p.d, h);
         load_weight<E>(p.weight, p.weight_fp32, column<kLongLanes>(i, t), p.d, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = st.r * (h[e] * w[e] - mh - (v[e] - st.m0 - st.m1) * st.r * mhx);
+        for (int e = 0; e < 8; ++e) v[e] = st.r * (h[e] * w[e] - mh - fmaf(v[e] - m0, st.r, st.shift) * mhx);
         store8<E>(dx, column<kLongLanes>(i, t), p.d, v);
     }
 }
@@ -451,7 +490,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_column_sums_kernel(const 
     for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
         const float x = E::one(static_cast<const T*>(p.x)[row * p.ldx + c]);
         const float g = E::one(static_cast<const T*>(p.g)[row * p.ldg + c]);
-        dw += g * ((x - stats[row * 4] - stats[row * 4 + 1]) * stats[row * 4 + 2]);
+        dw = fmaf(g, fmaf(x - stats[row * 4], stats[row * 4 + 1], stats[row * 4 + 2]), dw);
         db += g;
     }
     float* to = partial + static_cast<int64_t>(blockIdx.y) * 2 * p.d;
