@@ -434,10 +434,11 @@ __global__ __launch_bounds__(WAVES* ROWS* kWave) void layer_norm_back_kernel(con
     }
 }
 
-// Long rows: dx and the rows' statistics, then the sums over rows.
+// Long rows: their statistics, then the sums over rows, and dx last, which may
+// overwrite dout.
 template <class E>
-__global__ __launch_bounds__(kLongLanes) void layer_norm_back_long_kernel(const LayerNormBackArgs p,
-                                                                          float* __restrict__ stats) {
+__global__ __launch_bounds__(kLongLanes) void layer_norm_back_long_stats_kernel(const LayerNormBackArgs p,
+                                                                                float* __restrict__ stats) {
     using T = typename E::T;
     __shared__ float red[3][kLongWaves * 2];
     const int64_t row = blockIdx.x;
@@ -460,20 +461,34 @@ __global__ __launch_bounds__(kLongLanes) void layer_norm_back_long_kernel(const 
         }
     }
     row_sums<kLongWaves, 2>(s, red[2], wave);
-    const float mh = s[0] * inv_d, mhx = s[1] * inv_d;
     if (t == 0) {
-        stats[row * 4] = m0;
-        stats[row * 4 + 1] = st.r;
-        stats[row * 4 + 2] = st.shift;
+        float* to = stats + row * kLayerNormStats;
+        to[0] = m0;
+        to[1] = st.r;
+        to[2] = st.shift;
+        to[3] = s[0] * inv_d;
+        to[4] = s[1] * inv_d;
     }
+}
+
+template <class E>
+__global__ __launch_bounds__(kLongLanes) void layer_norm_back_long_kernel(const LayerNormBackArgs p,
+                                                                          const float* __restrict__ stats) {
+    using T = typename E::T;
+    const int64_t row = blockIdx.x;
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    const T* g = static_cast<const T*>(p.g) + row * p.ldg;
     T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+    const float* of = stats + row * kLayerNormStats;
+    const float m0 = of[0], r = of[1], shift = of[2], mh = of[3], mhx = of[4];
+    const int t = threadIdx.x, pieces = (p.d + kLongLanes * 8 - 1) / (kLongLanes * 8);
     for (int i = 0; i < pieces; ++i) {
         float v[8], h[8], w[8];
         load8_any<E>(x, column<kLongLanes>(i, t), p.d, v);
         load8_any<E>(g, column<kLongLanes>(i, t), p.d, h);
         load_weight<E>(p.weight, p.weight_fp32, column<kLongLanes>(i, t), p.d, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = st.r * (h[e] * w[e] - mh - fmaf(v[e] - m0, st.r, st.shift) * mhx);
+        for (int e = 0; e < 8; ++e) v[e] = r * (h[e] * w[e] - mh - fmaf(v[e] - m0, r, shift) * mhx);
         store8<E>(dx, column<kLongLanes>(i, t), p.d, v);
     }
 }
@@ -490,7 +505,8 @@ __global__ __launch_bounds__(kThreads) void layer_norm_column_sums_kernel(const 
     for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
         const float x = E::one(static_cast<const T*>(p.x)[row * p.ldx + c]);
         const float g = E::one(static_cast<const T*>(p.g)[row * p.ldg + c]);
-        dw = fmaf(g, fmaf(x - stats[row * 4], stats[row * 4 + 1], stats[row * 4 + 2]), dw);
+        const float* of = stats + row * kLayerNormStats;
+        dw = fmaf(g, fmaf(x - of[0], of[1], of[2]), dw);
         db += g;
     }
     float* to = partial + static_cast<int64_t>(blockIdx.y) * 2 * p.d;
@@ -597,21 +613,26 @@ int launch_back_e(const LayerNormBackArgs& p, void* stream) {
     } else {
         groups = static_cast<int>(p.rows < kLayerNormPartials ? p.rows : kLayerNormPartials);
         float* stats = p.workspace + static_cast<int64_t>(groups) * 2 * p.d;
-        constexpr int64_t kMost = int64_t(1) << 21;
-        for (int64_t r = 0; r < p.rows && e == 0; r += kMost) {
+        // all rows, kMost a launch, in one kernel or the other
+        const auto rows = [&](auto kernel) {
             using T = typename E::T;
-            LayerNormBackArgs q = p;
-            q.x = static_cast<const T*>(p.x) + r * p.ldx;
-            q.g = static_cast<const T*>(p.g) + r * p.ldg;
-            q.dx = static_cast<T*>(p.dx) + r * p.lddx;
-            hipLaunchKernelGGL((layer_norm_back_long_kernel<E>), dim3(static_cast<unsigned>(p.rows - r < kMost ? p.rows - r : kMost)),
-                               dim3(kLongLanes), 0, static_cast<hipStream_t>(stream), q, stats + r * 4);
-            e = static_cast<int>(hipGetLastError());
-        }
+            constexpr int64_t kMost = int64_t(1) << 21;
+            for (int64_t r = 0; r < p.rows && e == 0; r += kMost) {
+                LayerNormBackArgs q = p;
+                q.x = static_cast<const T*>(p.x) + r * p.ldx;
+                q.g = static_cast<const T*>(p.g) + r * p.ldg;
+                q.dx = static_cast<T*>(p.dx) + r * p.lddx;
+                hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(p.rows - r < kMost ? p.rows - r : kMost)), dim3(kLongLanes),
+                                   0, static_cast<hipStream_t>(stream), q, stats + r * kLayerNormStats);
+                e = static_cast<int>(hipGetLastError());
+            }
+        };
+        rows(layer_norm_back_long_stats_kernel<E>);
         if (e != 0) return e;
         hipLaunchKernelGGL((layer_norm_column_sums_kernel<E>), dim3((p.d + kThreads - 1) / kThreads, groups), dim3(kThreads),
                            0, static_cast<hipStream_t>(stream), p, stats, p.workspace);
         e = static_cast<int>(hipGetLastError());
+        rows(layer_norm_back_long_kernel<E>);
     }
     if (e != 0) return e;
     hipLaunchKernelGGL(layer_norm_add_kernel,

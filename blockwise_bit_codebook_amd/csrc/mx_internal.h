@@ -151,10 +151,11 @@ constexpr int kLayerNormPartials = 512;
 // Longest row whose sums stay in registers; above it the rows' statistics go
 // to the workspace and a second pass sums over rows.
 constexpr int kLayerNormKept = 16384;
+constexpr int kLayerNormStats = 8;  // floats a row
 
 inline int64_t layer_norm_backward_bytes(int64_t rows, int d) {
     const int64_t groups = rows < kLayerNormPartials ? rows : kLayerNormPartials;
-    return 4 * (groups * 2 * d + (d > kLayerNormKept ? 4 * rows : 0));
+    return 4 * (groups * 2 * d + (d > kLayerNormKept ? kLayerNormStats * rows : 0));
 }
 
 struct LayerNormBackArgs {

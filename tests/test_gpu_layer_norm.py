@@ -56,6 +56,24 @@ def test_forward_and_backward(t, rows, d):
     assert_bits_equal(bits(X2), bits(y), "out over x")
 
 
+@pytest.mark.parametrize("t", DT)
+@pytest.mark.parametrize("rows,d", [(5, 2), (9, 64), (600, 777), (1030, 3000), (600, 8000), (600, 9001), (600, 16392), (3, 70001)])
+def test_gradients_over_dout(t, rows, d):
+    # the weights' gradients come from dout as it was
+    T = torch()
+    case(f"layer norm gradients over dout {t} {rows}x{d}")
+    b, x, wb, w, bb, bias, gb, g = data(t, rows, d, 3)
+    X, W = upload(b, t), upload(wb[None], t)[0]
+    want = kb.layer_norm_backward(upload(gb, t), X, W)
+    wide = T.full((rows, d + 3), 2.0, dtype=tdt(t), device=dev())
+    for G in (upload(gb, t), wide[:, 1:d + 1]):
+        G.copy_(upload(gb, t))
+        got = kb.layer_norm_backward(G, X, W, dx=G)
+        for a, c, name in zip((G.contiguous(), *got[1:]), want, ("dx", "dweight", "dbias")):
+            assert_bits_equal(bits(a), bits(c), name)
+    assert (wide[:, 0] == 2).all() and (wide[:, d + 1:] == 2).all()
+
+
 @pytest.mark.parametrize("t", ["fp16", "bf16"])
 @pytest.mark.parametrize("rows,d", [(3, 100), (40, 512), (70, 3000), (3, 12000), (2, 20000), (2, 70001)])
 def test_weights_in_fp32(t, rows, d):
