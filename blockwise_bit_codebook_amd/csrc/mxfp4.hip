@@ -1317,9 +1317,7 @@ int launch_few_tile(const MxProduct& p, Int8Few f, void* stream) {
         case 34: return launch_few<E, 3, 4, 5>(p, stream);
         case 44: return launch_few<E, 4, 4, 4>(p, stream);
         case 53: return launch_few<E, 5, 3, 4>(p, stream);
-        case 54: return launch_few<E, 5, 4, 4>(p, stream);
-        case 73: return launch_few<E, 7, 3, 4>(p, stream);
-        default: return launch_few<E, 8, 3, 3>(p, stream);
+        default: return launch_few<E, 5, 4, 4>(p, stream);
     }
 }
 
