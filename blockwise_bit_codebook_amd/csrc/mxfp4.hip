@@ -815,20 +815,14 @@ __device__ __forceinline__ void store_tile(const MxProduct& p, T* out, uint8_t* 
             }
         }
         wave_order();
-        if (packed) {
-            constexpr int kPieces = kRow / 16, kRows = kWave / kPieces;  // rows a store instruction
+        constexpr int kPieces = kRow / 16, kRows = kWave / kPieces;  // rows a store instruction
 #pragma unroll
-            for (int r0 = 0; r0 < kPass * 16; r0 += kRows) {
-                const int row = r0 + lane / kPieces, piece = lane % kPieces;
-                const u32x4 d = *reinterpret_cast<const u32x4*>(region + row * kRow + 16 * (piece ^ (row & 7)));
-                store16<NT>(out + (16 * i0 + row) * p.ldo + piece * (16 / kSize), d);
-            }
-        } else {
-            for (int row = 0; row < kPass * 16; ++row) {
-                const int piece = lane / (16 / kSize), at = lane % (16 / kSize);
-                out[(16 * i0 + row) * p.ldo + lane] = reinterpret_cast<const T*>(
-                    region + row * kRow + 16 * (piece ^ (row & 7)))[at];
-            }
+        for (int r0 = 0; r0 < kPass * 16; r0 += kRows) {
+            const int row = r0 + lane / kPieces, piece = lane % kPieces;
+            const u32x4 d = *reinterpret_cast<const u32x4*>(region + row * kRow + 16 * (piece ^ (row & 7)));
+            T* to = out + (16 * i0 + row) * p.ldo + piece * (16 / kSize);
+            if (packed) store16<NT>(to, d);
+            else store16_any(to, d);
         }
         if (i0 + kPass < TM) wave_order();  // the next pass goes over the region
     }
