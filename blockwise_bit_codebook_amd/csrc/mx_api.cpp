@@ -49,7 +49,8 @@ int do_quantize_columns(Dtype t, const void* X, int64_t rows, int32_t cols, int6
     if (!X || !codes || !scales) return KBIT_EINVAL;
     if (!aligned(X, elem_size(t)) || !codes_aligned(codes, cols, ldc)) return KBIT_EALIGN;
     if (!device_usable()) return KBIT_EDEVICE;
-    return map_launch(launch_mx_quantize_columns(t, X, rows, cols, ldx, MxCoded{codes, scales, ldc, lds, false}, MxCoded{}, nullptr, stream));
+    const MxColumns job{X, rows, ldx, cols, MxCoded{codes, scales, ldc, lds, false}, MxCoded{}, nullptr};
+    return map_launch(launch_mx_quantize_columns(t, &job, 1, stream));
 }
 
 int do_dequantize(Dtype t, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t rows, int32_t d,
@@ -156,17 +157,17 @@ int do_linear_backward(Dtype t, const void* g, int64_t ldg, const void* X, int64
     const bool pair_x = dX && mx_paired(M, K, mx_depth(N)), pair_w = dW && mx_paired(N, K, mx_depth(M));
     const MxCoded g_rows = coded_in(w, b.g_rows, M, pair_x), w_cols = coded_in(w + b.w_at, b.w_cols, K, pair_x),
                   g_cols = coded_in(w + b.gc_at, b.g_cols, N, pair_w), x_cols = coded_in(w + b.x_at, b.x_cols, K, pair_w);
-    // dout along its rows alone, or its columns with them
-    const int e = dW || db ? launch_mx_quantize_columns(t, g, M, N, ldg, dW ? g_cols : MxCoded{}, dX ? g_rows : MxCoded{},
-                                                        db ? sums : nullptr, stream)
-                           : launch_mx_quantize(t, g, M, N, ldg, g_rows, stream);
-    if (e != 0) return KBIT_ELAUNCH;
+    // dout's columns and their sums with its rows, W's and X's in one launch; dout's rows alone where nothing else needs it
+    MxColumns jobs[kMxColumnJobs];
+    int count = 0;
+    if (dW || db) jobs[count++] = MxColumns{g, M, ldg, N, dW ? g_cols : MxCoded{}, dX ? g_rows : MxCoded{}, db ? sums : nullptr};
+    else if (launch_mx_quantize(t, g, M, N, ldg, g_rows, stream) != 0) return KBIT_ELAUNCH;
+    if (dX) jobs[count++] = MxColumns{W, N, ldw, K, w_cols, MxCoded{}, nullptr};
+    if (dW) jobs[count++] = MxColumns{X, M, ldx, K, x_cols, MxCoded{}, nullptr};
+    if (launch_mx_quantize_columns(t, jobs, count, stream) != 0) return KBIT_ELAUNCH;
     if (db && launch_mx_add_sums(sums, mx_sum_groups(M), N, db, stream) != 0) return KBIT_ELAUNCH;
-    if (dX && (launch_mx_quantize_columns(t, W, N, K, ldw, w_cols, MxCoded{}, nullptr, stream) != 0 ||
-               launch_mx_product(t, product_of(g_rows, M, w_cols, K, N, dX, lddx), w + b.product_at, stream) != 0))
-        return KBIT_ELAUNCH;
-    if (dW && (launch_mx_quantize_columns(t, X, M, K, ldx, x_cols, MxCoded{}, nullptr, stream) != 0 ||
-               launch_mx_product(Dtype::fp32, product_of(g_cols, N, x_cols, K, M, dW, lddw), w + b.product_at, stream) != 0))
+    if (dX && launch_mx_product(t, product_of(g_rows, M, w_cols, K, N, dX, lddx), w + b.product_at, stream) != 0) return KBIT_ELAUNCH;
+    if (dW && launch_mx_product(Dtype::fp32, product_of(g_cols, N, x_cols, K, M, dW, lddw), w + b.product_at, stream) != 0)
         return KBIT_ELAUNCH;
     return KBIT_OK;
 }

@@ -18,7 +18,7 @@ constexpr int kMxBlockBytes = 16;  // of codes
 // Longest row: its codes' bytes and their steps count in 32 bits.
 constexpr int64_t kMxMaxDepth = int64_t(1) << 26;
 
-// Most columns that are quantized as such: two threads each, counted in 32 bits.
+// Most columns that are quantized as such.
 constexpr int64_t kMxMaxColumns = int64_t(1) << 30;
 
 inline int64_t mx_blocks(int64_t d) { return (d + kMxBlock - 1) / kMxBlock; }
@@ -37,11 +37,19 @@ int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx,
 // Columns of X [rows][cols], a column a row of codes, and its rows where
 // by_rows is there, in one reading of X.  sums: null, or mx_sum_groups(rows)
 // rows of cols floats, the columns' sums over kMxSumRows rows each; with
-// columns null they are all that is written.
+// columns null they are all that is written.  Up to kMxColumnJobs matrices in one
+// launch, by_rows for the first alone.
 constexpr int64_t kMxSumRows = 256;
 inline int64_t mx_sum_groups(int64_t rows) { return (rows + kMxSumRows - 1) / kMxSumRows; }
-int launch_mx_quantize_columns(Dtype t, const void* X, int64_t rows, int cols, int64_t ldx, const MxCoded& columns,
-                               const MxCoded& by_rows, float* sums, void* stream);
+constexpr int kMxColumnJobs = 3;
+struct MxColumns {
+    const void* X;
+    int64_t rows, ldx;
+    int cols;
+    MxCoded columns, by_rows;
+    float* sums;
+};
+int launch_mx_quantize_columns(Dtype t, const MxColumns* jobs, int count, void* stream);
 
 // out[c] = sum over groups of sums[group][c], in order.
 int launch_mx_add_sums(const float* sums, int64_t groups, int cols, float* out, void* stream);

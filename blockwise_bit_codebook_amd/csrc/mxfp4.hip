@@ -147,19 +147,34 @@ constexpr int kColBlocks = 8;
 template <class E>
 constexpr int kCols = 8 / sizeof(typename E::T);
 
+// The matrices of a launch, their workgroups one after the other: those of job
+// i are the ones below end[i] that job i - 1 leaves, `across` of them abreast.
+struct ColumnJobs {
+    MxColumns job[kMxColumnJobs];
+    uint32_t end[kMxColumnJobs], across[kMxColumnJobs];
+};
+
 template <class E, bool ROWS>
-__global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(
-    const typename E::T* __restrict__ X, int64_t rows, int cols, int64_t ldx, const MxCoded columns, const MxCoded by_rows,
-    int64_t first_row, float* __restrict__ sums) {
+__global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(const ColumnJobs jobs, uint32_t first) {
     using T = typename E::T;
     constexpr int C = kCols<E>, kTile = kWave * C;
+    const uint32_t group = first + blockIdx.x;
+    const int which = group < jobs.end[0] ? 0 : group < jobs.end[1] ? 1 : 2;
+    const uint32_t in_job = group - (which == 0 ? 0u : jobs.end[which - 1]), across = jobs.across[which];
+    const uint32_t down = in_job / across, over = in_job - down * across;
+    const MxColumns& job = jobs.job[which];
+    const T* __restrict__ X = static_cast<const T*>(job.X);
+    const int64_t rows = job.rows, ldx = job.ldx;
+    const int cols = job.cols;
+    const MxCoded columns = job.columns;
+    float* __restrict__ sums = job.sums;
     constexpr bool kWide = sizeof(T) == 4;
     __shared__ __align__(16) uint8_t tile[kTile * kColBlocks * kMxBlockBytes];
     __shared__ __align__(8) uint8_t bytes[kTile * kColBlocks];
     __shared__ float partial[kColBlocks][kTile];
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t block0 = static_cast<int64_t>(blockIdx.y) * kColBlocks, row_blocks = (rows + kMxBlock - 1) / kMxBlock;
-    const int col0 = blockIdx.x * kTile, col = col0 + C * lane;
+    const int64_t block0 = static_cast<int64_t>(down) * kColBlocks, row_blocks = (rows + kMxBlock - 1) / kMxBlock;
+    const int col0 = over * kTile, col = col0 + C * lane;
     const int64_t r0 = (block0 + wave) * kMxBlock;
     if (r0 < rows) {
         const int n = static_cast<int>(min<int64_t>(rows - r0, kMxBlock));
@@ -244,7 +259,8 @@ __global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(
                 partial[wave][C * lane + c] = total;
             }
         }
-        if constexpr (ROWS) {  // blocks of 32 columns: 32 / C lanes
+        if (ROWS && which == 0) {  // blocks of 32 columns: 32 / C lanes
+            const MxCoded by_rows = jobs.job[0].by_rows;
 #pragma unroll
             for (int r = 0; r < kMxBlock; ++r) {
                 uint32_t m = kWide ? max(v[r][0] & kAbs32, v[r][1] & kAbs32)
@@ -266,11 +282,11 @@ __global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(
                 if (byte == 255u) q = 0u;
                 const int end = (cols + kMxBlock - 1) / kMxBlock * kMxBlock;
                 if (r < n && col < end) {
-                    uint8_t* to = by_rows.codes + (first_row + r0 + r) * by_rows.ldc + col / 2;
+                    uint8_t* to = by_rows.codes + (r0 + r) * by_rows.ldc + col / 2;
                     if constexpr (kWide) *to = static_cast<uint8_t>(q);
                     else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(q);
                     if (col % kMxBlock == 0)
-                        *scale_place(by_rows, first_row + r0 + r, col / kMxBlock) = static_cast<uint8_t>(byte);
+                        *scale_place(by_rows, r0 + r, col / kMxBlock) = static_cast<uint8_t>(byte);
                 }
             }
         }
@@ -283,25 +299,24 @@ __global__ __launch_bounds__(kColBlocks* kWave) void mx_quantize_columns_kernel(
         float total = partial[0][threadIdx.x];
 #pragma unroll
         for (int w = 1; w < kColBlocks; ++w) total += partial[w][threadIdx.x];
-        sums[blockIdx.y * static_cast<int64_t>(cols) + col0 + threadIdx.x] = total;
+        sums[down * static_cast<int64_t>(cols) + col0 + threadIdx.x] = total;
     }
     if (!columns.codes) return;
     const int live = static_cast<int>(min<int64_t>(row_blocks - block0, kColBlocks));
-    const int64_t first_block = first_row / kMxBlock + block0;
 #pragma unroll
     for (int t = threadIdx.x; t < kTile * kColBlocks; t += kColBlocks * kWave) {
         const int c = t / kColBlocks, b = t % kColBlocks;
         if (b < live && col0 + c < cols)
-            *reinterpret_cast<u32x4*>(columns.codes + (col0 + c) * columns.ldc + (first_block + b) * kMxBlockBytes) =
+            *reinterpret_cast<u32x4*>(columns.codes + (col0 + c) * columns.ldc + (block0 + b) * kMxBlockBytes) =
                 *reinterpret_cast<const u32x4*>(tile + (c * kColBlocks + (b ^ (c / C & 7))) * kMxBlockBytes);
     }
     const int c = threadIdx.x;
     if (c < kTile && col0 + c < cols) {
         if (live == kColBlocks && !columns.paired) {
-            *reinterpret_cast<u32x2_any*>(columns.scales + (col0 + c) * columns.lds + first_block) =
+            *reinterpret_cast<u32x2_any*>(columns.scales + (col0 + c) * columns.lds + block0) =
                 *reinterpret_cast<const u32x2_any*>(bytes + c * kColBlocks);
         } else {
-            for (int b = 0; b < live; ++b) *scale_place(columns, col0 + c, first_block + b) = bytes[c * kColBlocks + b];
+            for (int b = 0; b < live; ++b) *scale_place(columns, col0 + c, block0 + b) = bytes[c * kColBlocks + b];
         }
     }
 }
@@ -312,8 +327,8 @@ __global__ __launch_bounds__(kWave) void mx_add_sums_kernel(const float* __restr
     const int c = blockIdx.x * kWave + threadIdx.x;
     if (c >= cols) return;
     float s = 0.0f;
-#pragma unroll 8
-    for (int64_t g = 0; g < groups; ++g) s += sums[g * cols + c];
+#pragma unroll 32
+    for (int64_t g = 0; g < groups; ++g) s += sums[g * cols + c];  // many on their way
     out[c] = s;
 }
 
@@ -1414,23 +1429,28 @@ int launch_quantize_e(const void* X, int64_t rows, int d, int64_t ldx, const MxC
 }
 
 template <class E>
-int launch_columns_e(const void* X, int64_t rows, int cols, int64_t ldx, const MxCoded& c, const MxCoded& r, float* sums,
-                     void* stream) {
-    using T = typename E::T;
+int launch_columns_e(const MxColumns* jobs, int count, void* stream) {
     static_assert(kMxSumRows == int64_t(kMxBlock) * kColBlocks, "a row of sums a row of workgroups");
-    constexpr int64_t kRows = kMxSumRows * 32768;  // of a launch: its grid's second axis
     constexpr int kTile = kWave * kCols<E>;
-    for (int64_t at = 0; at < rows; at += kRows) {
-        const int64_t n = rows - at < kRows ? rows - at : kRows;
-        const dim3 grid((cols + kTile - 1) / kTile, static_cast<unsigned>((n + kMxSumRows - 1) / kMxSumRows));
-        const T* x = static_cast<const T*>(X) + at * ldx;
-        float* f = sums ? sums + at / kMxSumRows * cols : nullptr;
-        if (r.codes)
+    constexpr uint32_t kMost = 1u << 22;  // workgroups of a launch: its threads count in 32 bits
+    ColumnJobs c{};
+    uint32_t all = 0;
+    for (int i = 0; i < kMxColumnJobs; ++i) {
+        if (i < count) {
+            c.job[i] = jobs[i];
+            c.across[i] = static_cast<uint32_t>((jobs[i].cols + kTile - 1) / kTile);
+            all += c.across[i] * static_cast<uint32_t>(mx_sum_groups(jobs[i].rows));
+        }
+        c.end[i] = all;
+    }
+    for (uint32_t first = 0; first < all; first += kMost) {
+        const dim3 grid(all - first < kMost ? all - first : kMost);
+        if (c.job[0].by_rows.codes)
             hipLaunchKernelGGL((mx_quantize_columns_kernel<E, true>), grid, dim3(kColBlocks * kWave), 0,
-                               static_cast<hipStream_t>(stream), x, n, cols, ldx, c, r, at, f);
+                               static_cast<hipStream_t>(stream), c, first);
         else
             hipLaunchKernelGGL((mx_quantize_columns_kernel<E, false>), grid, dim3(kColBlocks * kWave), 0,
-                               static_cast<hipStream_t>(stream), x, n, cols, ldx, c, r, at, f);
+                               static_cast<hipStream_t>(stream), c, first);
         const int e = static_cast<int>(hipGetLastError());
         if (e != 0) return e;
     }
@@ -1476,12 +1496,14 @@ int launch_mx_quantize(Dtype t, const void* X, int64_t rows, int d, int64_t ldx,
     KBIT_BY_DTYPE(launch_quantize_e, X, rows, d, ldx, c, stream)
 }
 
-int launch_mx_quantize_columns(Dtype t, const void* X, int64_t rows, int cols, int64_t ldx, const MxCoded& columns,
-                               const MxCoded& by_rows, float* sums, void* stream) {
-    int e = columns.codes ? clear_last_pair(columns, cols, mx_blocks(rows), stream) : 0;
-    if (e == 0 && by_rows.codes) e = clear_last_pair(by_rows, rows, mx_blocks(cols), stream);
-    if (e != 0) return e;
-    KBIT_BY_DTYPE(launch_columns_e, X, rows, cols, ldx, columns, by_rows, sums, stream)
+int launch_mx_quantize_columns(Dtype t, const MxColumns* jobs, int count, void* stream) {
+    for (int i = 0; i < count; ++i) {
+        const MxColumns& j = jobs[i];
+        int e = j.columns.codes ? clear_last_pair(j.columns, j.cols, mx_blocks(j.rows), stream) : 0;
+        if (e == 0 && j.by_rows.codes) e = clear_last_pair(j.by_rows, j.rows, mx_blocks(j.cols), stream);
+        if (e != 0) return e;
+    }
+    KBIT_BY_DTYPE(launch_columns_e, jobs, count, stream)
 }
 
 int launch_mx_add_sums(const float* sums, int64_t groups, int cols, float* out, void* stream) {
