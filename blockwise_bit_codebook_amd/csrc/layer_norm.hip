@@ -493,25 +493,31 @@ __global__ __launch_bounds__(kLongLanes) void layer_norm_back_long_kernel(const 
     }
 }
 
-// A column a thread, rows groups apart.
+// 8 columns a thread, rows groups apart.
 template <class E>
 __global__ __launch_bounds__(kThreads) void layer_norm_column_sums_kernel(const LayerNormBackArgs p,
                                                                           const float* __restrict__ stats,
                                                                           float* __restrict__ partial) {
     using T = typename E::T;
-    const int c = blockIdx.x * kThreads + threadIdx.x;
+    static_assert(kLayerNormColumns == 8 * kThreads, "the groups count workgroups of so many columns");
+    const int c = (blockIdx.x * kThreads + threadIdx.x) * 8;
     if (c >= p.d) return;
-    float dw = 0.0f, db = 0.0f;
+    float dw[8] = {}, db[8] = {};
     for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
-        const float x = E::one(static_cast<const T*>(p.x)[row * p.ldx + c]);
-        const float g = E::one(static_cast<const T*>(p.g)[row * p.ldg + c]);
+        float x[8], g[8];
+        load8_any<E>(static_cast<const T*>(p.x) + row * p.ldx, c, p.d, x);
+        load8_any<E>(static_cast<const T*>(p.g) + row * p.ldg, c, p.d, g);
         const float* of = stats + row * kLayerNormStats;
-        dw = fmaf(g, fmaf(x - of[0], of[1], of[2]), dw);
-        db += g;
+        const float m0 = of[0], r = of[1], shift = of[2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            dw[e] = fmaf(g[e], fmaf(x[e] - m0, r, shift), dw[e]);
+            db[e] += g[e];
+        }
     }
     float* to = partial + static_cast<int64_t>(blockIdx.y) * 2 * p.d;
-    to[c] = dw;
-    to[p.d + c] = db;
+    store8<QF32>(to, c, p.d, dw);
+    store8<QF32>(to + p.d, c, p.d, db);
 }
 
 // Adds the partial rows: 32 columns a workgroup, each half wave a run of the
@@ -611,7 +617,7 @@ int launch_back_e(const LayerNormBackArgs& p, void* stream) {
     } else if (p.d <= kLayerNormKept) {
         e = launch_back<E, 8, 1, 4>(p, &groups, stream);
     } else {
-        groups = static_cast<int>(p.rows < kLayerNormPartials ? p.rows : kLayerNormPartials);
+        groups = static_cast<int>(layer_norm_groups(p.rows, p.d));
         float* stats = p.workspace + static_cast<int64_t>(groups) * 2 * p.d;
         // all rows, kMost a launch, in one kernel or the other
         const auto rows = [&](auto kernel) {
@@ -629,7 +635,7 @@ int launch_back_e(const LayerNormBackArgs& p, void* stream) {
         };
         rows(layer_norm_back_long_stats_kernel<E>);
         if (e != 0) return e;
-        hipLaunchKernelGGL((layer_norm_column_sums_kernel<E>), dim3((p.d + kThreads - 1) / kThreads, groups), dim3(kThreads),
+        hipLaunchKernelGGL((layer_norm_column_sums_kernel<E>), dim3((p.d + kLayerNormColumns - 1) / kLayerNormColumns, groups), dim3(kThreads),
                            0, static_cast<hipStream_t>(stream), p, stats, p.workspace);
         e = static_cast<int>(hipGetLastError());
         rows(layer_norm_back_long_kernel<E>);

@@ -161,9 +161,18 @@ constexpr int kLayerNormPartials = 512;
 constexpr int kLayerNormKept = 16384;
 constexpr int kLayerNormStats = 8;  // floats a row
 
+// Rows of partial sums: of long rows, whose columns fill the device by
+// themselves, as many as keep 2048 workgroups of kLayerNormColumns at work.
+constexpr int kLayerNormColumns = 2048;
+inline int64_t layer_norm_groups(int64_t rows, int d) {
+    int64_t most = kLayerNormPartials;
+    if (d > kLayerNormKept) most = 2048 / ((d + kLayerNormColumns - 1) / kLayerNormColumns);
+    if (most < 1) most = 1;
+    return rows < most ? rows : most;
+}
+
 inline int64_t layer_norm_backward_bytes(int64_t rows, int d) {
-    const int64_t groups = rows < kLayerNormPartials ? rows : kLayerNormPartials;
-    return 4 * (groups * 2 * d + (d > kLayerNormKept ? kLayerNormStats * rows : 0));
+    return 4 * (layer_norm_groups(rows, d) * 2 * d + (d > kLayerNormKept ? kLayerNormStats * rows : 0));
 }
 
 struct LayerNormBackArgs {
