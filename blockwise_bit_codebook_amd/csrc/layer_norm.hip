@@ -185,7 +185,9 @@ __device__ __forceinline__ Stats stats_of(float sum1, float sum2, float inv_d, f
 // forward
 // ---------------------------------------------------------------------------
 // WAVES waves a row, 4 / WAVES rows a workgroup of at least four waves; P
-// pieces a thread.
+// pieces a thread.  Memory bounds it: 8192 x 4096 bf16 30 us (4.5 TB/s; a copy
+// of that size runs at 5.2), 8192 x 1024 8.9, 2048 x 16384 31; 16 x 4096 4.4 us is the
+// launch and two sums over a row.
 template <class E, int WAVES, int P, bool TINY>
 __global__ __launch_bounds__((WAVES < 4 ? 4 : WAVES) * kWave) void layer_norm_kernel(const LayerNormArgs p, bool streamed) {
     using T = typename E::T;
@@ -293,7 +295,10 @@ __global__ __launch_bounds__(kLongLanes) void layer_norm_long_kernel(const Layer
 // A workgroup takes ROWS rows at a time, WAVES waves each, and keeps the sums of
 // the weights' gradients in registers; at the end they are one row of the
 // workspace.  Two sums a row: its mean, then with c = x - m0 those of c, c^2, h
-// and h c, from which mean(h xh) = r (sum(h c) - m1 sum(h)) / d.
+// and h c, from which mean(h xh) = r (sum(h c) - m1 sum(h)) / d.  The next row
+// is on its way while one is summed.  8192 x 4096 bf16 41 us and 4 for the sums
+// of 512 workgroups (4.4 TB/s together); shorter rows wait for the two sums of each
+// row in turn: 8192 x 1024 22.6 us (2.2 TB/s).  256, 768 and 1024 workgroups were slower.
 template <class E, int WAVES, int ROWS, int P, bool TINY>
 __global__ __launch_bounds__(WAVES* ROWS* kWave) void layer_norm_back_kernel(const LayerNormBackArgs p,
                                                                              float* __restrict__ partial, bool streamed) {
@@ -435,7 +440,7 @@ __global__ __launch_bounds__(WAVES* ROWS* kWave) void layer_norm_back_kernel(con
 }
 
 // Long rows: their statistics, then the sums over rows, and dx last, which may
-// overwrite dout.
+// overwrite dout.  Three readings: 512 x 70000 bf16 126 us, 2048 x 20000 138.
 template <class E>
 __global__ __launch_bounds__(kLongLanes) void layer_norm_back_long_stats_kernel(const LayerNormBackArgs p,
                                                                                 float* __restrict__ stats) {
@@ -568,12 +573,18 @@ int launch_forward_e(const LayerNormArgs& whole, void* stream) {
         p.out = static_cast<T*>(p.out) + r * p.ldo;
         p.rows = whole.rows - r < kMost ? whole.rows - r : kMost;
         int e;
+        // As few waves a row as hold it in a few pieces a thread: 3001 x 777 fp16 4.9 us in
+        // one wave of two pieces, 5.7 in one of four; 8192 x 1024 8.9 in one, 12.1 in four
+        // waves; 8192 x 2048 16.6 in four, 17.5 in one; 8192 x 4096 30.0 in four, 30.5 in
+        // eight; 2048 x 8192 19.4 in four, 19.9 in sixteen.
         if (p.d < 8) {
             e = launch_forward<E, 1, 1, true>(p, stream);
         } else if (p.d <= 512) {
             e = launch_forward<E, 1, 1>(p, stream);
+        } else if (p.d <= 1024) {
+            e = launch_forward<E, 1, 2>(p, stream);
         } else if (p.d <= 2048) {
-            e = p.rows >= 4 * device_cu_count() ? launch_forward<E, 1, 4>(p, stream) : launch_forward<E, 4, 1>(p, stream);
+            e = launch_forward<E, 4, 1>(p, stream);
         } else if (p.d <= 4096) {
             e = launch_forward<E, 4, 2>(p, stream);
         } else if (p.d <= 16384) {
@@ -604,6 +615,10 @@ int launch_back_e(const LayerNormBackArgs& p, void* stream) {
     int groups = 0, e = 0;
     if (p.rows == 0) {
         // the sum of no rows: groups = 0 below
+    // One piece a thread up to 8192: 8192 x 1024 bf16 22.7 us with two rows of four
+    // waves, 34.5 with one row of eight; 8192 x 4096 45.7 with a row of eight waves, 48.4
+    // with two of four and two pieces; 2048 x 8192 36.6 and 36.7.  Above, four pieces in
+    // eight waves: two in sixteen do not fit the registers.
     } else if (p.d < 8) {
         e = launch_back<E, 1, 4, 1, true>(p, &groups, stream);
     } else if (p.d <= 512) {
