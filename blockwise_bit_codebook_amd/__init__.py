@@ -11,9 +11,10 @@ Entry points carry the C names (``quantize_kbit_bf16_k4``,
 few dtype/K-dispatching conveniences (``quantize_kbit``, ``dequantize_kbit``,
 ``dequantize_4bit_nested``, ``quantize_act_fwht_k4_bf16``).  The operators
 around a quantized layer (int8 linear, rotary positions, head norms, paged
-cache; C ABI in ``include/kbit_layer.h``) are in ``layer.py`` and reached from
-here as well.  The block scales
-are fp32 absmax values or, with ``absmax_format="e4m4"``, one E4M4 byte per
+cache; C ABI in ``include/kbit_layer.h``) are in ``layer.py``, the microscaled
+4-bit linear layers with their gradients and the layer norm
+(``include/kbit_mx.h``) in ``mx.py``; both are reached from here as well.  The
+block scales are fp32 absmax values or, with ``absmax_format="e4m4"``, one E4M4 byte per
 block (uint8 tensor).
 """
 
