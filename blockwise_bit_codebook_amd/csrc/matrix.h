@@ -109,10 +109,12 @@ __device__ __forceinline__ void store8(typename E::T* row, int c, int d, const f
 }
 
 // A barrier that waits for the wave's LDS accesses but not for its loads, as
-// __syncthreads would.  The fences emit nothing and hold the compiler to the order.
+// __syncthreads would.  The fences emit nothing and hold the compiler to the order:
+// the wait counts as touching no memory, so that without the one before it an
+// access might come to stand between wait and barrier.
 __device__ __forceinline__ void barrier_in_flight() {
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
