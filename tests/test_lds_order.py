@@ -28,3 +28,32 @@ def test_a_barrier_that_leaves_loads_in_flight():
     # accesses before it are done: fence, wait, barrier; those after it come after the second fence
     assert statements(body("matrix.h", "barrier_in_flight")) == [
         FENCE, "__builtin_amdgcn_s_waitcnt(0xC07F);", "__builtin_amdgcn_s_barrier();", FENCE]
+
+
+def test_what_states_the_order_within_a_wave():
+    assert statements(body("mxfp4.hip", "wave_order")) == [FENCE, "__builtin_amdgcn_wave_barrier();"]
+
+
+def test_partial_steps_of_few_rows_and_tokens():
+    for name, read in (("mx_few_rows_kernel", "read(e);"), ("mx_tokens_kernel", "read(e, steps);")):
+        text = body("mxfp4.hip", name)
+        at = text.index(read)
+        assert text[:at].rstrip().endswith("wave_order();"), name         # pieces stored, then read by other lanes
+        sums = text.index("sum_place(l16, q, TN * q + j)")
+        assert "wave_order();" in text[at:sums], name                      # operands read, then gone over by the sums
+
+
+def test_tiles_leave_through_a_region_of_the_wave():
+    text = body("mxfp4.hip", "store_tile")
+    stored, read = text.index("= d;"), text.index("if (packed)")
+    assert "wave_order();" in text[stored:read]
+    assert re.search(r"if \(i0 \+ kPass < TM\) wave_order\(\);", text[read:])
+
+
+def test_the_ring_waits_before_its_barriers():
+    # a step's operands have arrived, its predecessor's have been read: both before the next loads are issued
+    text = body("mxfp4.hip", "mx_ring_kernel")
+    waits = re.findall(r"landed<[^;]*>\(\);\s*(\w+)\(\);", text)
+    assert waits == ["barrier_in_flight", "barrier_in_flight"]
+    step = text[text.index("auto step ="):]
+    assert step.index("landed<") < step.index("barrier_in_flight") < step.index("put_scales(") < step.index("fetch_one(n, f, now)")
