@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <numeric>
 #include <sstream>
 #include <string>
 #include <utility>
@@ -164,8 +165,9 @@ bool reaches(int64_t v, const Axis* a, int n, int64_t low, int64_t high, bool mo
 }
 
 // Whether a row of x and a row of y, whose first elements are `apart` elements
-// apart, have an element in common; with `self` two different rows of x.
-bool rows_meet(const Rows& x, const Rows& y, int64_t apart, bool self) {
+// apart, have an element in common; with `self` two different rows of x.  `unsure`:
+// what a layout gives that the search does not get through.
+bool rows_meet(const Rows& x, const Rows& y, int64_t apart, bool self, bool unsure = false) {
     if (apart + y.last + y.length <= 0 || apart >= x.last + x.length) return false;
     Axis axes[6];
     int n = 0;
@@ -178,13 +180,20 @@ bool rows_meet(const Rows& x, const Rows& y, int64_t apart, bool self) {
             axes[n++] = Axis{sy, 0, y.size[i] - 1, 0, 0};
         }
     }
+    // every step moves by a multiple of what the strides share
+    int64_t g = 0;
+    for (int i = 0; i < n; ++i) g = std::gcd(g, axes[i].stride);
+    if (g > 0) {
+        const int64_t first = ((apart + y.length - 1) % g + g) % g;  // how far the least such distance is above -y.length + 1
+        if (first >= x.length + y.length - 1) return false;
+    }
     std::sort(axes, axes + n, [](const Axis& a, const Axis& b) { return a.stride > b.stride; });
     for (int i = n - 1; i > 0; --i) {
         axes[i - 1].down = axes[i].down + axes[i].lo * axes[i].stride;
         axes[i - 1].up = axes[i].up + axes[i].hi * axes[i].stride;
     }
     int budget = 4096;
-    return reaches(apart, axes, n, -y.length, x.length, !self, budget);
+    return reaches(apart, axes, n, -y.length, x.length, !self, budget) || (unsure && budget < 0);
 }
 
 // Refuses an output two rows of which share elements.

@@ -9,17 +9,23 @@ namespace {
 
 constexpr at::ScalarType kByte = at::kByte;
 
-// Refuses an output that shares bytes with a tensor of another type.
+// A tensor's rows in bytes; a contiguous one, of any shape, is one row.
+Rows byte_rows(const Tensor& t) {
+    const int64_t size = static_cast<int64_t>(t.element_size());
+    if (t.is_contiguous()) return Rows{{1, 1, 1}, {0, 0, 0}, t.numel() * size, 0};
+    Rows r = rows_in(t);
+    for (int64_t& s : r.stride) s *= size;
+    r.length *= size;
+    r.last *= size;
+    return r;
+}
+
+// Refuses an output that shares bytes with a tensor of another type; rows that
+// lie between each other's are apart.
 void apart(const Tensor& out, const char* what, const Tensor& other, const char* name) {
     if (!out.is_alias_of(other) || out.numel() == 0 || other.numel() == 0) return;
-    const auto span = [](const Tensor& t) {
-        int64_t last = 0;
-        for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
-        const char* p = static_cast<const char*>(t.data_ptr());
-        return std::pair<const char*, const char*>(p, p + (last + 1) * static_cast<int64_t>(t.element_size()));
-    };
-    const auto a = span(out), b = span(other);
-    if (a.first < b.second && b.first < a.second) value_error(cat(what, " overlaps ", name));
+    const int64_t bytes = static_cast<char*>(other.data_ptr()) - static_cast<char*>(out.data_ptr());
+    if (rows_meet(byte_rows(out), byte_rows(other), bytes, false, true)) value_error(cat(what, " overlaps ", name));
 }
 
 // Codes and scales of rows of d values.
@@ -74,8 +80,11 @@ PyObject* quantize(PyObject* const* a) {  // X, codes, scales
     const Tensor scales = a[2] == Py_None ? at::empty({rows, blocks}, X.options().dtype(kByte)) : tensor(a[2], "scales");
     const Coded c = coded(codes, "codes", scales, "scales", d, X);
     if (c.rows != rows) value_error(cat("codes: ", c.rows, " rows, X has ", rows));
-    apart(codes, "codes", X, "X");
-    apart(scales, "scales", X, "X");
+    if (codes.is_alias_of(X) || scales.is_alias_of(X)) {
+        const Tensor lines = by_rows ? X : X.t();  // what is contiguous of X as rows
+        apart(codes, "codes", lines, "X");
+        apart(scales, "scales", lines, "X");
+    }
     no_overlap(codes, "codes", scales, "scales", false);
     if (by_rows) {
         KBIT_BY_TYPE(X.scalar_type(), quantize_mxfp4, run("quantize_mxfp4", X, {&codes, &scales}, [&](void* stream) {
