@@ -28,6 +28,23 @@ void apart(const Tensor& out, const char* what, const Tensor& other, const char*
     if (rows_meet(byte_rows(out), byte_rows(other), bytes, false, true)) value_error(cat(what, " overlaps ", name));
 }
 
+// Refuses a given workspace whose first `used` bytes, which are all that the call
+// writes of it, are shared with one of the call's tensors.
+struct Named {
+    const Tensor& t;
+    const char* name;
+};
+void clear_of(const Space& ws, PyObject* given, int64_t used, std::initializer_list<Named> tensors) {
+    if (given == Py_None || used <= 0) return;
+    const Rows space{{1, 1, 1}, {0, 0, 0}, used, 0};
+    for (const auto& [t, name] : tensors) {
+        if (!t.defined() || t.numel() == 0 || !t.is_alias_of(THPVariable_Unpack(given))) continue;
+        const int64_t bytes = static_cast<char*>(t.data_ptr()) - static_cast<char*>(ws.p);
+        if (rows_meet(space, byte_rows(t), bytes, false, true)) value_error(cat("the workspace overlaps ", name));
+    }
+}
+Tensor or_none(PyObject* o) { return o == Py_None ? Tensor() : THPVariable_Unpack(o); }
+
 // Codes and scales of rows of d values.
 struct Coded {
     uint8_t *codes, *scales;
@@ -189,8 +206,10 @@ PyObject* linear(PyObject* const* a) {  // codes, scales, w_codes, w_scales, bia
     apart(w.out.t, "out", x, "codes");
     apart(w.out.t, "out", xs, "scales");
     const int64_t need = linear_mxfp4_workspace_bytes(c.rows, w.N, K);
-    const Space ws = workspace(need, need > 0 ? kbit::mx_product_workspace(c.rows, w.N, kbit::mx_depth(K)) : 0, a[7],
-                               "linear_mxfp4", x);
+    const int64_t take = need > 0 ? kbit::mx_product_workspace(c.rows, w.N, kbit::mx_depth(K)) : 0;
+    const Space ws = workspace(need, take, a[7], "linear_mxfp4", x);
+    clear_of(ws, a[7], take, {{x, "codes"}, {xs, "scales"}, {THPVariable_Unpack(a[2]), "w_codes"},
+                              {THPVariable_Unpack(a[3]), "w_scales"}, {or_none(a[4]), "bias"}, {w.out.t, "out"}});
     KBIT_BY_TYPE(type, linear_mxfp4, run("linear_mxfp4", x, {&w.out.t}, [&](void* stream) {
         return fn(c.codes, c.scales, c.rows, K, c.ldc, c.lds, w.c.codes, w.c.scales, w.N, w.c.ldc, w.c.lds,
                   static_cast<const T*>(w.bias), static_cast<T*>(w.out.t.data_ptr()), w.out.ld, ws.p, ws.bytes, stream);
@@ -213,6 +232,8 @@ PyObject* linear_dynamic(PyObject* const* a) {  // X, w_codes, w_scales, bias, o
                                          kbit::mx_product_workspace(M, w.N, kbit::mx_depth(K),
                                                                     kbit::mx_paired(M, w.N, kbit::mx_depth(K)));
     const Space ws = workspace(need, take, a[5], "linear_mxfp4_dynamic", x);
+    clear_of(ws, a[5], take, {{x, "X"}, {THPVariable_Unpack(a[1]), "w_codes"}, {THPVariable_Unpack(a[2]), "w_scales"},
+                              {or_none(a[3]), "bias"}, {w.out.t, "out"}});
     KBIT_BY_TYPE(type, linear_mxfp4_dynamic, run("linear_mxfp4_dynamic", x, {&w.out.t}, [&](void* stream) {
         return fn(static_cast<const T*>(x.data_ptr()), M, K, ldx, w.c.codes, w.c.scales, w.N, w.c.ldc, w.c.lds,
                   static_cast<const T*>(w.bias), static_cast<T*>(w.out.t.data_ptr()), w.out.ld, ws.p, ws.bytes, stream);
@@ -264,6 +285,7 @@ PyObject* linear_backward(PyObject* const* a) {
         const int64_t need = linear_mxfp4_backward_workspace_bytes(M, N, K);
         const int64_t take = need < 0 ? need : kbit::mx_back_workspace(M, N, K, input, weights);
         ws = workspace(need, take, a[8], "linear_mxfp4_backward", g);
+        clear_of(ws, a[8], take, {{g, "dout"}, {x, "X"}, {w, "weight"}, {dx.t, "dX"}, {dw.t, "dweight"}});
     }
     const auto ptr = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
     KBIT_BY_TYPE(type, linear_mxfp4_backward, run("linear_mxfp4_backward", g, {}, [&](void* stream) {
@@ -346,6 +368,7 @@ PyObject* layer_norm_backward(PyObject* const* a) {  // dout, x, weight, eps, dx
     const Tensor dw = at::empty({d}, x.options().dtype(at::kFloat)), db = at::empty_like(dw);
     const int64_t need = layer_norm_backward_workspace_bytes(rows, d);
     const Space ws = workspace(need, need, a[5], "layer_norm_backward", x);
+    clear_of(ws, a[5], need, {{g, "dout"}, {x, "x"}, {THPVariable_Unpack(a[2]), "weight"}, {dx.t, "dx"}});
     KBIT_BY_TYPE(type, layer_norm_backward, run("layer_norm_backward", x, {&dx.t}, [&](void* stream) {
         return fn(static_cast<const T*>(g.data_ptr()), ldg, static_cast<const T*>(x.data_ptr()), ldx, rows, d, n.weight,
                   n.fp32, eps, static_cast<T*>(dx.t.data_ptr()), dx.ld, static_cast<float*>(dw.data_ptr()),

@@ -6,7 +6,8 @@ the C entry points (``include/kbit_mx.h``) are in ``_layer``
 (``csrc/mx_bind.cpp``).  What ``layer.py`` says of its operators holds here:
 calls run on torch's current stream of the inputs' device; rows may be
 strided, their elements have to be contiguous; outputs that overlap themselves
-or an operand are refused where not said otherwise; nothing is recorded for
+or an operand are refused where not said otherwise, and so is a workspace that
+shares what a call uses of it with the call's tensors; nothing is recorded for
 autograd, gradients are calls of their own, an argument that requires one
 gives a UserWarning, and given outputs count as modified in place.
 

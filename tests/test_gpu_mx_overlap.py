@@ -159,3 +159,52 @@ def test_thousands_of_rows_at_two_distances():
     codes = b.view(T.uint8, 3000, 32, 128, 496)  # 16 bytes nearer from row to row: the second one meets the third of x
     bad("codes overlaps X", kb.quantize_mxfp4, x[:3000], codes, scales)
     same([scales], want[1:], "left alone")
+
+
+def test_workspaces_that_hold_a_tensor_of_the_call():
+    T, lib = torch(), kb.lib()
+    rows, n, k = 300, 256, 2048
+    t = T.bfloat16
+    x, g, w = (filled(T.empty(s, device=dev(), dtype=t), i) for i, s in enumerate(((rows, k), (rows, n), (n, k))))
+    wq, xq = kb.quantize_mxfp4(w), kb.quantize_mxfp4(x)
+    bias, out = T.zeros(n, device=dev(), dtype=t), T.empty(rows, n, device=dev(), dtype=t)
+    space = T.full((16 << 20,), 0xFF, dtype=T.uint8, device=dev())
+
+    def inside(v, at):  # a copy of v in the workspace's bytes
+        held = space[at:at + v.numel() * v.element_size()].view(v.dtype).view(v.shape)
+        return held.copy_(v)
+    case("mx overlap: workspaces")
+    # the values' codes are the first thing there
+    need = lib.linear_mxfp4_dynamic_workspace_bytes(rows, n, k)
+    want = kb.linear_mxfp4_dynamic(x, *wq, bias=bias)
+    for name, kw in (("X", dict(x=inside(x, 0))), ("w_codes", dict(c=inside(wq[0], 16))), ("w_scales", dict(s=inside(wq[1], 3))),
+                     ("bias", dict(bias=inside(bias, 2))), ("out", dict(out=inside(out, 64)))):
+        a = dict(dict(x=x, c=wq[0], s=wq[1], bias=bias, out=out), **kw)
+        bad(f"workspace overlaps {name}", kb.linear_mxfp4_dynamic, a["x"], a["c"], a["s"], bias=a["bias"], out=a["out"], workspace=space)
+    same([kb.linear_mxfp4_dynamic(inside(x, need), inside(wq[0], 8 << 20), wq[1], bias=bias, workspace=space)], [want], "behind its use")
+    few = kb.linear_mxfp4_dynamic(inside(x[:4], 0), *wq, workspace=space)  # nothing of it is used
+    same([few], [kb.linear_mxfp4_dynamic(x[:4], *wq)], "tokens")
+    # gradients
+    need = lib.linear_mxfp4_backward_workspace_bytes(rows, n, k)
+    want = kb.linear_mxfp4_backward(g, x, w)
+    for name, kw in (("dout", dict(g=inside(g, 0))), ("X", dict(x=inside(x, 2))), ("weight", dict(w=inside(w, 16)))):
+        a = dict(dict(g=g, x=x, w=w), **kw)
+        bad(f"workspace overlaps {name}", kb.linear_mxfp4_backward, a["g"], a["x"], a["w"], workspace=space)
+    bad("workspace overlaps dX", kb.linear_mxfp4_backward, g, x, w, dX=inside(x, 0), workspace=space)
+    bad("workspace overlaps dweight", kb.linear_mxfp4_backward, g, x, w, dweight=inside(w.float(), 0), workspace=space)
+    assert need + x.numel() * 2 + w.numel() * 4 < space.numel()
+    got = kb.linear_mxfp4_backward(g, inside(x, need), w, dweight=inside(w.float(), need + x.numel() * 2), workspace=space)
+    same(got, want, "behind its use")
+    # norm
+    nw = T.ones(k, device=dev())
+    for name, kw in (("dout", dict(g=inside(x, 0))), ("x", dict(x=inside(x, 0))), ("weight", dict(w=inside(nw, 4)))):
+        a = dict(dict(g=x.clone(), x=x, w=nw), **kw)
+        bad(f"workspace overlaps {name}", kb.layer_norm_backward, a["g"], a["x"], a["w"], workspace=space)
+    bad("workspace overlaps dx", kb.layer_norm_backward, x.clone(), x, nw, dx=inside(x, 0), workspace=space)
+    # sums of parts of the depth
+    a, w = T.zeros(1005, 8112, dtype=T.uint8, device=dev()), T.zeros(1301, 8112, dtype=T.uint8, device=dev())
+    sa, sw = T.zeros(1005, 507, dtype=T.uint8, device=dev()), T.zeros(1301, 507, dtype=T.uint8, device=dev())
+    space = T.empty(lib.linear_mxfp4_workspace_bytes(1005, 1301, 16224), dtype=T.uint8, device=dev())
+    for name, args in (("codes", (inside(a, 0), sa, w, sw)), ("scales", (a, inside(sa, 0), w, sw)), ("w_codes", (a, sa, inside(w, 0), sw)),
+                       ("w_scales", (a, sa, w, inside(sw, 0)))):
+        bad(f"workspace overlaps {name}", kb.linear_mxfp4, *args, workspace=space)
