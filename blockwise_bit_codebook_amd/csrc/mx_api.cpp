@@ -141,8 +141,9 @@ int do_linear_backward(Dtype t, const void* g, int64_t ldg, const void* X, int64
     if (!aligned(g, es) || !aligned(X, es) || !aligned(W, es) || !aligned(dX, es) || !aligned(dW, 4) || !aligned(db, 4) ||
         !aligned(workspace, 16))
         return KBIT_EALIGN;
-    const MxBackParts b = mx_back_parts(M, N, K);
-    if (M > 0 && (!workspace || workspace_bytes < mx_back_workspace(M, N, K, dX != nullptr, dW != nullptr))) return KBIT_EINVAL;
+    const MxBackParts b = mx_back_parts(M, N, K, dX != nullptr, dW != nullptr, db != nullptr);
+    if (M > 0 && (!workspace || workspace_bytes < mx_back_workspace(M, N, K, dX != nullptr, dW != nullptr, db != nullptr)))
+        return KBIT_EINVAL;
     // the operands' rows in the workspace, as the products need them
     if (M > 0 && ((dX && (!near_rows(M, b.g_rows.ldc) || !near_rows(K, b.w_cols.ldc))) ||
                   (dW && (!near_rows(N, b.g_cols.ldc) || !near_rows(K, b.x_cols.ldc)))))
@@ -230,7 +231,7 @@ int64_t linear_mxfp4_backward_workspace_bytes(int64_t M, int32_t N, int32_t K) {
     if (M == 0) return 0;
     const int64_t a = kbit::mx_product_workspace_up_to(M, K, kbit::mx_depth(N));
     const int64_t b = kbit::mx_product_workspace_up_to(N, K, kbit::mx_depth(M));
-    return kbit::mx_back_parts(M, N, K).product_at + (a > b ? a : b);
+    return kbit::mx_back_parts(M, N, K, true, true, true).product_at + (a > b ? a : b);
 }
 
 int64_t layer_norm_backward_workspace_bytes(int64_t rows, int32_t d) {

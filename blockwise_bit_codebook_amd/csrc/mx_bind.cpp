@@ -283,7 +283,7 @@ PyObject* linear_backward(PyObject* const* a) {
     Space ws;
     if (M > 0) {
         const int64_t need = linear_mxfp4_backward_workspace_bytes(M, N, K);
-        const int64_t take = need < 0 ? need : kbit::mx_back_workspace(M, N, K, input, weights);
+        const int64_t take = need < 0 ? need : kbit::mx_back_workspace(M, N, K, input, weights, bias);
         ws = workspace(need, take, a[8], "linear_mxfp4_backward", g);
         clear_of(ws, a[8], take, {{g, "dout"}, {x, "X"}, {w, "weight"}, {dx.t, "dX"}, {dw.t, "dweight"}});
     }

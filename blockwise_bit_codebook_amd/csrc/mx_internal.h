@@ -101,29 +101,30 @@ inline MxRows mx_rows(int64_t rows, int64_t d) {
 // Bytes of a row of codes.
 inline int mx_depth(int64_t d) { return static_cast<int>(mx_blocks(d) * kMxBlockBytes); }
 
-// Workspace of the backward pass: dout and W along N, dout and X along M, the
-// partial sums of the bias gradient, the products' own.
+// Workspace of the backward pass, of the gradients that are wanted: for dX dout's
+// rows and W's columns (along N), for dW dout's and X's columns (along M), for db
+// the partial sums; then the products' own.
 struct MxBackParts {
     MxRows g_rows, w_cols, g_cols, x_cols;
     int64_t w_at, gc_at, x_at, sums_at, product_at;
 };
-inline MxBackParts mx_back_parts(int64_t M, int N, int K) {
-    MxBackParts b;
-    b.g_rows = mx_rows(M, N);
-    b.w_cols = mx_rows(K, N);
-    b.g_cols = mx_rows(N, M);
-    b.x_cols = mx_rows(K, M);
+inline MxBackParts mx_back_parts(int64_t M, int N, int K, bool dX, bool dW, bool db) {
+    MxBackParts b{};
+    if (dX) b.g_rows = mx_rows(M, N);
+    if (dX) b.w_cols = mx_rows(K, N);
+    if (dW) b.g_cols = mx_rows(N, M);
+    if (dW) b.x_cols = mx_rows(K, M);
     const auto up = [](int64_t n) { return (n + kDepth - 1) / kDepth * kDepth; };
     b.w_at = up(b.g_rows.bytes);
     b.gc_at = b.w_at + up(b.w_cols.bytes);
     b.x_at = b.gc_at + up(b.g_cols.bytes);
     b.sums_at = b.x_at + up(b.x_cols.bytes);
-    b.product_at = b.sums_at + up(4 * mx_sum_groups(M) * N);
+    b.product_at = b.sums_at + (db ? up(4 * mx_sum_groups(M) * N) : 0);
     return b;
 }
 
 // Bytes of it that a call needs.
-inline int64_t mx_back_workspace(int64_t M, int N, int K, bool dX, bool dW) {
+inline int64_t mx_back_workspace(int64_t M, int N, int K, bool dX, bool dW, bool db) {
     int64_t own = 0;
     for (const auto& [rows, depth, wanted] : {std::make_tuple(M, mx_depth(N), dX), std::make_tuple(int64_t(N), mx_depth(M), dW)}) {
         if (!wanted) continue;
@@ -131,7 +132,7 @@ inline int64_t mx_back_workspace(int64_t M, int N, int K, bool dX, bool dW) {
         const int64_t need = mx_product_workspace(rows, K, depth, paired, paired);
         if (need > own) own = need;
     }
-    return mx_back_parts(M, N, K).product_at + own;
+    return mx_back_parts(M, N, K, dX, dW, db).product_at + own;
 }
 
 // p.x and p.xs are not looked at.

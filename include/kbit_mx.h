@@ -94,7 +94,8 @@ int linear_mxfp4_dynamic_fused(int64_t M, int32_t N, int32_t K, int64_t ldw, int
  * may be null and is not computed then; W is read for dX only, X for dW only
  * (null otherwise).  Sums are in a fixed order.  M = 0 gives zeros for dW and db.
  * workspace: linear_mxfp4_backward_workspace_bytes(M, N, K) bytes (not falling
- * with M), 16-byte aligned. */
+ * with M), 16-byte aligned, serve every choice of gradients; a call looks for no
+ * more than it uses. */
 #define KBIT_DECLARE_LINEAR_MXFP4_BACKWARD(T, CTYPE)                                                           \
     int linear_mxfp4_backward_##T(const CTYPE* dout, int64_t lddo, const CTYPE* X, int64_t ldx, const CTYPE* W,  \
                                   int64_t ldw, int64_t M, int32_t N, int32_t K, CTYPE* dX, int64_t lddx,         \
