@@ -200,7 +200,13 @@ int do_layer_norm_backward(Dtype t, const LayerNormBackArgs& p, int64_t workspac
     return map_launch(launch_layer_norm_back(t, p, stream));
 }
 
-bool product_sizes_ok(int64_t M, int32_t N, int32_t K) { return M >= 0 && M <= kMaxRows && N >= 1 && depth_ok(K); }
+// Sizes for which there is a product: several rows have to be in the kernels'
+// reach at the least distance that they can have, `row` and a weight's own row.
+bool product_sizes_ok(int64_t M, int32_t N, int32_t K, int64_t row) {
+    return M >= 0 && M <= kMaxRows && N >= 1 && depth_ok(K) && near_rows(M, row) && near_rows(N, mx_depth(K));
+}
+bool codes_sizes_ok(int64_t M, int32_t N, int32_t K) { return product_sizes_ok(M, N, K, mx_depth(K)); }
+bool values_sizes_ok(int64_t M, int32_t N, int32_t K) { return product_sizes_ok(M, N, K, mx_rows(1, K).ldc); }
 
 }  // namespace
 }  // namespace kbit
@@ -213,17 +219,17 @@ using kbit::MxProduct;
 extern "C" {
 
 int64_t linear_mxfp4_workspace_bytes(int64_t M, int32_t N, int32_t K) {
-    if (!kbit::product_sizes_ok(M, N, K)) return -1;
+    if (!kbit::codes_sizes_ok(M, N, K)) return -1;
     return kbit::mx_product_workspace_up_to(M, N, kbit::mx_depth(K));
 }
 
 int64_t linear_mxfp4_dynamic_workspace_bytes(int64_t M, int32_t N, int32_t K) {
-    if (!kbit::product_sizes_ok(M, N, K)) return -1;
+    if (!kbit::values_sizes_ok(M, N, K)) return -1;
     return (kbit::mx_rows(M, K).bytes + 15) / 16 * 16 + kbit::mx_product_workspace_up_to(M, N, kbit::mx_depth(K));
 }
 
 int linear_mxfp4_dynamic_fused(int64_t M, int32_t N, int32_t K, int64_t ldw, int64_t ldws) {
-    return M >= 1 && kbit::product_sizes_ok(M, N, K) && kbit::mx_tokens_fit(M, N, K, ldw, ldws);
+    return M >= 1 && kbit::values_sizes_ok(M, N, K) && kbit::mx_tokens_fit(M, N, K, ldw, ldws);
 }
 
 int64_t linear_mxfp4_backward_workspace_bytes(int64_t M, int32_t N, int32_t K) {

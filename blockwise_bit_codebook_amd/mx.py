@@ -64,7 +64,8 @@ def linear_mxfp4(codes, scales, w_codes, w_scales, bias=None, dtype=torch.bfloat
 
 def linear_mxfp4_dynamic(X, w_codes, w_scales, bias=None, out=None, workspace=None):
     """linear_mxfp4 of X [M, K] (fp32/fp16/bf16) quantized on the way, the output
-    in X's type; a few tokens in one launch.  workspace: as there, of
+    in X's type; a few tokens in one launch.  K is at most 2^23 - 256 for more than
+    one row.  workspace: as there, of
     ``lib().linear_mxfp4_dynamic_workspace_bytes(M, N, K)`` bytes."""
     return _layer.linear_mxfp4_dynamic(X, w_codes, w_scales, bias, out, workspace)
 
@@ -76,8 +77,9 @@ def linear_mxfp4_backward(dout, X, weight, input_grad=True, weight_grad=True, bi
     None for those that are not asked for.
 
     dX = dout @ weight and dweight = dout^T @ X with both operands quantized to
-    MXFP4 along the axis that is summed over (N, then M); dbias sums dout itself.
-    workspace: ``lib().linear_mxfp4_backward_workspace_bytes(M, N, K)`` bytes."""
+    MXFP4 along the axis that is summed over (N, then M, at most 2^23 - 256 of
+    either); dbias sums dout itself.  workspace:
+    ``lib().linear_mxfp4_backward_workspace_bytes(M, N, K)`` bytes."""
     return _layer.linear_mxfp4_backward(dout, X, weight, input_grad, weight_grad, bias_grad, dX, dweight, workspace)
 
 

@@ -66,14 +66,17 @@ extern "C" {
                          int64_t ldws, const CTYPE* bias, CTYPE* out, int64_t ldo, void* workspace,              \
                          int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace on the current device (-1 for arguments out of range).
- * It does not fall with M: one workspace for the largest batch serves every
- * smaller one. */
+/* Bytes of workspace on the current device; -1 for arguments out of range, and
+ * where several rows of x or w would be 2^22 bytes of codes and more, K about
+ * 2^23, apart.  It does not fall with M: one workspace for the largest batch
+ * serves every smaller one. */
 int64_t linear_mxfp4_workspace_bytes(int64_t M, int32_t N, int32_t K);
 
 /* quantize_mxfp4 of X, then linear_mxfp4: the same values as the two calls up
  * to the order of sums.  workspace: linear_mxfp4_dynamic_workspace_bytes(M, N, K)
- * bytes (not falling with M), 16-byte aligned.  A few tokens are quantized
+ * bytes (not falling with M; -1 as there), 16-byte aligned.  Several rows of X
+ * have at most 2^23 - 256 values: their codes stand in the workspace, in whole
+ * 128 bytes a row, less than 2^22 apart.  A few tokens are quantized
  * inside the product's kernel: where linear_mxfp4_dynamic_fused(M, N, K, ldw,
  * ldws) is 1 no workspace is needed and it may be null. */
 #define KBIT_DECLARE_LINEAR_MXFP4_DYNAMIC(T, CTYPE)                                                            \
@@ -93,6 +96,9 @@ int linear_mxfp4_dynamic_fused(int64_t M, int32_t N, int32_t K, int64_t ldw, int
  * where q quantizes that row or column in blocks of 32.  Each of dX, dW and db
  * may be null and is not computed then; W is read for dX only, X for dW only
  * (null otherwise).  Sums are in a fixed order.  M = 0 gives zeros for dW and db.
+ * M, N and K are at most 2^26, and what a product sums over, in several rows of
+ * codes in the workspace, at most 2^23 - 256: N for dX unless M = K = 1, M for dW
+ * unless N = K = 1.
  * workspace: linear_mxfp4_backward_workspace_bytes(M, N, K) bytes (not falling
  * with M), 16-byte aligned, serve every choice of gradients; a call looks for no
  * more than it uses. */
