@@ -793,9 +793,9 @@ __global__ __launch_bounds__(WAVES* kWave) void mx_tokens_kernel(const MxProduct
 // ---------------------------------------------------------------------------
 // Many rows: tiles through LDS.
 // ---------------------------------------------------------------------------
-// A workgroup of WM x WN waves takes a tile of 16 TM WM rows and 64 WN
-// channels, two steps of both operands in LDS: while the matrix cores work on
-// one, the loads of the next go into the other.
+// A workgroup of WM x WN waves takes a tile of 16 TM WM rows and 64 WN channels:
+// 256 x 256 with two steps of both operands in LDS (mx_large_kernel), the smaller
+// ones with a ring of two or four (mx_ring_kernel).
 template <class E>
 constexpr bool kSums = std::is_same<typename E::T, void>::value;  // the sums themselves, no bias
 
@@ -1330,6 +1330,14 @@ int launch_split(const MxProduct& p, int parts, void* workspace, void* stream) {
     return static_cast<int>(hipGetLastError());
 }
 
+// The waves that split the depth: up to eight whose operands do not fill the LDS
+// (another one that does took 8 x 16256 x 3968 from 12.8 to 13.9 us, 48 x 6272 x 3200
+// from 9.2 to 10.3, 7007 x 103 x 2304 from 8.4 to 8.9; two fewer 13.0, 9.7, 8.8), but
+// for the smallest pieces, several of which share a compute unit.  16 x 16, in 4 / 8 /
+// 16 waves with operands from memory: 6 x 1216 x 768 3.1 / 3.4 / 4.0 us, 16 x 4096 x 4096
+// 5.5 / 5.9 / 7.2, 16 x 1024 x 8192 6.8 / 6.9 / 8.1, 1 x 4096 x 8192 7.1 / 6.9 / 7.7, 16 x
+// 2048 x 16384 10.2 / 10.5 / 11.9, 8 x 1024 x 32768 15.0 / 14.3 / 16.1: 4 up to a depth of
+// 8192, beyond which the two are within 5% of each other.
 template <class E>
 int launch_few_tile(const MxProduct& p, Int8Few f, void* stream) {
     switch (10 * f.mt + f.tn) {
