@@ -277,10 +277,7 @@ __global__ __launch_bounds__(kThreads) void int8_generic_kernel(const Int8Produc
 // positions xor-ed with a key of the row, so that the 8 rows which a read
 // touches at a time lie in different banks (no conflicts counted), and each
 // lane fetches the piece that belongs at its position.
-//
-// The weight is the first matrix operand, so that lane l holds channels
-// 4 (l / 16) .. + 3 of row l % 16; channel 4 TN (i / 4) + 4 j + i % 4 sits in
-// row i of operand j, which makes a lane's 4 TN channels neighbours.
+
 // Between LDS accesses of one wave whose lanes read what other lanes wrote, or
 // write over what other lanes read, without a barrier: the hardware executes a
 // wave's LDS accesses in order, and this holds the compiler to it as well.  No
