@@ -234,7 +234,8 @@ __global__ __launch_bounds__((WAVES < 4 ? 4 : WAVES) * kWave) void layer_norm_ke
 }
 
 // Rows that no workgroup holds: read once for each of the three steps, a row a
-// workgroup of 16 waves.
+// workgroup of 16 waves.  512 x 70000 bf16 55 us, of which one reading and the
+// outputs would be 28.
 constexpr int kLongWaves = 16, kLongLanes = kLongWaves * kWave;
 
 template <class E>
@@ -576,7 +577,9 @@ int launch_forward_e(const LayerNormArgs& whole, void* stream) {
         // As few waves a row as hold it in a few pieces a thread: 3001 x 777 fp16 4.9 us in
         // one wave of two pieces, 5.7 in one of four; 8192 x 1024 8.9 in one, 12.1 in four
         // waves; 8192 x 2048 16.6 in four, 17.5 in one; 8192 x 4096 30.0 in four, 30.5 in
-        // eight; 2048 x 8192 19.4 in four, 19.9 in sixteen.
+        // eight; 2048 x 8192 19.4 in four, 19.9 in sixteen.  A width between the forms
+        // pays for the pieces of the next one: 8192 x 4097 72 us, 8192 x 5120 56, 2048 x 8193
+        // 25, 2048 x 12288 29; rows under 512 for a whole wave: 16384 x 64 6.4.
         if (p.d < 8) {
             e = launch_forward<E, 1, 1, true>(p, stream);
         } else if (p.d <= 512) {
@@ -618,7 +621,8 @@ int launch_back_e(const LayerNormBackArgs& p, void* stream) {
     // One piece a thread up to 8192: 8192 x 1024 bf16 22.7 us with two rows of four
     // waves, 34.5 with one row of eight; 8192 x 4096 45.7 with a row of eight waves, 48.4
     // with two of four and two pieces; 2048 x 8192 36.6 and 36.7.  Above, four pieces in
-    // eight waves: two in sixteen do not fit the registers.
+    // eight waves: two in sixteen do not fit the registers (2048 x 8193 63, 2048 x 12288 62,
+    // 2048 x 16384 75).  Between the forms 8192 x 5120 takes 80.
     } else if (p.d < 8) {
         e = launch_back<E, 1, 4, 1, true>(p, &groups, stream);
     } else if (p.d <= 512) {

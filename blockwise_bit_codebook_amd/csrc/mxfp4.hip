@@ -862,7 +862,7 @@ __device__ __forceinline__ void store_tile(const MxProduct& p, T* out, uint8_t* 
 // from past the operand's range, which leaves zeros.
 //
 // The matrix pipes are busy 48 to 57% of the cycles.  Matrix instructions alone, on
-// registers, reach 7.0 PFLOP/s here with random codes (9.6 with zeros: the power
+// registers, reach 6.6 to 7.0 PFLOP/s with random codes (9.6 with zeros: the power
 // bounds them).  8192^3 takes 237 to 265 us over cards and runs (4.15 to 4.6
 // PFLOP/s), 8192 x 11008 x 4096 176 to 206; between them are the tiles' ends, rounds
 // that are not full (1376 tiles are 5.4 of 256) and the reads from LDS, 15% of whose
